@@ -21,7 +21,8 @@ import threading
 from ._build import LIB as LIB_PATH, build  # noqa: F401
 
 __all__ = ["Plan", "mttkrp", "all_modes", "apply_rotations", "ttm", "ttm_workspace_bytes", "ttm_multi",
-           "ttm_multi_workspace_bytes", "probe_fma", "probe_mma",
+           "ttm_multi_workspace_bytes", "embedding", "embedding_grad", "cp_entries", "cp_entries_grad",
+           "grad_norm", "clip_grad_norm", "probe_fma", "probe_mma",
            "MttkrpError",
            "build", "load_library",
            "exported_symbols", "PATH_AUTO", "PATH_SIMT", "PATH_TC", "PATH_TC_TF32", "PATH_TC_EXPLICIT_KRP"]
@@ -99,6 +100,25 @@ def load_library():
         lib.mttkrp_cp_als_scratch_bytes.restype = sz
         lib.mttkrp_cp_als_sweep.argtypes = [vp, vp, vp, vp, vp, ci, vp, vp, sz, vp]
         lib.mttkrp_cp_als_sweep.restype = ci
+        cf = ctypes.c_float
+        lib.mttkrp_embedding.argtypes = [vp, i64, i64, i64, ci, vp, i64, i64, ci, cf, vp, i64, vp]
+        lib.mttkrp_embedding.restype = ci
+        lib.mttkrp_embedding_grad_workspace_bytes.argtypes = [i64, i64, i64]
+        lib.mttkrp_embedding_grad_workspace_bytes.restype = sz
+        lib.mttkrp_embedding_grad.argtypes = [vp, i64, i64, ci, vp, ci, i64, i64, i64, cf, ci, vp, ci, i64, vp, sz, vp]
+        lib.mttkrp_embedding_grad.restype = ci
+        lib.mttkrp_cp_entries.argtypes = [ci, vp, i64, vp, ci, vp, i64, ci, vp, vp]
+        lib.mttkrp_cp_entries.restype = ci
+        lib.mttkrp_cp_entries_grad_workspace_bytes.argtypes = [ci, vp, i64, i64]
+        lib.mttkrp_cp_entries_grad_workspace_bytes.restype = sz
+        lib.mttkrp_cp_entries_grad.argtypes = [ci, vp, i64, vp, ci, vp, i64, ci, vp, vp, vp, sz, vp]
+        lib.mttkrp_cp_entries_grad.restype = ci
+        lib.mttkrp_grad_norm_workspace_bytes.argtypes = [ci]
+        lib.mttkrp_grad_norm_workspace_bytes.restype = sz
+        lib.mttkrp_grad_norm.argtypes = [ci, vp, vp, vp, vp, vp, sz, vp]
+        lib.mttkrp_grad_norm.restype = ci
+        lib.mttkrp_clip_grad_norm.argtypes = [ci, vp, vp, vp, vp, cf, cf, vp, vp, sz, vp]
+        lib.mttkrp_clip_grad_norm.restype = ci
         lib.mttkrp_probe_fma.argtypes = [ci, ci, vp, vp]
         lib.mttkrp_probe_fma.restype = ci
         lib.mttkrp_probe_mma.argtypes = [ci, ci, ci, vp]
@@ -531,6 +551,258 @@ def ttm_multi(X, modes, Ms, outs=None, stream=None, path: str = "auto", workspac
                                 ctypes.c_void_p(ws.data_ptr()) if ws is not None else None, ws_bytes,
                                 _stream_handle(X.device, stream)), "mttkrp_ttm_multi")
     return outs
+
+
+# ---------------------------------------------------------------------------
+# Operators of a sampled fit
+# ---------------------------------------------------------------------------
+
+def _type_code(t, name: str) -> int:
+    """MTTKRP_F32, MTTKRP_BF16 or MTTKRP_F16 for a CUDA tensor of that type."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dt = t.dtype
+    if dt == torch.float32:
+        return 0
+    if dt == torch.bfloat16:
+        return 1
+    if dt == torch.float16:
+        return 2
+    raise TypeError(f"{name} must be float32, bfloat16 or float16")
+
+
+def _index_args(idx, device, name: str = "idx"):
+    """(pointer, count, stride, bytes) of an index tensor: int32 or int64,
+    contiguous of any shape, or one-dimensional with any stride."""
+    import torch
+    if not isinstance(idx, torch.Tensor) or idx.device != device:
+        raise TypeError(f"{name} must be a CUDA tensor on the other tensors' device")
+    if idx.dtype == torch.int64:
+        nbytes = 8
+    elif idx.dtype == torch.int32:
+        nbytes = 4
+    else:
+        raise TypeError(f"{name} must be int32 or int64")
+    if idx.dim() == 1:
+        stride = idx.stride(0)
+    elif idx.is_contiguous():
+        stride = 1
+    else:
+        raise ValueError(f"{name} must be contiguous or one-dimensional")
+    return idx.data_ptr(), idx.numel(), stride, nbytes
+
+
+def _row_stride(t, rows: int, width: int, name: str) -> int:
+    """Elements from one row to the next of a tensor of `rows` rows (all dimensions
+    but the last) of `width` consecutive elements."""
+    if t.dim() == 2:
+        if t.shape[0] != rows or t.shape[1] != width:
+            raise ValueError(f"{name} must be {rows} x {width}")
+        if rows > 1 and (t.stride(1) != 1 and width > 1 or t.stride(0) < width) or rows == 1 and width > 1 \
+                and t.stride(1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be consecutive and rows must not overlap")
+        return t.stride(0) if rows > 1 else width
+    if t.dim() < 1 or t.shape[-1] != width or t.numel() != rows * width or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {rows} rows of {width}")
+    return width
+
+
+def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
+    """out[..., :] = scale * table[idx[...], :] (mttkrp_embedding): rows of a table
+    (rows x width, float32, bfloat16 or float16, rows any distance apart) for int32
+    or int64 indices of any shape.  An index outside the table, e.g. a negative mask,
+    gives a row of zeros.  Returns idx.shape + (width,) of the table's type, written
+    into `out` when given."""
+    import torch
+    lib = load_library()
+    code = _type_code(table, "table")
+    if table.dim() != 2:
+        raise ValueError("table must be rows x width")
+    rows, width = table.shape
+    stride = _row_stride(table, rows, width, "table")
+    ptr, n, idx_stride, nbytes = _index_args(idx, table.device)
+    shape = (*idx.shape, width)
+    if out is None:
+        out = torch.empty(shape, dtype=table.dtype, device=table.device)
+        out_stride = width
+    else:
+        if not isinstance(out, torch.Tensor) or out.device != table.device or out.dtype != table.dtype \
+                or tuple(out.shape) != shape:
+            raise ValueError(f"out must be a {table.dtype} CUDA tensor of shape {shape}")
+        out_stride = _row_stride(out, n, width, "out")
+    _check(lib.mttkrp_embedding(table.data_ptr(), rows, width, stride, code, ptr, n, idx_stride, nbytes, scale,
+                                out.data_ptr(), out_stride, _stream_handle(table.device, stream)),
+           "mttkrp_embedding")
+    return out
+
+
+def embedding_grad(idx, grad, rows: int, scale: float = 1.0, out=None, dtype=None, accumulate: bool = False,
+                   stream=None):
+    """Gradient of `embedding` with respect to its table (mttkrp_embedding_grad):
+    out[v, :] = scale * sum of grad[t, :] over the tokens t with idx[t] = v, in a
+    fixed order.  grad: idx.shape + (width,).  Returns rows x width of `dtype`
+    (float32 by default, or grad's type), written into `out` when given;
+    accumulate adds to `out` and leaves the rows that no token points to alone."""
+    import torch
+    lib = load_library()
+    code = _type_code(grad, "grad")
+    ptr, n, idx_stride, nbytes = _index_args(idx, grad.device)
+    if grad.dim() < 1 or grad.shape[:-1] != idx.shape:
+        raise ValueError("grad must have the shape of idx and one more dimension")
+    width = grad.shape[-1]
+    stride = _row_stride(grad, n, width, "grad")
+    rows = int(rows)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((rows, width), dtype=dtype or torch.float32, device=grad.device)
+        out_stride = width
+    else:
+        if not isinstance(out, torch.Tensor) or out.device != grad.device or out.dim() != 2 \
+                or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out must be a CUDA tensor of rows x width on grad's device, of dtype if that is given")
+        out_stride = _row_stride(out, rows, width, "out")
+    need = lib.mttkrp_embedding_grad_workspace_bytes(n, rows, width)
+    ws = torch.empty(need, dtype=torch.uint8, device=grad.device)
+    _check(lib.mttkrp_embedding_grad(ptr, n, idx_stride, nbytes, grad.data_ptr(), code, stride, rows, width, scale,
+                                     accumulate, out.data_ptr(), _type_code(out, "out"), out_stride, ws.data_ptr(),
+                                     need, _stream_handle(grad.device, stream)), "mttkrp_embedding_grad")
+    return out
+
+
+def _model_args(factors, coords):
+    """(d, dims, R, factor pointers, type code) of a CP model's factors, checked
+    together with its coordinates (samples x d, contiguous)."""
+    import torch
+    factors = list(factors)
+    d = len(factors)
+    if d < 1:
+        raise ValueError("at least one factor is needed")
+    code = _type_code(factors[0], "factor 0")
+    device, dtype, R = factors[0].device, factors[0].dtype, factors[0].shape[-1] if factors[0].dim() else 0
+    for n, a in enumerate(factors):
+        if not isinstance(a, torch.Tensor) or a.device != device or a.dtype != dtype or a.dim() != 2 \
+                or a.shape[1] != R or not a.is_contiguous():
+            raise ValueError(f"factor {n} must be a contiguous {dtype} tensor of {R} columns on {device}")
+    if not isinstance(coords, torch.Tensor) or coords.device != device \
+            or coords.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"coords must be an int32 or int64 tensor on {device}")
+    if coords.dim() != 2 or coords.shape[1] != d or not coords.is_contiguous():
+        raise ValueError(f"coords must be contiguous, samples x {d}")
+    dims = (ctypes.c_int64 * d)(*[a.shape[0] for a in factors])
+    ptrs = (ctypes.c_void_p * d)(*[a.data_ptr() for a in factors])
+    return d, dims, R, ptrs, code
+
+
+def cp_entries(factors, coords, out=None, stream=None):
+    """Entries of the CP model sum_r prod_n A_n(c_n, r) at coordinates
+    (mttkrp_cp_entries): factors I_n x R of one type (float32, bfloat16 or
+    float16), coords samples x d (int32 or int64).  Returns `samples` float32 values;
+    0 where a coordinate is out of range.  Component weights go into a factor, or in
+    as a factor with one row."""
+    import torch
+    lib = load_library()
+    d, dims, R, ptrs, code = _model_args(factors, coords)
+    n, device = coords.shape[0], coords.device
+    if out is None:
+        out = torch.empty(n, dtype=torch.float32, device=device)
+    elif not isinstance(out, torch.Tensor) or out.device != device or out.dtype != torch.float32 \
+            or tuple(out.shape) != (n,) or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous float32 CUDA tensor of {n} elements")
+    _check(lib.mttkrp_cp_entries(d, dims, R, ptrs, code, coords.data_ptr(), n, coords.element_size(),
+                                 out.data_ptr(), _stream_handle(device, stream)), "mttkrp_cp_entries")
+    return out
+
+
+def cp_entries_grad(factors, coords, grad, outs=None, stream=None):
+    """Gradient of `cp_entries` for every factor (mttkrp_cp_entries_grad): for mode n
+    the I_n x R sums over the samples of grad[s] * prod over m != n of A_m(c_m, :),
+    float32, in a fixed order.  grad: one float32 value a sample.  Returns the list
+    of gradients (written into `outs` when given)."""
+    import torch
+    lib = load_library()
+    d, dims, R, ptrs, code = _model_args(factors, coords)
+    n, device = coords.shape[0], coords.device
+    if not isinstance(grad, torch.Tensor) or grad.device != device or grad.dtype != torch.float32 \
+            or tuple(grad.shape) != (n,) or not grad.is_contiguous():
+        raise ValueError(f"grad must be a contiguous float32 CUDA tensor of {n} elements")
+    if outs is None:
+        outs = [torch.empty((i, R), dtype=torch.float32, device=device) for i in dims]
+    else:
+        outs = list(outs)
+        if len(outs) != d:
+            raise ValueError("outs must hold one tensor per factor")
+        for m, o in enumerate(outs):
+            if not isinstance(o, torch.Tensor) or o.device != device or o.dtype != torch.float32 \
+                    or tuple(o.shape) != (dims[m], R) or not o.is_contiguous():
+                raise ValueError(f"outs[{m}] must be a contiguous float32 CUDA tensor of shape {(dims[m], R)}")
+    optrs = (ctypes.c_void_p * d)(*[o.data_ptr() for o in outs])
+    need = lib.mttkrp_cp_entries_grad_workspace_bytes(d, dims, R, n)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _check(lib.mttkrp_cp_entries_grad(d, dims, R, ptrs, code, coords.data_ptr(), n, coords.element_size(),
+                                      grad.data_ptr(), optrs, ws.data_ptr(), need,
+                                      _stream_handle(device, stream)), "mttkrp_cp_entries_grad")
+    return outs
+
+
+def _tensor_args(tensors, name: str):
+    """(pointers, element counts, type codes) of contiguous CUDA tensors on one device."""
+    n = len(tensors)
+    codes = [_type_code(t, f"{name}[{k}]") for k, t in enumerate(tensors)]
+    device = tensors[0].device
+    for k, t in enumerate(tensors):
+        if not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name}[{k}] must be contiguous and on {device}")
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), (ctypes.c_int * n)(*codes))
+
+
+def grad_norm(tensors, stream=None):
+    """sqrt of the sum of squares over all elements of a list of CUDA tensors
+    (mttkrp_grad_norm), as a float32 scalar on the device.  The tensors are
+    contiguous, float32, bfloat16 or float16 in any mix, on one device."""
+    return _norm_and_clip(tensors, None, None, None, stream)
+
+
+def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, stream=None):
+    """Multiplies every tensor of a list by min(1, max_norm / (norm + eps)), norm
+    being `grad_norm` of the list (mttkrp_clip_grad_norm), in place or, when `outs` is
+    given, into its tensors (each of its input's size and type).  Returns the norm
+    before clipping as a float32 scalar on the device."""
+    return _norm_and_clip(tensors, float(max_norm), float(eps), outs, stream)
+
+
+def _norm_and_clip(tensors, max_norm, eps, outs, stream):
+    import torch
+    lib = load_library()
+    tensors = list(tensors)
+    n = len(tensors)
+    if n < 1:
+        raise ValueError("at least one tensor is needed")
+    ptrs, numels, codes = _tensor_args(tensors, "tensors")
+    device = tensors[0].device
+    optrs = None
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError("outs must hold one tensor per input")
+        for k, (o, t) in enumerate(zip(outs, tensors)):
+            if not isinstance(o, torch.Tensor) or o.device != device or o.dtype != t.dtype \
+                    or o.numel() != t.numel() or not o.is_contiguous():
+                raise ValueError(f"outs[{k}] must be a contiguous {t.dtype} CUDA tensor of {t.numel()} elements")
+        optrs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    need = lib.mttkrp_grad_norm_workspace_bytes(n)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    st = _stream_handle(device, stream)
+    if max_norm is None:
+        _check(lib.mttkrp_grad_norm(n, ptrs, numels, codes, norm.data_ptr(), ws.data_ptr(), need, st),
+               "mttkrp_grad_norm")
+    else:
+        _check(lib.mttkrp_clip_grad_norm(n, ptrs, numels, codes, optrs, max_norm, eps, norm.data_ptr(),
+                                         ws.data_ptr(), need, st), "mttkrp_clip_grad_norm")
+    return norm
 
 
 def probe_fma(blocks: int, iters: int, out, stream=None):

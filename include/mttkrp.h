@@ -34,7 +34,9 @@
  * (mttkrp_cp_als_sweep, on a plan), and two dense kernels of the Jacobi-type
  * Tucker diagonalization setting that take plain pointers and no plan: the
  * mode-n product (mttkrp_ttm) and Givens rotations along a mode
- * (mttkrp_apply_rotations).
+ * (mttkrp_apply_rotations).  For fitting on samples of entries instead of full
+ * sweeps there are row lookups with their gradient, CP model entries with the
+ * gradient of every factor, and clipping by the norm over many tensors.
  *
  * Errors: every int-returning call returns MTTKRP_OK (0) or one of the codes
  * below; nothing is thrown across the ABI.  mttkrp_strerror() names a code and
@@ -328,6 +330,107 @@ size_t mttkrp_ttm_multi_workspace_bytes(int d, const int64_t* dims, int nmodes, 
 int mttkrp_ttm_multi(int d, const int64_t* dims, const float* X, int nmodes, const int* modes,
                      const float* const* Ms, const int64_t* Js, float* const* Ts, void* workspace,
                      size_t workspace_bytes, void* stream);
+
+/*
+ * Operators of a sampled fit: rows of factor matrices (or of any table) for a
+ * batch of indices and their gradient, the entries of a CP model at given
+ * coordinates and the gradient of every factor, and the norm over many gradients
+ * with clipping.  (No counterpart on the pages: they fit with full sweeps.)
+ *
+ * Types: MTTKRP_F32, MTTKRP_BF16, MTTKRP_F16 for tables, factors and gradients;
+ * products and sums are fp32 (the norm's: fp32 over 16 elements, then fp64), each
+ * result is rounded once.  Pointers need the alignment of their element; rows that
+ * start at multiples of 16 bytes (fp32 results of 16-bit gradients: 32) are read
+ * and written in vectors, others one element at a time.
+ * Indices: int32 or int64 (idx_bytes 4 or 8) on the device, and so checked there:
+ * a token (or sample) with an index outside [0, rows) takes no part, which makes
+ * any negative index a mask.  At most 2^31 - 1 tokens or samples and rows.
+ * No result may overlap an input, except where a call says so.
+ * Every call enqueues on `stream` and returns without synchronising; results are
+ * bitwise reproducible (no floating-point atomics, every sum in a fixed order).
+ * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_WORKSPACE (a workspace missing, too small
+ * or not 256-byte aligned), MTTKRP_ERR_CUDA.
+ */
+enum mttkrp_type { MTTKRP_F32 = 0, MTTKRP_BF16 = 1, MTTKRP_F16 = 2 };
+
+/*
+ * Lookup with scaling: out[t, :] = scale * table[idx[t], :], a row of zeros where
+ * idx[t] is outside [0, rows).
+ *
+ * table     rows x width, consecutive elements in a row, rows table_stride elements
+ *           apart (table_stride >= width); width in [1, 65536].
+ * idx       n indices, idx_stride elements apart (a column of a coordinate list has
+ *           the list's width as stride).
+ * out       n x width of the table's type, rows out_stride >= width elements apart.
+ */
+int mttkrp_embedding(const void* table, int64_t rows, int64_t width, int64_t table_stride, int type, const void* idx,
+                     int64_t n, int64_t idx_stride, int idx_bytes, float scale, void* out, int64_t out_stride,
+                     void* stream);
+
+/*
+ * Gradient of the lookup with respect to the table, by sorted tokens:
+ *     out[v, :] = scale * sum over t with idx[t] = v of grad[t, :]
+ * (accumulate != 0: added to out[v, :]; rows no token points to are then left
+ * alone, else they become zero).  grad rows of tokens outside [0, rows) are not read.
+ *
+ * grad      n x width of `type`, rows grad_stride >= width elements apart.
+ * out       rows x width of out_type (MTTKRP_F32 or `type`), out_stride >= width.
+ * workspace device, 256-byte aligned, mttkrp_embedding_grad_workspace_bytes() bytes
+ *           (0 for invalid arguments).
+ */
+size_t mttkrp_embedding_grad_workspace_bytes(int64_t n, int64_t rows, int64_t width);
+int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int idx_bytes, const void* grad, int type,
+                          int64_t grad_stride, int64_t rows, int64_t width, float scale, int accumulate, void* out,
+                          int out_type, int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Entries of the CP model with factors A_n (dims[n] x R, row-major) at n_samples
+ * coordinates:
+ *     out[s] = sum over r of prod over n of A_n(c_sn, r),
+ * 0 where a coordinate is out of range.  Weights of the components (the lambda of
+ * mttkrp_cp_als_sweep) go in as a factor with one row, or into one of the factors.
+ *
+ * d, dims   the model's order (1 <= d <= MTTKRP_MAX_ORDER) and shape.
+ * factors   HOST array of d device pointers, all of `type`, contiguous.
+ * coords    n_samples x d indices, row-major (sample s, mode n at s * d + n).
+ */
+int mttkrp_cp_entries(int d, const int64_t* dims, int64_t R, const void* const* factors, int type, const void* coords,
+                      int64_t n_samples, int idx_bytes, float* out, void* stream);
+
+/*
+ * Its gradient for every factor, given the gradient g of a loss with respect to
+ * the entries (an MTTKRP of the sparse tensor that holds g at the coordinates):
+ *     outs[n](i, :) = sum over s with c_sn = i of g[s] * prod over m != n of A_m(c_sm, :)
+ * outs      HOST array of d device pointers, outs[n] dims[n] x R fp32, overwritten.
+ * Samples with a coordinate out of range take no part (their g is not read).
+ */
+size_t mttkrp_cp_entries_grad_workspace_bytes(int d, const int64_t* dims, int64_t R, int64_t n_samples);
+int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* const* factors, int type,
+                           const void* coords, int64_t n_samples, int idx_bytes, const float* g, float* const* outs,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Norm over many tensors, and clipping by it:
+ *     norm = sqrt(sum over all tensors and elements of x^2),
+ *     y = x * min(1, max_norm / (norm + eps)).
+ * A norm that is infinite or NaN goes through the formula (coefficient 0 or NaN).
+ *
+ * n         number of tensors (0: norm 0), at most 2^20.
+ * tensors   HOST array of n device pointers (contiguous; NULL allowed where
+ *           numels[k] is 0), numels[k] elements of types[k] each (HOST arrays).
+ * outs      HOST array of n device pointers that receive y, each of its tensor's
+ *           type; outs[k] == tensors[k] clips in place (and writes nothing when the
+ *           coefficient is 1).  No result may overlap another one or another tensor.  mttkrp_clip_grad_norm with outs == NULL clips every
+ *           tensor in place.
+ * norm      device, one float (output).
+ * workspace device, 256-byte aligned, mttkrp_grad_norm_workspace_bytes(n) bytes.
+ */
+size_t mttkrp_grad_norm_workspace_bytes(int n);
+int mttkrp_grad_norm(int n, const void* const* tensors, const int64_t* numels, const int* types, float* norm,
+                     void* workspace, size_t workspace_bytes, void* stream);
+int mttkrp_clip_grad_norm(int n, const void* const* tensors, const int64_t* numels, const int* types,
+                          void* const* outs, float max_norm, float eps, float* norm, void* workspace,
+                          size_t workspace_bytes, void* stream);
 
 /*
  * Peak probes for the roofline of a benchmark (measurement only; the pages have
