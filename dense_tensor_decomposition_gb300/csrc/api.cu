@@ -1204,7 +1204,7 @@ int mttkrp_embedding(const void* table, int64_t rows, int64_t width, int64_t tab
 
 size_t mttkrp_embedding_grad_workspace_bytes(int64_t n, int64_t rows, int64_t width) {
     if (n < 0 || n > kMaxTokens || rows < 1 || rows > kMaxTokens || width < 1 || width > kMaxWidth) return 0;
-    return row_sum_workspace_bytes(n, 1, width);
+    return row_sum_workspace_bytes(IndexArgs{nullptr, 4, 1, n, 1, {rows}}, width);
 }
 
 int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int idx_bytes, const void* grad, int type,
@@ -1221,9 +1221,9 @@ int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int id
     if (overlap(out, no, grad, span_bytes(n, width, grad_stride, type_bytes(type))) ||
         overlap(out, no, idx, span_bytes(n, 1, idx_stride, idx_bytes)))
         return fail(MTTKRP_ERR_INVALID, "the result overlaps the gradient or the indices");
-    if (int rc = check_workspace(workspace, workspace_bytes, row_sum_workspace_bytes(n, 1, width))) return rc;
     RowSumArgs a{};
     a.index = IndexArgs{idx, idx_bytes, idx_stride, n, 1, {rows}};
+    if (int rc = check_workspace(workspace, workspace_bytes, row_sum_workspace_bytes(a.index, width))) return rc;
     a.width = width;
     a.type = type;
     a.grad = grad;
@@ -1263,7 +1263,12 @@ int mttkrp_cp_entries(int d, const int64_t* dims, int64_t R, const void* const* 
 size_t mttkrp_cp_entries_grad_workspace_bytes(int d, const int64_t* dims, int64_t R, int64_t n_samples) {
     if (d < 1 || d > kMaxD || dims == nullptr || R < 1 || R > kMaxR || n_samples < 0 || n_samples > kMaxTokens)
         return 0;
-    return row_sum_workspace_bytes(n_samples, d, R);
+    IndexArgs index{nullptr, 4, d, n_samples, d, {}};
+    for (int m = 0; m < d; ++m) {
+        if (dims[m] < 1 || dims[m] > kMaxTokens) return 0;
+        index.rows[m] = dims[m];
+    }
+    return row_sum_workspace_bytes(index, R);
 }
 
 int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* const* factors, int type,
@@ -1288,7 +1293,8 @@ int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* co
         a.factor[m] = factors[m];
         a.out[m] = outs[m];
     }
-    if (int rc = check_workspace(workspace, workspace_bytes, row_sum_workspace_bytes(n_samples, d, R))) return rc;
+    if (int rc = check_workspace(workspace, workspace_bytes, row_sum_workspace_bytes(a.index, R))) return rc;
+    a.model = true;
     a.width = R;
     a.type = type;
     a.g = g;

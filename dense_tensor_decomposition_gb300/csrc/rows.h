@@ -37,10 +37,11 @@ struct LookupArgs {
 
 // Sums of rows over the tokens of each index: for table m,
 //   out[m][v, :] (+)= scale * sum over tokens t with index v of row(m, t, :)
-// row = grad[t, :] for a lookup's gradient (factor[] unused), or
+// row = grad[t, :] for a lookup's gradient, or
 // g[t] * prod over l != m of factor[l][idx(t, l), :] for a CP model's.
 struct RowSumArgs {
     IndexArgs index;
+    bool model;             // rows are products of factor rows
     int64_t width;
     int type;               // of grad or the factors (MTTKRP_F32, ...)
     const void* grad;
@@ -63,7 +64,7 @@ struct EntriesArgs {
 };
 
 cudaError_t launch_lookup(const LookupArgs& a, int type, cudaStream_t s);
-size_t row_sum_workspace_bytes(int64_t n, int d, int64_t width);
+size_t row_sum_workspace_bytes(const IndexArgs& index, int64_t width);
 cudaError_t launch_row_sum(const RowSumArgs& a, cudaStream_t s);
 cudaError_t launch_entries(const EntriesArgs& a, int type, cudaStream_t s);
 
