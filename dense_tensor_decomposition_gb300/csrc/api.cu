@@ -1204,7 +1204,7 @@ int mttkrp_embedding(const void* table, int64_t rows, int64_t width, int64_t tab
 
 size_t mttkrp_embedding_grad_workspace_bytes(int64_t n, int64_t rows, int64_t width) {
     if (n < 0 || n > kMaxTokens || rows < 1 || rows > kMaxTokens || width < 1 || width > kMaxWidth) return 0;
-    return row_sum_workspace_bytes(IndexArgs{nullptr, 4, 1, n, 1, {rows}}, width);
+    return lookup_grad_workspace_bytes(IndexArgs{nullptr, 4, 1, n, 1, {rows}}, width);
 }
 
 int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int idx_bytes, const void* grad, int type,
@@ -1223,7 +1223,7 @@ int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int id
         return fail(MTTKRP_ERR_INVALID, "the result overlaps the gradient or the indices");
     RowSumArgs a{};
     a.index = IndexArgs{idx, idx_bytes, idx_stride, n, 1, {rows}};
-    if (int rc = check_workspace(workspace, workspace_bytes, row_sum_workspace_bytes(a.index, width))) return rc;
+    if (int rc = check_workspace(workspace, workspace_bytes, lookup_grad_workspace_bytes(a.index, width))) return rc;
     a.width = width;
     a.type = type;
     a.grad = grad;
@@ -1234,7 +1234,7 @@ int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int id
     a.out_type = out_type;
     a.accumulate = accumulate != 0;
     a.ws = workspace;
-    cudaError_t err = launch_row_sum(a, static_cast<cudaStream_t>(stream));
+    cudaError_t err = launch_lookup_grad(a, static_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return fail(MTTKRP_ERR_CUDA, "lookup gradient launch: %s", cudaGetErrorString(err));
     return MTTKRP_OK;
 }
@@ -1255,7 +1255,8 @@ int mttkrp_cp_entries(int d, const int64_t* dims, int64_t R, const void* const* 
         return fail(MTTKRP_ERR_INVALID, "the result overlaps the coordinates");
     a.width = R;
     a.out = out;
-    cudaError_t err = launch_entries(a, type, static_cast<cudaStream_t>(stream));
+    a.type = type;
+    cudaError_t err = launch_entries(a, static_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return fail(MTTKRP_ERR_CUDA, "entries launch: %s", cudaGetErrorString(err));
     return MTTKRP_OK;
 }
@@ -1268,7 +1269,7 @@ size_t mttkrp_cp_entries_grad_workspace_bytes(int d, const int64_t* dims, int64_
         if (dims[m] < 1 || dims[m] > kMaxTokens) return 0;
         index.rows[m] = dims[m];
     }
-    return row_sum_workspace_bytes(index, R);
+    return entries_grad_workspace_bytes(index, R);
 }
 
 int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* const* factors, int type,
@@ -1293,8 +1294,7 @@ int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* co
         a.factor[m] = factors[m];
         a.out[m] = outs[m];
     }
-    if (int rc = check_workspace(workspace, workspace_bytes, row_sum_workspace_bytes(a.index, R))) return rc;
-    a.model = true;
+    if (int rc = check_workspace(workspace, workspace_bytes, entries_grad_workspace_bytes(a.index, R))) return rc;
     a.width = R;
     a.type = type;
     a.g = g;
@@ -1302,7 +1302,7 @@ int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* co
     a.out_stride = R;
     a.out_type = MTTKRP_F32;
     a.ws = workspace;
-    cudaError_t err = launch_row_sum(a, static_cast<cudaStream_t>(stream));
+    cudaError_t err = launch_entries_grad(a, static_cast<cudaStream_t>(stream));
     if (err != cudaSuccess) return fail(MTTKRP_ERR_CUDA, "entries gradient launch: %s", cudaGetErrorString(err));
     return MTTKRP_OK;
 }

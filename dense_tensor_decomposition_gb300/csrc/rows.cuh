@@ -1,0 +1,88 @@
+// Device helpers of the operators on rows: indices, scans.
+#pragma once
+
+#include <atomic>
+
+#include "sort.h"
+#include "types.cuh"
+
+namespace mk {
+
+__host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+constexpr size_t elem_bytes(int type) { return type == MTTKRP_F32 ? 4 : 2; }
+
+constexpr int kSms = 152;
+
+// Dynamic shared memory that a CTA may ask for, of the 227 KB that it can have.
+constexpr size_t kMaxSmem = 226 * 1024;
+
+// lets a kernel have that much on the current device
+template <auto kernel>
+cudaError_t allow_smem() {
+    static std::atomic<uint64_t> done{0};       // a bit a device; setting it twice is harmless
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1) != 0)) return e;
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kMaxSmem - attr.sharedSizeBytes));
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    return e;
+}
+
+__device__ __forceinline__ int64_t index_at(const IndexArgs& a, int64_t t, int m) {
+    const int64_t at = t * a.stride + m;
+    return a.bytes == 8 ? static_cast<const int64_t*>(a.idx)[at] : (int64_t) static_cast<const int32_t*>(a.idx)[at];
+}
+
+// the row that token t points to in column m, kNone where it takes no part
+__device__ __forceinline__ uint32_t sort_key(const IndexArgs& a, int64_t t, int m) {
+    uint32_t key = kNone;
+    bool inside = true;
+    for (int l = 0; l < a.d; ++l) {
+        const int64_t v = index_at(a, t, l);
+        inside = inside && v >= 0 && v < a.rows[l];
+        if (l == m) key = (uint32_t)v;
+    }
+    return inside ? key : kNone;
+}
+
+// Sum of x over the threads before this one of a CTA of 32 warps, and over all (in
+// `all`); sums: one word a warp.  The threads wait twice.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums, uint32_t& all) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t scan = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += up;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = scan;
+    __syncthreads();
+    const uint32_t w = sums[lane];
+    uint32_t wscan = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, wscan, o);
+        if (lane >= o) wscan += up;
+    }
+    all = __shfl_sync(0xFFFFFFFFu, wscan, 31);
+    const uint32_t before = __shfl_sync(0xFFFFFFFFu, wscan - w, warp);
+    return before + scan - x;
+}
+
+// row of a group's table for the sample at token t
+__device__ __forceinline__ uint32_t table_row(const IndexArgs& a, const Tables::Group& g, int64_t t) {
+    uint32_t row = 0;
+    for (int k = 0; k < g.modes; ++k)
+        row = row * (uint32_t)a.rows[g.mode[k]] + (uint32_t)index_at(a, t, g.mode[k]);
+    return g.first + row;
+}
+
+}  // namespace mk

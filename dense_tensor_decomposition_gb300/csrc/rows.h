@@ -1,6 +1,7 @@
-// Operators on rows of tables (rows.cu): lookup of a table's rows, the gradient
-// of a lookup by sorted tokens, and the entries of a CP model at coordinates with
-// the gradient of every factor.  Nothing here is part of the C ABI.
+// Operators on rows of tables: lookup of a table's rows and its gradient by sorted
+// tokens (rows.cu), the entries of a CP model at coordinates and the gradient of
+// every factor (model.cu), norm and clipping (gradnorm.cu).  Nothing here is part of
+// the C ABI.
 //
 // Where an index is outside its table the token (or sample) takes no part.
 #pragma once
@@ -41,7 +42,6 @@ struct LookupArgs {
 // g[t] * prod over l != m of factor[l][idx(t, l), :] for a CP model's.
 struct RowSumArgs {
     IndexArgs index;
-    bool model;             // rows are products of factor rows
     int64_t width;
     int type;               // of grad or the factors (MTTKRP_F32, ...)
     const void* grad;
@@ -59,14 +59,18 @@ struct RowSumArgs {
 struct EntriesArgs {
     IndexArgs index;
     int64_t width;
+    int type;
     const void* factor[MTTKRP_MAX_ORDER];
     float* out;
 };
 
 cudaError_t launch_lookup(const LookupArgs& a, int type, cudaStream_t s);
-size_t row_sum_workspace_bytes(const IndexArgs& index, int64_t width);
-cudaError_t launch_row_sum(const RowSumArgs& a, cudaStream_t s);
-cudaError_t launch_entries(const EntriesArgs& a, int type, cudaStream_t s);
+cudaError_t launch_lookup_grad(const RowSumArgs& a, cudaStream_t s);
+size_t lookup_grad_workspace_bytes(const IndexArgs& index, int64_t width);
+
+cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s);
+size_t entries_grad_workspace_bytes(const IndexArgs& index, int64_t width);
+cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s);
 
 // Norm over many tensors and clipping by it (gradnorm.cu).  outs = nullptr: the
 // norm alone.

@@ -1,0 +1,47 @@
+// Sort of tokens by the row that they point to (sort.cu), as the sums over sorted
+// tokens use it (sums.cuh).
+#pragma once
+
+#include "rows.h"
+
+namespace mk {
+
+constexpr uint32_t kNone = 0xFFFFFFFFu;     // no row: above every table's last one
+
+// Factors of a CP model as tables in shared memory: neighbouring modes form groups,
+// and a group's table has the products of its modes' rows, one for every combination
+// of their indices (the last mode's fastest).
+constexpr int kMaxGroups = 4;
+
+struct Tables {
+    int groups;
+    int rows;                               // of all groups
+    struct Group {
+        int modes;
+        int mode[MTTKRP_MAX_ORDER];
+        int first;                          // the group's first row
+    } group[kMaxGroups];
+};
+
+// Sorted tokens: d lists of n entries of `bytes` bytes, which begin with the row
+// (kNone, behind all others, for tokens that take no part).  8 bytes: the token
+// follows.  16 bytes: g of the token, then its row in the table of each group of
+// `tables` as 16-bit numbers.
+struct Sorted {
+    const char* entries;
+    int bytes;
+};
+
+struct SortPlan {
+    int passes, bits, ctas;
+    int64_t per_cta;
+    size_t pairs, counts;                   // bytes of one buffer of entries, and of the counts
+    size_t total() const { return 2 * pairs + counts; }
+};
+
+SortPlan plan_sort(const IndexArgs& index, int entry_bytes);
+// tables: nullptr, or one for each index column, for entries of 16 bytes
+cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, const Tables* tables, const float* g,
+                        Sorted& sorted, cudaStream_t s);
+
+}  // namespace mk

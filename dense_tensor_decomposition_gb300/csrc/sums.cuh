@@ -1,0 +1,489 @@
+// Sums of rows over the tokens that point to them: for every row of a table a term of
+// each of its tokens is added, in the order of the tokens, so that results repeat bit
+// by bit.  Two ways:
+//   * few tokens (own_kernel): one launch.  Every CTA owns some of the rows, finds the
+//     tokens that point to them, groups them by row and writes its rows, zeros included.
+//   * many tokens: the tokens are sorted by row (sort.cu), and CTAs walk the sorted
+//     tokens in tiles of equal length, however long a row's run of tokens is
+//     (row_sum_kernel); runs that cross tile borders are joined, and rows without
+//     tokens set to zero, by a last launch (finish_kernel).
+// Both add with sum_list(), which splits a list of sorted tokens over groups of lanes
+// and joins the runs that cross the groups' borders.
+#pragma once
+
+#include "rows.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------- sums over a list of sorted tokens
+
+template <typename TO, int VEC>
+__device__ __forceinline__ void write_row(const RowSumArgs& a, int m, uint32_t v, int64_t col, const float* acc) {
+    Pack<TO, VEC>* p = reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out[m]) + (int64_t)v * a.out_stride + col);
+    Pack<TO, VEC> x;
+    if (a.accumulate) x = *p;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const float s = a.scale * acc[e];
+        x.v[e] = from_f32<TO>(a.accumulate ? to_f32(x.v[e]) + s : s);
+    }
+    *p = x;
+}
+
+// What lies around a list: whether its first run began before it, whether its last
+// one goes on after it, and where such runs' sums go (indexed by column).
+struct Around {
+    bool before, after;
+    float* head;
+    float* tail;
+};
+
+// Adds the terms of a list of `count` >= 1 tokens sorted by row over the columns from
+// col0 on, and writes the finished rows.  list(p): entry p, its row first (.x); Terms
+// loads the terms of B entries at VEC columns, all before the first is used.  A group of
+// L = 2^log2L threads (of kN in all, which sync() makes wait for one another) walks
+// count / groups consecutive tokens; a lane has VEC columns.  A run that crosses
+// groups is finished by the group in which it began, from the other groups' parts
+// in `heads` (kN * VEC floats), in the order of the groups.
+template <typename TO, int VEC, int B, typename Terms, int kN, typename Context, typename List, typename Row,
+          typename Sync>
+__device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Context& context, const List& list,
+                                         const Row& row_of, int count, int log2L, int64_t col0, float* heads,
+                                         const Around& around, const Sync& sync) {
+    const int L = 1 << log2L, groups = kN >> log2L;
+    const int group = threadIdx.x >> log2L, lane = threadIdx.x & (L - 1);
+    const int64_t col = col0 + lane * VEC;
+    const bool on = col < a.width;
+    const int share = (count + groups - 1) / groups;
+    const int p0 = group * share < count ? group * share : count;
+    const int p1 = p0 + share < count ? p0 + share : count;
+    float acc[VEC];
+    auto put = [&](float* dst) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dst[e] = acc[e];
+    };
+    auto add = [&](const float* src) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] += src[e];
+    };
+    float* own_head = heads + (size_t)threadIdx.x * VEC;
+    uint32_t cur = 0;
+    bool open = false;          // the run at the end began in this group and goes on
+    if (p0 < p1 && on) {
+        cur = list(p0).x;
+        bool began_before = p0 > 0 ? list(p0 - 1).x == cur : around.before;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+        for (int p = p0; p < p1; p += B) {
+            decltype(list(0)) entry[B];
+#pragma unroll
+            for (int j = 0; j < B; ++j) entry[j] = list(p + j < p1 ? p + j : p);
+            Terms terms;
+            terms.load(context, entry, col);
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                if (p + j < p1) {
+                    if (entry[j].x != cur) {
+                        if (began_before) put(own_head);
+                        else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+                        began_before = false;
+                        cur = entry[j].x;
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) acc[e] += terms.at(j, e);
+                }
+            }
+        }
+        const bool goes_on = p1 < count ? list(p1).x == cur : around.after;
+        if (began_before) put(own_head);
+        else if (goes_on) open = true;
+        else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+    }
+    sync();
+    if (!on) return;
+    if (open) {
+        int g = group + 1;
+        for (; g * share < count && list(g * share).x == cur; ++g) add(heads + ((size_t)(g << log2L) + lane) * VEC);
+        if (g * share >= count && around.after && list(count - 1).x == cur) put(around.tail + col);
+        else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+    }
+    if (group == 0 && around.before) {
+        const uint32_t first = list(0).x;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = own_head[e];
+        for (int g = 1; g * share < count && list(g * share).x == first; ++g)
+            add(heads + ((size_t)(g << log2L) + lane) * VEC);
+        put(around.head + col);
+    }
+}
+
+// Zeros for those of `rows` local rows, from local row r0 on, that no token points
+// to, by one warp; row_of gives a local row's number in the table (kNone: none).
+template <typename TO, int VEC, typename Touched, typename Row>
+__device__ __forceinline__ void zero_rows(const RowSumArgs& a, int m, uint32_t r0, uint32_t rows, int64_t col0,
+                                          uint32_t vecs, const Touched& touched, const Row& row_of) {
+    Pack<TO, VEC> zero;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) zero.v[e] = from_f32<TO>(0.f);
+    for (uint32_t i = threadIdx.x & 31; i < rows * vecs; i += 32) {
+        const uint32_t r = i / vecs, c = i - r * vecs;
+        if (touched(r0 + r)) continue;
+        const uint32_t v = row_of(r0 + r);
+        if (v == kNone) continue;
+        *reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out[m]) + (int64_t)v * a.out_stride + col0 +
+                                          (int64_t)c * VEC) = zero;
+    }
+}
+
+// what the terms of (row, token) entries are made from
+struct TermsOf {
+    const RowSumArgs& a;
+    int m;
+};
+
+// ---------------------------------------------------------------- few tokens: one launch
+
+constexpr int kOwnThreads = 1024;
+constexpr int kOwnWarps = kOwnThreads / 32;
+constexpr int kSumThreads = 512;        // of which these add, while the others write zeros
+constexpr int kTokenBits = 14;
+constexpr int kOwnTokens = 1 << kTokenBits;
+constexpr int kOwnRows = 1 << 13;       // rows of a CTA
+
+// Owners: blocks of 2^row_shift consecutive rows go to the CTAs (blockIdx.x) in turn,
+// so that frequent rows, which often have small numbers, are spread.
+struct OwnArgs {
+    RowSumArgs a;
+    int row_shift;
+    uint32_t owned;         // most rows a CTA owns
+    uint32_t per_warp;      // tokens a warp looks at
+    int log2L;
+    int64_t part;           // columns of a CTA (blockIdx.y)
+};
+
+template <typename TO, int VEC, int B, typename Terms>
+__global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_constant__ OwnArgs o) {
+    extern __shared__ float4 own_smem[];
+    const RowSumArgs& a = o.a;
+    float* heads = reinterpret_cast<float*>(own_smem);                          // kSumThreads * VEC
+    uint32_t* cursor = reinterpret_cast<uint32_t*>(heads + kSumThreads * VEC);  // owned: tokens of each row, then their places
+    uint32_t* touched = cursor + o.owned;                                       // a bit for each owned row
+    uint32_t* found = touched + (o.owned + 31) / 32;                            // tokens of the CTA's rows, a part a warp
+    uint32_t* list = found + kOwnWarps * o.per_warp;                            // the same without gaps, then sorted
+    __shared__ uint32_t warp_found[kOwnWarps], sums[kOwnWarps], next_unit;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m = blockIdx.z;
+    const uint32_t G = gridDim.x, n = (uint32_t)a.index.n, rows = (uint32_t)a.index.rows[m];
+    const uint32_t low = (1u << o.row_shift) - 1;
+    auto row_of = [&](uint32_t r) -> uint32_t {
+        const uint64_t v = (((uint64_t)(r >> o.row_shift) * G + blockIdx.x) << o.row_shift) | (r & low);
+        return v < rows ? (uint32_t)v : kNone;
+    };
+
+    // the CTA's tokens, as (owned row, token), in order in every warp's part
+    for (uint32_t i = threadIdx.x; i < o.owned; i += kOwnThreads) cursor[i] = 0;
+    if (threadIdx.x == 0) next_unit = 0;
+    __syncthreads();
+    uint32_t count = 0;
+    for (uint32_t k = 0; k < o.per_warp; k += 32) {
+        const uint32_t t = warp * o.per_warp + k + lane;
+        const uint32_t v = t < n ? sort_key(a.index, t, m) : kNone;
+        const uint32_t block = v >> o.row_shift, turn = block / G;
+        const bool mine = v != kNone && block - turn * G == blockIdx.x;
+        const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
+        if (mine) {
+            const uint32_t r = (turn << o.row_shift) | (v & low);
+            found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
+            atomicAdd(cursor + r, 1u);
+        }
+        count += __popc(ballot);
+    }
+    if (lane == 0) warp_found[warp] = count;
+    __syncthreads();
+    // gaps out; the counts become the rows' first places
+    uint32_t total = 0, base = 0;
+    for (int w = 0; w < kOwnWarps; ++w) {
+        const uint32_t c = warp_found[w];
+        base += w < warp ? c : 0;
+        total += c;
+    }
+    for (uint32_t k = lane; k < count; k += 32) list[base + k] = found[warp * o.per_warp + k];
+    const uint32_t per = (o.owned + kOwnThreads - 1) / kOwnThreads;
+    uint32_t mine = 0, all;
+    for (uint32_t k = 0; k < per; ++k) {
+        const uint32_t r = threadIdx.x * per + k;
+        mine += r < o.owned ? cursor[r] : 0;
+    }
+    uint32_t at = block_scan(mine, sums, all);
+    for (uint32_t r = threadIdx.x; r < (o.owned + 31) / 32 * 32; r += kOwnThreads) {
+        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, r < o.owned && cursor[r] != 0);
+        if (lane == 0) touched[r / 32] = bits;
+    }
+    __syncthreads();
+    for (uint32_t k = 0; k < per; ++k) {
+        const uint32_t r = threadIdx.x * per + k;
+        if (r >= o.owned) break;
+        const uint32_t c = cursor[r];
+        cursor[r] = at;
+        at += c;
+    }
+    __syncthreads();
+
+    const int64_t col0 = (int64_t)blockIdx.y * o.part;
+    if (warp < kSumThreads / 32 && total > 0) {
+        auto sync = [] { asm volatile("barrier.sync 1, %0;" ::"n"(kSumThreads) : "memory"); };
+        // in order of the tokens within each row: one warp places them 32 at a time
+        if (warp == 0) {
+            for (uint32_t k = 0; k < total; k += 32) {
+                const uint32_t x = k + lane < total ? list[k + lane] : kNone;
+                const uint32_t r = x >> kTokenBits;
+                const uint32_t peers = __match_any_sync(0xFFFFFFFFu, r);
+                uint32_t to = 0;
+                if (k + lane < total) to = cursor[r] + __popc(peers & ((1u << lane) - 1));
+                __syncwarp();
+                if (k + lane < total) {
+                    found[to] = x;
+                    if ((peers >> lane) == 1u) cursor[r] = to + 1;      // the last of its row
+                }
+                __syncwarp();
+            }
+        }
+        sync();
+        auto at_place = [&](int p) { return make_uint2(found[p] >> kTokenBits, found[p] & (kOwnTokens - 1)); };
+        sum_list<TO, VEC, B, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, (int)total, o.log2L, col0,
+                                                 heads, Around{false, false, nullptr, nullptr}, sync);
+    }
+    if (a.accumulate) return;
+    const uint32_t vecs = (uint32_t)((a.width - col0 < o.part ? a.width - col0 : o.part) / VEC);
+    const uint32_t unit = vecs >= 1024 ? 1 : 1024 / vecs;
+    auto is_touched = [&](uint32_t r) { return r >= o.owned || (touched[r >> 5] >> (r & 31) & 1u) != 0; };
+    for (;;) {
+        uint32_t u = 0;
+        if (lane == 0) u = atomicAdd(&next_unit, 1u);
+        u = __shfl_sync(0xFFFFFFFFu, u, 0);
+        if ((uint64_t)u * unit >= o.owned) break;
+        zero_rows<TO, VEC>(a, m, u * unit, unit, col0, vecs, is_touched, row_of);
+    }
+}
+
+// ---------------------------------------------------------------- many tokens
+
+constexpr int kTile = 256;              // sorted tokens of a CTA of row_sum_kernel
+
+struct SumArgs {
+    RowSumArgs a;
+    Sorted sorted;
+    float* part;            // d x tiles x 2 x width: sums of the tile's first run that began before, of its last that goes on
+    int64_t tile;           // tokens of a tile
+    int64_t tiles;
+    int log2L;
+    int64_t columns;        // columns of a CTA (blockIdx.y)
+};
+
+__device__ __forceinline__ uint32_t key_at(const SumArgs& s, int m, int64_t p) {
+    return *reinterpret_cast<const uint32_t*>(s.sorted.entries + (m * s.a.index.n + p) * s.sorted.bytes);
+}
+
+template <typename TO, int VEC, int B, typename Terms>
+__global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant__ SumArgs s) {
+    static_assert(kTile == kThreads, "a thread stages one entry");
+    __shared__ uint2 pairs[kTile];
+    __shared__ float4 heads[(kThreads * VEC + 3) / 4];
+    const RowSumArgs& a = s.a;
+    const int m = blockIdx.z;
+    const int64_t n = a.index.n;
+    const uint2* sorted = reinterpret_cast<const uint2*>(s.sorted.entries) + m * n;
+    const int64_t col0 = (int64_t)blockIdx.y * s.columns;
+    const int64_t p0 = blockIdx.x * (int64_t)kTile;
+    const uint2 kt = p0 + threadIdx.x < n ? sorted[p0 + threadIdx.x] : make_uint2(kNone, 0u);
+    pairs[threadIdx.x] = kt;
+    const int count = __syncthreads_count(kt.x != kNone);
+    if (count == 0) return;
+    float* part = s.part + ((int64_t)m * s.tiles + blockIdx.x) * 2 * a.width;
+    Around around;
+    around.before = p0 > 0 && sorted[p0 - 1].x == pairs[0].x;
+    around.after = p0 + count < n && sorted[p0 + count].x == pairs[count - 1].x;
+    around.head = part;
+    around.tail = part + a.width;
+    sum_list<TO, VEC, B, Terms, kThreads>(
+        a, m, TermsOf{a, m}, [&](int p) { return pairs[p]; }, [](uint32_t v) { return v; }, count, s.log2L, col0,
+        reinterpret_cast<float*>(heads), around, [] { __syncthreads(); });
+}
+
+// The first `joins` CTAs (blockIdx.x) add the sums of the runs that begin in a tile
+// and go on in the next ones: a warp has a tile and 32 columns (blockIdx.y); runs of
+// many tiles are added by all of the CTA's warps, every 8th tile each, and the warps'
+// sums in order.  The other CTAs write the zeros, 32 rows a warp: a lane looks one row
+// up among the sorted tokens.
+constexpr int kLongRun = 32;
+
+template <typename TO, int VEC>
+__global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant__ SumArgs s, int64_t joins) {
+    constexpr int kWarps = kThreads / 32;
+    const RowSumArgs& a = s.a;
+    const int m = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t n = a.index.n;
+    if (blockIdx.x >= joins) {
+        const int64_t r0 = ((blockIdx.x - joins) * kWarps + warp) * 32, rows = a.index.rows[m];
+        if (blockIdx.y > 0 || r0 >= rows) return;
+        const int64_t v = r0 + lane;
+        int64_t lo = 0, hi = n;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (key_at(s, m, mid) < v) lo = mid + 1;
+            else hi = mid;
+        }
+        const bool has = v >= rows || (lo < n && key_at(s, m, lo) == (uint32_t)v);
+        const uint32_t touched = __ballot_sync(0xFFFFFFFFu, has);
+        zero_rows<TO, VEC>(
+            a, m, 0, 32, 0, (uint32_t)(a.width / VEC), [&](uint32_t r) { return (touched >> r & 1u) != 0; },
+            [&](uint32_t r) { return (uint32_t)(r0 + r); });
+        return;
+    }
+    const int64_t tile = blockIdx.x * (int64_t)kWarps + warp;
+    const int64_t p0 = tile * s.tile, p1 = p0 + s.tile;
+    const float* part = s.part + (int64_t)m * s.tiles * 2 * a.width;
+    const int64_t col = (int64_t)blockIdx.y * 32 + lane;
+    __shared__ uint32_t long_key[kWarps];
+    __shared__ int64_t long_last[kWarps];
+    __shared__ float sums[kWarps][32];
+    uint32_t key = kNone;
+    int64_t last = 0;           // the last tile whose first token is of the run
+    if (p1 < n) {
+        const uint32_t next = key_at(s, m, p1), end = key_at(s, m, p1 - 1);
+        const uint32_t before = p0 > 0 ? key_at(s, m, p0 - 1) : kNone;
+        if (end == next && end != before) key = end;
+    }
+    if (key != kNone) {
+        auto has = [&](int64_t t) { return t < s.tiles && key_at(s, m, t * s.tile) == key; };
+        int64_t step = 1;
+        last = tile + 1;
+        while (has(last + step)) {
+            last += step;
+            step *= 2;
+        }
+        for (; step > 0; step >>= 1)
+            if (has(last + step)) last += step;
+    }
+    const bool is_long = key != kNone && last - tile > kLongRun;
+    if (lane == 0) {
+        long_key[warp] = is_long ? key : kNone;
+        long_last[warp] = last;
+    }
+    float acc = 0.f;
+    if (key != kNone && !is_long && col < a.width) {
+        acc = part[(tile * 2 + 1) * a.width + col];
+#pragma unroll 4
+        for (int64_t t = tile + 1; t <= last; ++t) acc += part[t * 2 * a.width + col];
+        write_row<TO, 1>(a, m, key, col, &acc);
+    }
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+        if (long_key[w] == kNone) continue;
+        const int64_t t0 = blockIdx.x * (int64_t)kWarps + w;
+        acc = 0.f;
+        if (col < a.width) {
+            if (warp == 0) acc = part[(t0 * 2 + 1) * a.width + col];
+#pragma unroll 8
+            for (int64_t t = t0 + 1 + warp; t <= long_last[w]; t += kWarps) acc += part[t * 2 * a.width + col];
+        }
+        sums[warp][lane] = acc;
+        __syncthreads();
+        if (warp == 0 && col < a.width) {
+            for (int k = 1; k < kWarps; ++k) acc += sums[k][lane];
+            write_row<TO, 1>(a, m, long_key[w], col, &acc);
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+inline int64_t most_rows(const IndexArgs& x) {
+    int64_t rows = 0;
+    for (int m = 0; m < x.d; ++m) rows = x.rows[m] > rows ? x.rows[m] : rows;
+    return rows;
+}
+
+// The rows' distribution over the CTAs of own_kernel for rows in vectors of `vec`
+// elements; false where there are too many tokens or rows for it.
+inline bool plan_own(const RowSumArgs& a, int vec, OwnArgs& o, dim3& grid) {
+    if (a.index.n > kOwnTokens) return false;
+    const int64_t rows = most_rows(a.index);
+    o.a = a;
+    o.log2L = 0;
+    while ((1 << o.log2L) < kSumThreads && ((int64_t)vec << o.log2L) < a.width) ++o.log2L;
+    o.part = (int64_t)vec << o.log2L;
+    const int64_t parts = cdiv(a.width, o.part);
+    int64_t owners = kSms / (parts * a.index.d);
+    owners = owners < 1 ? 1 : owners;
+    // neighbouring rows stay together up to 1 KB, as long as every CTA gets eight blocks of them
+    o.row_shift = 0;
+    const int64_t row_bytes = a.width * elem_bytes(a.out_type);
+    while ((row_bytes << o.row_shift) < 1024 && (rows >> (o.row_shift + 1)) >= 8 * owners) ++o.row_shift;
+    const int64_t blocks = cdiv(rows, (int64_t)1 << o.row_shift);
+    owners = owners < blocks ? owners : blocks;
+    const int64_t owned = cdiv(blocks, owners) << o.row_shift;
+    if (owned > kOwnRows || parts > 65535) return false;
+    o.owned = (uint32_t)owned;
+    o.per_warp = (uint32_t)(cdiv(a.index.n, kOwnThreads) * 32);
+    grid = dim3((unsigned)owners, (unsigned)parts, a.index.d);
+    return true;
+}
+
+// bytes of the partial sums, two rows for every kTile tokens
+inline size_t part_bytes(const IndexArgs& x, int64_t width) {
+    return sizeof(float) * x.d * cdiv(x.n, kTile) * 2 * width;
+}
+
+// joins the tiles' crossing runs and writes the zeros
+template <typename TO, int VEC>
+cudaError_t finish(const SumArgs& s, cudaStream_t st) {
+    const int64_t joins = s.tiles > 1 ? cdiv(s.tiles, kThreads / 32) : 0;
+    const int64_t zeros = s.a.accumulate ? 0 : cdiv(most_rows(s.a.index), kThreads);
+    if (joins + zeros == 0) return cudaGetLastError();
+    const dim3 grid((unsigned)(joins + zeros), joins > 0 ? (unsigned)cdiv(s.a.width, 32) : 1u, s.a.index.d);
+    finish_kernel<TO, VEC><<<grid, kThreads, 0, st>>>(s, joins);
+    return cudaGetLastError();
+}
+
+// Terms<B>: terms of B tokens at VEC columns; B = kAhead of them are in flight where
+// the tokens are many (own_kernel's CTAs of 1024 threads have registers for 4)
+template <typename TO, int VEC, int kAhead, template <int> typename Terms>
+cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
+    OwnArgs o;
+    dim3 grid;
+    if (plan_own(a, VEC, o, grid)) {
+        const size_t smem = sizeof(float) * kSumThreads * VEC +
+                            sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32 + 2 * kOwnWarps * o.per_warp);
+        constexpr auto kernel = own_kernel<TO, VEC, 4, Terms<4>>;
+        cudaError_t e = allow_smem<kernel>();
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, kOwnThreads, smem, st>>>(o);
+        return cudaGetLastError();
+    }
+    const SortPlan p = plan_sort(a.index, sizeof(uint2));
+    SumArgs s;
+    s.a = a;
+    s.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.total());
+    s.tile = kTile;
+    s.tiles = cdiv(a.index.n, kTile);
+    s.log2L = 0;
+    while ((1 << s.log2L) < kThreads && ((int64_t)VEC << s.log2L) < a.width) ++s.log2L;
+    s.columns = (int64_t)VEC << s.log2L;
+    if (s.tiles > 0) {
+        cudaError_t e = sort_tokens(a.index, p, a.ws, nullptr, nullptr, s.sorted, st);
+        if (e != cudaSuccess) return e;
+        const dim3 sum_grid((unsigned)s.tiles, (unsigned)cdiv(a.width, s.columns), a.index.d);
+        row_sum_kernel<TO, VEC, kAhead, Terms<kAhead>><<<sum_grid, kThreads, 0, st>>>(s);
+    }
+    return finish<TO, VEC>(s, st);
+}
+
+}  // namespace
+}  // namespace mk

@@ -186,7 +186,12 @@ def test_lookup_gradient_masks_leave_nothing():
 MODELS = [  # dims, R, samples
     ((5,), 3, 40), ((1, 1), 1, 7), ((6, 7), 8, 1), ((32, 32, 32), 8, 1000), ((9, 4, 7), 33, 500),
     ((20,) * 6, 128, 3001), ((300, 2, 50), 64, 5000), ((2,) * 8, 20, 2000), ((40, 50, 60), 257, 700),
-    ((512, 1, 3), 100, 9001), ((64, 64, 64), 2000, 130), ((1500, 1100), 16, 20000), ((7, 8, 9), 4, 0)]
+    ((512, 1, 3), 100, 9001), ((64, 64, 64), 2000, 130), ((1500, 1100), 16, 20000), ((7, 8, 9), 4, 0),
+    # more samples than one CTA groups, factors that fit shared memory in slices of 32, 16 and 8 columns or
+    # not at all, as tables of single modes and of products, ranks that end inside a slice
+    ((20,) * 5 + (21,), 128, 40001), ((512, 512, 513), 96, 50000), ((40, 50, 60), 257, 30000),
+    ((1000, 900, 800), 48, 33000), ((2000, 1500, 1900), 20, 33001), ((3,) * 8, 36, 20003), ((30, 17), 1, 17000),
+    ((100003, 9, 4), 24, 40000), ((9,), 33, 25000), ((5, 1, 1, 1, 1, 1, 1), 12, 18000), ((250, 250), 1000, 17001)]
 
 
 def coords_of(gen, dims, S, dtype=torch.int32, masked=0.05):
