@@ -124,54 +124,66 @@ __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant
     if (any && lane == 0) a.out[t] = sum;
 }
 
-// A CTA has `share` consecutive samples and goes through the slices of CS columns.  A
-// warp takes 32 samples at a time: each lane works out the table rows of one, then
-// L = CS / 4 lanes form the products of L samples, one after the other, and add them
-// up so that every lane ends with its own sample's sum.
+// A CTA has `share` consecutive samples and goes through the slices of CS columns.  The
+// samples' table rows stand behind the tables, worked out once.  A warp takes 32 samples
+// at a time: L = CS / 4 lanes form the products of L samples, one after the other, and
+// add them up so that every lane ends with its own sample's sum.
+constexpr uint32_t kOutside = 0xFFFFFFFFu;     // of a sample that takes no part
+
 template <int CS>
 __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const __grid_constant__ EntriesArgs a,
                                                                           const __grid_constant__ StageArgs stage_args,
                                                                           const __grid_constant__ Tables tables,
-                                                                          int64_t share) {
+                                                                          int share) {
     extern __shared__ float4 stage_smem[];
     constexpr int L = CS / 4;
     float* tab = reinterpret_cast<float*>(stage_smem);
+    uint2* rows = reinterpret_cast<uint2*>(tab + (size_t)tables.rows * CS);     // 4 numbers of 16 bits a sample
     const int lane = threadIdx.x & 31;
-    const int64_t t0 = blockIdx.x * share;
-    const int64_t t1 = t0 + share < a.index.n ? t0 + share : a.index.n;
+    const int64_t t0 = (int64_t)blockIdx.x * share;
+    const int count = (int)(t0 + share < a.index.n ? share : a.index.n - t0);
+    for (int i = threadIdx.x; i < count; i += kStageThreads) {
+        uint2 r = make_uint2(kOutside, kOutside);
+        if (sort_key(a.index, t0 + i, 0) != kNone) {
+            r = make_uint2(0u, 0u);
+            for (int k = 0; k < tables.groups; ++k) {
+                const uint32_t row = table_row(a.index, tables.group[k], t0 + i) << (k & 1) * 16;
+                if (k < 2) r.x |= row;
+                else r.y |= row;
+            }
+        }
+        rows[i] = r;
+    }
     const float* mine = tab + (lane & (L - 1)) * 4;
     for (int64_t col0 = 0; col0 < a.width; col0 += CS) {
         stage<CS>(stage_args, tables, col0, tab);
         __syncthreads();
-        for (int64_t base = t0 + (threadIdx.x & ~31); base < t1; base += kStageThreads) {
-            const int64_t t = base + lane;
-            const bool inside = t < t1 && sort_key(a.index, t, 0) != kNone;
-            uint32_t lo = 0, hi = 0;
-            if (inside) {
-                uint32_t row[kMaxGroups] = {};
-#pragma unroll
-                for (int k = 0; k < kMaxGroups; ++k)
-                    if (k < tables.groups) row[k] = table_row(a.index, tables.group[k], t);
-                lo = row[0] | row[1] << 16;
-                hi = row[2] | row[3] << 16;
-            }
+        for (int base = threadIdx.x & ~31; base < count; base += kStageThreads) {
+            const int i = base + lane;
+            const uint2 own = i < count ? rows[i] : make_uint2(kOutside, kOutside);
+            const bool inside = own.x != kOutside;
+            const uint32_t lo = inside ? own.x : 0u, hi = inside ? own.y : 0u;
             float acc[L];
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                const float4 p = product<CS>(mine, tables.groups, __shfl_sync(0xFFFFFFFFu, lo, i, L),
-                                             __shfl_sync(0xFFFFFFFFu, hi, i, L));
-                acc[i] = (p.x + p.y) + (p.z + p.w);
+            for (int k = 0; k < L; ++k) {
+                const uint32_t lo_k = __shfl_sync(0xFFFFFFFFu, lo, k, L);
+                const uint32_t hi_k = tables.groups > 2 ? __shfl_sync(0xFFFFFFFFu, hi, k, L) : 0u;
+                const float4 p = product<CS>(mine, tables.groups, lo_k, hi_k);
+                acc[k] = (p.x + p.y) + (p.z + p.w);
             }
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) {
                 const bool upper = (lane & o) != 0;
 #pragma unroll
-                for (int i = 0; i < o; ++i) {
-                    const float send = upper ? acc[i] : acc[i + o];
-                    acc[i] = (upper ? acc[i + o] : acc[i]) + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+                for (int k = 0; k < o; ++k) {
+                    const float send = upper ? acc[k] : acc[k + o];
+                    acc[k] = (upper ? acc[k + o] : acc[k]) + __shfl_xor_sync(0xFFFFFFFFu, send, o);
                 }
             }
-            if (t < t1) a.out[t] = !inside ? 0.f : col0 == 0 ? acc[0] : a.out[t] + acc[0];
+            if (i < count) {
+                float* x = a.out + t0 + i;
+                *x = !inside ? 0.f : col0 == 0 ? acc[0] : *x + acc[0];
+            }
         }
         __syncthreads();
     }
@@ -179,67 +191,102 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
 
 // ---------------------------------------------------------------- gradient
 
+// products of factor rows from the caches
 template <typename T, int VEC>
 struct Model {
-    template <int B>
+    template <typename List>
     struct Terms {
-        float v[B][VEC];
-        __device__ __forceinline__ void load(const TermsOf& of, const uint2* entry, int64_t col) {
+        static constexpr int kB = 4;
+        const TermsOf& of;
+        const List& list;
+        const int p1;
+        const int64_t col;
+        uint32_t keys[kB];
+        float v[kB][VEC];
+        __device__ __forceinline__ Terms(const TermsOf& of, const List& list, int, int p1, int64_t col)
+            : of(of), list(list), p1(p1), col(col) {}
+        __device__ __forceinline__ void load(int p) {
             const RowSumArgs& a = of.a;
+            uint32_t tok[kB];
 #pragma unroll
-            for (int j = 0; j < B; ++j) {
-                const float g = a.g[entry[j].y];
+            for (int j = 0; j < kB; ++j) {
+                const uint2 entry = list(p + j < p1 ? p + j : p);
+                keys[j] = entry.x;
+                tok[j] = entry.y;
+                const float g = a.g[tok[j]];
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) v[j][e] = g;
             }
             for (int l = 0; l < a.index.d; ++l) {
                 if (l == of.m) continue;
-                Pack<T, VEC> x[B];
+                Pack<T, VEC> x[kB];
 #pragma unroll
-                for (int j = 0; j < B; ++j)
+                for (int j = 0; j < kB; ++j)
                     x[j] = *reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(a.factor[l]) +
-                                                                  index_at(a.index, entry[j].y, l) * a.width + col);
+                                                                  index_at(a.index, tok[j], l) * a.width + col);
 #pragma unroll
-                for (int j = 0; j < B; ++j)
+                for (int j = 0; j < kB; ++j)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) v[j][e] *= to_f32(x[j].v[e]);
             }
         }
-        __device__ __forceinline__ float at(int j, int e) const { return v[j][e]; }
+        __device__ __forceinline__ uint32_t key(int j) const { return keys[j]; }
+        __device__ __forceinline__ void add(int j, float* acc) const {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] += v[j][e];
+        }
     };
 };
 
-// terms of entries of 16 bytes from tables in shared memory
+// products of table rows in shared memory, of entries of 16 bytes; the next entries are
+// on their way while these are used
 struct StagedOf {
     const float* tab;       // at the lane's columns
     int groups;
 };
 
-template <int CS, int VEC, int B>
-struct StagedTerms {
-    float v[B][VEC];
-    __device__ __forceinline__ void load(const StagedOf& of, const uint4* entry, int64_t) {
+template <int CS, int VEC>
+struct Staged {
+    template <typename List>
+    struct Terms {
+        static constexpr int kB = 4;
+        const StagedOf& of;
+        const List& list;
+        const int p1;
+        uint4 entry[kB], next[kB];
+        __device__ __forceinline__ Terms(const StagedOf& of, const List& list, int p0, int p1, int64_t)
+            : of(of), list(list), p1(p1) {
+            fetch(p0);
+        }
+        __device__ __forceinline__ void fetch(int p) {
 #pragma unroll
-        for (int j = 0; j < B; ++j) {
+            for (int j = 0; j < kB; ++j) next[j] = list(p + j < p1 ? p + j : p1 - 1);
+        }
+        __device__ __forceinline__ void load(int p) {
+#pragma unroll
+            for (int j = 0; j < kB; ++j) entry[j] = next[j];
+            fetch(p + kB);
+        }
+        __device__ __forceinline__ uint32_t key(int j) const { return entry[j].x; }
+        __device__ __forceinline__ void add(int j, float* acc) const {
             const float g = __uint_as_float(entry[j].y);
             if constexpr (VEC == 4) {
                 float4 p = make_float4(1.f, 1.f, 1.f, 1.f);
                 if (of.groups > 0) p = product<CS>(of.tab, of.groups, entry[j].z, entry[j].w);
-                v[j][0] = g * p.x;
-                v[j][1] = g * p.y;
-                v[j][2] = g * p.z;
-                v[j][3] = g * p.w;
+                acc[0] = fmaf(g, p.x, acc[0]);
+                acc[1] = fmaf(g, p.y, acc[1]);
+                acc[2] = fmaf(g, p.z, acc[2]);
+                acc[3] = fmaf(g, p.w, acc[3]);
             } else {
-                float p = g;
+                float p = 1.f;
                 if (of.groups > 0) p *= of.tab[(entry[j].z & 0xFFFFu) * CS];
                 if (of.groups > 1) p *= of.tab[(entry[j].z >> 16) * CS];
                 if (of.groups > 2) p *= of.tab[(entry[j].w & 0xFFFFu) * CS];
                 if (of.groups > 3) p *= of.tab[(entry[j].w >> 16) * CS];
-                v[j][0] = p;
+                acc[0] = fmaf(g, p, acc[0]);
             }
         }
-    }
-    __device__ __forceinline__ float at(int j, int e) const { return v[j][e]; }
+    };
 };
 
 struct StagedArgs {
@@ -248,8 +295,8 @@ struct StagedArgs {
     Tables tables[MTTKRP_MAX_ORDER];
 };
 
-// A CTA has a slice of CS columns (blockIdx.x) and s.tile sorted samples (blockIdx.y)
-// of one mode (blockIdx.z).
+// A CTA (blockIdx.x) has a slice of CS columns and s.tile sorted samples of one mode
+// (blockIdx.y); those behind the slices' and tiles' write zeros, 32 rows a warp.
 template <int CS, int VEC>
 __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __grid_constant__ StagedArgs a) {
     extern __shared__ float4 stage_smem[];
@@ -258,10 +305,17 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     float* heads = reinterpret_cast<float*>(stage_smem);        // kStageThreads * VEC
     float* tab = heads + kStageThreads * VEC;
     const SumArgs& s = a.s;
-    const int m = blockIdx.z;
-    const int64_t n = s.a.index.n, col0 = (int64_t)blockIdx.x * CS;
+    const int m = blockIdx.y;
+    const int64_t n = s.a.index.n;
+    const uint32_t tile = blockIdx.x % (uint32_t)s.tiles, slice = blockIdx.x / (uint32_t)s.tiles;
+    const int64_t col0 = (int64_t)slice * CS;
+    if (col0 >= s.a.width) {
+        const int64_t warp = (blockIdx.x - cdiv(s.a.width, CS) * s.tiles) * (kStageThreads / 32) + (threadIdx.x >> 5);
+        zero_unsorted_rows<float, VEC>(s.a, m, warp * 32, [&](int64_t p) { return key_at(s, m, p); });
+        return;
+    }
     const uint4* sorted = reinterpret_cast<const uint4*>(s.sorted.entries) + m * n;
-    const int64_t p0 = blockIdx.y * s.tile, p1 = p0 + s.tile < n ? p0 + s.tile : n;
+    const int64_t p0 = tile * s.tile, p1 = p0 + s.tile < n ? p0 + s.tile : n;
     stage<CS>(a.stage, a.tables[m], col0, tab);
     // entries that take part come first: find the end in two steps of 1024 probes
     int64_t lo = p0, hi = p1;
@@ -280,14 +334,14 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     __syncthreads();
     if (count == 0) return;
     const uint4* list = sorted + p0;
-    float* part = s.part + ((int64_t)m * s.tiles + blockIdx.y) * 2 * s.a.width;
+    float* part = s.part + ((int64_t)m * s.tiles + tile) * 2 * s.a.width;
     Around around;
     around.before = p0 > 0 && list[-1].x == list[0].x;
     around.after = p0 + count < n && list[count].x == list[count - 1].x;
     around.head = part;
     around.tail = part + s.a.width;
     const StagedOf of{tab + (threadIdx.x & (L - 1)) * VEC, a.tables[m].groups};
-    sum_list<float, VEC, 4, StagedTerms<CS, VEC, 4>, kStageThreads>(
+    sum_list<float, VEC, Staged<CS, VEC>::template Terms, kStageThreads>(
         s.a, m, of, [&](int p) { return __ldg(list + p); }, [](uint32_t v) { return v; }, count, kLog2L, col0, heads,
         around, [] { __syncthreads(); });
 }
@@ -383,8 +437,9 @@ template <int CS>
 cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share, cudaStream_t s) {
     cudaError_t e = allow_smem<entries_staged_kernel<CS>>();
     if (e != cudaSuccess) return e;
-    entries_staged_kernel<CS><<<(unsigned)cdiv(a.index.n, share), kStageThreads, sizeof(float) * t.rows * CS, s>>>(
-        a, stage_args(a.index, a.factor, a.type, a.width), t, share);
+    const size_t smem = sizeof(float) * t.rows * CS + sizeof(uint2) * share;
+    entries_staged_kernel<CS><<<(unsigned)cdiv(a.index.n, share), kStageThreads, smem, s>>>(
+        a, stage_args(a.index, a.factor, a.type, a.width), t, (int)share);
     return cudaGetLastError();
 }
 
@@ -394,8 +449,8 @@ cudaError_t grad_cached(const RowSumArgs& a, cudaStream_t s) {
     for (int m = 0; m < a.index.d; ++m)
         w = w && (reinterpret_cast<uintptr_t>(a.factor[m]) % (4 * sizeof(T))) == 0 &&
             (reinterpret_cast<uintptr_t>(a.out[m]) % (4 * sizeof(float))) == 0;
-    if (w) return sums_by<float, 4, 4, Model<T, 4>::template Terms>(a, s);
-    return sums_by<float, 1, 4, Model<T, 1>::template Terms>(a, s);
+    if (w) return sums_by<float, 4, Model<T, 4>::template Terms, Model<T, 4>::template Terms, 0>(a, s);
+    return sums_by<float, 1, Model<T, 1>::template Terms, Model<T, 1>::template Terms, 0>(a, s);
 }
 
 template <int CS, int VEC>
@@ -406,10 +461,10 @@ cudaError_t grad_staged(StagedArgs& a, const SortPlan& p, cudaStream_t st) {
     cudaError_t e = allow_smem<staged_sum_kernel<CS, VEC>>();
     if (e == cudaSuccess) e = sort_tokens(r.index, p, r.ws, a.tables, r.g, a.s.sorted, st);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)cdiv(r.width, CS), (unsigned)a.s.tiles, r.index.d);
+    const dim3 grid((unsigned)(cdiv(r.width, CS) * a.s.tiles + cdiv(most_rows(r.index), kStageThreads)), r.index.d);
     const size_t smem = sizeof(float) * (kStageThreads * VEC + (size_t)rows * CS);
     staged_sum_kernel<CS, VEC><<<grid, kStageThreads, smem, st>>>(a);
-    return finish<float, VEC>(a.s, st);
+    return join<float, VEC>(a.s, st);
 }
 
 }  // namespace
@@ -417,17 +472,22 @@ cudaError_t grad_staged(StagedArgs& a, const SortPlan& p, cudaStream_t st) {
 cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
     const int64_t n = a.index.n;
     if (n == 0) return cudaSuccess;
-    const int64_t share = cdiv(cdiv(n, kSms), 32) * 32;
     double least = kGatherCache * a.index.d * cdiv(a.width, 32) * (double)n / kSms;
     int cs = 0;
+    int64_t share = 0;
     Tables tables;
     for (int c = 32; c >= 8; c /= 2) {
+        // as few rounds of CTAs over the SMs as leave two thirds of the shared memory to the tables
+        constexpr int64_t kMost = kMaxSmem / 3 / sizeof(uint2);
+        const int64_t rounds = cdiv(n, kSms * kMost);
+        const int64_t part = cdiv(cdiv(n, kSms * rounds), 32) * 32;
         Tables t;
-        const double slice = plan_tables(a.index, -1, c, table_rows(0, c), (double)share, t);
-        const double work = slice * cdiv(a.width, c);
+        const double slice = plan_tables(a.index, -1, c, table_rows(sizeof(uint2) * part, c), (double)part, t);
+        const double work = slice * cdiv(a.width, c) * rounds;
         if (slice >= 0.0 && work < least) {
             least = work;
             tables = t;
+            share = part;
             cs = c;
         }
     }

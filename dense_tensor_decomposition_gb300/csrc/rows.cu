@@ -68,18 +68,93 @@ cudaError_t lookup(const LookupArgs& a, cudaStream_t s) {
 
 // ---------------------------------------------------------------- gradient
 
-template <typename T, int VEC>
+// the gradient's rows, kB of them loaded at a time
+template <typename T, int VEC, int B>
 struct Grad {
-    template <int B>
+    template <typename List>
     struct Terms {
+        static constexpr int kB = B;
+        const TermsOf& of;
+        const List& list;
+        const int p1;
+        const int64_t col;
+        uint32_t keys[B];
         Pack<T, VEC> x[B];
-        __device__ __forceinline__ void load(const TermsOf& of, const uint2* entry, int64_t col) {
-#pragma unroll
-            for (int j = 0; j < B; ++j)
+        __device__ __forceinline__ Terms(const TermsOf& of, const List& list, int, int p1, int64_t col)
+            : of(of), list(list), p1(p1), col(col) {}
+        __device__ __forceinline__ void load(int p) {
+    #pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const uint2 entry = list(p + j < p1 ? p + j : p);
+                keys[j] = entry.x;
                 x[j] = *reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(of.a.grad) +
-                                                              (int64_t)entry[j].y * of.a.grad_stride + col);
+                                                              (int64_t)entry.y * of.a.grad_stride + col);
+            }
         }
-        __device__ __forceinline__ float at(int j, int e) const { return to_f32(x[j].v[e]); }
+        __device__ __forceinline__ uint32_t key(int j) const { return keys[j]; }
+        __device__ __forceinline__ void add(int j, float* acc) const {
+    #pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] += to_f32(x[j].v[e]);
+        }
+    };
+};
+
+// Rows of 16-byte vectors: a thread keeps the next kSlots tokens' vectors of its
+// columns on their way into shared memory, which takes no registers and, as only the
+// thread itself reads them, no barrier.
+template <typename T>
+struct Ring {
+    static constexpr int kVec = 16 / sizeof(T);
+    static constexpr int kSlots = 16, kBytes = 16 * kSlots;
+
+    template <typename List>
+    struct Terms {
+        static constexpr int kB = 4;
+        const TermsOf& of;
+        const List& list;
+        const int p0, p1;
+        const T* at;                // the lane's columns of row 0
+        uint32_t ring;              // shared-memory address of the thread's slot 0
+        uint32_t keys[kB];
+        Pack<T, kVec> x[kB];
+        __device__ __forceinline__ Terms(const TermsOf& of, const List& list, int p0, int p1, int64_t col)
+            : of(of), list(list), p0(p0), p1(p1), at(static_cast<const T*>(of.a.grad) + col) {
+            extern __shared__ float4 ring_smem[];
+            ring = (uint32_t)__cvta_generic_to_shared(ring_smem + threadIdx.x);
+    #pragma unroll
+            for (int k = 0; k < kSlots - kB; k += kB) copy(p0 + k);
+        }
+        // tokens p .. p + kB towards their slots; a group of copies even where there are none
+        __device__ __forceinline__ void copy(int p) {
+    #pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                if (p + j < p1) {
+                    const uint32_t slot = ring + ((p + j - p0) & (kSlots - 1)) * (kThreads * 16);
+                    const T* src = at + (int64_t)list(p + j).y * of.a.grad_stride;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(slot), "l"(src) : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+        }
+        __device__ __forceinline__ void load(int p) {
+            copy(p + kSlots - kB);
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(kSlots / kB - 1) : "memory");
+    #pragma unroll
+            for (int j = 0; j < kB; ++j) {
+                keys[j] = list(p + j < p1 ? p + j : p).x;
+                const uint32_t slot = ring + ((p + j - p0) & (kSlots - 1)) * (kThreads * 16);
+                uint32_t* w = reinterpret_cast<uint32_t*>(x[j].v);
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(slot)
+                             : "memory");
+            }
+        }
+        __device__ __forceinline__ uint32_t key(int j) const { return keys[j]; }
+        __device__ __forceinline__ void add(int j, float* acc) const {
+    #pragma unroll
+            for (int e = 0; e < kVec; ++e) acc[e] += to_f32(x[j].v[e]);
+        }
     };
 };
 
@@ -89,8 +164,9 @@ cudaError_t lookup_grad(const RowSumArgs& a, cudaStream_t s) {
     constexpr int kVec = 16 / sizeof(T);
     const size_t from = reinterpret_cast<uintptr_t>(a.grad) | (a.grad_stride * sizeof(T)) | (a.width * sizeof(T));
     const size_t to = reinterpret_cast<uintptr_t>(a.out[0]) | (a.out_stride * sizeof(TO));
-    if (from % 16 == 0 && to % (kVec * sizeof(TO)) == 0) return sums_by<TO, kVec, 8, Grad<T, kVec>::template Terms>(a, s);
-    return sums_by<TO, 1, 8, Grad<T, 1>::template Terms>(a, s);
+    if (from % 16 == 0 && to % (kVec * sizeof(TO)) == 0)
+        return sums_by<TO, kVec, Grad<T, kVec, 4>::template Terms, Ring<T>::template Terms, Ring<T>::kBytes>(a, s);
+    return sums_by<TO, 1, Grad<T, 1, 4>::template Terms, Grad<T, 1, 8>::template Terms, 0>(a, s);
 }
 
 }  // namespace

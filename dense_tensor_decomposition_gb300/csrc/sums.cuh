@@ -42,17 +42,21 @@ struct Around {
 };
 
 // Adds the terms of a list of `count` >= 1 tokens sorted by row over the columns from
-// col0 on, and writes the finished rows.  list(p): entry p, its row first (.x); Terms
-// loads the terms of B entries at VEC columns, all before the first is used.  A group of
-// L = 2^log2L threads (of kN in all, which sync() makes wait for one another) walks
-// count / groups consecutive tokens; a lane has VEC columns.  A run that crosses
-// groups is finished by the group in which it began, from the other groups' parts
-// in `heads` (kN * VEC floats), in the order of the groups.
-template <typename TO, int VEC, int B, typename Terms, int kN, typename Context, typename List, typename Row,
-          typename Sync>
+// col0 on, and writes the finished rows.  list(p): entry p, its row first (.x).  A group
+// of L = 2^log2L threads (of kN in all, which sync() makes wait for one another) walks
+// count / groups consecutive tokens; a lane has VEC columns.  A run that crosses groups
+// is finished by the group in which it began, from the other groups' parts in `heads`
+// (kN * VEC floats), in the order of the groups.
+//
+// Terms<List> terms(context, list, p0, p1, col) gives a lane the terms of tokens p0 .. p1,
+// kB at a time: after load(p), key(j) is the row of token p + j and add(j, acc) adds its
+// term; behind p1 these repeat some token of the list.
+template <typename TO, int VEC, template <typename> typename Terms, int kN, typename Context, typename List,
+          typename Row, typename Sync>
 __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Context& context, const List& list,
                                          const Row& row_of, int count, int log2L, int64_t col0, float* heads,
                                          const Around& around, const Sync& sync) {
+    constexpr int B = Terms<List>::kB;
     const int L = 1 << log2L, groups = kN >> log2L;
     const int group = threadIdx.x >> log2L, lane = threadIdx.x & (L - 1);
     const int64_t col = col0 + lane * VEC;
@@ -77,25 +81,26 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
         bool began_before = p0 > 0 ? list(p0 - 1).x == cur : around.before;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+        Terms<List> terms(context, list, p0, p1, col);
         for (int p = p0; p < p1; p += B) {
-            decltype(list(0)) entry[B];
+            terms.load(p);
+            if (p + B <= p1 && terms.key(B - 1) == cur) {       // all of one row
 #pragma unroll
-            for (int j = 0; j < B; ++j) entry[j] = list(p + j < p1 ? p + j : p);
-            Terms terms;
-            terms.load(context, entry, col);
+                for (int j = 0; j < B; ++j) terms.add(j, acc);
+                continue;
+            }
 #pragma unroll
             for (int j = 0; j < B; ++j) {
                 if (p + j < p1) {
-                    if (entry[j].x != cur) {
+                    if (terms.key(j) != cur) {
                         if (began_before) put(own_head);
                         else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
                         began_before = false;
-                        cur = entry[j].x;
+                        cur = terms.key(j);
 #pragma unroll
                         for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
                     }
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) acc[e] += terms.at(j, e);
+                    terms.add(j, acc);
                 }
             }
         }
@@ -127,17 +132,47 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
 template <typename TO, int VEC, typename Touched, typename Row>
 __device__ __forceinline__ void zero_rows(const RowSumArgs& a, int m, uint32_t r0, uint32_t rows, int64_t col0,
                                           uint32_t vecs, const Touched& touched, const Row& row_of) {
+    const uint32_t lane = threadIdx.x & 31;
     Pack<TO, VEC> zero;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) zero.v[e] = from_f32<TO>(0.f);
-    for (uint32_t i = threadIdx.x & 31; i < rows * vecs; i += 32) {
-        const uint32_t r = i / vecs, c = i - r * vecs;
-        if (touched(r0 + r)) continue;
-        const uint32_t v = row_of(r0 + r);
-        if (v == kNone) continue;
-        *reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out[m]) + (int64_t)v * a.out_stride + col0 +
-                                          (int64_t)c * VEC) = zero;
+    auto at = [&](uint32_t v) {
+        return reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out[m]) + (int64_t)v * a.out_stride + col0);
+    };
+    if (vecs >= 32) {
+        for (uint32_t r = r0; r < r0 + rows; ++r) {
+            const uint32_t v = touched(r) ? kNone : row_of(r);
+            if (v == kNone) continue;
+            Pack<TO, VEC>* dst = at(v);
+#pragma unroll 4
+            for (uint32_t c = lane; c < vecs; c += 32) dst[c] = zero;
+        }
+    } else {
+        for (uint32_t i = lane; i < rows * vecs; i += 32) {
+            const uint32_t r = i / vecs, v = touched(r0 + r) ? kNone : row_of(r0 + r);
+            if (v != kNone) at(v)[i - r * vecs] = zero;
+        }
     }
+}
+
+// 32 rows of a warp from r0 on: a lane looks one of them up among the sorted tokens,
+// then those without tokens become zero
+template <typename TO, int VEC, typename Key>
+__device__ __forceinline__ void zero_unsorted_rows(const RowSumArgs& a, int m, int64_t r0, const Key& key) {
+    const int64_t n = a.index.n, rows = a.index.rows[m], v = r0 + (threadIdx.x & 31);
+    if (r0 >= rows) return;
+    int64_t lo = 0, hi = n;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (key(mid) < v) lo = mid + 1;
+        else hi = mid;
+    }
+    const bool has = v >= rows || (lo < n && key(lo) == (uint32_t)v);
+    const uint32_t touched = __ballot_sync(0xFFFFFFFFu, has);
+    if (touched == 0xFFFFFFFFu) return;
+    zero_rows<TO, VEC>(
+        a, m, 0, 32, 0, (uint32_t)(a.width / VEC), [&](uint32_t r) { return (touched >> r & 1u) != 0; },
+        [&](uint32_t r) { return (uint32_t)(r0 + r); });
 }
 
 // what the terms of (row, token) entries are made from
@@ -166,7 +201,7 @@ struct OwnArgs {
     int64_t part;           // columns of a CTA (blockIdx.y)
 };
 
-template <typename TO, int VEC, int B, typename Terms>
+template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_constant__ OwnArgs o) {
     extern __shared__ float4 own_smem[];
     const RowSumArgs& a = o.a;
@@ -255,7 +290,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
         }
         sync();
         auto at_place = [&](int p) { return make_uint2(found[p] >> kTokenBits, found[p] & (kOwnTokens - 1)); };
-        sum_list<TO, VEC, B, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, (int)total, o.log2L, col0,
+        sum_list<TO, VEC, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, (int)total, o.log2L, col0,
                                                  heads, Around{false, false, nullptr, nullptr}, sync);
     }
     if (a.accumulate) return;
@@ -289,7 +324,9 @@ __device__ __forceinline__ uint32_t key_at(const SumArgs& s, int m, int64_t p) {
     return *reinterpret_cast<const uint32_t*>(s.sorted.entries + (m * s.a.index.n + p) * s.sorted.bytes);
 }
 
-template <typename TO, int VEC, int B, typename Terms>
+// The first s.tiles CTAs (blockIdx.x) have a tile of the sorted tokens each; those
+// behind write zeros, 32 rows a warp.
+template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant__ SumArgs s) {
     static_assert(kTile == kThreads, "a thread stages one entry");
     __shared__ uint2 pairs[kTile];
@@ -297,6 +334,12 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant
     const RowSumArgs& a = s.a;
     const int m = blockIdx.z;
     const int64_t n = a.index.n;
+    if (blockIdx.x >= s.tiles) {
+        if (blockIdx.y > 0) return;
+        const int64_t warp = (blockIdx.x - s.tiles) * (kThreads / 32) + (threadIdx.x >> 5);
+        zero_unsorted_rows<TO, VEC>(a, m, warp * 32, [&](int64_t p) { return key_at(s, m, p); });
+        return;
+    }
     const uint2* sorted = reinterpret_cast<const uint2*>(s.sorted.entries) + m * n;
     const int64_t col0 = (int64_t)blockIdx.y * s.columns;
     const int64_t p0 = blockIdx.x * (int64_t)kTile;
@@ -310,50 +353,32 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant
     around.after = p0 + count < n && sorted[p0 + count].x == pairs[count - 1].x;
     around.head = part;
     around.tail = part + a.width;
-    sum_list<TO, VEC, B, Terms, kThreads>(
+    sum_list<TO, VEC, Terms, kThreads>(
         a, m, TermsOf{a, m}, [&](int p) { return pairs[p]; }, [](uint32_t v) { return v; }, count, s.log2L, col0,
         reinterpret_cast<float*>(heads), around, [] { __syncthreads(); });
 }
 
-// The first `joins` CTAs (blockIdx.x) add the sums of the runs that begin in a tile
-// and go on in the next ones: a warp has a tile and 32 columns (blockIdx.y); runs of
-// many tiles are added by all of the CTA's warps, every 8th tile each, and the warps'
-// sums in order.  The other CTAs write the zeros, 32 rows a warp: a lane looks one row
-// up among the sorted tokens.
-constexpr int kLongRun = 32;
+// Adds the sums of the runs that begin in a tile and go on in the next ones.  A warp
+// has a tile and 32 vectors of columns (blockIdx.y); runs of many tiles are added by
+// all of the CTA's warps, every 8th tile each, and the warps' sums in order.
+constexpr int kLongRun = 16;
 
 template <typename TO, int VEC>
-__global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant__ SumArgs s, int64_t joins) {
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs s) {
     constexpr int kWarps = kThreads / 32;
+    using P = Pack<float, VEC>;
     const RowSumArgs& a = s.a;
     const int m = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n = a.index.n;
-    if (blockIdx.x >= joins) {
-        const int64_t r0 = ((blockIdx.x - joins) * kWarps + warp) * 32, rows = a.index.rows[m];
-        if (blockIdx.y > 0 || r0 >= rows) return;
-        const int64_t v = r0 + lane;
-        int64_t lo = 0, hi = n;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (key_at(s, m, mid) < v) lo = mid + 1;
-            else hi = mid;
-        }
-        const bool has = v >= rows || (lo < n && key_at(s, m, lo) == (uint32_t)v);
-        const uint32_t touched = __ballot_sync(0xFFFFFFFFu, has);
-        zero_rows<TO, VEC>(
-            a, m, 0, 32, 0, (uint32_t)(a.width / VEC), [&](uint32_t r) { return (touched >> r & 1u) != 0; },
-            [&](uint32_t r) { return (uint32_t)(r0 + r); });
-        return;
-    }
     const int64_t tile = blockIdx.x * (int64_t)kWarps + warp;
     const int64_t p0 = tile * s.tile, p1 = p0 + s.tile;
-    const float* part = s.part + (int64_t)m * s.tiles * 2 * a.width;
-    const int64_t col = (int64_t)blockIdx.y * 32 + lane;
+    const int64_t col = ((int64_t)blockIdx.y * 32 + lane) * VEC;
+    const float* part = s.part + (int64_t)m * s.tiles * 2 * a.width + col;
     __shared__ uint32_t long_key[kWarps];
     __shared__ int64_t long_last[kWarps];
-    __shared__ float sums[kWarps][32];
+    __shared__ P sums[kWarps][32];
     uint32_t key = kNone;
-    int64_t last = 0;           // the last tile whose first token is of the run
+    int64_t last = tile + 1;    // the last tile whose first token is of the run
     if (p1 < n) {
         const uint32_t next = key_at(s, m, p1), end = key_at(s, m, p1 - 1);
         const uint32_t before = p0 > 0 ? key_at(s, m, p0 - 1) : kNone;
@@ -362,7 +387,6 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
     if (key != kNone) {
         auto has = [&](int64_t t) { return t < s.tiles && key_at(s, m, t * s.tile) == key; };
         int64_t step = 1;
-        last = tile + 1;
         while (has(last + step)) {
             last += step;
             step *= 2;
@@ -375,28 +399,34 @@ __global__ void __launch_bounds__(kThreads) finish_kernel(const __grid_constant_
         long_key[warp] = is_long ? key : kNone;
         long_last[warp] = last;
     }
-    float acc = 0.f;
+    P acc;
+    auto add = [&](const float* src) {
+        const P x = *reinterpret_cast<const P*>(src);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc.v[e] += x.v[e];
+    };
     if (key != kNone && !is_long && col < a.width) {
-        acc = part[(tile * 2 + 1) * a.width + col];
+        acc = *reinterpret_cast<const P*>(part + (tile * 2 + 1) * a.width);
 #pragma unroll 4
-        for (int64_t t = tile + 1; t <= last; ++t) acc += part[t * 2 * a.width + col];
-        write_row<TO, 1>(a, m, key, col, &acc);
+        for (int64_t t = tile + 1; t <= last; ++t) add(part + t * 2 * a.width);
+        write_row<TO, VEC>(a, m, key, col, acc.v);
     }
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) {
         if (long_key[w] == kNone) continue;
         const int64_t t0 = blockIdx.x * (int64_t)kWarps + w;
-        acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc.v[e] = 0.f;
         if (col < a.width) {
-            if (warp == 0) acc = part[(t0 * 2 + 1) * a.width + col];
-#pragma unroll 8
-            for (int64_t t = t0 + 1 + warp; t <= long_last[w]; t += kWarps) acc += part[t * 2 * a.width + col];
+            if (warp == 0) add(part + (t0 * 2 + 1) * a.width);
+#pragma unroll 4
+            for (int64_t t = t0 + 1 + warp; t <= long_last[w]; t += kWarps) add(part + t * 2 * a.width);
         }
         sums[warp][lane] = acc;
         __syncthreads();
         if (warp == 0 && col < a.width) {
-            for (int k = 1; k < kWarps; ++k) acc += sums[k][lane];
-            write_row<TO, 1>(a, m, long_key[w], col, &acc);
+            for (int k = 1; k < kWarps; ++k) add(sums[k][lane].v);
+            write_row<TO, VEC>(a, m, long_key[w], col, acc.v);
         }
         __syncthreads();
     }
@@ -441,27 +471,26 @@ inline size_t part_bytes(const IndexArgs& x, int64_t width) {
     return sizeof(float) * x.d * cdiv(x.n, kTile) * 2 * width;
 }
 
-// joins the tiles' crossing runs and writes the zeros
+// joins the tiles' crossing runs
 template <typename TO, int VEC>
-cudaError_t finish(const SumArgs& s, cudaStream_t st) {
-    const int64_t joins = s.tiles > 1 ? cdiv(s.tiles, kThreads / 32) : 0;
-    const int64_t zeros = s.a.accumulate ? 0 : cdiv(most_rows(s.a.index), kThreads);
-    if (joins + zeros == 0) return cudaGetLastError();
-    const dim3 grid((unsigned)(joins + zeros), joins > 0 ? (unsigned)cdiv(s.a.width, 32) : 1u, s.a.index.d);
-    finish_kernel<TO, VEC><<<grid, kThreads, 0, st>>>(s, joins);
+cudaError_t join(const SumArgs& s, cudaStream_t st) {
+    if (s.tiles < 2) return cudaGetLastError();
+    const dim3 grid((unsigned)cdiv(s.tiles, kThreads / 32), (unsigned)cdiv(s.a.width, 32 * VEC), s.a.index.d);
+    join_kernel<TO, VEC><<<grid, kThreads, 0, st>>>(s);
     return cudaGetLastError();
 }
 
-// Terms<B>: terms of B tokens at VEC columns; B = kAhead of them are in flight where
-// the tokens are many (own_kernel's CTAs of 1024 threads have registers for 4)
-template <typename TO, int VEC, int kAhead, template <int> typename Terms>
+// Few: the terms as own_kernel takes them, whose CTAs of 1024 threads have few
+// registers a thread; Many: as row_sum_kernel takes them, with kRing bytes of dynamic
+// shared memory a thread
+template <typename TO, int VEC, template <typename> typename Few, template <typename> typename Many, int kRing>
 cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     OwnArgs o;
     dim3 grid;
     if (plan_own(a, VEC, o, grid)) {
         const size_t smem = sizeof(float) * kSumThreads * VEC +
                             sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32 + 2 * kOwnWarps * o.per_warp);
-        constexpr auto kernel = own_kernel<TO, VEC, 4, Terms<4>>;
+        constexpr auto kernel = own_kernel<TO, VEC, Few>;
         cudaError_t e = allow_smem<kernel>();
         if (e != cudaSuccess) return e;
         kernel<<<grid, kOwnThreads, smem, st>>>(o);
@@ -476,13 +505,15 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     s.log2L = 0;
     while ((1 << s.log2L) < kThreads && ((int64_t)VEC << s.log2L) < a.width) ++s.log2L;
     s.columns = (int64_t)VEC << s.log2L;
-    if (s.tiles > 0) {
-        cudaError_t e = sort_tokens(a.index, p, a.ws, nullptr, nullptr, s.sorted, st);
-        if (e != cudaSuccess) return e;
-        const dim3 sum_grid((unsigned)s.tiles, (unsigned)cdiv(a.width, s.columns), a.index.d);
-        row_sum_kernel<TO, VEC, kAhead, Terms<kAhead>><<<sum_grid, kThreads, 0, st>>>(s);
-    }
-    return finish<TO, VEC>(s, st);
+    cudaError_t e = sort_tokens(a.index, p, a.ws, nullptr, nullptr, s.sorted, st);
+    const int64_t zeros = a.accumulate ? 0 : cdiv(most_rows(a.index), kThreads);
+    if (e != cudaSuccess || s.tiles + zeros == 0) return e;
+    constexpr auto kernel = row_sum_kernel<TO, VEC, Many>;
+    e = allow_smem<kernel>();
+    if (e != cudaSuccess) return e;
+    const dim3 sum_grid((unsigned)(s.tiles + zeros), (unsigned)cdiv(a.width, s.columns), a.index.d);
+    kernel<<<sum_grid, kThreads, kThreads * kRing, st>>>(s);
+    return join<TO, VEC>(s, st);
 }
 
 }  // namespace
