@@ -9,6 +9,8 @@
 // where they fit, products of neighbouring modes' rows instead of the rows themselves,
 // which makes the gathers fewer (Tables).  Small problems, and factors whose slices do
 // not fit, gather from the caches.
+#include <type_traits>
+
 #include "sums.cuh"
 
 namespace mk {
@@ -55,7 +57,7 @@ __device__ __forceinline__ float4 times(float4 a, float4 b) {
 // are in flight.
 template <int CS>
 __device__ __forceinline__ void stage(const StageArgs& a, const Tables& t, int64_t col0, float* tab) {
-    constexpr int kQuads = CS / 4, kAhead = 4;
+    constexpr int kQuads = CS / 4, kAhead = 5;
     const int items = t.rows * kQuads;
     for (int i0 = threadIdx.x; i0 < items; i0 += kAhead * kStageThreads) {
         float4 v[kAhead];
@@ -85,14 +87,14 @@ __device__ __forceinline__ void stage(const StageArgs& a, const Tables& t, int64
     }
 }
 
-// product of a sample's rows, as 16-bit numbers in lo and hi, at four columns
-template <int CS>
-__device__ __forceinline__ float4 product(const float* tab, int groups, uint32_t lo, uint32_t hi) {
+// product of a sample's rows in G tables, as 16-bit numbers in lo and hi, at four columns
+template <int CS, int G>
+__device__ __forceinline__ float4 product(const float* tab, uint32_t lo, uint32_t hi) {
     auto row = [&](uint32_t r) { return *reinterpret_cast<const float4*>(tab + r * CS); };
     float4 p = row(lo & 0xFFFFu);
-    if (groups > 1) p = times(p, row(lo >> 16));
-    if (groups > 2) p = times(p, row(hi & 0xFFFFu));
-    if (groups > 3) p = times(p, row(hi >> 16));
+    if constexpr (G > 1) p = times(p, row(lo >> 16));
+    if constexpr (G > 2) p = times(p, row(hi & 0xFFFFu));
+    if constexpr (G > 3) p = times(p, row(hi >> 16));
     return p;
 }
 
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant
 // add them up so that every lane ends with its own sample's sum.
 constexpr uint32_t kOutside = 0xFFFFFFFFu;     // of a sample that takes no part
 
-template <int CS>
+template <int CS, int G>
 __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const __grid_constant__ EntriesArgs a,
                                                                           const __grid_constant__ StageArgs stage_args,
                                                                           const __grid_constant__ Tables tables,
@@ -146,7 +148,8 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
         uint2 r = make_uint2(kOutside, kOutside);
         if (sort_key(a.index, t0 + i, 0) != kNone) {
             r = make_uint2(0u, 0u);
-            for (int k = 0; k < tables.groups; ++k) {
+#pragma unroll
+            for (int k = 0; k < G; ++k) {
                 const uint32_t row = table_row(a.index, tables.group[k], t0 + i) << (k & 1) * 16;
                 if (k < 2) r.x |= row;
                 else r.y |= row;
@@ -167,8 +170,8 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
 #pragma unroll
             for (int k = 0; k < L; ++k) {
                 const uint32_t lo_k = __shfl_sync(0xFFFFFFFFu, lo, k, L);
-                const uint32_t hi_k = tables.groups > 2 ? __shfl_sync(0xFFFFFFFFu, hi, k, L) : 0u;
-                const float4 p = product<CS>(mine, tables.groups, lo_k, hi_k);
+                const uint32_t hi_k = G > 2 ? __shfl_sync(0xFFFFFFFFu, hi, k, L) : 0u;
+                const float4 p = product<CS, G>(mine, lo_k, hi_k);
                 acc[k] = (p.x + p.y) + (p.z + p.w);
             }
 #pragma unroll
@@ -242,10 +245,9 @@ struct Model {
 // on their way while these are used
 struct StagedOf {
     const float* tab;       // at the lane's columns
-    int groups;
 };
 
-template <int CS, int VEC>
+template <int CS, int VEC, int G>
 struct Staged {
     template <typename List>
     struct Terms {
@@ -271,18 +273,16 @@ struct Staged {
         __device__ __forceinline__ void add(int j, float* acc) const {
             const float g = __uint_as_float(entry[j].y);
             if constexpr (VEC == 4) {
-                float4 p = make_float4(1.f, 1.f, 1.f, 1.f);
-                if (of.groups > 0) p = product<CS>(of.tab, of.groups, entry[j].z, entry[j].w);
+                const float4 p = product<CS, G>(of.tab, entry[j].z, entry[j].w);
                 acc[0] = fmaf(g, p.x, acc[0]);
                 acc[1] = fmaf(g, p.y, acc[1]);
                 acc[2] = fmaf(g, p.z, acc[2]);
                 acc[3] = fmaf(g, p.w, acc[3]);
             } else {
-                float p = 1.f;
-                if (of.groups > 0) p *= of.tab[(entry[j].z & 0xFFFFu) * CS];
-                if (of.groups > 1) p *= of.tab[(entry[j].z >> 16) * CS];
-                if (of.groups > 2) p *= of.tab[(entry[j].w & 0xFFFFu) * CS];
-                if (of.groups > 3) p *= of.tab[(entry[j].w >> 16) * CS];
+                float p = of.tab[(entry[j].z & 0xFFFFu) * CS];
+                if constexpr (G > 1) p *= of.tab[(entry[j].z >> 16) * CS];
+                if constexpr (G > 2) p *= of.tab[(entry[j].w & 0xFFFFu) * CS];
+                if constexpr (G > 3) p *= of.tab[(entry[j].w >> 16) * CS];
                 acc[0] = fmaf(g, p, acc[0]);
             }
         }
@@ -340,10 +340,18 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     around.after = p0 + count < n && list[count].x == list[count - 1].x;
     around.head = part;
     around.tail = part + s.a.width;
-    const StagedOf of{tab + (threadIdx.x & (L - 1)) * VEC, a.tables[m].groups};
-    sum_list<float, VEC, Staged<CS, VEC>::template Terms, kStageThreads>(
-        s.a, m, of, [&](int p) { return __ldg(list + p); }, [](uint32_t v) { return v; }, count, kLog2L, col0, heads,
-        around, [] { __syncthreads(); });
+    const StagedOf of{tab + (threadIdx.x & (L - 1)) * VEC};
+    auto sum = [&](auto g) {
+        sum_list<float, VEC, Staged<CS, VEC, decltype(g)::value>::template Terms, kStageThreads>(
+            s.a, m, of, [&](int p) { return __ldg(list + p); }, [](uint32_t v) { return v; }, count, kLog2L, col0,
+            heads, around, [] { __syncthreads(); });
+    };
+    switch (a.tables[m].groups) {
+        case 1: sum(std::integral_constant<int, 1>()); break;
+        case 2: sum(std::integral_constant<int, 2>()); break;
+        case 3: sum(std::integral_constant<int, 3>()); break;
+        default: sum(std::integral_constant<int, 4>()); break;
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -433,14 +441,25 @@ StageArgs stage_args(const IndexArgs& index, const void* const* factor, int type
     return a;
 }
 
-template <int CS>
+template <int CS, int G>
 cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share, cudaStream_t s) {
-    cudaError_t e = allow_smem<entries_staged_kernel<CS>>();
+    constexpr auto kernel = entries_staged_kernel<CS, G>;
+    cudaError_t e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(float) * t.rows * CS + sizeof(uint2) * share;
-    entries_staged_kernel<CS><<<(unsigned)cdiv(a.index.n, share), kStageThreads, smem, s>>>(
+    kernel<<<(unsigned)cdiv(a.index.n, share), kStageThreads, smem, s>>>(
         a, stage_args(a.index, a.factor, a.type, a.width), t, (int)share);
     return cudaGetLastError();
+}
+
+template <int CS>
+cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share, cudaStream_t s) {
+    switch (t.groups) {
+        case 1: return entries_staged<CS, 1>(a, t, share, s);
+        case 2: return entries_staged<CS, 2>(a, t, share, s);
+        case 3: return entries_staged<CS, 3>(a, t, share, s);
+        default: return entries_staged<CS, 4>(a, t, share, s);
+    }
 }
 
 template <typename T>

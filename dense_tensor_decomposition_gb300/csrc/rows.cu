@@ -8,34 +8,41 @@ namespace {
 
 // ---------------------------------------------------------------- lookup
 
-// Bound by memory (the rows met, and the result).  L lanes take one part of one
-// row: U vectors of VEC elements each, L vectors apart, all loaded before the first
-// is stored.
-template <typename T, int VEC, int U>
-__global__ void __launch_bounds__(kThreads) lookup_kernel(LookupArgs a, int log2L) {
+// Bound by memory (the rows met, and the result).  L lanes take one part of K tokens'
+// rows: U vectors of VEC elements each, L vectors apart.  The tokens' indices, then all
+// vectors are loaded before the first is stored.
+template <typename T, int VEC, int U, int K>
+__global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupArgs a, int log2L) {
     using P = Pack<T, VEC>;
     const int lane = threadIdx.x & ((1 << log2L) - 1);
-    const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> log2L;
-    if (t >= a.index.n) return;
+    const int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> log2L) * K;
     const int step = VEC << log2L;
     const int c0 = (int)blockIdx.y * U * step + lane * VEC;
     const int width = (int)a.width;
-    const int64_t v = index_at(a.index, t, 0);
-    const bool inside = v >= 0 && v < a.index.rows[0];
-    P x[U];
-    if (inside) {
-        const T* src = static_cast<const T*>(a.table) + v * a.table_stride;
+    int64_t v[K];
+    P x[K][U];
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = t0 + k < a.index.n ? index_at(a.index, t0 + k, 0) : -1;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        if (v[k] < 0 || v[k] >= a.index.rows[0]) v[k] = -1;
+        const T* src = static_cast<const T*>(a.table) + v[k] * a.table_stride;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (c0 + u * step < width) x[u] = *reinterpret_cast<const P*>(src + c0 + u * step);
+            if (v[k] >= 0 && c0 + u * step < width) x[k][u] = *reinterpret_cast<const P*>(src + c0 + u * step);
     }
-    T* dst = static_cast<T*>(a.out) + t * a.out_stride;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (c0 + u * step >= width) break;
+    for (int k = 0; k < K; ++k) {
+        if (t0 + k >= a.index.n) break;
+        T* dst = static_cast<T*>(a.out) + (t0 + k) * a.out_stride;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[u].v[e] = from_f32<T>(inside ? a.scale * to_f32(x[u].v[e]) : 0.f);
-        *reinterpret_cast<P*>(dst + c0 + u * step) = x[u];
+        for (int u = 0; u < U; ++u) {
+            if (c0 + u * step >= width) break;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                x[k][u].v[e] = from_f32<T>(v[k] >= 0 ? a.scale * to_f32(x[k][u].v[e]) : 0.f);
+            *reinterpret_cast<P*>(dst + c0 + u * step) = x[k][u];
+        }
     }
 }
 
@@ -46,11 +53,12 @@ int log2_lanes(int64_t items) {
     return l;
 }
 
-template <typename T, int VEC, int U>
+template <typename T, int VEC, int U, int K>
 cudaError_t lookup_by(const LookupArgs& a, cudaStream_t s) {
     const int l = log2_lanes(cdiv(a.width, VEC));
-    const dim3 grid((unsigned)cdiv(a.index.n << l, kThreads), (unsigned)cdiv(a.width, (int64_t)(VEC * U) << l));
-    lookup_kernel<T, VEC, U><<<grid, kThreads, 0, s>>>(a, l);
+    const dim3 grid((unsigned)cdiv(cdiv(a.index.n, K) << l, kThreads),
+                    (unsigned)cdiv(a.width, (int64_t)(VEC * U) << l));
+    lookup_kernel<T, VEC, U, K><<<grid, kThreads, 0, s>>>(a, l);
     return cudaGetLastError();
 }
 
@@ -60,9 +68,9 @@ cudaError_t lookup(const LookupArgs& a, cudaStream_t s) {
     constexpr int e = sizeof(T);
     const size_t all = reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.out) |
                        (a.table_stride * e) | (a.out_stride * e) | (a.width * e);
-    if (all % 16 == 0) return lookup_by<T, 16 / e, 4>(a, s);
-    if (all % 4 == 0) return lookup_by<T, 4 / e, 8>(a, s);
-    if constexpr (e < 4) return lookup_by<T, 1, 16>(a, s);
+    if (all % 16 == 0) return lookup_by<T, 16 / e, 4, 1>(a, s);
+    if (all % 4 == 0) return lookup_by<T, 4 / e, 8, 2>(a, s);
+    if constexpr (e < 4) return lookup_by<T, 1, 8, 4>(a, s);
     return cudaErrorInvalidValue;
 }
 

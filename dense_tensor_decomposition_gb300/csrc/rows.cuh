@@ -40,16 +40,30 @@ __device__ __forceinline__ int64_t index_at(const IndexArgs& a, int64_t t, int m
     return a.bytes == 8 ? static_cast<const int64_t*>(a.idx)[at] : (int64_t) static_cast<const int32_t*>(a.idx)[at];
 }
 
-// the row that token t points to in column m, kNone where it takes no part
-__device__ __forceinline__ uint32_t sort_key(const IndexArgs& a, int64_t t, int m) {
-    uint32_t key = kNone;
+// the row that token t points to in column m, kNone where it takes no part; the
+// loads of all columns are issued together
+template <typename I>
+__device__ __forceinline__ uint32_t sort_key_as(const IndexArgs& a, int64_t t, int m) {
+    const I* idx = static_cast<const I*>(a.idx) + t * a.stride;
+    I v[MTTKRP_MAX_ORDER];
+#pragma unroll
+    for (int l = 0; l < MTTKRP_MAX_ORDER; ++l) v[l] = l < a.d ? idx[l] : 0;
+    uint32_t key = 0;
     bool inside = true;
-    for (int l = 0; l < a.d; ++l) {
-        const int64_t v = index_at(a, t, l);
-        inside = inside && v >= 0 && v < a.rows[l];
-        if (l == m) key = (uint32_t)v;
+#pragma unroll
+    for (int l = 0; l < MTTKRP_MAX_ORDER; ++l) {
+        inside &= l >= a.d || (v[l] >= 0 && (int64_t)v[l] < a.rows[l]);
+        key = l == m ? (uint32_t)v[l] : key;
     }
     return inside ? key : kNone;
+}
+
+__device__ __forceinline__ uint32_t sort_key(const IndexArgs& a, int64_t t, int m) {
+    if (a.d == 1) {
+        const int64_t v = index_at(a, t, 0);
+        return v >= 0 && v < a.rows[0] ? (uint32_t)v : kNone;
+    }
+    return a.bytes == 8 ? sort_key_as<int64_t>(a, t, m) : sort_key_as<int32_t>(a, t, m);
 }
 
 // Sum of x over the threads before this one of a CTA of 32 warps, and over all (in

@@ -13,11 +13,11 @@ namespace {
 // `bits` bits counts the digits (every warp those of its own consecutive tokens), waits
 // for the grid, adds up the counts of smaller digits and of the CTAs before, and places
 // the tokens.  With one tile a CTA the tokens and their ranks stay in registers between
-// the two halves.  Tokens that take no part have row kNone, whose digits are all ones,
-// and end up last.
+// the two halves.  Tokens that take no part have row kNone and end up last: a single
+// pass gives them the digit above the last row's, more passes see digits of all ones.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortItems = 4;
+constexpr int kSortItems = 8;
 constexpr int kSortTile = kSortThreads * kSortItems;
 constexpr int kMaxDigit = 10;
 
@@ -26,6 +26,7 @@ struct SortArgs {
     uint2* buf[2];          // d x n pairs each; pass k writes buf[k & 1]
     uint32_t* counts;       // d x ctas x 2^bits
     int passes, bits;
+    int bins;               // digits: 2^bits, or one more than the most rows in a single pass
     int64_t per_cta;
     uint4* entries;         // the last pass's output as entries of 16 bytes, or nullptr
     const float* g;
@@ -58,7 +59,7 @@ __device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits) {
 
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ uint32_t sort_smem[];
-    const int nb = 1 << a.bits, m = blockIdx.y;
+    const int nb = a.bins, m = blockIdx.y;
     uint32_t* whist = sort_smem;                    // kSortWarps x nb
     uint32_t* first = sort_smem + kSortWarps * nb;  // nb: counts of the CTA's digits, then their next places
     uint32_t* extra = first + nb;                   // 2 x kSortThreads
@@ -71,8 +72,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
 
     // a warp has kSortItems * 32 consecutive tokens of a tile
     uint2 kt[kSortItems];
-    uint32_t digit[kSortItems];     // kNone: no token
-    uint32_t before[kSortItems];    // tokens of the warp with the same digit that come first
+    uint32_t place[kSortItems];     // digit, and << 16 how many of the warp's tokens with it come first; kNone: no token
     auto rank_tile = [&](int pass, int64_t tile) {
         const uint2* src = a.buf[(pass + 1) & 1] + m * n;
 #pragma unroll
@@ -80,25 +80,22 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
             const int64_t t = tile + warp * (kSortItems * 32) + i * 32 + lane;
             kt[i] = make_uint2(kNone, 0u);
             if (t < t1) kt[i] = pass == 0 ? make_uint2(sort_key(a.index, t, m), (uint32_t)t) : __ldcg(src + t);
-            digit[i] = t < t1 ? (kt[i].x >> pass * a.bits) & (nb - 1) : kNone;
+            place[i] = kNone;
+            if (t < t1)
+                place[i] = a.passes == 1 ? min(kt[i].x, (uint32_t)nb - 1) : (kt[i].x >> pass * a.bits) & (nb - 1);
         }
         __syncthreads();            // what stood in whist has been read
         for (int i = tid; i < kSortWarps * nb; i += kSortThreads) whist[i] = 0;
-        uint32_t peers[kSortItems];
-#pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
-            peers[i] = same_digit(digit[i], a.bits);
-            // a lane without a token is not among the peers of those with digits of all ones
-            peers[i] &= __ballot_sync(0xFFFFFFFFu, digit[i] != kNone);
-        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
-            const uint32_t rank = __popc(peers[i] & ((1u << lane) - 1));
-            before[i] = 0;
-            if (digit[i] != kNone) before[i] = wh[digit[i]] + rank;
+            // a lane without a token is not among the peers of those with digits of all ones
+            const uint32_t digit = place[i];
+            const uint32_t peers = same_digit(digit, a.bits) & __ballot_sync(0xFFFFFFFFu, digit != kNone);
+            const uint32_t rank = __popc(peers & ((1u << lane) - 1));
+            if (digit != kNone) place[i] = digit | (wh[digit] + rank) << 16;
             __syncwarp();
-            if (digit[i] != kNone && rank == 0) wh[digit[i]] += __popc(peers[i]);
+            if (digit != kNone && rank == 0) wh[digit] += __popc(peers);
             __syncwarp();
         }
         __syncthreads();
@@ -122,15 +119,17 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
         for (int b = tid; b < nb; b += kSortThreads) __stcg(counts + blockIdx.x * nb + b, first[b]);
         cg::this_grid().sync();
         // tokens with this digit in the CTAs before, and in all: every digit is added up
-        // by kSortThreads / nb threads
+        // by kSortThreads / nb threads (nb <= kSortThreads)
         {
-            const int b = tid & (nb - 1), split = tid >> a.bits, splits = kSortThreads >> a.bits;
+            const int splits = kSortThreads / nb, split = tid / nb, b = tid - split * nb;
             uint32_t less = 0, total = 0;
+            if (split < splits) {
 #pragma unroll 8
-            for (int k = split; k < (int)gridDim.x; k += splits) {
-                const uint32_t x = __ldcg(counts + k * nb + b);
-                total += x;
-                less += k < (int)blockIdx.x ? x : 0;
+                for (int k = split; k < (int)gridDim.x; k += splits) {
+                    const uint32_t x = __ldcg(counts + k * nb + b);
+                    total += x;
+                    less += k < (int)blockIdx.x ? x : 0;
+                }
             }
             extra[tid] = less;
             extra[kSortThreads + tid] = total;
@@ -152,35 +151,35 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
             if (tile != t0) rank_tile(pass, at);    // more than one: the tile is no longer in the registers
             __syncthreads();
             for (int b = tid; b < nb; b += kSortThreads) {
-                uint32_t place = first[b];
+                uint32_t next = first[b];
                 for (int w = 0; w < kSortWarps; w += 8) {
                     uint32_t c[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) c[k] = whist[(w + k) * nb + b];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        whist[(w + k) * nb + b] = place;
-                        place += c[k];
+                        whist[(w + k) * nb + b] = next;
+                        next += c[k];
                     }
                 }
-                first[b] = place;
+                first[b] = next;
             }
             __syncthreads();
 #pragma unroll 1
             for (int i = 0; i < kSortItems; ++i) {
                 uint2 x = kt[0];
-                uint32_t g = digit[0], r = before[0];
+                uint32_t where = place[0];
 #pragma unroll
                 for (int k = 1; k < kSortItems; ++k) {
                     if (i == k) {
                         x = kt[k];
-                        g = digit[k];
-                        r = before[k];
+                        where = place[k];
                     }
                 }
-                if (g == kNone) continue;
-                if (last && a.entries) a.entries[m * n + wh[g] + r] = entry_of(a, x, m);
-                else __stcg(dst + wh[g] + r, x);
+                if (where == kNone) continue;
+                const uint32_t to = wh[where & 0xFFFFu] + (where >> 16);
+                if (last && a.entries) a.entries[m * n + to] = entry_of(a, x, m);
+                else __stcg(dst + to, x);
             }
         }
         if (!last) cg::this_grid().sync();
@@ -198,12 +197,13 @@ SortPlan plan_sort(const IndexArgs& x, int entry_bytes) {
     while (((int64_t)1 << bits) <= most) ++bits;
     p.passes = (int)cdiv(bits, kMaxDigit);
     p.bits = (int)cdiv(bits, p.passes);
+    p.bins = p.passes == 1 ? (int)most + 1 : 1 << p.bits;
     // as many CTAs as are resident at once, of one tile each if that is enough
     const int64_t n = x.n > 0 ? x.n : 1;
     p.per_cta = cdiv(cdiv(n, kSms / x.d), kSortTile) * kSortTile;
     p.ctas = (int)cdiv(n, p.per_cta);
     p.pairs = align256((size_t)entry_bytes * x.d * x.n);
-    p.counts = align256(sizeof(uint32_t) * x.d * p.ctas << p.bits);
+    p.counts = align256(sizeof(uint32_t) * x.d * p.ctas * p.bins);
     return p;
 }
 
@@ -212,7 +212,7 @@ cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, con
     sorted.entries = static_cast<char*>(ws) + ((p.passes - 1) & 1) * p.pairs;
     sorted.bytes = tables ? sizeof(uint4) : sizeof(uint2);
     if (index.n == 0) return cudaSuccess;
-    const size_t smem = sizeof(uint32_t) * (((kSortWarps + 1) << p.bits) + 2 * kSortThreads);
+    const size_t smem = sizeof(uint32_t) * ((kSortWarps + 1) * p.bins + 2 * kSortThreads);
     cudaError_t e = allow_smem<sort_kernel>();
     if (e != cudaSuccess) return e;
     SortArgs a;
@@ -221,6 +221,7 @@ cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, con
     a.counts = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + 2 * p.pairs);
     a.passes = p.passes;
     a.bits = p.bits;
+    a.bins = p.bins;
     a.per_cta = p.per_cta;
     a.entries = tables ? static_cast<uint4*>(static_cast<void*>(a.buf[(p.passes - 1) & 1])) : nullptr;
     a.g = g;

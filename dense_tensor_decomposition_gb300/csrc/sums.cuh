@@ -225,18 +225,27 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
     if (threadIdx.x == 0) next_unit = 0;
     __syncthreads();
     uint32_t count = 0;
-    for (uint32_t k = 0; k < o.per_warp; k += 32) {
-        const uint32_t t = warp * o.per_warp + k + lane;
-        const uint32_t v = t < n ? sort_key(a.index, t, m) : kNone;
-        const uint32_t block = v >> o.row_shift, turn = block / G;
-        const bool mine = v != kNone && block - turn * G == blockIdx.x;
-        const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
-        if (mine) {
-            const uint32_t r = (turn << o.row_shift) | (v & low);
-            found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
-            atomicAdd(cursor + r, 1u);
+    constexpr int kLook = 4;        // tokens a lane looks up at once
+    for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
+        uint32_t key[kLook];
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+            const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
+            key[u] = k < o.per_warp && t < n ? sort_key(a.index, t, m) : kNone;
         }
-        count += __popc(ballot);
+#pragma unroll
+        for (int u = 0; u < kLook; ++u) {
+            const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
+            const uint32_t block = v >> o.row_shift, turn = block / G;
+            const bool mine = v != kNone && block - turn * G == blockIdx.x;
+            const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
+            if (mine) {
+                const uint32_t r = (turn << o.row_shift) | (v & low);
+                found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
+                atomicAdd(cursor + r, 1u);
+            }
+            count += __popc(ballot);
+        }
     }
     if (lane == 0) warp_found[warp] = count;
     __syncthreads();
