@@ -17,6 +17,8 @@ import ctypes
 import os
 import re
 import threading
+from array import array
+from operator import attrgetter
 
 from ._build import LIB as LIB_PATH, build  # noqa: F401
 
@@ -557,32 +559,41 @@ def ttm_multi(X, modes, Ms, outs=None, stream=None, path: str = "auto", workspac
 # Operators of a sampled fit
 # ---------------------------------------------------------------------------
 
+_type_codes: dict = {}      # torch dtype -> MTTKRP_F32, MTTKRP_BF16 or MTTKRP_F16
+_dtype_of = attrgetter("dtype")
+_raw_stream = None          # device index -> its current stream's handle
+
+
+def _sampled_library():
+    """The library, with what the functions below look up once."""
+    global _raw_stream
+    lib = load_library()
+    if not _type_codes:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _type_codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    return lib
+
+
 def _type_code(t, name: str) -> int:
-    """MTTKRP_F32, MTTKRP_BF16 or MTTKRP_F16 for a CUDA tensor of that type."""
+    """The code of a CUDA tensor's type."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    dt = t.dtype
-    if dt == torch.float32:
-        return 0
-    if dt == torch.bfloat16:
-        return 1
-    if dt == torch.float16:
-        return 2
-    raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    code = _type_codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    return code
 
 
-def _index_args(idx, device, name: str = "idx"):
-    """(pointer, count, stride, bytes) of an index tensor: int32 or int64,
-    contiguous of any shape, or one-dimensional with any stride."""
+def _index_args(idx, like, name: str = "idx"):
+    """(pointer, count, stride, bytes) of an index tensor on the device of `like`:
+    int32 or int64, contiguous of any shape, or one-dimensional with any stride."""
     import torch
-    if not isinstance(idx, torch.Tensor) or idx.device != device:
+    if not isinstance(idx, torch.Tensor) or idx.get_device() != like.get_device():
         raise TypeError(f"{name} must be a CUDA tensor on the other tensors' device")
-    if idx.dtype == torch.int64:
-        nbytes = 8
-    elif idx.dtype == torch.int32:
-        nbytes = 4
-    else:
+    if idx.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"{name} must be int32 or int64")
     if idx.dim() == 1:
         stride = idx.stride(0)
@@ -590,22 +601,22 @@ def _index_args(idx, device, name: str = "idx"):
         stride = 1
     else:
         raise ValueError(f"{name} must be contiguous or one-dimensional")
-    return idx.data_ptr(), idx.numel(), stride, nbytes
+    return idx.data_ptr(), idx.numel(), stride, idx.element_size()
 
 
 def _row_stride(t, rows: int, width: int, name: str) -> int:
     """Elements from one row to the next of a tensor of `rows` rows (all dimensions
     but the last) of `width` consecutive elements."""
-    if t.dim() == 2:
-        if t.shape[0] != rows or t.shape[1] != width:
-            raise ValueError(f"{name} must be {rows} x {width}")
-        if rows > 1 and (t.stride(1) != 1 and width > 1 or t.stride(0) < width) or rows == 1 and width > 1 \
-                and t.stride(1) != 1:
-            raise ValueError(f"{name}: the elements of a row must be consecutive and rows must not overlap")
-        return t.stride(0) if rows > 1 else width
-    if t.dim() < 1 or t.shape[-1] != width or t.numel() != rows * width or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {rows} rows of {width}")
-    return width
+    if t.is_contiguous():
+        if t.dim() < 1 or t.shape[-1] != width or t.numel() != rows * width:
+            raise ValueError(f"{name} must have {rows} rows of {width}")
+        return width
+    if t.dim() != 2 or tuple(t.shape) != (rows, width):
+        raise ValueError(f"{name} must be {rows} x {width}, or contiguous with as many rows")
+    step, inner = t.stride()
+    if width > 1 and inner != 1 or rows > 1 and step < width:
+        raise ValueError(f"{name}: the elements of a row must be consecutive and rows must not overlap")
+    return step if rows > 1 else width
 
 
 def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
@@ -615,13 +626,13 @@ def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
     gives a row of zeros.  Returns idx.shape + (width,) of the table's type, written
     into `out` when given."""
     import torch
-    lib = load_library()
+    lib = _sampled_library()
     code = _type_code(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be rows x width")
     rows, width = table.shape
     stride = _row_stride(table, rows, width, "table")
-    ptr, n, idx_stride, nbytes = _index_args(idx, table.device)
+    ptr, n, idx_stride, nbytes = _index_args(idx, table)
     shape = (*idx.shape, width)
     if out is None:
         out = torch.empty(shape, dtype=table.dtype, device=table.device)
@@ -631,9 +642,11 @@ def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
                 or tuple(out.shape) != shape:
             raise ValueError(f"out must be a {table.dtype} CUDA tensor of shape {shape}")
         out_stride = _row_stride(out, n, width, "out")
-    _check(lib.mttkrp_embedding(table.data_ptr(), rows, width, stride, code, ptr, n, idx_stride, nbytes, scale,
-                                out.data_ptr(), out_stride, _stream_handle(table.device, stream)),
-           "mttkrp_embedding")
+    rc = lib.mttkrp_embedding(table.data_ptr(), rows, width, stride, code, ptr, n, idx_stride, nbytes, scale,
+                              out.data_ptr(), out_stride,
+                              _raw_stream(table.get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mttkrp_embedding")
     return out
 
 
@@ -645,9 +658,9 @@ def embedding_grad(idx, grad, rows: int, scale: float = 1.0, out=None, dtype=Non
     (float32 by default, or grad's type), written into `out` when given;
     accumulate adds to `out` and leaves the rows that no token points to alone."""
     import torch
-    lib = load_library()
+    lib = _sampled_library()
     code = _type_code(grad, "grad")
-    ptr, n, idx_stride, nbytes = _index_args(idx, grad.device)
+    ptr, n, idx_stride, nbytes = _index_args(idx, grad)
     if grad.dim() < 1 or grad.shape[:-1] != idx.shape:
         raise ValueError("grad must have the shape of idx and one more dimension")
     width = grad.shape[-1]
@@ -664,35 +677,45 @@ def embedding_grad(idx, grad, rows: int, scale: float = 1.0, out=None, dtype=Non
             raise ValueError("out must be a CUDA tensor of rows x width on grad's device, of dtype if that is given")
         out_stride = _row_stride(out, rows, width, "out")
     need = lib.mttkrp_embedding_grad_workspace_bytes(n, rows, width)
-    ws = torch.empty(need, dtype=torch.uint8, device=grad.device)
-    _check(lib.mttkrp_embedding_grad(ptr, n, idx_stride, nbytes, grad.data_ptr(), code, stride, rows, width, scale,
-                                     accumulate, out.data_ptr(), _type_code(out, "out"), out_stride, ws.data_ptr(),
-                                     need, _stream_handle(grad.device, stream)), "mttkrp_embedding_grad")
+    ws = torch.empty(need, dtype=torch.uint8, device=grad.device) if need else None
+    rc = lib.mttkrp_embedding_grad(ptr, n, idx_stride, nbytes, grad.data_ptr(), code, stride, rows, width, scale,
+                                   accumulate, out.data_ptr(), _type_code(out, "out"), out_stride,
+                                   ws.data_ptr() if need else None, need,
+                                   _raw_stream(grad.get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mttkrp_embedding_grad")
     return out
 
 
 def _model_args(factors, coords):
     """(d, dims, R, factor pointers, type code) of a CP model's factors, checked
-    together with its coordinates (samples x d, contiguous)."""
+    together with its coordinates (samples x d, contiguous); dims and pointers as
+    arrays."""
     import torch
-    factors = list(factors)
-    d = len(factors)
-    if d < 1:
+    if not factors:
         raise ValueError("at least one factor is needed")
-    code = _type_code(factors[0], "factor 0")
-    device, dtype, R = factors[0].device, factors[0].dtype, factors[0].shape[-1] if factors[0].dim() else 0
+    first = factors[0]
+    code = _type_code(first, "factor 0")
+    dtype, device, R = first.dtype, first.get_device(), first.shape[-1] if first.dim() else 0
+    dims, ptrs = array("q"), array("Q")
     for n, a in enumerate(factors):
-        if not isinstance(a, torch.Tensor) or a.device != device or a.dtype != dtype or a.dim() != 2 \
+        if not isinstance(a, torch.Tensor) or a.get_device() != device or a.dtype != dtype or a.dim() != 2 \
                 or a.shape[1] != R or not a.is_contiguous():
-            raise ValueError(f"factor {n} must be a contiguous {dtype} tensor of {R} columns on {device}")
-    if not isinstance(coords, torch.Tensor) or coords.device != device \
+            raise ValueError(f"factor {n} must be a contiguous {dtype} tensor of {R} columns on {first.device}")
+        dims.append(a.shape[0])
+        ptrs.append(a.data_ptr())
+    d = len(dims)
+    if not isinstance(coords, torch.Tensor) or coords.get_device() != device \
             or coords.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"coords must be an int32 or int64 tensor on {device}")
+        raise TypeError(f"coords must be an int32 or int64 tensor on {first.device}")
     if coords.dim() != 2 or coords.shape[1] != d or not coords.is_contiguous():
         raise ValueError(f"coords must be contiguous, samples x {d}")
-    dims = (ctypes.c_int64 * d)(*[a.shape[0] for a in factors])
-    ptrs = (ctypes.c_void_p * d)(*[a.data_ptr() for a in factors])
     return d, dims, R, ptrs, code
+
+
+def _address(a) -> int:
+    """Where an array's elements are."""
+    return a.buffer_info()[0]
 
 
 def cp_entries(factors, coords, out=None, stream=None):
@@ -702,16 +725,19 @@ def cp_entries(factors, coords, out=None, stream=None):
     0 where a coordinate is out of range.  Component weights go into a factor, or in
     as a factor with one row."""
     import torch
-    lib = load_library()
-    d, dims, R, ptrs, code = _model_args(factors, coords)
-    n, device = coords.shape[0], coords.device
+    lib = _sampled_library()
+    d, dims, R, ptrs, code = _model_args(list(factors), coords)
+    n = coords.shape[0]
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=device)
-    elif not isinstance(out, torch.Tensor) or out.device != device or out.dtype != torch.float32 \
+        out = torch.empty(n, dtype=torch.float32, device=coords.device)
+    elif not isinstance(out, torch.Tensor) or out.device != coords.device or out.dtype != torch.float32 \
             or tuple(out.shape) != (n,) or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous float32 CUDA tensor of {n} elements")
-    _check(lib.mttkrp_cp_entries(d, dims, R, ptrs, code, coords.data_ptr(), n, coords.element_size(),
-                                 out.data_ptr(), _stream_handle(device, stream)), "mttkrp_cp_entries")
+    rc = lib.mttkrp_cp_entries(d, _address(dims), R, _address(ptrs), code, coords.data_ptr(), n,
+                               coords.element_size(), out.data_ptr(),
+                               _raw_stream(coords.get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mttkrp_cp_entries")
     return out
 
 
@@ -721,8 +747,8 @@ def cp_entries_grad(factors, coords, grad, outs=None, stream=None):
     float32, in a fixed order.  grad: one float32 value a sample.  Returns the list
     of gradients (written into `outs` when given)."""
     import torch
-    lib = load_library()
-    d, dims, R, ptrs, code = _model_args(factors, coords)
+    lib = _sampled_library()
+    d, dims, R, ptrs, code = _model_args(list(factors), coords)
     n, device = coords.shape[0], coords.device
     if not isinstance(grad, torch.Tensor) or grad.device != device or grad.dtype != torch.float32 \
             or tuple(grad.shape) != (n,) or not grad.is_contiguous():
@@ -737,32 +763,38 @@ def cp_entries_grad(factors, coords, grad, outs=None, stream=None):
             if not isinstance(o, torch.Tensor) or o.device != device or o.dtype != torch.float32 \
                     or tuple(o.shape) != (dims[m], R) or not o.is_contiguous():
                 raise ValueError(f"outs[{m}] must be a contiguous float32 CUDA tensor of shape {(dims[m], R)}")
-    optrs = (ctypes.c_void_p * d)(*[o.data_ptr() for o in outs])
-    need = lib.mttkrp_cp_entries_grad_workspace_bytes(d, dims, R, n)
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _check(lib.mttkrp_cp_entries_grad(d, dims, R, ptrs, code, coords.data_ptr(), n, coords.element_size(),
-                                      grad.data_ptr(), optrs, ws.data_ptr(), need,
-                                      _stream_handle(device, stream)), "mttkrp_cp_entries_grad")
+    optrs = array("Q", [o.data_ptr() for o in outs])
+    need = lib.mttkrp_cp_entries_grad_workspace_bytes(d, _address(dims), R, n)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    rc = lib.mttkrp_cp_entries_grad(d, _address(dims), R, _address(ptrs), code, coords.data_ptr(), n,
+                                    coords.element_size(), grad.data_ptr(), _address(optrs),
+                                    ws.data_ptr() if need else None, need,
+                                    _raw_stream(coords.get_device()) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "mttkrp_cp_entries_grad")
     return outs
 
 
 def _tensor_args(tensors, name: str):
-    """(pointers, element counts, type codes) of contiguous CUDA tensors on one device."""
-    n = len(tensors)
-    codes = [_type_code(t, f"{name}[{k}]") for k, t in enumerate(tensors)]
-    device = tensors[0].device
-    for k, t in enumerate(tensors):
-        if not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name}[{k}] must be contiguous and on {device}")
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]), (ctypes.c_int * n)(*codes))
+    """(device index, types, pointers, element counts) of contiguous CUDA tensors on
+    one device, the last two as arrays.  The lists can be long: each property is read
+    in one pass without Python code for the elements."""
+    import torch
+    T = torch.Tensor
+    devices = set(map(T.get_device, tensors))       # TypeError where one is not a tensor
+    if len(devices) > 1 or -1 in devices:
+        raise (TypeError if -1 in devices else ValueError)(f"{name} must be CUDA tensors on one device")
+    if not all(map(T.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    types = list(map(_dtype_of, tensors))
+    return devices.pop(), types, array("Q", map(T.data_ptr, tensors)), array("q", map(T.numel, tensors))
 
 
 def grad_norm(tensors, stream=None):
     """sqrt of the sum of squares over all elements of a list of CUDA tensors
     (mttkrp_grad_norm), as a float32 scalar on the device.  The tensors are
     contiguous, float32, bfloat16 or float16 in any mix, on one device."""
-    return _norm_and_clip(tensors, None, None, None, stream)
+    return _norm_and_clip(tensors, None, 0.0, None, stream)
 
 
 def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, stream=None):
@@ -775,33 +807,38 @@ def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, strea
 
 def _norm_and_clip(tensors, max_norm, eps, outs, stream):
     import torch
-    lib = load_library()
+    lib = _sampled_library()
     tensors = list(tensors)
     n = len(tensors)
     if n < 1:
         raise ValueError("at least one tensor is needed")
-    ptrs, numels, codes = _tensor_args(tensors, "tensors")
-    device = tensors[0].device
+    index, types, ptrs, numels = _tensor_args(tensors, "tensors")
+    try:
+        codes = array("i", map(_type_codes.__getitem__, types))
+    except KeyError:
+        raise TypeError("tensors must be float32, bfloat16 or float16") from None
     optrs = None
     if outs is not None:
         outs = list(outs)
         if len(outs) != n:
             raise ValueError("outs must hold one tensor per input")
-        for k, (o, t) in enumerate(zip(outs, tensors)):
-            if not isinstance(o, torch.Tensor) or o.device != device or o.dtype != t.dtype \
-                    or o.numel() != t.numel() or not o.is_contiguous():
-                raise ValueError(f"outs[{k}] must be a contiguous {t.dtype} CUDA tensor of {t.numel()} elements")
-        optrs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in outs])
+        oindex, otypes, optrs, onumels = _tensor_args(outs, "outs")
+        if oindex != index or otypes != types or onumels != numels:
+            raise ValueError("every tensor of outs must have its input's type, number of elements and device")
+    device = tensors[0].device
     norm = torch.empty((), dtype=torch.float32, device=device)
     need = lib.mttkrp_grad_norm_workspace_bytes(n)
     ws = torch.empty(need, dtype=torch.uint8, device=device)
-    st = _stream_handle(device, stream)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
     if max_norm is None:
-        _check(lib.mttkrp_grad_norm(n, ptrs, numels, codes, norm.data_ptr(), ws.data_ptr(), need, st),
-               "mttkrp_grad_norm")
+        rc = lib.mttkrp_grad_norm(n, _address(ptrs), _address(numels), _address(codes), norm.data_ptr(),
+                                  ws.data_ptr(), need, handle)
     else:
-        _check(lib.mttkrp_clip_grad_norm(n, ptrs, numels, codes, optrs, max_norm, eps, norm.data_ptr(),
-                                         ws.data_ptr(), need, st), "mttkrp_clip_grad_norm")
+        rc = lib.mttkrp_clip_grad_norm(n, _address(ptrs), _address(numels), _address(codes),
+                                       None if optrs is None else _address(optrs), max_norm, eps, norm.data_ptr(),
+                                       ws.data_ptr(), need, handle)
+    if rc:
+        _check(rc, "mttkrp_grad_norm" if max_norm is None else "mttkrp_clip_grad_norm")
     return norm
 
 

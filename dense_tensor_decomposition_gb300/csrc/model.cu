@@ -520,6 +520,7 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
 
 // for the larger entries that the sums from shared memory sort
 size_t entries_grad_workspace_bytes(const IndexArgs& index, int64_t width) {
+    if (always_owned(index, width)) return 0;
     return plan_sort(index, sizeof(uint4)).total() + part_bytes(index, width);
 }
 

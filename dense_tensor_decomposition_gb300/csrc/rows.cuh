@@ -66,9 +66,12 @@ __device__ __forceinline__ uint32_t sort_key(const IndexArgs& a, int64_t t, int 
     return a.bytes == 8 ? sort_key_as<int64_t>(a, t, m) : sort_key_as<int32_t>(a, t, m);
 }
 
-// Sum of x over the threads before this one of a CTA of 32 warps, and over all (in
-// `all`); sums: one word a warp.  The threads wait twice.
-__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums, uint32_t& all) {
+// Sum of x over the threads before this one of the first kWarps warps of a CTA, which
+// sync() makes wait for one another, and over all (in `all`); sums: one word a warp.
+// The threads wait twice.
+template <int kWarps, typename Sync>
+__device__ __forceinline__ uint32_t scan_warps(uint32_t x, uint32_t* sums, uint32_t& all, const Sync& sync) {
+    static_assert(kWarps <= 32, "a lane for each warp");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t scan = x;
 #pragma unroll
@@ -76,10 +79,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* sums, uint3
         const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, scan, o);
         if (lane >= o) scan += up;
     }
-    __syncthreads();
+    sync();
     if (lane == 31) sums[warp] = scan;
-    __syncthreads();
-    const uint32_t w = sums[lane];
+    sync();
+    const uint32_t w = lane < kWarps ? sums[lane] : 0;
     uint32_t wscan = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -33,7 +33,7 @@ struct Sorted {
 };
 
 struct SortPlan {
-    int passes, bits, bins, ctas;
+    int passes, bits, bins, ctas, items;
     int64_t per_cta;
     size_t pairs, counts;                   // bytes of one buffer of entries, and of the counts
     size_t total() const { return 2 * pairs + counts; }

@@ -184,8 +184,8 @@ struct TermsOf {
 // ---------------------------------------------------------------- few tokens: one launch
 
 constexpr int kOwnThreads = 1024;
-constexpr int kOwnWarps = kOwnThreads / 32;
-constexpr int kSumThreads = 512;        // of which these add, while the others write zeros
+constexpr int kSumThreads = 512;        // of which these group and add, while the others write zeros
+constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kTokenBits = 14;
 constexpr int kOwnTokens = 1 << kTokenBits;
 constexpr int kOwnRows = 1 << 13;       // rows of a CTA
@@ -196,11 +196,15 @@ struct OwnArgs {
     RowSumArgs a;
     int row_shift;
     uint32_t owned;         // most rows a CTA owns
-    uint32_t per_warp;      // tokens a warp looks at
+    uint32_t per_warp;      // tokens that each of the first kSumWarps warps looks at
     int log2L;
     int64_t part;           // columns of a CTA (blockIdx.y)
 };
 
+// Bound by memory: the rows' writes, most of them zeros where tokens are few, and the
+// terms' reads.  The zeros begin before it is known which rows have tokens: until the
+// tokens are grouped, the other half of the CTA writes them to all rows, from the last
+// one on; rows with tokens are written again.
 template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_constant__ OwnArgs o) {
     extern __shared__ float4 own_smem[];
@@ -209,78 +213,91 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
     uint32_t* cursor = reinterpret_cast<uint32_t*>(heads + kSumThreads * VEC);  // owned: tokens of each row, then their places
     uint32_t* touched = cursor + o.owned;                                       // a bit for each owned row
     uint32_t* found = touched + (o.owned + 31) / 32;                            // tokens of the CTA's rows, a part a warp
-    uint32_t* list = found + kOwnWarps * o.per_warp;                            // the same without gaps, then sorted
-    __shared__ uint32_t warp_found[kOwnWarps], sums[kOwnWarps], next_unit;
+    uint32_t* list = found + kSumWarps * o.per_warp;                            // the same without gaps, then sorted
+    __shared__ uint32_t warp_found[kSumWarps], sums[kSumWarps], tokens, next_unit, last_unit;
+    __shared__ volatile int grouped;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m = blockIdx.z;
     const uint32_t G = gridDim.x, n = (uint32_t)a.index.n, rows = (uint32_t)a.index.rows[m];
     const uint32_t low = (1u << o.row_shift) - 1;
     auto row_of = [&](uint32_t r) -> uint32_t {
         const uint64_t v = (((uint64_t)(r >> o.row_shift) * G + blockIdx.x) << o.row_shift) | (r & low);
-        return v < rows ? (uint32_t)v : kNone;
+        return r < o.owned && v < rows ? (uint32_t)v : kNone;
+    };
+    auto sync = [] { asm volatile("barrier.sync 1, %0;" ::"n"(kSumThreads) : "memory"); };
+    // zeros are written a unit of rows at a time
+    const int64_t col0 = (int64_t)blockIdx.y * o.part;
+    const uint32_t vecs = (uint32_t)((a.width - col0 < o.part ? a.width - col0 : o.part) / VEC);
+    const uint32_t unit = vecs >= 512 ? 1 : 512 / vecs, units = (o.owned + unit - 1) / unit;
+    auto take = [&](uint32_t* counter) {
+        uint32_t u = 0;
+        if (lane == 0) u = atomicAdd(counter, 1u);
+        return __shfl_sync(0xFFFFFFFFu, u, 0);
     };
 
-    // the CTA's tokens, as (owned row, token), in order in every warp's part
-    for (uint32_t i = threadIdx.x; i < o.owned; i += kOwnThreads) cursor[i] = 0;
-    if (threadIdx.x == 0) next_unit = 0;
+    if (threadIdx.x == 0) {
+        next_unit = 0;
+        last_unit = 0;
+        grouped = 0;
+    }
     __syncthreads();
-    uint32_t count = 0;
-    constexpr int kLook = 4;        // tokens a lane looks up at once
-    for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
-        uint32_t key[kLook];
+    if (warp < kSumWarps) {
+        // the CTA's tokens, as (owned row, token), in order in every warp's part
+        for (uint32_t i = threadIdx.x; i < o.owned; i += kSumThreads) cursor[i] = 0;
+        sync();
+        uint32_t count = 0;
+        constexpr int kLook = 4;        // tokens a lane looks up at once
+        for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
+            uint32_t key[kLook];
 #pragma unroll
-        for (int u = 0; u < kLook; ++u) {
-            const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
-            key[u] = k < o.per_warp && t < n ? sort_key(a.index, t, m) : kNone;
-        }
-#pragma unroll
-        for (int u = 0; u < kLook; ++u) {
-            const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
-            const uint32_t block = v >> o.row_shift, turn = block / G;
-            const bool mine = v != kNone && block - turn * G == blockIdx.x;
-            const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
-            if (mine) {
-                const uint32_t r = (turn << o.row_shift) | (v & low);
-                found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
-                atomicAdd(cursor + r, 1u);
+            for (int u = 0; u < kLook; ++u) {
+                const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
+                key[u] = k < o.per_warp && t < n ? sort_key(a.index, t, m) : kNone;
             }
-            count += __popc(ballot);
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
+                const uint32_t block = v >> o.row_shift, turn = block / G;
+                const bool mine = v != kNone && block - turn * G == blockIdx.x;
+                const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
+                if (mine) {
+                    const uint32_t r = (turn << o.row_shift) | (v & low);
+                    found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
+                    atomicAdd(cursor + r, 1u);
+                }
+                count += __popc(ballot);
+            }
         }
-    }
-    if (lane == 0) warp_found[warp] = count;
-    __syncthreads();
-    // gaps out; the counts become the rows' first places
-    uint32_t total = 0, base = 0;
-    for (int w = 0; w < kOwnWarps; ++w) {
-        const uint32_t c = warp_found[w];
-        base += w < warp ? c : 0;
-        total += c;
-    }
-    for (uint32_t k = lane; k < count; k += 32) list[base + k] = found[warp * o.per_warp + k];
-    const uint32_t per = (o.owned + kOwnThreads - 1) / kOwnThreads;
-    uint32_t mine = 0, all;
-    for (uint32_t k = 0; k < per; ++k) {
-        const uint32_t r = threadIdx.x * per + k;
-        mine += r < o.owned ? cursor[r] : 0;
-    }
-    uint32_t at = block_scan(mine, sums, all);
-    for (uint32_t r = threadIdx.x; r < (o.owned + 31) / 32 * 32; r += kOwnThreads) {
-        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, r < o.owned && cursor[r] != 0);
-        if (lane == 0) touched[r / 32] = bits;
-    }
-    __syncthreads();
-    for (uint32_t k = 0; k < per; ++k) {
-        const uint32_t r = threadIdx.x * per + k;
-        if (r >= o.owned) break;
-        const uint32_t c = cursor[r];
-        cursor[r] = at;
-        at += c;
-    }
-    __syncthreads();
-
-    const int64_t col0 = (int64_t)blockIdx.y * o.part;
-    if (warp < kSumThreads / 32 && total > 0) {
-        auto sync = [] { asm volatile("barrier.sync 1, %0;" ::"n"(kSumThreads) : "memory"); };
+        if (lane == 0) warp_found[warp] = count;
+        sync();
+        // gaps out; the counts become the rows' first places
+        uint32_t total = 0, base = 0;
+        for (int w = 0; w < kSumWarps; ++w) {
+            const uint32_t c = warp_found[w];
+            base += w < warp ? c : 0;
+            total += c;
+        }
+        for (uint32_t k = lane; k < count; k += 32) list[base + k] = found[warp * o.per_warp + k];
+        const uint32_t per = (o.owned + kSumThreads - 1) / kSumThreads;
+        uint32_t mine = 0, all;
+        for (uint32_t k = 0; k < per; ++k) {
+            const uint32_t r = threadIdx.x * per + k;
+            mine += r < o.owned ? cursor[r] : 0;
+        }
+        uint32_t at = scan_warps<kSumWarps>(mine, sums, all, sync);
+        for (uint32_t r = threadIdx.x; r < (o.owned + 31) / 32 * 32; r += kSumThreads) {
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, r < o.owned && cursor[r] != 0);
+            if (lane == 0) touched[r / 32] = bits;
+        }
+        sync();
+        for (uint32_t k = 0; k < per; ++k) {
+            const uint32_t r = threadIdx.x * per + k;
+            if (r >= o.owned) break;
+            const uint32_t c = cursor[r];
+            cursor[r] = at;
+            at += c;
+        }
+        sync();
         // in order of the tokens within each row: one warp places them 32 at a time
         if (warp == 0) {
             for (uint32_t k = 0; k < total; k += 32) {
@@ -296,23 +313,30 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
                 }
                 __syncwarp();
             }
+            if (lane == 0) {
+                tokens = total;
+                grouped = 1;
+            }
         }
-        sync();
+    } else if (!a.accumulate) {
+        while (!grouped) {
+            const uint32_t u = take(&last_unit);
+            if (u >= units) break;
+            zero_rows<TO, VEC>(a, m, (units - 1 - u) * unit, unit, col0, vecs, [](uint32_t) { return false; }, row_of);
+        }
+    }
+    __syncthreads();
+    const uint32_t left = units - (last_unit < units ? last_unit : units);
+    const int total = (int)tokens;
+    if (warp < kSumWarps && total > 0) {
         auto at_place = [&](int p) { return make_uint2(found[p] >> kTokenBits, found[p] & (kOwnTokens - 1)); };
-        sum_list<TO, VEC, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, (int)total, o.log2L, col0,
-                                                 heads, Around{false, false, nullptr, nullptr}, sync);
+        sum_list<TO, VEC, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, total, o.log2L, col0, heads,
+                                              Around{false, false, nullptr, nullptr}, sync);
     }
     if (a.accumulate) return;
-    const uint32_t vecs = (uint32_t)((a.width - col0 < o.part ? a.width - col0 : o.part) / VEC);
-    const uint32_t unit = vecs >= 1024 ? 1 : 1024 / vecs;
     auto is_touched = [&](uint32_t r) { return r >= o.owned || (touched[r >> 5] >> (r & 31) & 1u) != 0; };
-    for (;;) {
-        uint32_t u = 0;
-        if (lane == 0) u = atomicAdd(&next_unit, 1u);
-        u = __shfl_sync(0xFFFFFFFFu, u, 0);
-        if ((uint64_t)u * unit >= o.owned) break;
+    for (uint32_t u = take(&next_unit); u < left; u = take(&next_unit))
         zero_rows<TO, VEC>(a, m, u * unit, unit, col0, vecs, is_touched, row_of);
-    }
 }
 
 // ---------------------------------------------------------------- many tokens
@@ -451,28 +475,38 @@ inline int64_t most_rows(const IndexArgs& x) {
 
 // The rows' distribution over the CTAs of own_kernel for rows in vectors of `vec`
 // elements; false where there are too many tokens or rows for it.
-inline bool plan_own(const RowSumArgs& a, int vec, OwnArgs& o, dim3& grid) {
-    if (a.index.n > kOwnTokens) return false;
-    const int64_t rows = most_rows(a.index);
-    o.a = a;
+inline bool plan_own(const IndexArgs& index, int64_t width, int out_type, int vec, OwnArgs& o, dim3& grid) {
+    if (index.n > kOwnTokens) return false;
+    const int64_t rows = most_rows(index);
     o.log2L = 0;
-    while ((1 << o.log2L) < kSumThreads && ((int64_t)vec << o.log2L) < a.width) ++o.log2L;
+    while ((1 << o.log2L) < kSumThreads && ((int64_t)vec << o.log2L) < width) ++o.log2L;
     o.part = (int64_t)vec << o.log2L;
-    const int64_t parts = cdiv(a.width, o.part);
-    int64_t owners = kSms / (parts * a.index.d);
+    const int64_t parts = cdiv(width, o.part);
+    int64_t owners = kSms / (parts * index.d);
     owners = owners < 1 ? 1 : owners;
     // neighbouring rows stay together up to 1 KB, as long as every CTA gets eight blocks of them
     o.row_shift = 0;
-    const int64_t row_bytes = a.width * elem_bytes(a.out_type);
+    const int64_t row_bytes = width * elem_bytes(out_type);
     while ((row_bytes << o.row_shift) < 1024 && (rows >> (o.row_shift + 1)) >= 8 * owners) ++o.row_shift;
     const int64_t blocks = cdiv(rows, (int64_t)1 << o.row_shift);
     owners = owners < blocks ? owners : blocks;
     const int64_t owned = cdiv(blocks, owners) << o.row_shift;
     if (owned > kOwnRows || parts > 65535) return false;
     o.owned = (uint32_t)owned;
-    o.per_warp = (uint32_t)(cdiv(a.index.n, kOwnThreads) * 32);
-    grid = dim3((unsigned)owners, (unsigned)parts, a.index.d);
+    o.per_warp = (uint32_t)(cdiv(index.n, kSumThreads) * 32);
+    grid = dim3((unsigned)owners, (unsigned)parts, index.d);
     return true;
+}
+
+// whether own_kernel takes the sums whatever the alignment of the rows (one launch that
+// needs no workspace)
+inline bool always_owned(const IndexArgs& index, int64_t width) {
+    OwnArgs o;
+    dim3 grid;
+    bool all = true;
+    for (int type : {MTTKRP_F32, MTTKRP_F16})
+        for (int vec : {1, 4, 8}) all = all && plan_own(index, width, type, vec, o, grid);
+    return all;
 }
 
 // bytes of the partial sums, two rows for every kTile tokens
@@ -496,9 +530,10 @@ template <typename TO, int VEC, template <typename> typename Few, template <type
 cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     OwnArgs o;
     dim3 grid;
-    if (plan_own(a, VEC, o, grid)) {
+    if (plan_own(a.index, a.width, a.out_type, VEC, o, grid)) {
+        o.a = a;
         const size_t smem = sizeof(float) * kSumThreads * VEC +
-                            sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32 + 2 * kOwnWarps * o.per_warp);
+                            sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32 + 2 * kSumWarps * o.per_warp);
         constexpr auto kernel = own_kernel<TO, VEC, Few>;
         cudaError_t e = allow_smem<kernel>();
         if (e != cudaSuccess) return e;

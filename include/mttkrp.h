@@ -375,8 +375,8 @@ int mttkrp_embedding(const void* table, int64_t rows, int64_t width, int64_t tab
  *
  * grad      n x width of `type`, rows grad_stride >= width elements apart.
  * out       rows x width of out_type (MTTKRP_F32 or `type`), out_stride >= width.
- * workspace device, 256-byte aligned, mttkrp_embedding_grad_workspace_bytes() bytes
- *           (0 for invalid arguments).
+ * workspace device, 256-byte aligned, mttkrp_embedding_grad_workspace_bytes() bytes;
+ *           that is 0, and NULL is taken, for few tokens (and for invalid arguments).
  */
 size_t mttkrp_embedding_grad_workspace_bytes(int64_t n, int64_t rows, int64_t width);
 int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int idx_bytes, const void* grad, int type,
@@ -403,6 +403,7 @@ int mttkrp_cp_entries(int d, const int64_t* dims, int64_t R, const void* const* 
  *     outs[n](i, :) = sum over s with c_sn = i of g[s] * prod over m != n of A_m(c_sm, :)
  * outs      HOST array of d device pointers, outs[n] dims[n] x R fp32, overwritten.
  * Samples with a coordinate out of range take no part (their g is not read).
+ * The workspace is needed as for mttkrp_embedding_grad.
  */
 size_t mttkrp_cp_entries_grad_workspace_bytes(int d, const int64_t* dims, int64_t R, int64_t n_samples);
 int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* const* factors, int type,

@@ -37,7 +37,8 @@ def test_lookup_refuses(lib, change, why):
     refused(lib, lib.mttkrp_embedding(*{**LOOKUP, **change}.values(), None), why)
 
 
-GRAD = dict(idx=0x10000, n=16, idx_stride=1, idx_bytes=4, grad=0x100000, type=BF16, grad_stride=8, rows=100, width=8,
+# tokens and samples enough for the gradients to need their workspace
+GRAD = dict(idx=0x10000, n=20000, idx_stride=1, idx_bytes=4, grad=0x100000, type=BF16, grad_stride=8, rows=100, width=8,
             scale=1.0, accumulate=0, out=0x200000, out_type=F32, out_stride=8, ws=0x400000, ws_bytes=1 << 20)
 
 
@@ -51,7 +52,7 @@ def test_lookup_gradient_refuses(lib, change, why, code):
     refused(lib, lib.mttkrp_embedding_grad(*{**GRAD, **change}.values(), None), why, code)
 
 
-def model(d=3, dims=(30, 20, 10), R=8, factors=(0x100000, 0x110000, 0x120000), type=F32, coords=0x10000, n=16,
+def model(d=3, dims=(30, 20, 10), R=8, factors=(0x100000, 0x110000, 0x120000), type=F32, coords=0x10000, n=20000,
           idx_bytes=4):
     cd = (ctypes.c_int64 * len(dims))(*dims) if dims is not None else None
     cf = (ctypes.c_void_p * len(factors))(*factors) if factors is not None else None
@@ -92,7 +93,7 @@ def test_entries_gradient_refuses(lib, change, why):
     ((0x300000, 0x310000, 0x120010), 0x20000, 0x400000, 1 << 20, "overlap", 1),
     ((0x300000, 0x310000, 0x20010), 0x20000, 0x400000, 1 << 20, "overlap", 1),
     (OUTS, 0x20000, 0, 0, "workspace", 3), (OUTS, 0x20000, 0x400000, 64, "workspace", 3),
-    (OUTS, 0x20000, 0x400010, 1 << 20, "256-byte", 3)])
+    (OUTS, 0x20000, 0x400010, 1 << 24, "256-byte", 3)])
 def test_entries_gradient_refuses_results(lib, outs, g, ws, ws_bytes, why, code):
     co = (ctypes.c_void_p * 3)(*outs) if outs is not None else None
     refused(lib, lib.mttkrp_cp_entries_grad(*model(), g, co, ws, ws_bytes, None), why, code)
@@ -128,9 +129,11 @@ def test_workspace_sizes(lib):
     assert lib.mttkrp_embedding_grad_workspace_bytes(-1, 5, 5) == 0
     assert lib.mttkrp_embedding_grad_workspace_bytes(5, 0, 5) == 0
     dims = (ctypes.c_int64 * 3)(4, 5, 6)
-    one = lib.mttkrp_embedding_grad_workspace_bytes(1000, 50, 64)
-    assert one >= 1000 * 8
-    assert lib.mttkrp_cp_entries_grad_workspace_bytes(3, dims, 64, 1000) >= 3 * 1000 * 8
+    assert lib.mttkrp_embedding_grad_workspace_bytes(1000, 50, 64) == 0       # one launch, no workspace
+    assert lib.mttkrp_embedding_grad_workspace_bytes(1000, 1 << 24, 64) >= 1000 * 8
+    assert lib.mttkrp_embedding_grad_workspace_bytes(100000, 50, 64) >= 100000 * 8
+    assert lib.mttkrp_cp_entries_grad_workspace_bytes(3, dims, 64, 1000) == 0
+    assert lib.mttkrp_cp_entries_grad_workspace_bytes(3, dims, 64, 100000) >= 3 * 100000 * 16
     assert lib.mttkrp_cp_entries_grad_workspace_bytes(9, dims, 64, 1000) == 0
     assert lib.mttkrp_grad_norm_workspace_bytes(-1) == 0
     assert 0 < lib.mttkrp_grad_norm_workspace_bytes(1) < lib.mttkrp_grad_norm_workspace_bytes(1 << 20)
