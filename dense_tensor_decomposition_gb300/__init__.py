@@ -1,6 +1,7 @@
 """Dense, matrix-free MTTKRP on one GB300 (sm_103a).
 
-A thin ctypes binding of ``libmttkrp.so`` (C ABI in ``include/mttkrp.h``):
+A thin binding of ``libmttkrp.so`` (C ABI in ``include/mttkrp.h``), by ctypes and,
+for the short operators of a sampled fit, a small module (``csrc/binding.cpp``):
 it only checks and marshals arguments.  Every step of the computation runs in
 the library's CUDA kernels; PyTorch supplies device memory and streams.  There
 is no CPU fallback: if the library is missing this module raises.
@@ -14,11 +15,10 @@ Khatri-Rao matrix.)
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import re
 import threading
-from array import array
-from operator import attrgetter
 
 from ._build import LIB as LIB_PATH, build  # noqa: F401
 
@@ -559,95 +559,39 @@ def ttm_multi(X, modes, Ms, outs=None, stream=None, path: str = "auto", workspac
 # Operators of a sampled fit
 # ---------------------------------------------------------------------------
 
+_sampled = None             # the module that checks, allocates and calls for these operators
 _type_codes: dict = {}      # torch dtype -> MTTKRP_F32, MTTKRP_BF16 or MTTKRP_F16
-_dtype_of = attrgetter("dtype")
-_raw_stream = None          # device index -> its current stream's handle
 
 
-def _sampled_library():
-    """The library, with what the functions below look up once."""
-    global _raw_stream
-    lib = load_library()
-    if not _type_codes:
+def _load_binding():
+    global _sampled
+    if _sampled is None:
         import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+        load_library()
+        try:
+            module = importlib.import_module("._binding", __package__)
+        except ImportError as e:
+            raise ImportError("the module _binding.so is missing or does not fit this PyTorch: build it with "
+                              "dense_tensor_decomposition_gb300.build()") from e
         _type_codes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    return lib
+        _sampled = module
+    return _sampled
 
 
-def _type_code(t, name: str) -> int:
-    """The code of a CUDA tensor's type."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    code = _type_codes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16")
-    return code
-
-
-def _index_args(idx, like, name: str = "idx"):
-    """(pointer, count, stride, bytes) of an index tensor on the device of `like`:
-    int32 or int64, contiguous of any shape, or one-dimensional with any stride."""
-    import torch
-    if not isinstance(idx, torch.Tensor) or idx.get_device() != like.get_device():
-        raise TypeError(f"{name} must be a CUDA tensor on the other tensors' device")
-    if idx.dtype not in (torch.int64, torch.int32):
-        raise TypeError(f"{name} must be int32 or int64")
-    if idx.dim() == 1:
-        stride = idx.stride(0)
-    elif idx.is_contiguous():
-        stride = 1
-    else:
-        raise ValueError(f"{name} must be contiguous or one-dimensional")
-    return idx.data_ptr(), idx.numel(), stride, idx.element_size()
-
-
-def _row_stride(t, rows: int, width: int, name: str) -> int:
-    """Elements from one row to the next of a tensor of `rows` rows (all dimensions
-    but the last) of `width` consecutive elements."""
-    if t.is_contiguous():
-        if t.dim() < 1 or t.shape[-1] != width or t.numel() != rows * width:
-            raise ValueError(f"{name} must have {rows} rows of {width}")
-        return width
-    if t.dim() != 2 or tuple(t.shape) != (rows, width):
-        raise ValueError(f"{name} must be {rows} x {width}, or contiguous with as many rows")
-    step, inner = t.stride()
-    if width > 1 and inner != 1 or rows > 1 and step < width:
-        raise ValueError(f"{name}: the elements of a row must be consecutive and rows must not overlap")
-    return step if rows > 1 else width
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
     """out[..., :] = scale * table[idx[...], :] (mttkrp_embedding): rows of a table
     (rows x width, float32, bfloat16 or float16, rows any distance apart) for int32
-    or int64 indices of any shape.  An index outside the table, e.g. a negative mask,
-    gives a row of zeros.  Returns idx.shape + (width,) of the table's type, written
-    into `out` when given."""
-    import torch
-    lib = _sampled_library()
-    code = _type_code(table, "table")
-    if table.dim() != 2:
-        raise ValueError("table must be rows x width")
-    rows, width = table.shape
-    stride = _row_stride(table, rows, width, "table")
-    ptr, n, idx_stride, nbytes = _index_args(idx, table)
-    shape = (*idx.shape, width)
-    if out is None:
-        out = torch.empty(shape, dtype=table.dtype, device=table.device)
-        out_stride = width
-    else:
-        if not isinstance(out, torch.Tensor) or out.device != table.device or out.dtype != table.dtype \
-                or tuple(out.shape) != shape:
-            raise ValueError(f"out must be a {table.dtype} CUDA tensor of shape {shape}")
-        out_stride = _row_stride(out, n, width, "out")
-    rc = lib.mttkrp_embedding(table.data_ptr(), rows, width, stride, code, ptr, n, idx_stride, nbytes, scale,
-                              out.data_ptr(), out_stride,
-                              _raw_stream(table.get_device()) if stream is None else stream.cuda_stream)
-    if rc:
-        _check(rc, "mttkrp_embedding")
-    return out
+    or int64 indices of any shape (contiguous, or one-dimensional with any stride).
+    An index outside the table, e.g. a negative mask, gives a row of zeros.  Returns
+    idx.shape + (width,) of the table's type, written into `out` when given."""
+    r = (_sampled or _load_binding()).embedding(table, idx, scale, out, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_embedding")
+    return r if out is None else out
 
 
 def embedding_grad(idx, grad, rows: int, scale: float = 1.0, out=None, dtype=None, accumulate: bool = False,
@@ -657,65 +601,14 @@ def embedding_grad(idx, grad, rows: int, scale: float = 1.0, out=None, dtype=Non
     fixed order.  grad: idx.shape + (width,).  Returns rows x width of `dtype`
     (float32 by default, or grad's type), written into `out` when given;
     accumulate adds to `out` and leaves the rows that no token points to alone."""
-    import torch
-    lib = _sampled_library()
-    code = _type_code(grad, "grad")
-    ptr, n, idx_stride, nbytes = _index_args(idx, grad)
-    if grad.dim() < 1 or grad.shape[:-1] != idx.shape:
-        raise ValueError("grad must have the shape of idx and one more dimension")
-    width = grad.shape[-1]
-    stride = _row_stride(grad, n, width, "grad")
-    rows = int(rows)
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = torch.empty((rows, width), dtype=dtype or torch.float32, device=grad.device)
-        out_stride = width
-    else:
-        if not isinstance(out, torch.Tensor) or out.device != grad.device or out.dim() != 2 \
-                or (dtype is not None and out.dtype != dtype):
-            raise ValueError("out must be a CUDA tensor of rows x width on grad's device, of dtype if that is given")
-        out_stride = _row_stride(out, rows, width, "out")
-    need = lib.mttkrp_embedding_grad_workspace_bytes(n, rows, width)
-    ws = torch.empty(need, dtype=torch.uint8, device=grad.device) if need else None
-    rc = lib.mttkrp_embedding_grad(ptr, n, idx_stride, nbytes, grad.data_ptr(), code, stride, rows, width, scale,
-                                   accumulate, out.data_ptr(), _type_code(out, "out"), out_stride,
-                                   ws.data_ptr() if need else None, need,
-                                   _raw_stream(grad.get_device()) if stream is None else stream.cuda_stream)
-    if rc:
-        _check(rc, "mttkrp_embedding_grad")
-    return out
-
-
-def _model_args(factors, coords):
-    """(d, dims, R, factor pointers, type code) of a CP model's factors, checked
-    together with its coordinates (samples x d, contiguous); dims and pointers as
-    arrays."""
-    import torch
-    if not factors:
-        raise ValueError("at least one factor is needed")
-    first = factors[0]
-    code = _type_code(first, "factor 0")
-    dtype, device, R = first.dtype, first.get_device(), first.shape[-1] if first.dim() else 0
-    dims, ptrs = array("q"), array("Q")
-    for n, a in enumerate(factors):
-        if not isinstance(a, torch.Tensor) or a.get_device() != device or a.dtype != dtype or a.dim() != 2 \
-                or a.shape[1] != R or not a.is_contiguous():
-            raise ValueError(f"factor {n} must be a contiguous {dtype} tensor of {R} columns on {first.device}")
-        dims.append(a.shape[0])
-        ptrs.append(a.data_ptr())
-    d = len(dims)
-    if not isinstance(coords, torch.Tensor) or coords.get_device() != device \
-            or coords.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"coords must be an int32 or int64 tensor on {first.device}")
-    if coords.dim() != 2 or coords.shape[1] != d or not coords.is_contiguous():
-        raise ValueError(f"coords must be contiguous, samples x {d}")
-    return d, dims, R, ptrs, code
-
-
-def _address(a) -> int:
-    """Where an array's elements are."""
-    return a.buffer_info()[0]
+    module = _sampled or _load_binding()
+    code = -1 if dtype is None else _type_codes.get(dtype)
+    if code is None:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    r = module.embedding_grad(idx, grad, rows, scale, out, code, accumulate, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_embedding_grad")
+    return r if out is None else out
 
 
 def cp_entries(factors, coords, out=None, stream=None):
@@ -724,21 +617,10 @@ def cp_entries(factors, coords, out=None, stream=None):
     float16), coords samples x d (int32 or int64).  Returns `samples` float32 values;
     0 where a coordinate is out of range.  Component weights go into a factor, or in
     as a factor with one row."""
-    import torch
-    lib = _sampled_library()
-    d, dims, R, ptrs, code = _model_args(list(factors), coords)
-    n = coords.shape[0]
-    if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=coords.device)
-    elif not isinstance(out, torch.Tensor) or out.device != coords.device or out.dtype != torch.float32 \
-            or tuple(out.shape) != (n,) or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous float32 CUDA tensor of {n} elements")
-    rc = lib.mttkrp_cp_entries(d, _address(dims), R, _address(ptrs), code, coords.data_ptr(), n,
-                               coords.element_size(), out.data_ptr(),
-                               _raw_stream(coords.get_device()) if stream is None else stream.cuda_stream)
-    if rc:
-        _check(rc, "mttkrp_cp_entries")
-    return out
+    r = (_sampled or _load_binding()).cp_entries(factors, coords, out, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_cp_entries")
+    return r if out is None else out
 
 
 def cp_entries_grad(factors, coords, grad, outs=None, stream=None):
@@ -746,55 +628,20 @@ def cp_entries_grad(factors, coords, grad, outs=None, stream=None):
     the I_n x R sums over the samples of grad[s] * prod over m != n of A_m(c_m, :),
     float32, in a fixed order.  grad: one float32 value a sample.  Returns the list
     of gradients (written into `outs` when given)."""
-    import torch
-    lib = _sampled_library()
-    d, dims, R, ptrs, code = _model_args(list(factors), coords)
-    n, device = coords.shape[0], coords.device
-    if not isinstance(grad, torch.Tensor) or grad.device != device or grad.dtype != torch.float32 \
-            or tuple(grad.shape) != (n,) or not grad.is_contiguous():
-        raise ValueError(f"grad must be a contiguous float32 CUDA tensor of {n} elements")
-    if outs is None:
-        outs = [torch.empty((i, R), dtype=torch.float32, device=device) for i in dims]
-    else:
-        outs = list(outs)
-        if len(outs) != d:
-            raise ValueError("outs must hold one tensor per factor")
-        for m, o in enumerate(outs):
-            if not isinstance(o, torch.Tensor) or o.device != device or o.dtype != torch.float32 \
-                    or tuple(o.shape) != (dims[m], R) or not o.is_contiguous():
-                raise ValueError(f"outs[{m}] must be a contiguous float32 CUDA tensor of shape {(dims[m], R)}")
-    optrs = array("Q", [o.data_ptr() for o in outs])
-    need = lib.mttkrp_cp_entries_grad_workspace_bytes(d, _address(dims), R, n)
-    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    rc = lib.mttkrp_cp_entries_grad(d, _address(dims), R, _address(ptrs), code, coords.data_ptr(), n,
-                                    coords.element_size(), grad.data_ptr(), _address(optrs),
-                                    ws.data_ptr() if need else None, need,
-                                    _raw_stream(coords.get_device()) if stream is None else stream.cuda_stream)
-    if rc:
-        _check(rc, "mttkrp_cp_entries_grad")
-    return outs
-
-
-def _tensor_args(tensors, name: str):
-    """(device index, types, pointers, element counts) of contiguous CUDA tensors on
-    one device, the last two as arrays.  The lists can be long: each property is read
-    in one pass without Python code for the elements."""
-    import torch
-    T = torch.Tensor
-    devices = set(map(T.get_device, tensors))       # TypeError where one is not a tensor
-    if len(devices) > 1 or -1 in devices:
-        raise (TypeError if -1 in devices else ValueError)(f"{name} must be CUDA tensors on one device")
-    if not all(map(T.is_contiguous, tensors)):
-        raise ValueError(f"{name} must be contiguous")
-    types = list(map(_dtype_of, tensors))
-    return devices.pop(), types, array("Q", map(T.data_ptr, tensors)), array("q", map(T.numel, tensors))
+    r = (_sampled or _load_binding()).cp_entries_grad(factors, coords, grad, outs, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_cp_entries_grad")
+    return r
 
 
 def grad_norm(tensors, stream=None):
     """sqrt of the sum of squares over all elements of a list of CUDA tensors
     (mttkrp_grad_norm), as a float32 scalar on the device.  The tensors are
     contiguous, float32, bfloat16 or float16 in any mix, on one device."""
-    return _norm_and_clip(tensors, None, 0.0, None, stream)
+    r = (_sampled or _load_binding()).clip_grad_norm(tensors, None, 0.0, None, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_grad_norm")
+    return r
 
 
 def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, stream=None):
@@ -802,44 +649,10 @@ def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, strea
     being `grad_norm` of the list (mttkrp_clip_grad_norm), in place or, when `outs` is
     given, into its tensors (each of its input's size and type).  Returns the norm
     before clipping as a float32 scalar on the device."""
-    return _norm_and_clip(tensors, float(max_norm), float(eps), outs, stream)
-
-
-def _norm_and_clip(tensors, max_norm, eps, outs, stream):
-    import torch
-    lib = _sampled_library()
-    tensors = list(tensors)
-    n = len(tensors)
-    if n < 1:
-        raise ValueError("at least one tensor is needed")
-    index, types, ptrs, numels = _tensor_args(tensors, "tensors")
-    try:
-        codes = array("i", map(_type_codes.__getitem__, types))
-    except KeyError:
-        raise TypeError("tensors must be float32, bfloat16 or float16") from None
-    optrs = None
-    if outs is not None:
-        outs = list(outs)
-        if len(outs) != n:
-            raise ValueError("outs must hold one tensor per input")
-        oindex, otypes, optrs, onumels = _tensor_args(outs, "outs")
-        if oindex != index or otypes != types or onumels != numels:
-            raise ValueError("every tensor of outs must have its input's type, number of elements and device")
-    device = tensors[0].device
-    norm = torch.empty((), dtype=torch.float32, device=device)
-    need = lib.mttkrp_grad_norm_workspace_bytes(n)
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if max_norm is None:
-        rc = lib.mttkrp_grad_norm(n, _address(ptrs), _address(numels), _address(codes), norm.data_ptr(),
-                                  ws.data_ptr(), need, handle)
-    else:
-        rc = lib.mttkrp_clip_grad_norm(n, _address(ptrs), _address(numels), _address(codes),
-                                       None if optrs is None else _address(optrs), max_norm, eps, norm.data_ptr(),
-                                       ws.data_ptr(), need, handle)
-    if rc:
-        _check(rc, "mttkrp_grad_norm" if max_norm is None else "mttkrp_clip_grad_norm")
-    return norm
+    r = (_sampled or _load_binding()).clip_grad_norm(tensors, float(max_norm), eps, outs, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_clip_grad_norm")
+    return r
 
 
 def probe_fma(blocks: int, iters: int, out, stream=None):

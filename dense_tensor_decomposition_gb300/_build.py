@@ -1,8 +1,10 @@
-"""Build libmttkrp.so in-tree with nvcc for sm_103a (GB300).
+"""Build libmttkrp.so in-tree with nvcc for sm_103a (GB300), and the Python
+module _binding.so with the host compiler.
 
-Every .cu file under csrc/ is compiled in parallel into _build/, then linked
-into a shared library next to this file.  Rebuilds only when a source or
-header is newer than the library.
+Every source under csrc/ is compiled in parallel into _build/, then the .cu
+files are linked into a shared library next to this file, and binding.cpp,
+which calls that library, into a module next to it.  Rebuilds only when a
+source or header is newer than what it goes into.
 """
 from __future__ import annotations
 
@@ -11,12 +13,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmttkrp.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -34,16 +38,40 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _binding_source():
+    return os.path.join(CSRC, "binding.cpp")
+
+
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
+    return _sources() + [_binding_source()] + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
         sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "mttkrp.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _torch_flags():
+    """Flags to compile and link against the installed PyTorch and CUDA runtime headers."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    include = os.path.join(home, "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    flags = [f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", "-isystem", include, "-isystem",
+             os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    links = [f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    return flags, links
+
+
+def _run(cmd, what):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stderr}")
+    return res
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -52,25 +80,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
 
+    flags, links = _torch_flags()
+
     def compile_one(src):
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc] + NVCC_FLAGS + ["-c", src, "-o", obj]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{res.stderr}")
+        name = os.path.basename(src)
+        obj = os.path.join(BUILD, os.path.splitext(name)[0] + ".o")
+        if src.endswith(".cu"):
+            cmd = [cc] + NVCC_FLAGS + ["-c", src, "-o", obj]
+        else:
+            cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall"] + flags + ["-c", src, "-o", obj]
+        res = _run(cmd, f"compiling {src}")
         if verbose and res.stderr:
             print(res.stderr)
         return obj
 
-    srcs = _sources()
+    srcs = _sources() + [_binding_source()]
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
-        objs = list(ex.map(compile_one, srcs))
+        *objs, binding = list(ex.map(compile_one, srcs))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stderr}")
+    _run([cc] + ARCH + ["-shared", "-o", tmp] + objs, "linking the library")
     os.replace(tmp, LIB)
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, binding, f"-L{HERE}", "-lmttkrp", "-Wl,-rpath,$ORIGIN"] + links,
+         "linking the binding")
+    os.replace(tmp, BINDING)
     return LIB
 
 
