@@ -4,12 +4,19 @@
 //
 // Bound by memory: 2 reads and 1 write of every element, less what of the first
 // read is still in the L2 cache at the second.  The tensors are described in the
-// kernel's arguments and cut into 16 KB tiles; every block takes consecutive
-// tiles, so each of the GPU's blocks has the same bytes to move whatever the
-// tensors' sizes.  One cooperative launch does it all: squares, a barrier over the
-// grid, every block adds the blocks' sums in the same order, then the products,
-// from the last tile back to the first (the last ones are the ones still cached).
+// kernel's arguments and cut into units of 8 KB; every block takes consecutive units,
+// so each of the GPU's blocks has the same bytes to move whatever the tensors' sizes.
+// One cooperative launch does it all: squares, a barrier over the grid, every block
+// adds the blocks' sums in the same order, then the products, from the last unit back
+// to the first (the last ones are the ones still cached: reads that will not be
+// repeated and all writes are marked for the cache to drop first).  A launch for each
+// step, with blocks for the SMs to take as they get free, is no faster (2 GB of fp32:
+// 948 us against 941) and loses the cache's order (192 MB of bf16: 112 us against 99).
 // More tensors than a table holds take one launch a table and step.
+//
+// The squares of 16 elements are added in fp32, the sums of 16 in pairs of fp32 numbers
+// (the second holds what the first rounds away): fp64 additions would take longer than
+// the reads, at 2 a cycle and SM.
 #include <cooperative_groups.h>
 
 #include "rows.h"
@@ -20,10 +27,12 @@ namespace cg = cooperative_groups;
 namespace mk {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                          // 16-byte vectors a thread has in flight
-constexpr int kTileVecs = kThreads * kUnroll;       // 16 KB
-constexpr int kMaxBlocks = 2048;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;                          // 16-byte vectors a thread has in flight, a unit each
+constexpr int kUnitVecs = kThreads;                 // 8 KB
+constexpr int kMaxBlocks = 2048;                    // most sums a table
+constexpr int64_t kCached = 64 << 20;               // bytes of the first read to find in L2 at the second
 constexpr int kSmallTable = 32, kLargeTable = 1024;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -35,10 +44,10 @@ struct Table {
     const void* in[N];
     void* out[N];
     int64_t numel[N];
-    uint32_t first[N];      // number of the tensor's first tile
+    uint32_t first[N];      // number of the tensor's first unit
     uint8_t type[N];
     int n;
-    uint32_t tiles;
+    uint32_t units;
 };
 
 // Vectors of a tensor start at multiples of 16 bytes, the first one at or before
@@ -46,6 +55,7 @@ struct Table {
 template <typename T>
 struct Vecs {
     static constexpr int kVec = 16 / sizeof(T);
+    using P = Pack<T, kVec>;
     const T* x;
     int64_t n;
     int shift;              // elements of the first vector that lie before x
@@ -53,98 +63,128 @@ struct Vecs {
         : x(static_cast<const T*>(p)), n(numel), shift((int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T)) {}
     __device__ bool whole(int64_t i) const { return i * kVec >= shift && (i + 1) * kVec - shift <= n; }
     __device__ bool holds(int64_t e) const { return e >= 0 && e < n; }
-    __device__ Pack<T, kVec> load(int64_t i) const {
-        const int64_t e0 = i * kVec - shift;
-        if (whole(i)) return *reinterpret_cast<const Pack<T, kVec>*>(x + e0);
-        Pack<T, kVec> v;
+    __device__ const uint4* at(int64_t i) const { return reinterpret_cast<const uint4*>(x - shift) + i; }
+    // zeros for elements that are not the tensor's
+    __device__ P load(int64_t i) const {
+        if (whole(i)) return *reinterpret_cast<const P*>(at(i));
+        P v;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v.v[e] = holds(e0 + e) ? x[e0 + e] : from_f32<T>(0.f);
+        for (int e = 0; e < kVec; ++e) v.v[e] = holds(i * kVec - shift + e) ? x[i * kVec - shift + e] : from_f32<T>(0.f);
         return v;
+    }
+    // vectors i, i + kUnitVecs, ... of `units` <= kUnroll units; keep: for the cache to keep
+    __device__ void load_units(int64_t i, int units, bool keep, P* v) const {
+        if (units == kUnroll && whole(i - threadIdx.x) && whole(i - threadIdx.x + (int64_t)kUnroll * kUnitVecs - 1)) {
+            uint4 w[kUnroll];
+            if (keep) {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) w[u] = *at(i + u * kUnitVecs);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) w[u] = __ldcs(at(i + u * kUnitVecs));
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) v[u] = *reinterpret_cast<const P*>(&w[u]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) v[u].v[e] = from_f32<T>(0.f);
+                if (u < units) v[u] = load(i + u * kUnitVecs);
+            }
+        }
     }
 };
 
-__device__ __forceinline__ double block_sum(double x) {
-    __shared__ double sums[kThreads / 32];
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) x += sums[w];
-    __syncthreads();
-    return x;
-}
-
-// Sum of 16 squares in fp32; where it leaves the fp32 range, or is so small that
-// fp32 drops bits of it, the same sum in fp64.
-__device__ __forceinline__ double squares16(const float* v) {
-    float s = 0.f, most = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        s = fmaf(v[e], v[e], s);
-        most = fmaxf(most, fabsf(v[e]));
+// a sum as hi + lo, and in fp64 what does not fit fp32's range
+struct Sum {
+    float hi = 0.f, lo = 0.f;
+    double wide = 0.0;
+    __device__ __forceinline__ void add(float x) {
+        const float s = hi + x, b = s - hi;     // s + rounding error = hi + x, exactly
+        lo += (hi - (s - b)) + (x - b);
+        hi = s;
     }
-    if ((s >= 0x1p-100f && s <= 0x1p127f) || (s == 0.f && most == 0.f)) return (double)s;
-    double d = 0.0;
+    // 16 squares; sums up to 2^90 can be added 2^36 times
+    __device__ __forceinline__ void squares16(const float* v) {
+        float s = 0.f, most = 0.f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) d = fma((double)v[e], (double)v[e], d);
-    return d;
-}
-
-template <typename T>
-__device__ __forceinline__ double tile_squares(const void* p, int64_t numel, uint32_t tile) {
-    constexpr int kVec = Vecs<T>::kVec, kVecs16 = 16 / kVec;
-    const Vecs<T> x(p, numel);
-    const int64_t i0 = (int64_t)tile * kTileVecs + threadIdx.x;
-    Pack<T, kVec> v[kUnroll];
-    if (x.whole((int64_t)tile * kTileVecs) && x.whole((int64_t)(tile + 1) * kTileVecs - 1)) {
-        const Pack<T, kVec>* src = reinterpret_cast<const Pack<T, kVec>*>(x.x - x.shift) + i0;
+        for (int e = 0; e < 16; ++e) {
+            s = fmaf(v[e], v[e], s);
+            most = fmaxf(most, fabsf(v[e]));
+        }
+        if ((s >= 0x1p-100f && s <= 0x1p90f) || (s == 0.f && most == 0.f)) {
+            add(s);
+        } else {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = src[u * kThreads];
-    } else {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = x.load(i0 + u * kThreads);
+            for (int e = 0; e < 16; ++e) wide = fma((double)v[e], (double)v[e], wide);
+        }
     }
+};
+
+// over the block; the result in thread 0
+__device__ __forceinline__ double block_sum(Sum s) {
+    __shared__ float hi[kWarps], lo[kWarps];
+    __shared__ double wide[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool any = __syncthreads_or(s.wide != 0.0) != 0;      // NaN too
+    for (int o = 16; o > 0; o >>= 1) {
+        const float l = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
+        s.add(__shfl_xor_sync(0xFFFFFFFFu, s.hi, o));
+        s.lo += l;
+        if (any) s.wide += __shfl_xor_sync(0xFFFFFFFFu, s.wide, o);
+    }
+    if (lane == 0) {
+        hi[warp] = s.hi;
+        lo[warp] = s.lo;
+        wide[warp] = s.wide;
+    }
+    __syncthreads();
     double sum = 0.0;
-#pragma unroll
-    for (int u = 0; u < kUnroll; u += kVecs16) {
-        float f[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = to_f32(v[u + e / kVec].v[e % kVec]);
-        sum += squares16(f);
+    if (threadIdx.x == 0) {
+        Sum t;
+        for (int w = 0; w < kWarps; ++w) {
+            t.add(hi[w]);
+            t.lo += lo[w];
+            if (any) t.wide += wide[w];
+        }
+        sum = (double)t.hi + (double)t.lo + t.wide;
     }
     return sum;
 }
 
 template <typename T>
-__device__ __forceinline__ void tile_scale(const void* p, void* q, int64_t numel, uint32_t tile, float coef) {
+__device__ __forceinline__ void add_squares(const void* p, int64_t numel, int64_t unit, int units, bool keep, Sum& sum) {
+    constexpr int kVec = Vecs<T>::kVec;
+    const Vecs<T> x(p, numel);
+    Pack<T, kVec> v[kUnroll];
+    x.load_units(unit * kUnitVecs + threadIdx.x, units, keep, v);
+#pragma unroll
+    for (int u = 0; u < kUnroll; u += 16 / kVec) {
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[e] = to_f32(v[u + e / kVec].v[e % kVec]);
+        sum.squares16(f);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void scale(const void* p, void* q, int64_t numel, int64_t unit, int units, float coef) {
     constexpr int kVec = Vecs<T>::kVec;
     const Vecs<T> x(p, numel);
     T* y = static_cast<T*>(q);
     const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
-    const int64_t i0 = (int64_t)tile * kTileVecs + threadIdx.x;
+    const int64_t i = unit * kUnitVecs + threadIdx.x;
     Pack<T, kVec> v[kUnroll];
-    if (same && x.whole((int64_t)tile * kTileVecs) && x.whole((int64_t)(tile + 1) * kTileVecs - 1)) {
-        const Pack<T, kVec>* src = reinterpret_cast<const Pack<T, kVec>*>(x.x - x.shift) + i0;
-        Pack<T, kVec>* dst = reinterpret_cast<Pack<T, kVec>*>(y - x.shift) + i0;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) v[u] = src[u * kThreads];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) v[u].v[e] = from_f32<T>(coef * to_f32(v[u].v[e]));
-            dst[u * kThreads] = v[u];
-        }
-        return;
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) v[u] = x.load(i0 + u * kThreads);
+    x.load_units(i, units, false, v);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        const int64_t e0 = (i0 + u * kThreads) * kVec - x.shift;
+        if (u >= units) break;
+        const int64_t at = i + u * kUnitVecs, e0 = at * kVec - x.shift;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v[u].v[e] = from_f32<T>(coef * to_f32(v[u].v[e]));
-        if (same && x.whole(i0 + u * kThreads)) {
-            *reinterpret_cast<Pack<T, kVec>*>(y + e0) = v[u];
+        if (same && x.whole(at)) {
+            __stcs(reinterpret_cast<uint4*>(y + e0), *reinterpret_cast<const uint4*>(&v[u]));
         } else {
 #pragma unroll
             for (int e = 0; e < kVec; ++e)
@@ -153,37 +193,44 @@ __device__ __forceinline__ void tile_scale(const void* p, void* q, int64_t numel
     }
 }
 
-// the tensor that a tile is of: the last one whose first tile is not above it
+// the tensor that a unit is of: the last one whose first unit is not above it
 template <int N>
-__device__ __forceinline__ int tensor_of(const Table<N>& a, uint32_t tile) {
+__device__ __forceinline__ int tensor_of(const Table<N>& a, uint32_t unit) {
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (a.first[mid] <= tile) lo = mid;
+        if (a.first[mid] <= unit) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
 
-// this block's share of the tiles
+// this block's share of the units
 template <int N>
 __device__ __forceinline__ void share(const Table<N>& a, uint32_t& t0, uint32_t& t1) {
-    t0 = (uint32_t)((uint64_t)a.tiles * blockIdx.x / gridDim.x);
-    t1 = (uint32_t)((uint64_t)a.tiles * (blockIdx.x + 1) / gridDim.x);
+    t0 = (uint32_t)((uint64_t)a.units * blockIdx.x / gridDim.x);
+    t1 = (uint32_t)((uint64_t)a.units * (blockIdx.x + 1) / gridDim.x);
 }
 
 template <int N>
 __device__ __forceinline__ double share_squares(const Table<N>& a) {
     uint32_t t0, t1;
     share(a, t0, t1);
-    double sum = 0.0;
+    // the last ones are read again first
+    const uint32_t kept = (uint32_t)(kCached / (kUnitVecs * 16)) / gridDim.x;
+    const uint32_t keep_from = t1 - t0 > kept ? t1 - kept : t0;
+    Sum sum;
     int k = t0 < t1 ? tensor_of(a, t0) : 0;
-    for (uint32_t t = t0; t < t1; ++t) {
+    for (uint32_t t = t0; t < t1;) {
         while (k + 1 < a.n && a.first[k + 1] <= t) ++k;
+        const uint32_t end = k + 1 < a.n && a.first[k + 1] < t1 ? a.first[k + 1] : t1;
+        const int units = end - t < kUnroll ? (int)(end - t) : kUnroll;
         const uint32_t at = t - a.first[k];
-        if (a.type[k] == MTTKRP_F32) sum += tile_squares<float>(a.in[k], a.numel[k], at);
-        else if (a.type[k] == MTTKRP_BF16) sum += tile_squares<__nv_bfloat16>(a.in[k], a.numel[k], at);
-        else sum += tile_squares<__half>(a.in[k], a.numel[k], at);
+        const bool keep = t >= keep_from;
+        if (a.type[k] == MTTKRP_F32) add_squares<float>(a.in[k], a.numel[k], at, units, keep, sum);
+        else if (a.type[k] == MTTKRP_BF16) add_squares<__nv_bfloat16>(a.in[k], a.numel[k], at, units, keep, sum);
+        else add_squares<__half>(a.in[k], a.numel[k], at, units, keep, sum);
+        t += units;
     }
     return block_sum(sum);
 }
@@ -193,58 +240,89 @@ __device__ __forceinline__ void share_scale(const Table<N>& a, float coef) {
     uint32_t t0, t1;
     share(a, t0, t1);
     int k = t0 < t1 ? tensor_of(a, t1 - 1) : 0;
-    for (uint32_t t = t1; t-- > t0;) {
-        while (a.first[k] > t) --k;
+    for (uint32_t t = t1; t > t0;) {
+        while (a.first[k] >= t) --k;
+        const uint32_t begin = a.first[k] > t0 ? a.first[k] : t0;
+        const int units = t - begin < kUnroll ? (int)(t - begin) : kUnroll;
+        t -= units;
         if (coef == 1.f && a.in[k] == a.out[k]) continue;       // nothing changes
         const uint32_t at = t - a.first[k];
-        if (a.type[k] == MTTKRP_F32) tile_scale<float>(a.in[k], a.out[k], a.numel[k], at, coef);
-        else if (a.type[k] == MTTKRP_BF16) tile_scale<__nv_bfloat16>(a.in[k], a.out[k], a.numel[k], at, coef);
-        else tile_scale<__half>(a.in[k], a.out[k], a.numel[k], at, coef);
+        if (a.type[k] == MTTKRP_F32) scale<float>(a.in[k], a.out[k], a.numel[k], at, units, coef);
+        else if (a.type[k] == MTTKRP_BF16) scale<__nv_bfloat16>(a.in[k], a.out[k], a.numel[k], at, units, coef);
+        else scale<__half>(a.in[k], a.out[k], a.numel[k], at, units, coef);
     }
 }
 
-// The norm from the blocks' sums, and the coefficient (which follows the formula
-// for infinite and NaN norms too: 0 and NaN).
-__device__ __forceinline__ float norm_of(const double* part, int n, float max_norm, float eps, float& norm) {
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) sum += __ldcg(part + i);
-    const double r = sqrt(block_sum(sum));
-    norm = (float)r;
-    const double c = (double)max_norm / (r + (double)eps);
-    return c >= 1.0 ? 1.f : (float)c;
+// The norm from the blocks' sums, by one warp, and the coefficient (which follows the
+// formula for infinite and NaN norms too: 0 and NaN).
+struct Norm {
+    float norm, coef;
+};
+
+__device__ __forceinline__ Norm norm_of(const double* part, int n, float max_norm, float eps) {
+    __shared__ Norm found;
+    if (threadIdx.x < 32) {
+        double sum = 0.0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n; i += 32) sum += static_cast<const volatile double*>(part)[i];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (threadIdx.x == 0) {
+            Norm r;
+            if (sum >= 0x1p-100 && sum <= 0x1p100) {        // fp32 will do
+                r.norm = sqrtf((float)sum);
+                const float c = max_norm / (r.norm + eps);
+                r.coef = c >= 1.f ? 1.f : c;
+            } else {
+                const double root = sqrt(sum), c = (double)max_norm / (root + (double)eps);
+                r.norm = (float)root;
+                r.coef = c >= 1.0 ? 1.f : (float)c;
+            }
+            found = r;
+        }
+    }
+    __syncthreads();
+    return found;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 4) clip_kernel(const __grid_constant__ Table<N> a, double* part,
+__global__ void __launch_bounds__(kThreads, 2) clip_kernel(const __grid_constant__ Table<N> a, double* part,
                                                            float max_norm, float eps, float* norm) {
     const double sum = share_squares(a);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
     cg::this_grid().sync();
-    float r;
-    const float coef = norm_of(part, gridDim.x, max_norm, eps, r);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = r;
-    share_scale(a, coef);
+    const Norm r = norm_of(part, gridDim.x, max_norm, eps);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = r.norm;
+    share_scale(a, r.coef);
 }
 
 // the same steps as launches of their own
 template <int N>
-__global__ void __launch_bounds__(kThreads, 4) squares_kernel(const __grid_constant__ Table<N> a, double* part) {
+__global__ void __launch_bounds__(kThreads, 2) squares_kernel(const __grid_constant__ Table<N> a, double* part) {
     const double sum = share_squares(a);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int n, float max_norm, float eps,
-                                                        float* norm, float* coef) {
-    float r;
-    const float c = norm_of(part, n, max_norm, eps, r);
+__global__ void __launch_bounds__(1024) norm_kernel(const double* part, int n, float max_norm, float eps, float* norm,
+                                                    float* coef) {
+    // sums of the warps' consecutive parts, then those in order
+    __shared__ double sums[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = (n + 31) / 32;
+    const int end = (warp + 1) * per < n ? (warp + 1) * per : n;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = warp * per + lane; i < end; i += 32) sum += part[i];
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    const Norm r = norm_of(sums, 32, max_norm, eps);
     if (threadIdx.x == 0) {
-        *norm = r;
-        *coef = c;
+        *norm = r.norm;
+        *coef = r.coef;
     }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 4) scale_kernel(const __grid_constant__ Table<N> a, const float* coef) {
+__global__ void __launch_bounds__(kThreads, 2) scale_kernel(const __grid_constant__ Table<N> a, const float* coef) {
     share_scale(a, *coef);
 }
 
@@ -274,7 +352,7 @@ template <int N>
 int fill(Table<N>& t, int n, int k, const void* const* tensors, const int64_t* numels, const int* types,
          void* const* outs) {
     int used = 0;
-    int64_t tiles = 0;
+    int64_t units = 0;
     t.n = 0;
     for (; k + used < n && t.n < N; ++used) {
         const int i = k + used;
@@ -283,12 +361,12 @@ int fill(Table<N>& t, int n, int k, const void* const* tensors, const int64_t* n
         t.out[t.n] = outs ? outs[i] : nullptr;
         t.numel[t.n] = numels[i];
         t.type[t.n] = (uint8_t)types[i];
-        t.first[t.n] = (uint32_t)tiles;
+        t.first[t.n] = (uint32_t)units;
         const int e = types[i] == MTTKRP_F32 ? 4 : 2;
-        tiles += cdiv(numels[i] + (int64_t)(reinterpret_cast<uintptr_t>(tensors[i]) & 15) / e, kTileVecs * 16 / e);
+        units += cdiv(numels[i] + (int64_t)(reinterpret_cast<uintptr_t>(tensors[i]) & 15) / e, kUnitVecs * 16 / e);
         ++t.n;
     }
-    t.tiles = (uint32_t)tiles;
+    t.units = (uint32_t)units;
     return used;
 }
 
@@ -300,25 +378,25 @@ cudaError_t norm_and_clip(int n, const void* const* tensors, const int64_t* nume
     int most = 0;
     cudaError_t e = resident_blocks<N>(most);
     if (e != cudaSuccess) return e;
-    auto blocks = [&](const Table<N>& t) { return t.tiles < (uint32_t)most ? (int)t.tiles : most; };
+    auto blocks = [&](const Table<N>& t) { return t.units < (uint32_t)most ? (int)t.units : most; };
     Table<N> t;
     int k = fill(t, n, 0, tensors, numels, types, outs);
-    if (outs && k == n && t.tiles > 0) {
+    if (outs && k == n && t.units > 0) {
         void* args[] = {&t, &part, &max_norm, &eps, &norm};
         return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(clip_kernel<N>), dim3(blocks(t)),
                                            dim3(kThreads), args, 0, s);
     }
     int parts = 0;
     for (;;) {
-        if (t.tiles > 0) squares_kernel<N><<<blocks(t), kThreads, 0, s>>>(t, part + parts);
+        if (t.units > 0) squares_kernel<N><<<blocks(t), kThreads, 0, s>>>(t, part + parts);
         parts += blocks(t);
         if (k == n) break;
         k += fill(t, n, k, tensors, numels, types, outs);
     }
-    norm_kernel<<<1, kThreads, 0, s>>>(part, parts, max_norm, eps, norm, coef);
+    norm_kernel<<<1, 1024, 0, s>>>(part, parts, max_norm, eps, norm, coef);
     for (k = 0; outs && k < n;) {
         k += fill(t, n, k, tensors, numels, types, outs);
-        if (t.tiles > 0) scale_kernel<N><<<blocks(t), kThreads, 0, s>>>(t, coef);
+        if (t.units > 0) scale_kernel<N><<<blocks(t), kThreads, 0, s>>>(t, coef);
     }
     return cudaGetLastError();
 }

@@ -468,8 +468,8 @@ cudaError_t grad_cached(const RowSumArgs& a, cudaStream_t s) {
     for (int m = 0; m < a.index.d; ++m)
         w = w && (reinterpret_cast<uintptr_t>(a.factor[m]) % (4 * sizeof(T))) == 0 &&
             (reinterpret_cast<uintptr_t>(a.out[m]) % (4 * sizeof(float))) == 0;
-    if (w) return sums_by<float, 4, Model<T, 4>::template Terms, Model<T, 4>::template Terms, 0>(a, s);
-    return sums_by<float, 1, Model<T, 1>::template Terms, Model<T, 1>::template Terms, 0>(a, s);
+    if (w) return sums_by<float, 4, Model<T, 4>::template Terms, 0, Model<T, 4>::template Terms, 0>(a, s);
+    return sums_by<float, 1, Model<T, 1>::template Terms, 0, Model<T, 1>::template Terms, 0>(a, s);
 }
 
 template <int CS, int VEC>

@@ -107,13 +107,13 @@ struct Grad {
     };
 };
 
-// Rows of 16-byte vectors: a thread keeps the next kSlots tokens' vectors of its
-// columns on their way into shared memory, which takes no registers and, as only the
+// Rows of 16-byte vectors: each of kThreads threads keeps the next kSlots tokens' vectors
+// of its columns on their way into shared memory, which takes no registers and, as only the
 // thread itself reads them, no barrier.
-template <typename T>
+template <typename T, int kThreads, int kSlots>
 struct Ring {
     static constexpr int kVec = 16 / sizeof(T);
-    static constexpr int kSlots = 16, kBytes = 16 * kSlots;
+    static constexpr int kBytes = 16 * kSlots;
 
     template <typename List>
     struct Terms {
@@ -173,8 +173,9 @@ cudaError_t lookup_grad(const RowSumArgs& a, cudaStream_t s) {
     const size_t from = reinterpret_cast<uintptr_t>(a.grad) | (a.grad_stride * sizeof(T)) | (a.width * sizeof(T));
     const size_t to = reinterpret_cast<uintptr_t>(a.out[0]) | (a.out_stride * sizeof(TO));
     if (from % 16 == 0 && to % (kVec * sizeof(TO)) == 0)
-        return sums_by<TO, kVec, Grad<T, kVec, 4>::template Terms, Ring<T>::template Terms, Ring<T>::kBytes>(a, s);
-    return sums_by<TO, 1, Grad<T, 1, 4>::template Terms, Grad<T, 1, 8>::template Terms, 0>(a, s);
+        return sums_by<TO, kVec, Ring<T, kSumThreads, 8>::template Terms, Ring<T, kSumThreads, 8>::kBytes,
+                       Ring<T, kThreads, 16>::template Terms, Ring<T, kThreads, 16>::kBytes>(a, s);
+    return sums_by<TO, 1, Grad<T, 1, 4>::template Terms, 0, Grad<T, 1, 8>::template Terms, 0>(a, s);
 }
 
 }  // namespace

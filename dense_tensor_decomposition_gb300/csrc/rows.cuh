@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "sort.h"
 #include "types.cuh"
@@ -40,30 +41,46 @@ __device__ __forceinline__ int64_t index_at(const IndexArgs& a, int64_t t, int m
     return a.bytes == 8 ? static_cast<const int64_t*>(a.idx)[at] : (int64_t) static_cast<const int32_t*>(a.idx)[at];
 }
 
-// the row that token t points to in column m, kNone where it takes no part; the
-// loads of all columns are issued together
-template <typename I>
-__device__ __forceinline__ uint32_t sort_key_as(const IndexArgs& a, int64_t t, int m) {
+// the row that token t points to in column m, kNone where it takes no part; the loads
+// of all columns (at most kCols) are issued together
+template <typename I, int kCols>
+__device__ __forceinline__ uint32_t sort_key_of(const IndexArgs& a, int64_t t, int m) {
+    using U = std::make_unsigned_t<I>;
     const I* idx = static_cast<const I*>(a.idx) + t * a.stride;
-    I v[MTTKRP_MAX_ORDER];
+    I v[kCols];
 #pragma unroll
-    for (int l = 0; l < MTTKRP_MAX_ORDER; ++l) v[l] = l < a.d ? idx[l] : 0;
+    for (int l = 0; l < kCols; ++l) v[l] = l < a.d ? idx[l] : 0;
     uint32_t key = 0;
     bool inside = true;
 #pragma unroll
-    for (int l = 0; l < MTTKRP_MAX_ORDER; ++l) {
-        inside &= l >= a.d || (v[l] >= 0 && (int64_t)v[l] < a.rows[l]);
+    for (int l = 0; l < kCols; ++l) {
+        inside &= l >= a.d || (U)v[l] < (U)a.rows[l];       // negative: above every row
         key = l == m ? (uint32_t)v[l] : key;
     }
     return inside ? key : kNone;
 }
 
-__device__ __forceinline__ uint32_t sort_key(const IndexArgs& a, int64_t t, int m) {
-    if (a.d == 1) {
-        const int64_t v = index_at(a, t, 0);
-        return v >= 0 && v < a.rows[0] ? (uint32_t)v : kNone;
+template <typename I, int kCols>
+struct KeyOf {
+    static constexpr int kLook = kCols == 1 ? 8 : kCols == 4 ? 4 : 2;       // tokens whose loads fit the registers
+    __device__ __forceinline__ uint32_t operator()(const IndexArgs& a, int64_t t, int m) const {
+        return sort_key_of<I, kCols>(a, t, m);
     }
-    return a.bytes == 8 ? sort_key_as<int64_t>(a, t, m) : sort_key_as<int32_t>(a, t, m);
+};
+
+// calls f with the KeyOf for these indices: loops over tokens go inside f, so that
+// nothing stands between the loads of several tokens
+template <typename F>
+__device__ __forceinline__ void with_key(const IndexArgs& a, const F& f) {
+    if (a.d == 1) a.bytes == 8 ? f(KeyOf<int64_t, 1>()) : f(KeyOf<int32_t, 1>());
+    else if (a.d <= 4) a.bytes == 8 ? f(KeyOf<int64_t, 4>()) : f(KeyOf<int32_t, 4>());
+    else a.bytes == 8 ? f(KeyOf<int64_t, MTTKRP_MAX_ORDER>()) : f(KeyOf<int32_t, MTTKRP_MAX_ORDER>());
+}
+
+__device__ __forceinline__ uint32_t sort_key(const IndexArgs& a, int64_t t, int m) {
+    uint32_t key = kNone;
+    with_key(a, [&](auto key_of) { key = key_of(a, t, m); });
+    return key;
 }
 
 // Sum of x over the threads before this one of the first kWarps warps of a CTA, which

@@ -75,13 +75,25 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
     uint32_t place[kSortItems];     // digit, and << 16 how many of the warp's tokens with it come first; kNone: no token
     auto rank_tile = [&](int pass, int64_t tile) {
         const uint2* src = a.buf[(pass + 1) & 1] + m * n;
+        const int64_t w0 = tile + warp * (kSortItems * 32) + lane;
+        if (pass == 0) {
+            with_key(a.index, [&](auto key_of) {
+#pragma unroll
+                for (int i = 0; i < kSortItems; ++i) {
+                    const int64_t t = w0 + i * 32;
+                    kt[i] = make_uint2(t < t1 ? key_of(a.index, t, m) : kNone, (uint32_t)t);
+                    if (i % 4 == 3) asm volatile("" ::: "memory");      // four tokens' loads at once: registers
+                }
+            });
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSortItems; ++i)
+                kt[i] = w0 + i * 32 < t1 ? __ldcg(src + w0 + i * 32) : make_uint2(kNone, 0u);
+        }
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
-            const int64_t t = tile + warp * (kSortItems * 32) + i * 32 + lane;
-            kt[i] = make_uint2(kNone, 0u);
-            if (t < t1) kt[i] = pass == 0 ? make_uint2(sort_key(a.index, t, m), (uint32_t)t) : __ldcg(src + t);
             place[i] = kNone;
-            if (t < t1)
+            if (w0 + i * 32 < t1)
                 place[i] = a.passes == 1 ? min(kt[i].x, (uint32_t)nb - 1) : (kt[i].x >> pass * a.bits) & (nb - 1);
         }
         __syncthreads();            // what stood in whist has been read

@@ -199,6 +199,8 @@ struct OwnArgs {
     uint32_t per_warp;      // tokens that each of the first kSumWarps warps looks at
     int log2L;
     int64_t part;           // columns of a CTA (blockIdx.y)
+    uint32_t first_bytes;   // of shared memory, for `list` and then the terms
+    bool zeros;             // rows without tokens are set to zero here
 };
 
 // Bound by memory: the rows' writes, most of them zeros where tokens are few, and the
@@ -209,11 +211,11 @@ template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_constant__ OwnArgs o) {
     extern __shared__ float4 own_smem[];
     const RowSumArgs& a = o.a;
-    float* heads = reinterpret_cast<float*>(own_smem);                          // kSumThreads * VEC
+    uint32_t* list = reinterpret_cast<uint32_t*>(own_smem);                     // tokens of the CTA's rows; then the terms'
+    float* heads = reinterpret_cast<float*>(reinterpret_cast<char*>(own_smem) + o.first_bytes);     // kSumThreads * VEC
     uint32_t* cursor = reinterpret_cast<uint32_t*>(heads + kSumThreads * VEC);  // owned: tokens of each row, then their places
     uint32_t* touched = cursor + o.owned;                                       // a bit for each owned row
-    uint32_t* found = touched + (o.owned + 31) / 32;                            // tokens of the CTA's rows, a part a warp
-    uint32_t* list = found + kSumWarps * o.per_warp;                            // the same without gaps, then sorted
+    uint32_t* found = touched + (o.owned + 31) / 32;                            // the same with gaps, a part a warp; then sorted
     __shared__ uint32_t warp_found[kSumWarps], sums[kSumWarps], tokens, next_unit, last_unit;
     __shared__ volatile int grouped;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -246,28 +248,30 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
         for (uint32_t i = threadIdx.x; i < o.owned; i += kSumThreads) cursor[i] = 0;
         sync();
         uint32_t count = 0;
-        constexpr int kLook = 4;        // tokens a lane looks up at once
-        for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
-            uint32_t key[kLook];
+        with_key(a.index, [&](auto key_of) {
+            constexpr int kLook = decltype(key_of)::kLook;      // tokens a lane looks up at once
+            for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
+                uint32_t key[kLook];
 #pragma unroll
-            for (int u = 0; u < kLook; ++u) {
-                const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
-                key[u] = k < o.per_warp && t < n ? sort_key(a.index, t, m) : kNone;
-            }
-#pragma unroll
-            for (int u = 0; u < kLook; ++u) {
-                const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
-                const uint32_t block = v >> o.row_shift, turn = block / G;
-                const bool mine = v != kNone && block - turn * G == blockIdx.x;
-                const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
-                if (mine) {
-                    const uint32_t r = (turn << o.row_shift) | (v & low);
-                    found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
-                    atomicAdd(cursor + r, 1u);
+                for (int u = 0; u < kLook; ++u) {
+                    const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
+                    key[u] = k < o.per_warp && t < n ? key_of(a.index, t, m) : kNone;
                 }
-                count += __popc(ballot);
+#pragma unroll
+                for (int u = 0; u < kLook; ++u) {
+                    const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
+                    const uint32_t block = v >> o.row_shift, turn = block / G;
+                    const bool mine = v != kNone && block - turn * G == blockIdx.x;
+                    const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
+                    if (mine) {
+                        const uint32_t r = (turn << o.row_shift) | (v & low);
+                        found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
+                        atomicAdd(cursor + r, 1u);
+                    }
+                    count += __popc(ballot);
+                }
             }
-        }
+        });
         if (lane == 0) warp_found[warp] = count;
         sync();
         // gaps out; the counts become the rows' first places
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
                 grouped = 1;
             }
         }
-    } else if (!a.accumulate) {
+    } else if (o.zeros) {
         while (!grouped) {
             const uint32_t u = take(&last_unit);
             if (u >= units) break;
@@ -333,7 +337,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
         sum_list<TO, VEC, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, total, o.log2L, col0, heads,
                                               Around{false, false, nullptr, nullptr}, sync);
     }
-    if (a.accumulate) return;
+    if (!o.zeros) return;
     auto is_touched = [&](uint32_t r) { return r >= o.owned || (touched[r >> 5] >> (r & 31) & 1u) != 0; };
     for (uint32_t u = take(&next_unit); u < left; u = take(&next_unit))
         zero_rows<TO, VEC>(a, m, u * unit, unit, col0, vecs, is_touched, row_of);
@@ -514,6 +518,22 @@ inline size_t part_bytes(const IndexArgs& x, int64_t width) {
     return sizeof(float) * x.d * cdiv(x.n, kTile) * 2 * width;
 }
 
+// Zeros for all rows, one vector a thread.  A grid of many CTAs, which go to the SMs as
+// these get free, fills 537 MB in 72 us; own_kernel's 152, each with its share, take 84
+// us, as the SMs do not all reach the memory equally fast.
+template <typename TO, int VEC>
+__global__ void __launch_bounds__(kThreads) fill_kernel(TO* out, int64_t rows, uint32_t vecs, int64_t stride) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, r = i / vecs;
+    if (r >= rows) return;
+    Pack<TO, VEC> zero;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) zero.v[e] = from_f32<TO>(0.f);
+    *reinterpret_cast<Pack<TO, VEC>*>(out + r * stride + (i - r * vecs) * VEC) = zero;
+}
+
+// Bytes of zeros that are worth a launch of their own
+constexpr int64_t kFillBytes = 96 << 20;
+
 // joins the tiles' crossing runs
 template <typename TO, int VEC>
 cudaError_t join(const SumArgs& s, cudaStream_t st) {
@@ -524,19 +544,34 @@ cudaError_t join(const SumArgs& s, cudaStream_t st) {
 }
 
 // Few: the terms as own_kernel takes them, whose CTAs of 1024 threads have few
-// registers a thread; Many: as row_sum_kernel takes them, with kRing bytes of dynamic
-// shared memory a thread
-template <typename TO, int VEC, template <typename> typename Few, template <typename> typename Many, int kRing>
+// registers a thread; Many: as row_sum_kernel takes them; with kFewRing and kManyRing
+// bytes of dynamic shared memory a thread that adds
+template <typename TO, int VEC, template <typename> typename Few, int kFewRing, template <typename> typename Many,
+          int kManyRing>
 cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     OwnArgs o;
     dim3 grid;
     if (plan_own(a.index, a.width, a.out_type, VEC, o, grid)) {
         o.a = a;
-        const size_t smem = sizeof(float) * kSumThreads * VEC +
-                            sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32 + 2 * kSumWarps * o.per_warp);
+        o.zeros = !a.accumulate;
+        const size_t list = sizeof(uint32_t) * kSumWarps * o.per_warp;
+        o.first_bytes = (uint32_t)align256(list > kFewRing * kSumThreads ? list : kFewRing * kSumThreads);
+        const size_t smem = o.first_bytes + sizeof(float) * kSumThreads * VEC +
+                            sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32) + list;
         constexpr auto kernel = own_kernel<TO, VEC, Few>;
         cudaError_t e = allow_smem<kernel>();
         if (e != cudaSuccess) return e;
+        if (o.zeros && a.index.d == 1 && a.index.rows[0] * a.width * (int64_t)sizeof(TO) > kFillBytes) {
+            const bool dense = a.out_stride == a.width;     // then one row
+            const int64_t rows = dense ? 1 : a.index.rows[0];
+            const int64_t vecs = (dense ? a.index.rows[0] : 1) * a.width / VEC;
+            const int64_t blocks = cdiv(rows * vecs, kThreads);
+            if (vecs <= UINT32_MAX && blocks <= INT32_MAX) {
+                fill_kernel<TO, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(static_cast<TO*>(a.out[0]), rows,
+                                                                            (uint32_t)vecs, a.out_stride);
+                o.zeros = false;
+            }
+        }
         kernel<<<grid, kOwnThreads, smem, st>>>(o);
         return cudaGetLastError();
     }
@@ -556,7 +591,7 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
     const dim3 sum_grid((unsigned)(s.tiles + zeros), (unsigned)cdiv(a.width, s.columns), a.index.d);
-    kernel<<<sum_grid, kThreads, kThreads * kRing, st>>>(s);
+    kernel<<<sum_grid, kThreads, kThreads * kManyRing, st>>>(s);
     return join<TO, VEC>(s, st);
 }
 
