@@ -536,7 +536,7 @@ cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
     for (int c = 32; c >= 8 && n > kOwnTokens; c /= 2) {
         const int64_t combos = cdiv(a.width, c) * d;
         int64_t tiles = combos < kSms ? kSms / combos : 1;
-        tiles = tiles < cdiv(n, kTile) ? tiles : cdiv(n, kTile);
+        tiles = tiles < cdiv(n, tile_tokens(n)) ? tiles : cdiv(n, tile_tokens(n));     // part_bytes()
         const int64_t waves = cdiv(combos * tiles, kSms);
         double work = 0.0;
         Tables t[MTTKRP_MAX_ORDER];

@@ -8,10 +8,10 @@ namespace cg = cooperative_groups;
 namespace mk {
 namespace {
 
-// Stable radix sort of tokens by the row that they point to, in one cooperative launch:
-// `ctas` CTAs for each index column, each with `per_cta` consecutive tokens.  A pass of
+// Stable radix sort of tokens by the row that they point to: `ctas` CTAs for each index
+// column, each with `per_cta` consecutive tokens, in one cooperative launch.  A pass of
 // `bits` bits counts the digits (every warp those of its own consecutive tokens), waits
-// for the grid, adds up the counts of smaller digits and of the CTAs before, and places
+// for all CTAs, adds up the counts of smaller digits and of the CTAs before, and places
 // the tokens.  With one tile a CTA the tokens and their ranks stay in registers between
 // the two halves.  Tokens that take no part have row kNone and end up last: a single
 // pass gives them the digit above the last row's, more passes see digits of all ones.
@@ -44,29 +44,30 @@ __device__ __noinline__ uint4 entry_of(const SortArgs& a, uint2 kt, int m) {
     return e;
 }
 
-// lanes of the warp with this lane's digit, which has `bits` bits
-__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits) {
-    uint32_t peers = 0xFFFFFFFFu;
-    for (int b = 0; b < bits; ++b) {
-        const bool one = (digit >> b & 1u) != 0;
-        const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one);
-        peers &= one ? ones : ~ones;
+// lanes of the warp with this lane's digit, which has at most kMaxDigit bits or is kNone
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit) {
+    uint32_t peers = __ballot_sync(0xFFFFFFFFu, digit != kNone);
+#pragma unroll
+    for (int b = 0; b < kMaxDigit; ++b) {
+        const uint32_t ones = __ballot_sync(0xFFFFFFFFu, (digit >> b & 1u) != 0);
+        peers &= (digit >> b & 1u) != 0 ? ones : ~ones;
     }
     return peers;
 }
 
-template <int kSortItems>
-__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
+// Column m by CTA `cta` of `ctas`, which wait(): wait for one another
+template <int kSortItems, typename Wait>
+__device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, int ctas, const Wait& wait) {
     extern __shared__ uint32_t sort_smem[];
     constexpr int kSortTile = kSortThreads * kSortItems;
-    const int nb = a.bins, m = blockIdx.y;
+    const int nb = a.bins;
     uint32_t* whist = sort_smem;                    // kSortWarps x nb
     uint32_t* first = sort_smem + kSortWarps * nb;  // nb: counts of the CTA's digits, then their next places
     uint32_t* extra = first + nb;                   // 2 x kSortThreads
     __shared__ uint32_t sums[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t n = a.index.n;
-    const int64_t t0 = blockIdx.x * a.per_cta;
+    const int64_t t0 = cta * a.per_cta;
     const int64_t t1 = t0 + a.per_cta < n ? t0 + a.per_cta : n;
     uint32_t* wh = whist + warp * nb;
 
@@ -101,9 +102,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
-            // a lane without a token is not among the peers of those with digits of all ones
-            const uint32_t digit = place[i];
-            const uint32_t peers = same_digit(digit, a.bits) & __ballot_sync(0xFFFFFFFFu, digit != kNone);
+            const uint32_t digit = place[i], peers = same_digit(digit);
             const uint32_t rank = __popc(peers & ((1u << lane) - 1));
             if (digit != kNone) place[i] = digit | (wh[digit] + rank) << 16;
             __syncwarp();
@@ -127,9 +126,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
             if (tile + kSortTile >= t1) break;
             tile += kSortTile;
         }
-        uint32_t* counts = a.counts + (int64_t)m * gridDim.x * nb;
-        for (int b = tid; b < nb; b += kSortThreads) __stcg(counts + blockIdx.x * nb + b, first[b]);
-        cg::this_grid().sync();
+        uint32_t* counts = a.counts + (int64_t)m * ctas * nb;
+        for (int b = tid; b < nb; b += kSortThreads) __stcg(counts + cta * nb + b, first[b]);
+        wait();
         // tokens with this digit in the CTAs before, and in all: every digit is added up
         // by kSortThreads / nb threads (nb <= kSortThreads)
         {
@@ -137,10 +136,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
             uint32_t less = 0, total = 0;
             if (split < splits) {
 #pragma unroll 8
-                for (int k = split; k < (int)gridDim.x; k += splits) {
+                for (int k = split; k < ctas; k += splits) {
                     const uint32_t x = __ldcg(counts + k * nb + b);
                     total += x;
-                    less += k < (int)blockIdx.x ? x : 0;
+                    less += k < cta ? x : 0;
                 }
             }
             extra[tid] = less;
@@ -194,8 +193,33 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_cons
                 else __stcg(dst + to, x);
             }
         }
-        if (!last) cg::this_grid().sync();
+        if (!last) wait();
     }
+}
+
+template <int kSortItems>
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
+    sort_column<kSortItems>(a, blockIdx.y, blockIdx.x, gridDim.x, [] { cg::this_grid().sync(); });
+}
+
+// Zeros for a large result while one cluster of CTAs sorts few tokens, a tile each.  The
+// zeros are cut into many CTAs for the SMs to take as they get free: 537 MB take 72 us
+// so, and 84 us in equal shares of the SMs, which do not all reach the memory equally fast.
+constexpr int kFillCluster = 4;
+constexpr int kFillVecs = 16 * kSortThreads;    // 16-byte vectors of a CTA
+
+__global__ void __cluster_dims__(kFillCluster, 1, 1) __launch_bounds__(kSortThreads, 1)
+    sort_and_fill_kernel(const __grid_constant__ SortArgs a, char* out, int64_t bytes) {
+    if (blockIdx.x < kFillCluster) {
+        sort_column<4>(a, 0, blockIdx.x, kFillCluster, [] { cg::this_cluster().sync(); });
+        return;
+    }
+    const int64_t vecs = bytes / 16, v0 = (int64_t)(blockIdx.x - kFillCluster) * kFillVecs + threadIdx.x;
+    uint4* to = reinterpret_cast<uint4*>(out);
+#pragma unroll
+    for (int u = 0; u < kFillVecs / kSortThreads; ++u)
+        if (v0 + u * kSortThreads < vecs) to[v0 + u * kSortThreads] = make_uint4(0u, 0u, 0u, 0u);
+    if (blockIdx.x == kFillCluster && threadIdx.x < bytes % 16) out[vecs * 16 + threadIdx.x] = 0;
 }
 
 }  // namespace
@@ -219,18 +243,16 @@ SortPlan plan_sort(const IndexArgs& x, int entry_bytes) {
     p.per_cta = cdiv(cdiv(n, most_ctas), tile) * tile;
     p.ctas = (int)cdiv(n, p.per_cta);
     p.pairs = align256((size_t)entry_bytes * x.d * x.n);
-    p.counts = align256(sizeof(uint32_t) * x.d * p.ctas * p.bins);
+    p.counts = align256(sizeof(uint32_t) * x.d * (p.ctas > kFillCluster ? p.ctas : kFillCluster) * p.bins);
     return p;
 }
 
-cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, const Tables* tables, const float* g,
-                        Sorted& sorted, cudaStream_t s) {
-    sorted.entries = static_cast<char*>(ws) + ((p.passes - 1) & 1) * p.pairs;
-    sorted.bytes = tables ? sizeof(uint4) : sizeof(uint2);
-    if (index.n == 0) return cudaSuccess;
-    const size_t smem = sizeof(uint32_t) * ((kSortWarps + 1) * p.bins + 2 * kSortThreads);
-    cudaError_t e = p.items == 4 ? allow_smem<sort_kernel<4>>() : allow_smem<sort_kernel<8>>();
-    if (e != cudaSuccess) return e;
+namespace {
+
+size_t sort_smem_bytes(const SortPlan& p) { return sizeof(uint32_t) * ((kSortWarps + 1) * p.bins + 2 * kSortThreads); }
+
+// buffers in the workspace; the last pass's output is what `sorted` tells
+SortArgs sort_args(const IndexArgs& index, const SortPlan& p, void* ws, bool wide, Sorted& sorted) {
     SortArgs a;
     a.index = index;
     for (int k = 0; k < 2; ++k) a.buf[k] = reinterpret_cast<uint2*>(static_cast<char*>(ws) + k * p.pairs);
@@ -239,15 +261,40 @@ cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, con
     a.bits = p.bits;
     a.bins = p.bins;
     a.per_cta = p.per_cta;
-    a.entries = tables ? static_cast<uint4*>(static_cast<void*>(a.buf[(p.passes - 1) & 1])) : nullptr;
+    a.entries = wide ? reinterpret_cast<uint4*>(a.buf[(p.passes - 1) & 1]) : nullptr;
+    a.g = nullptr;
+    sorted.entries = static_cast<char*>(ws) + ((p.passes - 1) & 1) * p.pairs;
+    sorted.bytes = wide ? sizeof(uint4) : sizeof(uint2);
+    return a;
+}
+
+}  // namespace
+
+cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, const Tables* tables, const float* g,
+                        Sorted& sorted, cudaStream_t s) {
+    SortArgs a = sort_args(index, p, ws, tables != nullptr, sorted);
+    if (index.n == 0) return cudaSuccess;
+    cudaError_t e = p.items == 4 ? allow_smem<sort_kernel<4>>() : allow_smem<sort_kernel<8>>();
+    if (e != cudaSuccess) return e;
     a.g = g;
     if (tables)
         for (int m = 0; m < index.d; ++m) a.tables[m] = tables[m];
     void* args[] = {&a};
     const void* kernel = p.items == 4 ? reinterpret_cast<const void*>(sort_kernel<4>)
                                       : reinterpret_cast<const void*>(sort_kernel<8>);
-    return cudaLaunchCooperativeKernel(kernel, dim3(p.ctas, index.d),
-                                       dim3(kSortThreads), args, smem, s);
+    return cudaLaunchCooperativeKernel(kernel, dim3(p.ctas, index.d), dim3(kSortThreads), args, sort_smem_bytes(p), s);
+}
+
+cudaError_t sort_and_fill(const IndexArgs& index, const SortPlan& p, void* ws, void* out, int64_t bytes,
+                          Sorted& sorted, cudaStream_t s) {
+    SortArgs a = sort_args(index, p, ws, false, sorted);
+    a.per_cta = kSortThreads * 4;
+    if (index.n > kFillCluster * a.per_cta) return cudaErrorInvalidValue;
+    cudaError_t e = allow_smem<sort_and_fill_kernel>();
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = kFillCluster * (1 + (unsigned)cdiv(bytes, 16 * kFillVecs * kFillCluster));
+    sort_and_fill_kernel<<<blocks, kSortThreads, sort_smem_bytes(p), s>>>(a, static_cast<char*>(out), bytes);
+    return cudaGetLastError();
 }
 
 }  // namespace mk

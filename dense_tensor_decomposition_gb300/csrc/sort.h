@@ -43,5 +43,9 @@ SortPlan plan_sort(const IndexArgs& index, int entry_bytes);
 // tables: nullptr, or one for each index column, for entries of 16 bytes
 cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, const Tables* tables, const float* g,
                         Sorted& sorted, cudaStream_t s);
+// one index column of at most 16384 tokens, by one cluster of CTAs while the others set `bytes` bytes at `out`
+// (16-byte aligned) to zero
+cudaError_t sort_and_fill(const IndexArgs& index, const SortPlan& p, void* ws, void* out, int64_t bytes,
+                          Sorted& sorted, cudaStream_t s);
 
 }  // namespace mk

@@ -200,7 +200,6 @@ struct OwnArgs {
     int log2L;
     int64_t part;           // columns of a CTA (blockIdx.y)
     uint32_t first_bytes;   // of shared memory, for `list` and then the terms
-    bool zeros;             // rows without tokens are set to zero here
 };
 
 // Bound by memory: the rows' writes, most of them zeros where tokens are few, and the
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
                 grouped = 1;
             }
         }
-    } else if (o.zeros) {
+    } else if (!a.accumulate) {
         while (!grouped) {
             const uint32_t u = take(&last_unit);
             if (u >= units) break;
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
         sum_list<TO, VEC, Terms, kSumThreads>(a, m, TermsOf{a, m}, at_place, row_of, total, o.log2L, col0, heads,
                                               Around{false, false, nullptr, nullptr}, sync);
     }
-    if (!o.zeros) return;
+    if (a.accumulate) return;
     auto is_touched = [&](uint32_t r) { return r >= o.owned || (touched[r >> 5] >> (r & 31) & 1u) != 0; };
     for (uint32_t u = take(&next_unit); u < left; u = take(&next_unit))
         zero_rows<TO, VEC>(a, m, u * unit, unit, col0, vecs, is_touched, row_of);
@@ -345,7 +344,12 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- many tokens
 
-constexpr int kTile = 256;              // sorted tokens of a CTA of row_sum_kernel
+constexpr int kTile = kThreads;         // most sorted tokens of a CTA of row_sum_kernel
+
+// sorted tokens of a CTA: fewer where the GPU would not have two CTAs an SM
+inline int64_t tile_tokens(int64_t n) {
+    return n >= 2 * kSms * kTile ? kTile : n >= kSms * kTile ? kTile / 2 : kTile / 4;
+}
 
 struct SumArgs {
     RowSumArgs a;
@@ -365,7 +369,6 @@ __device__ __forceinline__ uint32_t key_at(const SumArgs& s, int m, int64_t p) {
 // behind write zeros, 32 rows a warp.
 template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant__ SumArgs s) {
-    static_assert(kTile == kThreads, "a thread stages one entry");
     __shared__ uint2 pairs[kTile];
     __shared__ float4 heads[(kThreads * VEC + 3) / 4];
     const RowSumArgs& a = s.a;
@@ -379,8 +382,8 @@ __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant
     }
     const uint2* sorted = reinterpret_cast<const uint2*>(s.sorted.entries) + m * n;
     const int64_t col0 = (int64_t)blockIdx.y * s.columns;
-    const int64_t p0 = blockIdx.x * (int64_t)kTile;
-    const uint2 kt = p0 + threadIdx.x < n ? sorted[p0 + threadIdx.x] : make_uint2(kNone, 0u);
+    const int64_t p0 = blockIdx.x * s.tile;
+    const uint2 kt = threadIdx.x < s.tile && p0 + threadIdx.x < n ? sorted[p0 + threadIdx.x] : make_uint2(kNone, 0u);
     pairs[threadIdx.x] = kt;
     const int count = __syncthreads_count(kt.x != kNone);
     if (count == 0) return;
@@ -502,37 +505,25 @@ inline bool plan_own(const IndexArgs& index, int64_t width, int out_type, int ve
     return true;
 }
 
+// bytes of the partial sums, two rows for every tile
+inline size_t part_bytes(const IndexArgs& x, int64_t width) {
+    return sizeof(float) * x.d * cdiv(x.n, tile_tokens(x.n)) * 2 * width;
+}
+
+// Zeros of more than this many bytes are worth a launch in which the SMs share them as
+// they get free, for few tokens too.
+constexpr int64_t kFillBytes = 96 << 20;
+
 // whether own_kernel takes the sums whatever the alignment of the rows (one launch that
 // needs no workspace)
 inline bool always_owned(const IndexArgs& index, int64_t width) {
     OwnArgs o;
     dim3 grid;
-    bool all = true;
+    bool all = index.d > 1 || index.rows[0] * width * 4 <= kFillBytes;
     for (int type : {MTTKRP_F32, MTTKRP_F16})
         for (int vec : {1, 4, 8}) all = all && plan_own(index, width, type, vec, o, grid);
     return all;
 }
-
-// bytes of the partial sums, two rows for every kTile tokens
-inline size_t part_bytes(const IndexArgs& x, int64_t width) {
-    return sizeof(float) * x.d * cdiv(x.n, kTile) * 2 * width;
-}
-
-// Zeros for all rows, one vector a thread.  A grid of many CTAs, which go to the SMs as
-// these get free, fills 537 MB in 72 us; own_kernel's 152, each with its share, take 84
-// us, as the SMs do not all reach the memory equally fast.
-template <typename TO, int VEC>
-__global__ void __launch_bounds__(kThreads) fill_kernel(TO* out, int64_t rows, uint32_t vecs, int64_t stride) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, r = i / vecs;
-    if (r >= rows) return;
-    Pack<TO, VEC> zero;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) zero.v[e] = from_f32<TO>(0.f);
-    *reinterpret_cast<Pack<TO, VEC>*>(out + r * stride + (i - r * vecs) * VEC) = zero;
-}
-
-// Bytes of zeros that are worth a launch of their own
-constexpr int64_t kFillBytes = 96 << 20;
 
 // joins the tiles' crossing runs
 template <typename TO, int VEC>
@@ -551,9 +542,11 @@ template <typename TO, int VEC, template <typename> typename Few, int kFewRing, 
 cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     OwnArgs o;
     dim3 grid;
-    if (plan_own(a.index, a.width, a.out_type, VEC, o, grid)) {
+    const int64_t bytes = a.index.rows[0] * a.width * (int64_t)sizeof(TO);
+    const bool fill = !a.accumulate && a.index.d == 1 && a.index.n > 0 && a.index.n <= kOwnTokens &&
+                      a.out_stride == a.width && reinterpret_cast<uintptr_t>(a.out[0]) % 16 == 0 && bytes > kFillBytes;
+    if (!fill && plan_own(a.index, a.width, a.out_type, VEC, o, grid)) {
         o.a = a;
-        o.zeros = !a.accumulate;
         const size_t list = sizeof(uint32_t) * kSumWarps * o.per_warp;
         o.first_bytes = (uint32_t)align256(list > kFewRing * kSumThreads ? list : kFewRing * kSumThreads);
         const size_t smem = o.first_bytes + sizeof(float) * kSumThreads * VEC +
@@ -561,17 +554,6 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
         constexpr auto kernel = own_kernel<TO, VEC, Few>;
         cudaError_t e = allow_smem<kernel>();
         if (e != cudaSuccess) return e;
-        if (o.zeros && a.index.d == 1 && a.index.rows[0] * a.width * (int64_t)sizeof(TO) > kFillBytes) {
-            const bool dense = a.out_stride == a.width;     // then one row
-            const int64_t rows = dense ? 1 : a.index.rows[0];
-            const int64_t vecs = (dense ? a.index.rows[0] : 1) * a.width / VEC;
-            const int64_t blocks = cdiv(rows * vecs, kThreads);
-            if (vecs <= UINT32_MAX && blocks <= INT32_MAX) {
-                fill_kernel<TO, VEC><<<(unsigned)blocks, kThreads, 0, st>>>(static_cast<TO*>(a.out[0]), rows,
-                                                                            (uint32_t)vecs, a.out_stride);
-                o.zeros = false;
-            }
-        }
         kernel<<<grid, kOwnThreads, smem, st>>>(o);
         return cudaGetLastError();
     }
@@ -579,13 +561,14 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     SumArgs s;
     s.a = a;
     s.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.total());
-    s.tile = kTile;
-    s.tiles = cdiv(a.index.n, kTile);
+    s.tile = tile_tokens(a.index.n);
+    s.tiles = cdiv(a.index.n, s.tile);
     s.log2L = 0;
     while ((1 << s.log2L) < kThreads && ((int64_t)VEC << s.log2L) < a.width) ++s.log2L;
     s.columns = (int64_t)VEC << s.log2L;
-    cudaError_t e = sort_tokens(a.index, p, a.ws, nullptr, nullptr, s.sorted, st);
-    const int64_t zeros = a.accumulate ? 0 : cdiv(most_rows(a.index), kThreads);
+    cudaError_t e = fill ? sort_and_fill(a.index, p, a.ws, a.out[0], bytes, s.sorted, st)
+                         : sort_tokens(a.index, p, a.ws, nullptr, nullptr, s.sorted, st);
+    const int64_t zeros = a.accumulate || fill ? 0 : cdiv(most_rows(a.index), kThreads);
     if (e != cudaSuccess || s.tiles + zeros == 0) return e;
     constexpr auto kernel = row_sum_kernel<TO, VEC, Many>;
     e = allow_smem<kernel>();
