@@ -23,28 +23,26 @@ constexpr int kStageThreads = 1024;
 struct StageArgs {
     IndexArgs index;
     const void* factor[MTTKRP_MAX_ORDER];
+    uint32_t inverse[MTTKRP_MAX_ORDER];     // of a mode's rows, see stage()
     int type;
+    bool quads;             // fp32, and every four columns stand at a multiple of 16 bytes
     int64_t width;
 };
 
 // four elements from a row's column c on, zeros behind the last column
-__device__ __forceinline__ float4 row4(const StageArgs& a, int mode, int64_t row, int64_t c) {
+__device__ __forceinline__ float4 row4(const StageArgs& a, int mode, uint32_t row, int64_t c) {
+    const int64_t at = (int64_t)row * a.width + c;
+    if (a.quads)
+        return c < a.width ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.factor[mode]) + at)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
     float v[4];
-    const int64_t at = row * a.width + c;
-    if (a.type == MTTKRP_F32) {
-        const float* p = static_cast<const float*>(a.factor[mode]) + at;
-        if (c + 4 <= a.width && (reinterpret_cast<uintptr_t>(p) & 15) == 0)
-            return *reinterpret_cast<const float4*>(p);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + e < a.width ? p[e] : 0.f;
-    } else if (a.type == MTTKRP_BF16) {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.factor[mode]) + at;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + e < a.width ? to_f32(p[e]) : 0.f;
-    } else {
-        const __half* p = static_cast<const __half*>(a.factor[mode]) + at;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + e < a.width ? to_f32(p[e]) : 0.f;
+    for (int e = 0; e < 4; ++e) {
+        v[e] = 0.f;
+        if (c + e >= a.width) continue;
+        if (a.type == MTTKRP_F32) v[e] = static_cast<const float*>(a.factor[mode])[at + e];
+        else if (a.type == MTTKRP_BF16) v[e] = to_f32(static_cast<const __nv_bfloat16*>(a.factor[mode])[at + e]);
+        else v[e] = to_f32(static_cast<const __half*>(a.factor[mode])[at + e]);
     }
     return make_float4(v[0], v[1], v[2], v[3]);
 }
@@ -53,36 +51,40 @@ __device__ __forceinline__ float4 times(float4 a, float4 b) {
     return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
 }
 
-// Columns col0 .. col0 + CS of the tables: row r at tab[r * CS].  kAhead rows a thread
-// are in flight.
+// Columns col0 .. col0 + CS of the tables: row r at tab[r * CS].  A group of CS / 4
+// lanes takes a row, kAhead rows in turn.
 template <int CS>
 __device__ __forceinline__ void stage(const StageArgs& a, const Tables& t, int64_t col0, float* tab) {
-    constexpr int kQuads = CS / 4, kAhead = 5;
-    const int items = t.rows * kQuads;
-    for (int i0 = threadIdx.x; i0 < items; i0 += kAhead * kStageThreads) {
-        float4 v[kAhead];
+    constexpr int kQuads = CS / 4, kGroups = kStageThreads / kQuads, kAhead = 4;
+    const int64_t c = col0 + (threadIdx.x % kQuads) * 4;
+    float* to = tab + (threadIdx.x % kQuads) * 4;
+    for (int g = 0; g < t.groups; ++g) {
+        const Tables::Group& group = t.group[g];
+        const uint32_t rows = (uint32_t)((g + 1 < t.groups ? t.group[g + 1].first : t.rows) - group.first);
+        for (uint32_t r0 = threadIdx.x / kQuads; r0 < rows; r0 += kAhead * kGroups) {
+            float4 v[kAhead];
+            uint32_t rest[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u * kStageThreads;
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i >= items) continue;
-            const int r = i / kQuads;
-            int g = 0;
-            while (g + 1 < t.groups && t.group[g + 1].first <= r) ++g;
-            uint32_t rest = (uint32_t)(r - t.group[g].first);
-            for (int k = t.group[g].modes - 1; k >= 0; --k) {
-                const int mode = t.group[g].mode[k];
-                const uint32_t rows = (uint32_t)a.index.rows[mode];
-                const uint32_t q = rest / rows;
-                const float4 x = row4(a, mode, rest - q * rows, col0 + (i % kQuads) * 4);
-                v[u] = k == t.group[g].modes - 1 ? x : times(v[u], x);
-                rest = q;
+            for (int u = 0; u < kAhead; ++u) rest[u] = min(r0 + u * kGroups, rows - 1);
+            for (int k = group.modes - 1; k >= 0; --k) {
+                const int mode = group.mode[k];
+                const uint32_t size = (uint32_t)a.index.rows[mode], inverse = a.inverse[mode];
+                float4 x[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    // rest / size for both below 2^16: inverse is 2^32 / size rounded up (0 for size 1)
+                    const uint32_t q = k == 0 ? 0 : inverse == 0 ? rest[u] : __umulhi(rest[u], inverse);
+                    x[u] = row4(a, mode, rest[u] - q * size, c);
+                    rest[u] = q;
+                }
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) v[u] = k == group.modes - 1 ? x[u] : times(v[u], x[u]);
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u * kStageThreads;
-            if (i < items) *reinterpret_cast<float4*>(tab + (size_t)i * 4) = v[u];
+            for (int u = 0; u < kAhead; ++u) {
+                const uint32_t r = r0 + u * kGroups;
+                if (r < rows) *reinterpret_cast<float4*>(to + (size_t)(group.first + r) * CS) = v[u];
+            }
         }
     }
 }
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant
 // samples' table rows stand behind the tables, worked out once.  A warp takes 32 samples
 // at a time: L = CS / 4 lanes form the products of L samples, one after the other, and
 // add them up so that every lane ends with its own sample's sum.
-constexpr uint32_t kOutside = 0xFFFFFFFFu;     // of a sample that takes no part
+constexpr int kSampleBytes = 32 * sizeof(uint2) + sizeof(uint32_t);     // of shared memory for 32 samples
 
 template <int CS, int G>
 __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const __grid_constant__ EntriesArgs a,
@@ -141,13 +143,15 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
     constexpr int L = CS / 4;
     float* tab = reinterpret_cast<float*>(stage_smem);
     uint2* rows = reinterpret_cast<uint2*>(tab + (size_t)tables.rows * CS);     // 4 numbers of 16 bits a sample
+    uint32_t* parts = reinterpret_cast<uint32_t*>(rows + share);                // a bit a sample: it takes part
     const int lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * share;
     const int count = (int)(t0 + share < a.index.n ? share : a.index.n - t0);
-    for (int i = threadIdx.x; i < count; i += kStageThreads) {
-        uint2 r = make_uint2(kOutside, kOutside);
-        if (sort_key(a.index, t0 + i, 0) != kNone) {
-            r = make_uint2(0u, 0u);
+    // samples that take no part, and those behind the last one of a warp's 32, read row 0
+    for (int i = threadIdx.x; i < (count + 31) / 32 * 32; i += kStageThreads) {
+        uint2 r = make_uint2(0u, 0u);
+        const bool inside = i < count && sort_key(a.index, t0 + i, 0) != kNone;
+        if (inside) {
 #pragma unroll
             for (int k = 0; k < G; ++k) {
                 const uint32_t row = table_row(a.index, tables.group[k], t0 + i) << (k & 1) * 16;
@@ -156,6 +160,8 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
             }
         }
         rows[i] = r;
+        const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, inside);
+        if (lane == 0) parts[i / 32] = ballot;
     }
     const float* mine = tab + (lane & (L - 1)) * 4;
     for (int64_t col0 = 0; col0 < a.width; col0 += CS) {
@@ -163,15 +169,11 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
         __syncthreads();
         for (int base = threadIdx.x & ~31; base < count; base += kStageThreads) {
             const int i = base + lane;
-            const uint2 own = i < count ? rows[i] : make_uint2(kOutside, kOutside);
-            const bool inside = own.x != kOutside;
-            const uint32_t lo = inside ? own.x : 0u, hi = inside ? own.y : 0u;
             float acc[L];
 #pragma unroll
             for (int k = 0; k < L; ++k) {
-                const uint32_t lo_k = __shfl_sync(0xFFFFFFFFu, lo, k, L);
-                const uint32_t hi_k = G > 2 ? __shfl_sync(0xFFFFFFFFu, hi, k, L) : 0u;
-                const float4 p = product<CS, G>(mine, lo_k, hi_k);
+                const uint2 r = rows[base + (lane & ~(L - 1)) + k];
+                const float4 p = product<CS, G>(mine, r.x, r.y);
                 acc[k] = (p.x + p.y) + (p.z + p.w);
             }
 #pragma unroll
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
             }
             if (i < count) {
                 float* x = a.out + t0 + i;
-                *x = !inside ? 0.f : col0 == 0 ? acc[0] : *x + acc[0];
+                *x = (parts[i / 32] >> lane & 1u) == 0 ? 0.f : col0 == 0 ? acc[0] : *x + acc[0];
             }
         }
         __syncthreads();
@@ -200,6 +202,7 @@ struct Model {
     template <typename List>
     struct Terms {
         static constexpr int kB = 4;
+        static constexpr bool kAllLanes = false;
         const TermsOf& of;
         const List& list;
         const int p1;
@@ -241,8 +244,10 @@ struct Model {
     };
 };
 
-// products of table rows in shared memory, of entries of 16 bytes; the next entries are
-// on their way while these are used
+// Products of table rows in shared memory, of entries of 16 bytes.  The L lanes of a
+// sample hold L entries, one each, which go round by shuffles (reading every entry in
+// every lane would take as many shared-memory cycles as half a table row); the next L
+// are on their way meanwhile.
 struct StagedOf {
     const float* tab;       // at the lane's columns
 };
@@ -251,38 +256,46 @@ template <int CS, int VEC, int G>
 struct Staged {
     template <typename List>
     struct Terms {
-        static constexpr int kB = 4;
+        static constexpr int L = CS / VEC, kB = L < 4 ? L : 4;
+        static constexpr bool kAllLanes = true;
         const StagedOf& of;
         const List& list;
-        const int p1;
-        uint4 entry[kB], next[kB];
+        const int p0, p1;
+        const uint32_t lanes;       // of the group
+        int at;                     // which of the held entries is token p of load(p)
+        uint4 held, next;
         __device__ __forceinline__ Terms(const StagedOf& of, const List& list, int p0, int p1, int64_t)
-            : of(of), list(list), p1(p1) {
+            : of(of), list(list), p0(p0), p1(p1),
+              lanes((0xFFFFFFFFu >> (32 - L)) << (threadIdx.x & 31 & ~(L - 1))), at(0) {
             fetch(p0);
         }
         __device__ __forceinline__ void fetch(int p) {
-#pragma unroll
-            for (int j = 0; j < kB; ++j) next[j] = list(p + j < p1 ? p + j : p1 - 1);
+            const int own = p + (threadIdx.x & (L - 1));
+            next = list(own < p1 ? own : p1 - 1);
         }
         __device__ __forceinline__ void load(int p) {
-#pragma unroll
-            for (int j = 0; j < kB; ++j) entry[j] = next[j];
-            fetch(p + kB);
+            at = (p - p0) & (L - 1);
+            if (at == 0) {
+                held = next;
+                fetch(p + L);
+            }
         }
-        __device__ __forceinline__ uint32_t key(int j) const { return entry[j].x; }
+        __device__ __forceinline__ uint32_t from(uint32_t x, int j) const { return __shfl_sync(lanes, x, at + j, L); }
+        __device__ __forceinline__ uint32_t key(int j) const { return from(held.x, j); }
         __device__ __forceinline__ void add(int j, float* acc) const {
-            const float g = __uint_as_float(entry[j].y);
+            const float g = __uint_as_float(from(held.y, j));
+            const uint32_t lo = from(held.z, j), hi = G > 2 ? from(held.w, j) : 0u;
             if constexpr (VEC == 4) {
-                const float4 p = product<CS, G>(of.tab, entry[j].z, entry[j].w);
+                const float4 p = product<CS, G>(of.tab, lo, hi);
                 acc[0] = fmaf(g, p.x, acc[0]);
                 acc[1] = fmaf(g, p.y, acc[1]);
                 acc[2] = fmaf(g, p.z, acc[2]);
                 acc[3] = fmaf(g, p.w, acc[3]);
             } else {
-                float p = of.tab[(entry[j].z & 0xFFFFu) * CS];
-                if constexpr (G > 1) p *= of.tab[(entry[j].z >> 16) * CS];
-                if constexpr (G > 2) p *= of.tab[(entry[j].w & 0xFFFFu) * CS];
-                if constexpr (G > 3) p *= of.tab[(entry[j].w >> 16) * CS];
+                float p = of.tab[(lo & 0xFFFFu) * CS];
+                if constexpr (G > 1) p *= of.tab[(lo >> 16) * CS];
+                if constexpr (G > 2) p *= of.tab[(hi & 0xFFFFu) * CS];
+                if constexpr (G > 3) p *= of.tab[(hi >> 16) * CS];
                 acc[0] = fmaf(g, p, acc[0]);
             }
         }
@@ -437,6 +450,11 @@ StageArgs stage_args(const IndexArgs& index, const void* const* factor, int type
     a.index = index;
     for (int m = 0; m < index.d; ++m) a.factor[m] = factor[m];
     a.type = type;
+    a.quads = type == MTTKRP_F32 && width % 4 == 0;
+    for (int m = 0; m < index.d; ++m) {
+        a.quads = a.quads && reinterpret_cast<uintptr_t>(factor[m]) % 16 == 0;
+        a.inverse[m] = (uint32_t)((((uint64_t)1 << 32) + index.rows[m] - 1) / index.rows[m]);
+    }
     a.width = width;
     return a;
 }
@@ -446,7 +464,7 @@ cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share,
     constexpr auto kernel = entries_staged_kernel<CS, G>;
     cudaError_t e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
-    const size_t smem = sizeof(float) * t.rows * CS + sizeof(uint2) * share;
+    const size_t smem = sizeof(float) * t.rows * CS + kSampleBytes * share / 32;
     kernel<<<(unsigned)cdiv(a.index.n, share), kStageThreads, smem, s>>>(
         a, stage_args(a.index, a.factor, a.type, a.width), t, (int)share);
     return cudaGetLastError();
@@ -501,7 +519,7 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
         const int64_t rounds = cdiv(n, kSms * kMost);
         const int64_t part = cdiv(cdiv(n, kSms * rounds), 32) * 32;
         Tables t;
-        const double slice = plan_tables(a.index, -1, c, table_rows(sizeof(uint2) * part, c), (double)part, t);
+        const double slice = plan_tables(a.index, -1, c, table_rows(kSampleBytes * part / 32, c), (double)part, t);
         const double work = slice * cdiv(a.width, c) * rounds;
         if (slice >= 0.0 && work < least) {
             least = work;

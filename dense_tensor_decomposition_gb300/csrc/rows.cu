@@ -82,6 +82,7 @@ struct Grad {
     template <typename List>
     struct Terms {
         static constexpr int kB = B;
+        static constexpr bool kAllLanes = false;
         const TermsOf& of;
         const List& list;
         const int p1;
@@ -118,6 +119,7 @@ struct Ring {
     template <typename List>
     struct Terms {
         static constexpr int kB = 4;
+        static constexpr bool kAllLanes = false;
         const TermsOf& of;
         const List& list;
         const int p0, p1;

@@ -50,7 +50,8 @@ struct Around {
 //
 // Terms<List> terms(context, list, p0, p1, col) gives a lane the terms of tokens p0 .. p1,
 // kB at a time: after load(p), key(j) is the row of token p + j and add(j, acc) adds its
-// term; behind p1 these repeat some token of the list.
+// term; behind p1 these repeat some token of the list.  Lanes behind the last column
+// take part only where the terms need all lanes of a group (kAllLanes).
 template <typename TO, int VEC, template <typename> typename Terms, int kN, typename Context, typename List,
           typename Row, typename Sync>
 __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Context& context, const List& list,
@@ -61,6 +62,7 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
     const int group = threadIdx.x >> log2L, lane = threadIdx.x & (L - 1);
     const int64_t col = col0 + lane * VEC;
     const bool on = col < a.width;
+    const bool part = on || Terms<List>::kAllLanes;
     const int share = (count + groups - 1) / groups;
     const int p0 = group * share < count ? group * share : count;
     const int p1 = p0 + share < count ? p0 + share : count;
@@ -76,7 +78,10 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
     float* own_head = heads + (size_t)threadIdx.x * VEC;
     uint32_t cur = 0;
     bool open = false;          // the run at the end began in this group and goes on
-    if (p0 < p1 && on) {
+    auto finish = [&]() {
+        if (on) write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+    };
+    if (p0 < p1 && part) {
         cur = list(p0).x;
         bool began_before = p0 > 0 ? list(p0 - 1).x == cur : around.before;
 #pragma unroll
@@ -94,7 +99,7 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
                 if (p + j < p1) {
                     if (terms.key(j) != cur) {
                         if (began_before) put(own_head);
-                        else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+                        else finish();
                         began_before = false;
                         cur = terms.key(j);
 #pragma unroll
@@ -107,7 +112,7 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
         const bool goes_on = p1 < count ? list(p1).x == cur : around.after;
         if (began_before) put(own_head);
         else if (goes_on) open = true;
-        else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+        else finish();
     }
     sync();
     if (!on) return;
@@ -115,7 +120,7 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
         int g = group + 1;
         for (; g * share < count && list(g * share).x == cur; ++g) add(heads + ((size_t)(g << log2L) + lane) * VEC);
         if (g * share >= count && around.after && list(count - 1).x == cur) put(around.tail + col);
-        else write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+        else finish();
     }
     if (group == 0 && around.before) {
         const uint32_t first = list(0).x;
