@@ -19,6 +19,7 @@
 // the reads, at 2 a cycle and SM.
 #include <cooperative_groups.h>
 
+#include "launch.cuh"
 #include "rows.h"
 #include "types.cuh"
 
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 2) clip_kernel(const __grid_constant
 // the same steps as launches of their own
 template <int N>
 __global__ void __launch_bounds__(kThreads, 2) squares_kernel(const __grid_constant__ Table<N> a, double* part) {
+    after_previous();
     const double sum = share_squares(a);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
@@ -306,6 +308,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const double* part, int n, f
                                                     float* coef) {
     // sums of the warps' consecutive parts, then those in order
     __shared__ double sums[32];
+    after_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = (n + 31) / 32;
     const int end = (warp + 1) * per < n ? (warp + 1) * per : n;
     double sum = 0.0;
@@ -323,6 +326,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const double* part, int n, f
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 2) scale_kernel(const __grid_constant__ Table<N> a, const float* coef) {
+    after_previous();
     share_scale(a, *coef);
 }
 
@@ -388,17 +392,20 @@ cudaError_t norm_and_clip(int n, const void* const* tensors, const int64_t* nume
     }
     int parts = 0;
     for (;;) {
-        if (t.units > 0) squares_kernel<N><<<blocks(t), kThreads, 0, s>>>(t, part + parts);
+        if (t.units > 0) {
+            e = launch_early(squares_kernel<N>, blocks(t), kThreads, 0, s, t, part + parts);
+            if (e != cudaSuccess) return e;
+        }
         parts += blocks(t);
         if (k == n) break;
         k += fill(t, n, k, tensors, numels, types, outs);
     }
-    norm_kernel<<<1, 1024, 0, s>>>(part, parts, max_norm, eps, norm, coef);
-    for (k = 0; outs && k < n;) {
+    e = launch_early(norm_kernel, 1, 1024, 0, s, part, parts, max_norm, eps, norm, coef);
+    for (k = 0; outs && k < n && e == cudaSuccess;) {
         k += fill(t, n, k, tensors, numels, types, outs);
-        if (t.units > 0) scale_kernel<N><<<blocks(t), kThreads, 0, s>>>(t, coef);
+        if (t.units > 0) e = launch_early(scale_kernel<N>, blocks(t), kThreads, 0, s, t, coef);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

@@ -105,6 +105,7 @@ __device__ __forceinline__ float4 product(const float* tab, uint32_t lo, uint32_
 // L lanes a sample, gathering from the caches.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant__ EntriesArgs a, int log2L) {
+    after_previous();
     const int L = 1 << log2L;
     const int lane = threadIdx.x & (L - 1);
     const int64_t t = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> log2L;
@@ -144,6 +145,7 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
     float* tab = reinterpret_cast<float*>(stage_smem);
     uint2* rows = reinterpret_cast<uint2*>(tab + (size_t)tables.rows * CS);     // 4 numbers of 16 bits a sample
     uint32_t* parts = reinterpret_cast<uint32_t*>(rows + share);                // a bit a sample: it takes part
+    after_previous();
     const int lane = threadIdx.x & 31;
     const int64_t t0 = (int64_t)blockIdx.x * share;
     const int count = (int)(t0 + share < a.index.n ? share : a.index.n - t0);
@@ -322,6 +324,9 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     const int64_t n = s.a.index.n;
     const uint32_t tile = blockIdx.x % (uint32_t)s.tiles, slice = blockIdx.x / (uint32_t)s.tiles;
     const int64_t col0 = (int64_t)slice * CS;
+    // the factors were there before the sort, this launch's previous one, began
+    if (col0 < s.a.width) stage<CS>(a.stage, a.tables[m], col0, tab);
+    after_previous();
     if (col0 >= s.a.width) {
         const int64_t warp = (blockIdx.x - cdiv(s.a.width, CS) * s.tiles) * (kStageThreads / 32) + (threadIdx.x >> 5);
         zero_unsorted_rows<float, VEC>(s.a, m, warp * 32, [&](int64_t p) { return key_at(s, m, p); });
@@ -329,7 +334,6 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     }
     const uint4* sorted = reinterpret_cast<const uint4*>(s.sorted.entries) + m * n;
     const int64_t p0 = tile * s.tile, p1 = p0 + s.tile < n ? p0 + s.tile : n;
-    stage<CS>(a.stage, a.tables[m], col0, tab);
     // entries that take part come first: find the end in two steps of 1024 probes
     int64_t lo = p0, hi = p1;
     while (lo < hi) {
@@ -440,9 +444,7 @@ cudaError_t entries_cached(const EntriesArgs& a, cudaStream_t s) {
     int l = 0;
     while (l < 5 && ((int64_t)(w ? kVec : 1) << l) < a.width) ++l;
     const unsigned blocks = (unsigned)cdiv(a.index.n << l, kThreads);
-    if (w) entries_kernel<T, kVec><<<blocks, kThreads, 0, s>>>(a, l);
-    else entries_kernel<T, 1><<<blocks, kThreads, 0, s>>>(a, l);
-    return cudaGetLastError();
+    return launch_early(w ? entries_kernel<T, kVec> : entries_kernel<T, 1>, blocks, kThreads, 0, s, a, l);
 }
 
 StageArgs stage_args(const IndexArgs& index, const void* const* factor, int type, int64_t width) {
@@ -465,9 +467,8 @@ cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share,
     cudaError_t e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
     const size_t smem = sizeof(float) * t.rows * CS + kSampleBytes * share / 32;
-    kernel<<<(unsigned)cdiv(a.index.n, share), kStageThreads, smem, s>>>(
-        a, stage_args(a.index, a.factor, a.type, a.width), t, (int)share);
-    return cudaGetLastError();
+    return launch_early(kernel, (unsigned)cdiv(a.index.n, share), kStageThreads, smem, s, a,
+                        stage_args(a.index, a.factor, a.type, a.width), t, (int)share);
 }
 
 template <int CS>
@@ -500,7 +501,8 @@ cudaError_t grad_staged(StagedArgs& a, const SortPlan& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(cdiv(r.width, CS) * a.s.tiles + cdiv(most_rows(r.index), kStageThreads)), r.index.d);
     const size_t smem = sizeof(float) * (kStageThreads * VEC + (size_t)rows * CS);
-    staged_sum_kernel<CS, VEC><<<grid, kStageThreads, smem, st>>>(a);
+    e = launch_early(staged_sum_kernel<CS, VEC>, grid, kStageThreads, smem, st, a);
+    if (e != cudaSuccess) return e;
     return join<float, VEC>(a.s, st);
 }
 

@@ -14,6 +14,7 @@ namespace {
 template <typename T, int VEC, int U, int K>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupArgs a, int log2L) {
     using P = Pack<T, VEC>;
+    after_previous();
     const int lane = threadIdx.x & ((1 << log2L) - 1);
     const int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> log2L) * K;
     const int step = VEC << log2L;
@@ -58,8 +59,7 @@ cudaError_t lookup_by(const LookupArgs& a, cudaStream_t s) {
     const int l = log2_lanes(cdiv(a.width, VEC));
     const dim3 grid((unsigned)cdiv(cdiv(a.index.n, K) << l, kThreads),
                     (unsigned)cdiv(a.width, (int64_t)(VEC * U) << l));
-    lookup_kernel<T, VEC, U, K><<<grid, kThreads, 0, s>>>(a, l);
-    return cudaGetLastError();
+    return launch_early(lookup_kernel<T, VEC, U, K>, grid, kThreads, 0, s, a, l);
 }
 
 // the widest vectors that the rows' starts and width allow

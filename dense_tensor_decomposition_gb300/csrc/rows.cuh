@@ -4,6 +4,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "sort.h"
 #include "types.cuh"
 

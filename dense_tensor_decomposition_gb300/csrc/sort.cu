@@ -199,6 +199,7 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
 
 template <int kSortItems>
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
+    allow_next();
     sort_column<kSortItems>(a, blockIdx.y, blockIdx.x, gridDim.x, [] { cg::this_grid().sync(); });
 }
 
@@ -210,6 +211,7 @@ constexpr int kFillVecs = 16 * kSortThreads;    // 16-byte vectors of a CTA
 
 __global__ void __cluster_dims__(kFillCluster, 1, 1) __launch_bounds__(kSortThreads, 1)
     sort_and_fill_kernel(const __grid_constant__ SortArgs a, char* out, int64_t bytes) {
+    after_previous();
     if (blockIdx.x < kFillCluster) {
         sort_column<4>(a, 0, blockIdx.x, kFillCluster, [] { cg::this_cluster().sync(); });
         return;
@@ -293,8 +295,8 @@ cudaError_t sort_and_fill(const IndexArgs& index, const SortPlan& p, void* ws, v
     cudaError_t e = allow_smem<sort_and_fill_kernel>();
     if (e != cudaSuccess) return e;
     const unsigned blocks = kFillCluster * (1 + (unsigned)cdiv(bytes, 16 * kFillVecs * kFillCluster));
-    sort_and_fill_kernel<<<blocks, kSortThreads, sort_smem_bytes(p), s>>>(a, static_cast<char*>(out), bytes);
-    return cudaGetLastError();
+    return launch_early(sort_and_fill_kernel, blocks, kSortThreads, sort_smem_bytes(p), s, a, static_cast<char*>(out),
+                        bytes);
 }
 
 }  // namespace mk

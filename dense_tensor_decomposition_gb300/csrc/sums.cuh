@@ -214,6 +214,7 @@ struct OwnArgs {
 template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_constant__ OwnArgs o) {
     extern __shared__ float4 own_smem[];
+    after_previous();
     const RowSumArgs& a = o.a;
     uint32_t* list = reinterpret_cast<uint32_t*>(own_smem);                     // tokens of the CTA's rows; then the terms'
     float* heads = reinterpret_cast<float*>(reinterpret_cast<char*>(own_smem) + o.first_bytes);     // kSumThreads * VEC
@@ -376,6 +377,7 @@ template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kThreads) row_sum_kernel(const __grid_constant__ SumArgs s) {
     __shared__ uint2 pairs[kTile];
     __shared__ float4 heads[(kThreads * VEC + 3) / 4];
+    after_previous();
     const RowSumArgs& a = s.a;
     const int m = blockIdx.z;
     const int64_t n = a.index.n;
@@ -412,6 +414,7 @@ template <typename TO, int VEC>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ SumArgs s) {
     constexpr int kWarps = kThreads / 32;
     using P = Pack<float, VEC>;
+    after_previous();
     const RowSumArgs& a = s.a;
     const int m = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t n = a.index.n;
@@ -535,8 +538,7 @@ template <typename TO, int VEC>
 cudaError_t join(const SumArgs& s, cudaStream_t st) {
     if (s.tiles < 2) return cudaGetLastError();
     const dim3 grid((unsigned)cdiv(s.tiles, kThreads / 32), (unsigned)cdiv(s.a.width, 32 * VEC), s.a.index.d);
-    join_kernel<TO, VEC><<<grid, kThreads, 0, st>>>(s);
-    return cudaGetLastError();
+    return launch_early(join_kernel<TO, VEC>, grid, kThreads, 0, st, s);
 }
 
 // Few: the terms as own_kernel takes them, whose CTAs of 1024 threads have few
@@ -559,8 +561,7 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
         constexpr auto kernel = own_kernel<TO, VEC, Few>;
         cudaError_t e = allow_smem<kernel>();
         if (e != cudaSuccess) return e;
-        kernel<<<grid, kOwnThreads, smem, st>>>(o);
-        return cudaGetLastError();
+        return launch_early(kernel, grid, kOwnThreads, smem, st, o);
     }
     const SortPlan p = plan_sort(a.index, sizeof(uint2));
     SumArgs s;
@@ -579,7 +580,8 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
     e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
     const dim3 sum_grid((unsigned)(s.tiles + zeros), (unsigned)cdiv(a.width, s.columns), a.index.d);
-    kernel<<<sum_grid, kThreads, kThreads * kManyRing, st>>>(s);
+    e = launch_early(kernel, sum_grid, kThreads, kThreads * kManyRing, st, s);
+    if (e != cudaSuccess) return e;
     return join<TO, VEC>(s, st);
 }
 
