@@ -6,24 +6,22 @@
 // read is still in the L2 cache at the second.  The tensors are described in the
 // kernel's arguments and cut into units of 8 KB; every block takes consecutive units,
 // so each of the GPU's blocks has the same bytes to move whatever the tensors' sizes.
-// One cooperative launch does it all: squares, a barrier over the grid, every block
-// adds the blocks' sums in the same order, then the products, from the last unit back
+// One launch adds the squares and leaves a sum a block; in a second one every block adds
+// the blocks' sums, in the same order, and multiplies its share, from the last unit back
 // to the first (the last ones are the ones still cached: reads that will not be
-// repeated and all writes are marked for the cache to drop first).  A launch for each
-// step, with blocks for the SMs to take as they get free, is no faster (2 GB of fp32:
-// 948 us against 941) and loses the cache's order (192 MB of bf16: 112 us against 99).
-// More tensors than a table holds take one launch a table and step.
+// repeated and all writes are marked for the cache to drop first).  One cooperative
+// launch with a barrier over the grid instead takes 12.3 us for 3 x 512 x 2000 fp32,
+// the two, of which the second is set up while the first runs, 11.4 us; more blocks than
+// are resident at once, for the SMs to take as they get free, lose the cache's order
+// (192 MB of bf16: 112 us against 99).  More tensors than a table holds take both
+// launches for each table.
 //
 // The squares of 16 elements are added in fp32, the sums of 16 in pairs of fp32 numbers
 // (the second holds what the first rounds away): fp64 additions would take longer than
 // the reads, at 2 a cycle and SM.
-#include <cooperative_groups.h>
-
 #include "launch.cuh"
 #include "rows.h"
 #include "types.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace mk {
 namespace {
@@ -265,7 +263,7 @@ __device__ __forceinline__ Norm norm_of(const double* part, int n, float max_nor
     if (threadIdx.x < 32) {
         double sum = 0.0;
 #pragma unroll 4
-        for (int i = threadIdx.x; i < n; i += 32) sum += static_cast<const volatile double*>(part)[i];
+        for (int i = threadIdx.x; i < n; i += 32) sum += part[i];
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         if (threadIdx.x == 0) {
             Norm r;
@@ -286,51 +284,29 @@ __device__ __forceinline__ Norm norm_of(const double* part, int n, float max_nor
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads, 2) clip_kernel(const __grid_constant__ Table<N> a, double* part,
-                                                           float max_norm, float eps, float* norm) {
-    const double sum = share_squares(a);
-    if (threadIdx.x == 0) part[blockIdx.x] = sum;
-    cg::this_grid().sync();
-    const Norm r = norm_of(part, gridDim.x, max_norm, eps);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = r.norm;
-    share_scale(a, r.coef);
-}
-
-// the same steps as launches of their own
-template <int N>
 __global__ void __launch_bounds__(kThreads, 2) squares_kernel(const __grid_constant__ Table<N> a, double* part) {
     after_previous();
     const double sum = share_squares(a);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(1024) norm_kernel(const double* part, int n, float max_norm, float eps, float* norm,
-                                                    float* coef) {
-    // sums of the warps' consecutive parts, then those in order
-    __shared__ double sums[32];
-    after_previous();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = (n + 31) / 32;
-    const int end = (warp + 1) * per < n ? (warp + 1) * per : n;
-    double sum = 0.0;
-#pragma unroll 4
-    for (int i = warp * per + lane; i < end; i += 32) sum += part[i];
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) sums[warp] = sum;
-    __syncthreads();
-    const Norm r = norm_of(sums, 32, max_norm, eps);
-    if (threadIdx.x == 0) {
-        *norm = r.norm;
-        *coef = r.coef;
-    }
-}
-
 template <int N>
-__global__ void __launch_bounds__(kThreads, 2) scale_kernel(const __grid_constant__ Table<N> a, const float* coef) {
+__global__ void __launch_bounds__(kThreads, 2) scale_kernel(const __grid_constant__ Table<N> a, const double* part,
+                                                            int parts, float max_norm, float eps, float* norm) {
     after_previous();
-    share_scale(a, *coef);
+    const Norm r = norm_of(part, parts, max_norm, eps);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = r.norm;
+    share_scale(a, r.coef);
 }
 
-// blocks of clip_kernel<N> that are resident at once on the current device
+// the norm alone
+__global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int parts, float* norm) {
+    after_previous();
+    const Norm r = norm_of(part, parts, 0.f, 0.f);
+    if (threadIdx.x == 0) *norm = r.norm;
+}
+
+// blocks of a launch that are resident at once on the current device
 template <int N>
 cudaError_t resident_blocks(int& blocks) {
     static int cached[64];      // by device; writing the same value twice is harmless
@@ -343,7 +319,7 @@ cudaError_t resident_blocks(int& blocks) {
     }
     int sms = 0, per_sm = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, clip_kernel<N>, kThreads, 0);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, scale_kernel<N>, kThreads, 0);
     if (e != cudaSuccess) return e;
     blocks = sms * per_sm < kMaxBlocks ? sms * per_sm : kMaxBlocks;
     if (dev < 64) cached[dev] = blocks;
@@ -377,43 +353,34 @@ int fill(Table<N>& t, int n, int k, const void* const* tensors, const int64_t* n
 template <int N>
 cudaError_t norm_and_clip(int n, const void* const* tensors, const int64_t* numels, const int* types,
                           void* const* outs, float max_norm, float eps, float* norm, void* ws, cudaStream_t s) {
-    float* coef = static_cast<float*>(ws);
-    double* part = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
+    double* part = static_cast<double*>(ws);
     int most = 0;
     cudaError_t e = resident_blocks<N>(most);
-    if (e != cudaSuccess) return e;
     auto blocks = [&](const Table<N>& t) { return t.units < (uint32_t)most ? (int)t.units : most; };
     Table<N> t;
-    int k = fill(t, n, 0, tensors, numels, types, outs);
-    if (outs && k == n && t.units > 0) {
-        void* args[] = {&t, &part, &max_norm, &eps, &norm};
-        return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(clip_kernel<N>), dim3(blocks(t)),
-                                           dim3(kThreads), args, 0, s);
-    }
-    int parts = 0;
-    for (;;) {
-        if (t.units > 0) {
-            e = launch_early(squares_kernel<N>, blocks(t), kThreads, 0, s, t, part + parts);
-            if (e != cudaSuccess) return e;
-        }
+    int parts = 0, tables = 0;
+    for (int k = 0; k < n && e == cudaSuccess; ++tables) {
+        k += fill(t, n, k, tensors, numels, types, outs);
+        if (t.units == 0) continue;
+        e = launch_early(squares_kernel<N>, blocks(t), kThreads, 0, s, t, part + parts);
         parts += blocks(t);
-        if (k == n) break;
-        k += fill(t, n, k, tensors, numels, types, outs);
     }
-    e = launch_early(norm_kernel, 1, 1024, 0, s, part, parts, max_norm, eps, norm, coef);
-    for (k = 0; outs && k < n && e == cudaSuccess;) {
-        k += fill(t, n, k, tensors, numels, types, outs);
-        if (t.units > 0) e = launch_early(scale_kernel<N>, blocks(t), kThreads, 0, s, t, coef);
+    if (e != cudaSuccess) return e;
+    if (!outs || parts == 0) return launch_early(norm_kernel, 1, kThreads, 0, s, part, parts, norm);
+    for (int k = 0; k < n && e == cudaSuccess;) {
+        k += tables == 1 ? n : fill(t, n, k, tensors, numels, types, outs);
+        if (t.units > 0)
+            e = launch_early(scale_kernel<N>, blocks(t), kThreads, 0, s, t, part, parts, max_norm, eps, norm);
     }
     return e;
 }
 
 }  // namespace
 
-// the coefficient, then at most kMaxBlocks partial sums a table
+// at most kMaxBlocks sums a table
 size_t grad_norm_workspace_bytes(int n) {
     const int64_t tables = n <= kSmallTable ? 1 : cdiv(n, kLargeTable);
-    return 256 + sizeof(double) * kMaxBlocks * tables;
+    return sizeof(double) * kMaxBlocks * tables;
 }
 
 cudaError_t launch_grad_norm(int n, const void* const* tensors, const int64_t* numels, const int* types,
