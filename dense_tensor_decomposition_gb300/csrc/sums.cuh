@@ -189,6 +189,7 @@ struct TermsOf {
 // ---------------------------------------------------------------- few tokens: one launch
 
 constexpr int kOwnThreads = 1024;
+constexpr int kOwnWarps = kOwnThreads / 32;
 constexpr int kSumThreads = 512;        // of which these group and add, while the others write zeros
 constexpr int kSumWarps = kSumThreads / 32;
 constexpr int kTokenBits = 14;
@@ -201,16 +202,17 @@ struct OwnArgs {
     RowSumArgs a;
     int row_shift;
     uint32_t owned;         // most rows a CTA owns
-    uint32_t per_warp;      // tokens that each of the first kSumWarps warps looks at
+    uint32_t per_warp;      // tokens that a warp looks at
     int log2L;
     int64_t part;           // columns of a CTA (blockIdx.y)
     uint32_t first_bytes;   // of shared memory, for `list` and then the terms
 };
 
 // Bound by memory: the rows' writes, most of them zeros where tokens are few, and the
-// terms' reads.  The zeros begin before it is known which rows have tokens: until the
-// tokens are grouped, the other half of the CTA writes them to all rows, from the last
-// one on; rows with tokens are written again.
+// terms' reads; for the smallest, by latencies: 4096 samples of a 256^3 model take about
+// 2 us to look through, 2 to group, 2.5 to add.  The zeros begin before it is known which
+// rows have tokens: while one half of the CTA groups the tokens, the other writes them to
+// all rows, from the last one on; rows with tokens are written again.
 template <typename TO, int VEC, template <typename> typename Terms>
 __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_constant__ OwnArgs o) {
     extern __shared__ float4 own_smem[];
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
     uint32_t* cursor = reinterpret_cast<uint32_t*>(heads + kSumThreads * VEC);  // owned: tokens of each row, then their places
     uint32_t* touched = cursor + o.owned;                                       // a bit for each owned row
     uint32_t* found = touched + (o.owned + 31) / 32;                            // the same with gaps, a part a warp; then sorted
-    __shared__ uint32_t warp_found[kSumWarps], sums[kSumWarps], tokens, next_unit, last_unit;
+    __shared__ uint32_t warp_found[kOwnWarps], sums[kSumWarps], tokens, next_unit, last_unit;
     __shared__ volatile int grouped;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int m = blockIdx.z;
@@ -242,51 +244,55 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
         return __shfl_sync(0xFFFFFFFFu, u, 0);
     };
 
+    // the CTA's tokens, as (owned row, token), in order in every warp's part
+    for (uint32_t i = threadIdx.x; i < o.owned; i += kOwnThreads) cursor[i] = 0;
     if (threadIdx.x == 0) {
         next_unit = 0;
         last_unit = 0;
         grouped = 0;
     }
     __syncthreads();
-    if (warp < kSumWarps) {
-        // the CTA's tokens, as (owned row, token), in order in every warp's part
-        for (uint32_t i = threadIdx.x; i < o.owned; i += kSumThreads) cursor[i] = 0;
-        sync();
-        uint32_t count = 0;
-        with_key(a.index, [&](auto key_of) {
-            constexpr int kLook = decltype(key_of)::kLook;      // tokens a lane looks up at once
-            for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
-                uint32_t key[kLook];
+    uint32_t count = 0;
+    with_key(a.index, [&](auto key_of) {
+        constexpr int kLook = decltype(key_of)::kLook;      // tokens a lane looks up at once
+        for (uint32_t k0 = 0; k0 < o.per_warp; k0 += kLook * 32) {
+            uint32_t key[kLook];
 #pragma unroll
-                for (int u = 0; u < kLook; ++u) {
-                    const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
-                    key[u] = k < o.per_warp && t < n ? key_of(a.index, t, m) : kNone;
-                }
-#pragma unroll
-                for (int u = 0; u < kLook; ++u) {
-                    const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
-                    const uint32_t block = v >> o.row_shift, turn = block / G;
-                    const bool mine = v != kNone && block - turn * G == blockIdx.x;
-                    const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
-                    if (mine) {
-                        const uint32_t r = (turn << o.row_shift) | (v & low);
-                        found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
-                        atomicAdd(cursor + r, 1u);
-                    }
-                    count += __popc(ballot);
-                }
+            for (int u = 0; u < kLook; ++u) {
+                const uint32_t k = k0 + u * 32 + lane, t = warp * o.per_warp + k;
+                key[u] = k < o.per_warp && t < n ? key_of(a.index, t, m) : kNone;
             }
-        });
-        if (lane == 0) warp_found[warp] = count;
-        sync();
-        // gaps out; the counts become the rows' first places
-        uint32_t total = 0, base = 0;
-        for (int w = 0; w < kSumWarps; ++w) {
-            const uint32_t c = warp_found[w];
-            base += w < warp ? c : 0;
-            total += c;
+#pragma unroll
+            for (int u = 0; u < kLook; ++u) {
+                const uint32_t t = warp * o.per_warp + k0 + u * 32 + lane, v = key[u];
+                const uint32_t block = v >> o.row_shift, turn = block / G;
+                const bool mine = v != kNone && block - turn * G == blockIdx.x;
+                const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, mine);
+                if (mine) {
+                    const uint32_t r = (turn << o.row_shift) | (v & low);
+                    found[warp * o.per_warp + count + __popc(ballot & ((1u << lane) - 1))] = (r << kTokenBits) | t;
+                    atomicAdd(cursor + r, 1u);
+                }
+                count += __popc(ballot);
+            }
         }
-        for (uint32_t k = lane; k < count; k += 32) list[base + k] = found[warp * o.per_warp + k];
+    });
+    if (lane == 0) warp_found[warp] = count;
+    __syncthreads();
+    if (warp < kSumWarps) {
+        // gaps out; the counts become the rows' first places
+        const uint32_t c = warp_found[lane];
+        uint32_t upto = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += up;
+        }
+        const uint32_t total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        for (int w = warp; w < kOwnWarps; w += kSumWarps) {
+            const uint32_t size = __shfl_sync(0xFFFFFFFFu, c, w), base = __shfl_sync(0xFFFFFFFFu, upto - c, w);
+            for (uint32_t k = lane; k < size; k += 32) list[base + k] = found[w * o.per_warp + k];
+        }
         const uint32_t per = (o.owned + kSumThreads - 1) / kSumThreads;
         uint32_t mine = 0, all;
         for (uint32_t k = 0; k < per; ++k) {
@@ -307,8 +313,19 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
             at += c;
         }
         sync();
-        // in order of the tokens within each row: one warp places them 32 at a time
-        if (warp == 0) {
+        // in order of the tokens within each row
+        if (total <= kSumThreads) {
+            // few: every thread counts the tokens of its row that come before its own
+            if (threadIdx.x < total) {
+                const uint32_t x = list[threadIdx.x], r = x >> kTokenBits;
+                uint32_t before = 0;
+#pragma unroll 8
+                for (uint32_t k = 0; k < threadIdx.x; ++k) before += list[k] >> kTokenBits == r;
+                found[cursor[r] + before] = x;
+            }
+            sync();
+        } else if (warp == 0) {
+            // one warp places them 32 at a time
             for (uint32_t k = 0; k < total; k += 32) {
                 const uint32_t x = k + lane < total ? list[k + lane] : kNone;
                 const uint32_t r = x >> kTokenBits;
@@ -322,10 +339,10 @@ __global__ void __launch_bounds__(kOwnThreads, 1) own_kernel(const __grid_consta
                 }
                 __syncwarp();
             }
-            if (lane == 0) {
-                tokens = total;
-                grouped = 1;
-            }
+        }
+        if (threadIdx.x == 0) {
+            tokens = total;
+            grouped = 1;
         }
     } else if (!a.accumulate) {
         while (!grouped) {
@@ -508,7 +525,7 @@ inline bool plan_own(const IndexArgs& index, int64_t width, int out_type, int ve
     const int64_t owned = cdiv(blocks, owners) << o.row_shift;
     if (owned > kOwnRows || parts > 65535) return false;
     o.owned = (uint32_t)owned;
-    o.per_warp = (uint32_t)(cdiv(index.n, kSumThreads) * 32);
+    o.per_warp = (uint32_t)(cdiv(index.n, kOwnThreads) * 32);
     grid = dim3((unsigned)owners, (unsigned)parts, index.d);
     return true;
 }
@@ -554,7 +571,7 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
                       a.out_stride == a.width && reinterpret_cast<uintptr_t>(a.out[0]) % 16 == 0 && bytes > kFillBytes;
     if (!fill && plan_own(a.index, a.width, a.out_type, VEC, o, grid)) {
         o.a = a;
-        const size_t list = sizeof(uint32_t) * kSumWarps * o.per_warp;
+        const size_t list = sizeof(uint32_t) * kOwnWarps * o.per_warp;
         o.first_bytes = (uint32_t)align256(list > kFewRing * kSumThreads ? list : kFewRing * kSumThreads);
         const size_t smem = o.first_bytes + sizeof(float) * kSumThreads * VEC +
                             sizeof(uint32_t) * (o.owned + (o.owned + 31) / 32) + list;
