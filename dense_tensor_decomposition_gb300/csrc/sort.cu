@@ -22,7 +22,7 @@ constexpr int kMaxDigit = 10;
 struct SortArgs {
     IndexArgs index;
     uint2* buf[2];          // d x n pairs each; pass k writes buf[k & 1]
-    uint32_t* counts;       // d x ctas x 2^bits
+    uint32_t* counts;       // d x ctas x bins
     int passes, bits;
     int bins;               // digits: 2^bits, or one more than the most rows in a single pass
     int64_t per_cta;
@@ -236,11 +236,14 @@ SortPlan plan_sort(const IndexArgs& x, int entry_bytes) {
     p.passes = (int)cdiv(bits, kMaxDigit);
     p.bits = (int)cdiv(bits, p.passes);
     p.bins = p.passes == 1 ? (int)most + 1 : 1 << p.bits;
-    // as many CTAs as are resident at once; tiles of 4096 tokens if one each is enough
-    // (524288 tokens in two passes: 24 us, against 33 us in tiles of 8192), else of 8192
+    // At most as many CTAs as are resident at once.  Tiles of 1024, 4096 or 8192 tokens: small
+    // ones for the shortest way through a pass, until adding up the CTAs' counts takes longer
+    // (20000 tokens in two passes: 19 us in tiles of 1024, 26 us in tiles of 4096; 524288: 29
+    // us in tiles of 4096, 33 us in tiles of 8192).
     const int64_t n = x.n > 0 ? x.n : 1;
     const int64_t most_ctas = kSms / x.d;
-    p.items = n <= most_ctas * kSortThreads * 4 ? 4 : 8;
+    const int64_t few = most_ctas < 64 ? most_ctas : 64;
+    p.items = n <= few * kSortThreads ? 1 : n <= most_ctas * kSortThreads * 4 ? 4 : 8;
     const int64_t tile = kSortThreads * p.items;
     p.per_cta = cdiv(cdiv(n, most_ctas), tile) * tile;
     p.ctas = (int)cdiv(n, p.per_cta);
@@ -270,21 +273,26 @@ SortArgs sort_args(const IndexArgs& index, const SortPlan& p, void* ws, bool wid
     return a;
 }
 
+template <int kSortItems>
+cudaError_t launch_sort(SortArgs& a, const SortPlan& p, cudaStream_t s) {
+    constexpr auto kernel = sort_kernel<kSortItems>;
+    cudaError_t e = allow_smem<kernel>();
+    if (e != cudaSuccess) return e;
+    void* args[] = {&a};
+    return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas, a.index.d),
+                                       dim3(kSortThreads), args, sort_smem_bytes(p), s);
+}
+
 }  // namespace
 
 cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, const Tables* tables, const float* g,
                         Sorted& sorted, cudaStream_t s) {
     SortArgs a = sort_args(index, p, ws, tables != nullptr, sorted);
     if (index.n == 0) return cudaSuccess;
-    cudaError_t e = p.items == 4 ? allow_smem<sort_kernel<4>>() : allow_smem<sort_kernel<8>>();
-    if (e != cudaSuccess) return e;
     a.g = g;
     if (tables)
         for (int m = 0; m < index.d; ++m) a.tables[m] = tables[m];
-    void* args[] = {&a};
-    const void* kernel = p.items == 4 ? reinterpret_cast<const void*>(sort_kernel<4>)
-                                      : reinterpret_cast<const void*>(sort_kernel<8>);
-    return cudaLaunchCooperativeKernel(kernel, dim3(p.ctas, index.d), dim3(kSortThreads), args, sort_smem_bytes(p), s);
+    return p.items == 1 ? launch_sort<1>(a, p, s) : p.items == 4 ? launch_sort<4>(a, p, s) : launch_sort<8>(a, p, s);
 }
 
 cudaError_t sort_and_fill(const IndexArgs& index, const SortPlan& p, void* ws, void* out, int64_t bytes,
