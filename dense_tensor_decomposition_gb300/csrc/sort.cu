@@ -199,7 +199,6 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
 
 template <int kSortItems>
 __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const __grid_constant__ SortArgs a) {
-    allow_next();
     sort_column<kSortItems>(a, blockIdx.y, blockIdx.x, gridDim.x, [] { cg::this_grid().sync(); });
 }
 
