@@ -65,7 +65,10 @@ __device__ __forceinline__ void stage(const StageArgs& a, const Tables& t, int64
             float4 v[kAhead];
             uint32_t rest[kAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) rest[u] = min(r0 + u * kGroups, rows - 1);
+            for (int u = 0; u < kAhead; ++u) {
+                rest[u] = min(r0 + u * kGroups, rows - 1);
+                v[u] = make_float4(1.f, 1.f, 1.f, 1.f);
+            }
             for (int k = group.modes - 1; k >= 0; --k) {
                 const int mode = group.mode[k];
                 const uint32_t size = (uint32_t)a.index.rows[mode], inverse = a.inverse[mode];
@@ -78,7 +81,7 @@ __device__ __forceinline__ void stage(const StageArgs& a, const Tables& t, int64
                     rest[u] = q;
                 }
 #pragma unroll
-                for (int u = 0; u < kAhead; ++u) v[u] = k == group.modes - 1 ? x[u] : times(v[u], x[u]);
+                for (int u = 0; u < kAhead; ++u) v[u] = times(v[u], x[u]);
             }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
@@ -89,14 +92,25 @@ __device__ __forceinline__ void stage(const StageArgs& a, const Tables& t, int64
     }
 }
 
-// product of a sample's rows in G tables, as 16-bit numbers in lo and hi, at four columns
-template <int CS, int G>
-__device__ __forceinline__ float4 product(const float* tab, uint32_t lo, uint32_t hi) {
-    auto row = [&](uint32_t r) { return *reinterpret_cast<const float4*>(tab + r * CS); };
-    float4 p = row(lo & 0xFFFFu);
-    if constexpr (G > 1) p = times(p, row(lo >> 16));
-    if constexpr (G > 2) p = times(p, row(hi & 0xFFFFu));
-    if constexpr (G > 3) p = times(p, row(hi >> 16));
+// a sample's rows in G tables, as 16-bit numbers
+template <int G>
+struct alignas(G > kFewGroups ? 16 : 8) Rows {
+    static constexpr int kWords = G > kFewGroups ? kMaxGroups / 2 : kFewGroups / 2;
+    uint32_t w[kWords];
+    __device__ __forceinline__ uint32_t row(int k) const { return k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu; }
+};
+
+// the product of the rows at VEC columns from tab on
+template <int CS, int VEC, int G>
+__device__ __forceinline__ Pack<float, VEC> product(const float* tab, const Rows<G>& r) {
+    using P = Pack<float, VEC>;
+    P p = *reinterpret_cast<const P*>(tab + r.row(0) * CS);
+#pragma unroll
+    for (int k = 1; k < G; ++k) {
+        const P x = *reinterpret_cast<const P*>(tab + r.row(k) * CS);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) p.v[e] *= x.v[e];
+    }
     return p;
 }
 
@@ -133,7 +147,8 @@ __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant
 // samples' table rows stand behind the tables, worked out once.  A warp takes 32 samples
 // at a time: L = CS / 4 lanes form the products of L samples, one after the other, and
 // add them up so that every lane ends with its own sample's sum.
-constexpr int kSampleBytes = 32 * sizeof(uint2) + sizeof(uint32_t);     // of shared memory for 32 samples
+// bytes of shared memory for 32 samples
+constexpr int sample_bytes(int groups) { return 32 * (groups > kFewGroups ? sizeof(Rows<kMaxGroups>) : sizeof(Rows<1>)) + 4; }
 
 template <int CS, int G>
 __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const __grid_constant__ EntriesArgs a,
@@ -143,7 +158,7 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
     extern __shared__ float4 stage_smem[];
     constexpr int L = CS / 4;
     float* tab = reinterpret_cast<float*>(stage_smem);
-    uint2* rows = reinterpret_cast<uint2*>(tab + (size_t)tables.rows * CS);     // 4 numbers of 16 bits a sample
+    Rows<G>* rows = reinterpret_cast<Rows<G>*>(tab + (size_t)tables.rows * CS);
     uint32_t* parts = reinterpret_cast<uint32_t*>(rows + share);                // a bit a sample: it takes part
     after_previous();
     const int lane = threadIdx.x & 31;
@@ -151,15 +166,11 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
     const int count = (int)(t0 + share < a.index.n ? share : a.index.n - t0);
     // samples that take no part, and those behind the last one of a warp's 32, read row 0
     for (int i = threadIdx.x; i < (count + 31) / 32 * 32; i += kStageThreads) {
-        uint2 r = make_uint2(0u, 0u);
+        Rows<G> r = {};
         const bool inside = i < count && sort_key(a.index, t0 + i, 0) != kNone;
         if (inside) {
 #pragma unroll
-            for (int k = 0; k < G; ++k) {
-                const uint32_t row = table_row(a.index, tables.group[k], t0 + i) << (k & 1) * 16;
-                if (k < 2) r.x |= row;
-                else r.y |= row;
-            }
+            for (int k = 0; k < G; ++k) r.w[k / 2] |= table_row(a.index, tables.group[k], t0 + i) << (k & 1) * 16;
         }
         rows[i] = r;
         const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, inside);
@@ -174,9 +185,8 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
             float acc[L];
 #pragma unroll
             for (int k = 0; k < L; ++k) {
-                const uint2 r = rows[base + (lane & ~(L - 1)) + k];
-                const float4 p = product<CS, G>(mine, r.x, r.y);
-                acc[k] = (p.x + p.y) + (p.z + p.w);
+                const Pack<float, 4> p = product<CS, 4, G>(mine, rows[base + (lane & ~(L - 1)) + k]);
+                acc[k] = (p.v[0] + p.v[1]) + (p.v[2] + p.v[3]);
             }
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) {
@@ -254,6 +264,31 @@ struct StagedOf {
     const float* tab;       // at the lane's columns
 };
 
+template <int G>
+struct Entry {
+    uint32_t x;                 // the row
+    float g;
+    Rows<G> rows;
+};
+
+// entry p of a list of entries of 16 or 32 bytes
+template <int G>
+__device__ __forceinline__ Entry<G> entry_at(const char* list, int64_t p) {
+    constexpr int kBytes = G > kFewGroups ? 32 : 16;
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(list + p * kBytes));
+    Entry<G> e;
+    e.x = a.x;
+    e.g = __uint_as_float(a.y);
+    e.rows.w[0] = a.z;
+    e.rows.w[1] = a.w;
+    if constexpr (G > kFewGroups) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(list + p * kBytes + 16));
+        e.rows.w[2] = b.x;
+        e.rows.w[3] = b.y;
+    }
+    return e;
+}
+
 template <int CS, int VEC, int G>
 struct Staged {
     template <typename List>
@@ -265,7 +300,7 @@ struct Staged {
         const int p0, p1;
         const uint32_t lanes;       // of the group
         int at;                     // which of the held entries is token p of load(p)
-        uint4 held, next;
+        Entry<G> held, next;
         __device__ __forceinline__ Terms(const StagedOf& of, const List& list, int p0, int p1, int64_t)
             : of(of), list(list), p0(p0), p1(p1),
               lanes((0xFFFFFFFFu >> (32 - L)) << (threadIdx.x & 31 & ~(L - 1))), at(0) {
@@ -282,24 +317,15 @@ struct Staged {
                 fetch(p + L);
             }
         }
-        __device__ __forceinline__ uint32_t from(uint32_t x, int j) const { return __shfl_sync(lanes, x, at + j, L); }
-        __device__ __forceinline__ uint32_t key(int j) const { return from(held.x, j); }
+        __device__ __forceinline__ uint32_t key(int j) const { return __shfl_sync(lanes, held.x, at + j, L); }
         __device__ __forceinline__ void add(int j, float* acc) const {
-            const float g = __uint_as_float(from(held.y, j));
-            const uint32_t lo = from(held.z, j), hi = G > 2 ? from(held.w, j) : 0u;
-            if constexpr (VEC == 4) {
-                const float4 p = product<CS, G>(of.tab, lo, hi);
-                acc[0] = fmaf(g, p.x, acc[0]);
-                acc[1] = fmaf(g, p.y, acc[1]);
-                acc[2] = fmaf(g, p.z, acc[2]);
-                acc[3] = fmaf(g, p.w, acc[3]);
-            } else {
-                float p = of.tab[(lo & 0xFFFFu) * CS];
-                if constexpr (G > 1) p *= of.tab[(lo >> 16) * CS];
-                if constexpr (G > 2) p *= of.tab[(hi & 0xFFFFu) * CS];
-                if constexpr (G > 3) p *= of.tab[(hi >> 16) * CS];
-                acc[0] = fmaf(g, p, acc[0]);
-            }
+            const float g = __shfl_sync(lanes, held.g, at + j, L);
+            Rows<G> r;
+#pragma unroll
+            for (int w = 0; w < (G + 1) / 2; ++w) r.w[w] = __shfl_sync(lanes, held.rows.w[w], at + j, L);
+            const Pack<float, VEC> p = product<CS, VEC, G>(of.tab, r);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[e] = fmaf(g, p.v[e], acc[e]);
         }
     };
 };
@@ -312,7 +338,7 @@ struct StagedArgs {
 
 // A CTA (blockIdx.x) has a slice of CS columns and s.tile sorted samples of one mode
 // (blockIdx.y); those behind the slices' and tiles' write zeros, 32 rows a warp.
-template <int CS, int VEC>
+template <int CS, int VEC, bool kMany>
 __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __grid_constant__ StagedArgs a) {
     extern __shared__ float4 stage_smem[];
     constexpr int L = CS / VEC, kLog2L = L == 32 ? 5 : L == 16 ? 4 : L == 8 ? 3 : L == 4 ? 2 : 1;
@@ -332,14 +358,13 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
         zero_unsorted_rows<float, VEC>(s.a, m, warp * 32, [&](int64_t p) { return key_at(s, m, p); });
         return;
     }
-    const uint4* sorted = reinterpret_cast<const uint4*>(s.sorted.entries) + m * n;
     const int64_t p0 = tile * s.tile, p1 = p0 + s.tile < n ? p0 + s.tile : n;
     // entries that take part come first: find the end in two steps of 1024 probes
     int64_t lo = p0, hi = p1;
     while (lo < hi) {
         const int64_t step = cdiv(hi - lo, kStageThreads);
         const int64_t p = lo + (int64_t)threadIdx.x * step;
-        const int have = __syncthreads_count(p < hi && sorted[p].x != kNone);
+        const int have = __syncthreads_count(p < hi && key_at(s, m, p) != kNone);
         if (have == 0) hi = lo;
         else {
             const int64_t end = lo + have * step;
@@ -350,24 +375,30 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     const int count = (int)(lo - p0);
     __syncthreads();
     if (count == 0) return;
-    const uint4* list = sorted + p0;
+    const char* list = s.sorted.entries + (m * n + p0) * s.sorted.bytes;
     float* part = s.part + ((int64_t)m * s.tiles + tile) * 2 * s.a.width;
     Around around;
-    around.before = p0 > 0 && list[-1].x == list[0].x;
-    around.after = p0 + count < n && list[count].x == list[count - 1].x;
+    around.before = p0 > 0 && key_at(s, m, p0 - 1) == key_at(s, m, p0);
+    around.after = p0 + count < n && key_at(s, m, p0 + count) == key_at(s, m, p0 + count - 1);
     around.head = part;
     around.tail = part + s.a.width;
     const StagedOf of{tab + (threadIdx.x & (L - 1)) * VEC};
     auto sum = [&](auto g) {
-        sum_list<float, VEC, Staged<CS, VEC, decltype(g)::value>::template Terms, kStageThreads>(
-            s.a, m, of, [&](int p) { return __ldg(list + p); }, [](uint32_t v) { return v; }, count, kLog2L, col0,
+        constexpr int G = decltype(g)::value;
+        sum_list<float, VEC, Staged<CS, VEC, G>::template Terms, kStageThreads>(
+            s.a, m, of, [&](int p) { return entry_at<G>(list, p); }, [](uint32_t v) { return v; }, count, kLog2L, col0,
             heads, around, [] { __syncthreads(); });
     };
-    switch (a.tables[m].groups) {
-        case 1: sum(std::integral_constant<int, 1>()); break;
-        case 2: sum(std::integral_constant<int, 2>()); break;
-        case 3: sum(std::integral_constant<int, 3>()); break;
-        default: sum(std::integral_constant<int, 4>()); break;
+    const int groups = a.tables[m].groups;
+    if constexpr (kMany) {
+        if (groups == 7) sum(std::integral_constant<int, 7>());
+        else if (groups == 6) sum(std::integral_constant<int, 6>());
+        else sum(std::integral_constant<int, 5>());
+    } else {
+        if (groups == 1) sum(std::integral_constant<int, 1>());
+        else if (groups == 2) sum(std::integral_constant<int, 2>());
+        else if (groups == 3) sum(std::integral_constant<int, 3>());
+        else sum(std::integral_constant<int, 4>());
     }
 }
 
@@ -385,9 +416,10 @@ constexpr double kStageStart = 3000.0, kStageRow = 3.0;
 double gather_cost(int cs) { return cs == 32 ? kGather32 : cs == 16 ? kGather16 : kGather8; }
 
 // The tables with the least work for `samples` samples an SM among the ways to split
-// the d modes but `skip` into consecutive groups; returns that work (a negative number
-// where no way fits max_rows rows and kMaxGroups groups).
-double plan_tables(const IndexArgs& x, int skip, int cs, int64_t max_rows, double samples, Tables& best) {
+// the d modes but `skip` into at most max_groups consecutive groups; returns that work (a
+// negative number where no way fits max_rows rows).
+double plan_tables(const IndexArgs& x, int skip, int cs, int64_t max_rows, int max_groups, double samples,
+                   Tables& best) {
     int mode[MTTKRP_MAX_ORDER], modes = 0;
     for (int m = 0; m < x.d; ++m)
         if (m != skip) mode[modes++] = m;
@@ -399,7 +431,7 @@ double plan_tables(const IndexArgs& x, int skip, int cs, int64_t max_rows, doubl
         double work = kStageStart;
         bool fits = true;
         for (int k = 0; k < modes && fits;) {
-            if (t.groups == kMaxGroups) {
+            if (t.groups == max_groups) {
                 fits = false;
                 break;
             }
@@ -466,7 +498,7 @@ cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share,
     constexpr auto kernel = entries_staged_kernel<CS, G>;
     cudaError_t e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
-    const size_t smem = sizeof(float) * t.rows * CS + kSampleBytes * share / 32;
+    const size_t smem = sizeof(float) * t.rows * CS + sample_bytes(G) * share / 32;
     return launch_early(kernel, (unsigned)cdiv(a.index.n, share), kStageThreads, smem, s, a,
                         stage_args(a.index, a.factor, a.type, a.width), t, (int)share);
 }
@@ -477,7 +509,11 @@ cudaError_t entries_staged(const EntriesArgs& a, const Tables& t, int64_t share,
         case 1: return entries_staged<CS, 1>(a, t, share, s);
         case 2: return entries_staged<CS, 2>(a, t, share, s);
         case 3: return entries_staged<CS, 3>(a, t, share, s);
-        default: return entries_staged<CS, 4>(a, t, share, s);
+        case 4: return entries_staged<CS, 4>(a, t, share, s);
+        case 5: return entries_staged<CS, 5>(a, t, share, s);
+        case 6: return entries_staged<CS, 6>(a, t, share, s);
+        case 7: return entries_staged<CS, 7>(a, t, share, s);
+        default: return entries_staged<CS, 8>(a, t, share, s);
     }
 }
 
@@ -491,19 +527,39 @@ cudaError_t grad_cached(const RowSumArgs& a, cudaStream_t s) {
     return sums_by<float, 1, Model<T, 1>::template Terms, 0, Model<T, 1>::template Terms, 0>(a, s);
 }
 
-template <int CS, int VEC>
-cudaError_t grad_staged(StagedArgs& a, const SortPlan& p, cudaStream_t st) {
+template <int CS, int VEC, bool kMany>
+cudaError_t grad_staged(StagedArgs& a, cudaStream_t st) {
     const RowSumArgs& r = a.s.a;
+    const SortPlan p = plan_sort(r.index, kMany ? 32 : 16);
+    a.s.part = reinterpret_cast<float*>(static_cast<char*>(r.ws) + p.total());
     int rows = 0;
     for (int m = 0; m < r.index.d; ++m) rows = a.tables[m].rows > rows ? a.tables[m].rows : rows;
-    cudaError_t e = allow_smem<staged_sum_kernel<CS, VEC>>();
+    constexpr auto kernel = staged_sum_kernel<CS, VEC, kMany>;
+    cudaError_t e = allow_smem<kernel>();
     if (e == cudaSuccess) e = sort_tokens(r.index, p, r.ws, a.tables, r.g, a.s.sorted, st);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(cdiv(r.width, CS) * a.s.tiles + cdiv(most_rows(r.index), kStageThreads)), r.index.d);
     const size_t smem = sizeof(float) * (kStageThreads * VEC + (size_t)rows * CS);
-    e = launch_early(staged_sum_kernel<CS, VEC>, grid, kStageThreads, smem, st, a);
+    e = launch_early(kernel, grid, kStageThreads, smem, st, a);
     if (e != cudaSuccess) return e;
     return join<float, VEC>(a.s, st);
+}
+
+// vec: 4 where results are written in vectors, else 1
+template <int CS>
+cudaError_t grad_staged(StagedArgs& a, int vec, cudaStream_t st) {
+    bool many = false;
+    for (int m = 0; m < a.s.a.index.d; ++m) many = many || a.tables[m].groups > kFewGroups;
+    if (!many) return vec == 4 ? grad_staged<CS, 4, false>(a, st) : grad_staged<CS, 1, false>(a, st);
+    // every mode gets more than kFewGroups groups: those that lack some, tables of a row of ones
+    for (int m = 0; m < a.s.a.index.d; ++m) {
+        Tables& t = a.tables[m];
+        while (t.groups <= kFewGroups) {
+            t.group[t.groups].modes = 0;
+            t.group[t.groups++].first = t.rows++;
+        }
+    }
+    return vec == 4 ? grad_staged<CS, 4, true>(a, st) : grad_staged<CS, 1, true>(a, st);
 }
 
 }  // namespace
@@ -516,18 +572,21 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
     int64_t share = 0;
     Tables tables;
     for (int c = 32; c >= 8; c /= 2) {
-        // as few rounds of CTAs over the SMs as leave two thirds of the shared memory to the tables
-        constexpr int64_t kMost = kMaxSmem / 3 / sizeof(uint2);
-        const int64_t rounds = cdiv(n, kSms * kMost);
-        const int64_t part = cdiv(cdiv(n, kSms * rounds), 32) * 32;
-        Tables t;
-        const double slice = plan_tables(a.index, -1, c, table_rows(kSampleBytes * part / 32, c), (double)part, t);
-        const double work = slice * cdiv(a.width, c) * rounds;
-        if (slice >= 0.0 && work < least) {
-            least = work;
-            tables = t;
-            share = part;
-            cs = c;
+        for (int groups : {kFewGroups, kMaxGroups}) {
+            // as few rounds of CTAs over the SMs as leave two thirds of the shared memory to the tables
+            const int64_t most = kMaxSmem / 3 / sample_bytes(groups) * 32;
+            const int64_t rounds = cdiv(n, kSms * most);
+            const int64_t part = cdiv(cdiv(n, kSms * rounds), 32) * 32;
+            Tables t;
+            const double slice = plan_tables(a.index, -1, c, table_rows(sample_bytes(groups) * part / 32, c), groups,
+                                             (double)part, t);
+            const double work = slice * cdiv(a.width, c) * rounds;
+            if (slice >= 0.0 && work < least) {
+                least = work;
+                tables = t;
+                share = part;
+                cs = c;
+            }
         }
     }
     if (cs == 32) return entries_staged<32>(a, tables, share, s);
@@ -538,10 +597,10 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
     return entries_cached<__half>(a, s);
 }
 
-// for the larger entries that the sums from shared memory sort
+// for the largest entries that the sums from shared memory can sort
 size_t entries_grad_workspace_bytes(const IndexArgs& index, int64_t width) {
     if (always_owned(index, width)) return 0;
-    return plan_sort(index, sizeof(uint4)).total() + part_bytes(index, width);
+    return plan_sort(index, index.d - 1 > kFewGroups ? 32 : 16).total() + part_bytes(index, width);
 }
 
 cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
@@ -561,8 +620,8 @@ cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
         double work = 0.0;
         Tables t[MTTKRP_MAX_ORDER];
         for (int m = 0; m < d && work >= 0.0; ++m) {
-            const double slice = plan_tables(a.index, m, c, table_rows(sizeof(float) * kStageThreads * vec, c),
-                                             (double)n / tiles, t[m]);
+            const double slice = plan_tables(a.index, m, c, table_rows(sizeof(float) * kStageThreads * vec, c) - kMaxGroups,
+                                             kMaxGroups, (double)n / tiles, t[m]);
             work = slice < 0.0 ? -1.0 : (slice > work ? slice : work);
         }
         if (work >= 0.0 && work * waves < least) {
@@ -574,13 +633,11 @@ cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
         }
     }
     if (cs != 0) {
-        const SortPlan p = plan_sort(a.index, sizeof(uint4));
         st.s.a = a;
-        st.s.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.total());
         st.stage = stage_args(a.index, a.factor, a.type, a.width);
-        if (cs == 32) return quads ? grad_staged<32, 4>(st, p, s) : grad_staged<32, 1>(st, p, s);
-        if (cs == 16) return quads ? grad_staged<16, 4>(st, p, s) : grad_staged<16, 1>(st, p, s);
-        return quads ? grad_staged<8, 4>(st, p, s) : grad_staged<8, 1>(st, p, s);
+        if (cs == 32) return grad_staged<32>(st, vec, s);
+        if (cs == 16) return grad_staged<16>(st, vec, s);
+        return grad_staged<8>(st, vec, s);
     }
     if (a.type == MTTKRP_F32) return grad_cached<float>(a, s);
     if (a.type == MTTKRP_BF16) return grad_cached<__nv_bfloat16>(a, s);

@@ -26,22 +26,23 @@ struct SortArgs {
     int passes, bits;
     int bins;               // digits: 2^bits, or one more than the most rows in a single pass
     int64_t per_cta;
-    uint4* entries;         // the last pass's output as entries of 16 bytes, or nullptr
+    char* entries;          // the last pass's output as entries of `entry_bytes` bytes, or nullptr
+    int entry_bytes;
     const float* g;
     Tables tables[MTTKRP_MAX_ORDER];
 };
 
-// the entry of 16 bytes for a token of column m
-__device__ __noinline__ uint4 entry_of(const SortArgs& a, uint2 kt, int m) {
-    uint4 e = make_uint4(kt.x, 0u, 0u, 0u);
-    if (kt.x == kNone) return e;
-    e.y = __float_as_uint(a.g[kt.y]);
-    for (int k = 0; k < a.tables[m].groups; ++k) {
-        const uint32_t row = table_row(a.index, a.tables[m].group[k], kt.y) << (k & 1) * 16;
-        if (k < 2) e.z |= row;
-        else e.w |= row;
+// writes the entry of 16 or 32 bytes for a token of column m
+__device__ __noinline__ void write_entry(const SortArgs& a, uint2 kt, int m, char* to) {
+    uint32_t g = 0, rows[kMaxGroups / 2] = {};
+    if (kt.x != kNone) {
+        g = __float_as_uint(a.g[kt.y]);
+#pragma unroll
+        for (int k = 0; k < kMaxGroups; ++k)
+            if (k < a.tables[m].groups) rows[k / 2] |= table_row(a.index, a.tables[m].group[k], kt.y) << (k & 1) * 16;
     }
-    return e;
+    *reinterpret_cast<uint4*>(to) = make_uint4(kt.x, g, rows[0], rows[1]);
+    if (a.entry_bytes > 16) *reinterpret_cast<uint2*>(to + 16) = make_uint2(rows[2], rows[3]);
 }
 
 // lanes of the warp with this lane's digit, which has at most kMaxDigit bits or is kNone
@@ -189,7 +190,7 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
                 }
                 if (where == kNone) continue;
                 const uint32_t to = wh[where & 0xFFFFu] + (where >> 16);
-                if (last && a.entries) a.entries[m * n + to] = entry_of(a, x, m);
+                if (last && a.entries) write_entry(a, x, m, a.entries + (m * n + to) * a.entry_bytes);
                 else __stcg(dst + to, x);
             }
         }
@@ -246,6 +247,7 @@ SortPlan plan_sort(const IndexArgs& x, int entry_bytes) {
     const int64_t tile = kSortThreads * p.items;
     p.per_cta = cdiv(cdiv(n, most_ctas), tile) * tile;
     p.ctas = (int)cdiv(n, p.per_cta);
+    p.entry_bytes = entry_bytes;
     p.pairs = align256((size_t)entry_bytes * x.d * x.n);
     p.counts = align256(sizeof(uint32_t) * x.d * (p.ctas > kFillCluster ? p.ctas : kFillCluster) * p.bins);
     return p;
@@ -256,7 +258,7 @@ namespace {
 size_t sort_smem_bytes(const SortPlan& p) { return sizeof(uint32_t) * ((kSortWarps + 1) * p.bins + 2 * kSortThreads); }
 
 // buffers in the workspace; the last pass's output is what `sorted` tells
-SortArgs sort_args(const IndexArgs& index, const SortPlan& p, void* ws, bool wide, Sorted& sorted) {
+SortArgs sort_args(const IndexArgs& index, const SortPlan& p, void* ws, bool tables, Sorted& sorted) {
     SortArgs a;
     a.index = index;
     for (int k = 0; k < 2; ++k) a.buf[k] = reinterpret_cast<uint2*>(static_cast<char*>(ws) + k * p.pairs);
@@ -265,10 +267,11 @@ SortArgs sort_args(const IndexArgs& index, const SortPlan& p, void* ws, bool wid
     a.bits = p.bits;
     a.bins = p.bins;
     a.per_cta = p.per_cta;
-    a.entries = wide ? reinterpret_cast<uint4*>(a.buf[(p.passes - 1) & 1]) : nullptr;
+    a.entries = tables ? reinterpret_cast<char*>(a.buf[(p.passes - 1) & 1]) : nullptr;
+    a.entry_bytes = p.entry_bytes;
     a.g = nullptr;
     sorted.entries = static_cast<char*>(ws) + ((p.passes - 1) & 1) * p.pairs;
-    sorted.bytes = wide ? sizeof(uint4) : sizeof(uint2);
+    sorted.bytes = p.entry_bytes;
     return a;
 }
 

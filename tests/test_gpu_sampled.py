@@ -191,7 +191,10 @@ MODELS = [  # dims, R, samples
     # not at all, as tables of single modes and of products, ranks that end inside a slice
     ((20,) * 5 + (21,), 128, 40001), ((512, 512, 513), 96, 50000), ((40, 50, 60), 257, 30000),
     ((1000, 900, 800), 48, 33000), ((2000, 1500, 1900), 20, 33001), ((3,) * 8, 36, 20003), ((30, 17), 1, 17000),
-    ((100003, 9, 4), 24, 40000), ((9,), 33, 25000), ((5, 1, 1, 1, 1, 1, 1), 12, 18000), ((250, 250), 1000, 17001)]
+    ((100003, 9, 4), 24, 40000), ((9,), 33, 25000), ((5, 1, 1, 1, 1, 1, 1), 12, 18000), ((250, 250), 1000, 17001),
+    # five to eight tables a sample, the same number for every mode and not
+    ((48,) * 6, 40, 20000), ((41,) * 8, 17, 17003), ((200, 3, 150, 70, 2, 90, 5), 36, 24001),
+    ((700, 900, 600, 30, 30, 20, 40), 8, 30000), ((45,) * 5, 64, 18000)]
 
 
 def coords_of(gen, dims, S, dtype=torch.int32, masked=0.05):
