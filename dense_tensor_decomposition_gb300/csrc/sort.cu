@@ -45,13 +45,13 @@ __device__ __noinline__ void write_entry(const SortArgs& a, uint2 kt, int m, cha
     if (a.entry_bytes > 16) *reinterpret_cast<uint2*>(to + 16) = make_uint2(rows[2], rows[3]);
 }
 
-// lanes of the warp with this lane's digit, which has at most kMaxDigit bits or is kNone
-__device__ __forceinline__ uint32_t same_digit(uint32_t digit) {
+// lanes of the warp with this lane's digit, which has at most `bits` bits or is kNone
+__device__ __forceinline__ uint32_t same_digit(uint32_t digit, int bits) {
     uint32_t peers = __ballot_sync(0xFFFFFFFFu, digit != kNone);
-#pragma unroll
-    for (int b = 0; b < kMaxDigit; ++b) {
-        const uint32_t ones = __ballot_sync(0xFFFFFFFFu, (digit >> b & 1u) != 0);
-        peers &= (digit >> b & 1u) != 0 ? ones : ~ones;
+    for (int b = 0; b < bits; b += 2) {
+        const bool one = (digit >> b & 1u) != 0, two = (digit >> b & 2u) != 0;
+        const uint32_t ones = __ballot_sync(0xFFFFFFFFu, one), twos = __ballot_sync(0xFFFFFFFFu, two);
+        peers &= (one ? ones : ~ones) & (two ? twos : ~twos);
     }
     return peers;
 }
@@ -72,10 +72,11 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
     const int64_t t1 = t0 + a.per_cta < n ? t0 + a.per_cta : n;
     uint32_t* wh = whist + warp * nb;
 
+    const bool one_tile = t0 + kSortTile >= t1;
     // a warp has kSortItems * 32 consecutive tokens of a tile
     uint2 kt[kSortItems];
     uint32_t place[kSortItems];     // digit, and << 16 how many of the warp's tokens with it come first; kNone: no token
-    auto rank_tile = [&](int pass, int64_t tile) {
+    auto load_tile = [&](int pass, int64_t tile) {
         const uint2* src = a.buf[(pass + 1) & 1] + m * n;
         const int64_t w0 = tile + warp * (kSortItems * 32) + lane;
         if (pass == 0) {
@@ -98,12 +99,14 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
             if (w0 + i * 32 < t1)
                 place[i] = a.passes == 1 ? min(kt[i].x, (uint32_t)nb - 1) : (kt[i].x >> pass * a.bits) & (nb - 1);
         }
+    };
+    auto rank_tile = [&]() {
         __syncthreads();            // what stood in whist has been read
         for (int i = tid; i < kSortWarps * nb; i += kSortThreads) whist[i] = 0;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kSortItems; ++i) {
-            const uint32_t digit = place[i], peers = same_digit(digit);
+            const uint32_t digit = place[i], peers = same_digit(digit, a.bits);
             const uint32_t rank = __popc(peers & ((1u << lane) - 1));
             if (digit != kNone) place[i] = digit | (wh[digit] + rank) << 16;
             __syncwarp();
@@ -114,18 +117,25 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
     };
 
     for (int pass = 0; pass < a.passes; ++pass) {
-        for (int b = tid; b < nb; b += kSortThreads) first[b] = 0;
-        int64_t tile = t0;
-        for (;;) {
-            rank_tile(pass, tile);
+        if (one_tile) {
+            load_tile(pass, t0);
+            rank_tile();
             for (int b = tid; b < nb; b += kSortThreads) {
                 uint32_t c = 0;
 #pragma unroll 8
                 for (int w = 0; w < kSortWarps; ++w) c += whist[w * nb + b];
-                first[b] += c;
+                first[b] = c;
             }
-            if (tile + kSortTile >= t1) break;
-            tile += kSortTile;
+        } else {
+            for (int b = tid; b < nb; b += kSortThreads) first[b] = 0;
+            __syncthreads();
+            for (int64_t tile = t0; tile < t1; tile += kSortTile) {
+                load_tile(pass, tile);
+#pragma unroll
+                for (int i = 0; i < kSortItems; ++i)
+                    if (place[i] != kNone) atomicAdd(first + place[i], 1u);
+            }
+            __syncthreads();
         }
         uint32_t* counts = a.counts + (int64_t)m * ctas * nb;
         for (int b = tid; b < nb; b += kSortThreads) __stcg(counts + cta * nb + b, first[b]);
@@ -160,7 +170,10 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
         uint2* dst = a.buf[pass & 1] + m * n;
         const bool last = pass == a.passes - 1;
         for (int64_t at = t0; at < t1; at += kSortTile) {
-            if (tile != t0) rank_tile(pass, at);    // more than one: the tile is no longer in the registers
+            if (!one_tile) {
+                load_tile(pass, at);
+                rank_tile();
+            }
             __syncthreads();
             for (int b = tid; b < nb; b += kSortThreads) {
                 uint32_t next = first[b];
