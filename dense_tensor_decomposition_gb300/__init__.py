@@ -563,7 +563,8 @@ _sampled = None             # the module that checks, allocates and calls for th
 _type_codes: dict = {}      # torch dtype -> MTTKRP_F32, MTTKRP_BF16 or MTTKRP_F16
 
 
-def _load_binding():
+def load_binding():
+    """Load the binding module (raises if it has not been built for this PyTorch)."""
     global _sampled
     if _sampled is None:
         import torch
@@ -588,7 +589,7 @@ def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
     or int64 indices of any shape (contiguous, or one-dimensional with any stride).
     An index outside the table, e.g. a negative mask, gives a row of zeros.  Returns
     idx.shape + (width,) of the table's type, written into `out` when given."""
-    r = (_sampled or _load_binding()).embedding(table, idx, scale, out, _handle(stream))
+    r = (_sampled or load_binding()).embedding(table, idx, scale, out, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_embedding")
     return r if out is None else out
@@ -601,7 +602,7 @@ def embedding_grad(idx, grad, rows: int, scale: float = 1.0, out=None, dtype=Non
     fixed order.  grad: idx.shape + (width,).  Returns rows x width of `dtype`
     (float32 by default, or grad's type), written into `out` when given;
     accumulate adds to `out` and leaves the rows that no token points to alone."""
-    module = _sampled or _load_binding()
+    module = _sampled or load_binding()
     code = -1 if dtype is None else _type_codes.get(dtype)
     if code is None:
         raise TypeError("dtype must be float32, bfloat16 or float16")
@@ -617,7 +618,7 @@ def cp_entries(factors, coords, out=None, stream=None):
     float16), coords samples x d (int32 or int64).  Returns `samples` float32 values;
     0 where a coordinate is out of range.  Component weights go into a factor, or in
     as a factor with one row."""
-    r = (_sampled or _load_binding()).cp_entries(factors, coords, out, _handle(stream))
+    r = (_sampled or load_binding()).cp_entries(factors, coords, out, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_cp_entries")
     return r if out is None else out
@@ -628,7 +629,7 @@ def cp_entries_grad(factors, coords, grad, outs=None, stream=None):
     the I_n x R sums over the samples of grad[s] * prod over m != n of A_m(c_m, :),
     float32, in a fixed order.  grad: one float32 value a sample.  Returns the list
     of gradients (written into `outs` when given)."""
-    r = (_sampled or _load_binding()).cp_entries_grad(factors, coords, grad, outs, _handle(stream))
+    r = (_sampled or load_binding()).cp_entries_grad(factors, coords, grad, outs, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_cp_entries_grad")
     return r
@@ -638,7 +639,7 @@ def grad_norm(tensors, stream=None):
     """sqrt of the sum of squares over all elements of a list of CUDA tensors
     (mttkrp_grad_norm), as a float32 scalar on the device.  The tensors are
     contiguous, float32, bfloat16 or float16 in any mix, on one device."""
-    r = (_sampled or _load_binding()).clip_grad_norm(tensors, None, 0.0, None, _handle(stream))
+    r = (_sampled or load_binding()).clip_grad_norm(tensors, None, 0.0, None, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_grad_norm")
     return r
@@ -649,7 +650,7 @@ def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, strea
     being `grad_norm` of the list (mttkrp_clip_grad_norm), in place or, when `outs` is
     given, into its tensors (each of its input's size and type).  Returns the norm
     before clipping as a float32 scalar on the device."""
-    r = (_sampled or _load_binding()).clip_grad_norm(tensors, float(max_norm), eps, outs, _handle(stream))
+    r = (_sampled or load_binding()).clip_grad_norm(tensors, float(max_norm), eps, outs, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_clip_grad_norm")
     return r

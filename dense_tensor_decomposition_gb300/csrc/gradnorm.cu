@@ -19,6 +19,8 @@
 // The squares of 16 elements are added in fp32, the sums of 16 in pairs of fp32 numbers
 // (the second holds what the first rounds away): fp64 additions would take longer than
 // the reads, at 2 a cycle and SM.
+#include <atomic>
+
 #include "launch.cuh"
 #include "rows.h"
 #include "types.cuh"
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int 
 // blocks of a launch that are resident at once on the current device
 template <int N>
 cudaError_t resident_blocks(int& blocks) {
-    static int cached[64];      // by device; writing the same value twice is harmless
+    static std::atomic<int> cached[64];     // by device; setting it twice is harmless
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

@@ -29,7 +29,9 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size
     config.stream = s;
     config.attrs = &early;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, kernel, static_cast<A&&>(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, static_cast<A&&>(args)...);
+    if (e != cudaSuccess) cudaGetLastError();       // the error is told by this call alone
+    return e;
 }
 
 }  // namespace mk

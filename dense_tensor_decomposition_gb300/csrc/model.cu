@@ -571,7 +571,9 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
     int cs = 0;
     int64_t share = 0;
     Tables tables;
-    for (int c = 32; c >= 8; c /= 2) {
+    // tables cost at least their start
+    const bool small = least < kStageStart * cdiv(a.width, 32);
+    for (int c = 32; c >= 8 && !small; c /= 2) {
         for (int groups : {kFewGroups, kMaxGroups}) {
             // as few rounds of CTAs over the SMs as leave two thirds of the shared memory to the tables
             const int64_t most = kMaxSmem / 3 / sample_bytes(groups) * 32;

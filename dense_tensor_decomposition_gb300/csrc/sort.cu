@@ -294,8 +294,10 @@ cudaError_t launch_sort(SortArgs& a, const SortPlan& p, cudaStream_t s) {
     cudaError_t e = allow_smem<kernel>();
     if (e != cudaSuccess) return e;
     void* args[] = {&a};
-    return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas, a.index.d),
-                                       dim3(kSortThreads), args, sort_smem_bytes(p), s);
+    e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(p.ctas, a.index.d), dim3(kSortThreads),
+                                    args, sort_smem_bytes(p), s);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
 }
 
 }  // namespace
