@@ -47,6 +47,46 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     }
 }
 
+// Narrow rows at any offset: the result as one array, 4 bytes of it a thread and step,
+// whatever rows they are of (read and write 4.8 TB/s in fp32 and 2.6 in 16 bits at every
+// width; by rows, 17 fp32 columns 0.6, 65 2.2, 333 6.9; 17 columns of 16 bits 0.3, 65 1.1,
+// 333 3.9).  The result's rows have no gaps, and it starts at a multiple of 4 bytes.
+constexpr int kFlatSteps = 8;
+constexpr int64_t flat_width(int elem) { return elem == 4 ? 255 : 159; }     // at most
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) lookup_flat_kernel(const __grid_constant__ LookupArgs a, uint32_t inverse) {
+    constexpr int P = 4 / sizeof(T), kSpan = kThreads * kFlatSteps * P;
+    after_previous();
+    const uint32_t width = (uint32_t)a.width;
+    const int64_t total = a.index.n * a.width, base = (int64_t)blockIdx.x * kSpan;
+    const int64_t t0 = base / a.width;
+    const uint32_t rest = (uint32_t)(base - t0 * a.width);
+    Pack<T, P> x[kFlatSteps];
+#pragma unroll
+    for (int u = 0; u < kFlatSteps; ++u) {
+        const uint32_t at = (u * kThreads + threadIdx.x) * P;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            // both are below 2^13, so the quotient is exact: inverse is 2^32 / width rounded up
+            const uint32_t i = rest + at + e, r = width == 1 ? i : __umulhi(i, inverse);
+            const int64_t v = base + at + e < total ? index_at(a.index, t0 + r, 0) : -1;
+            x[u].v[e] = from_f32<T>(0.f);
+            if (v >= 0 && v < a.index.rows[0])
+                x[u].v[e] = static_cast<const T*>(a.table)[v * a.table_stride + (i - r * width)];
+        }
+    }
+    T* out = static_cast<T*>(a.out) + base;
+#pragma unroll
+    for (int u = 0; u < kFlatSteps; ++u) {
+        const uint32_t at = (u * kThreads + threadIdx.x) * P;
+#pragma unroll
+        for (int e = 0; e < P; ++e) x[u].v[e] = from_f32<T>(a.scale * to_f32(x[u].v[e]));
+        if (base + at + P <= total) *reinterpret_cast<Pack<T, P>*>(out + at) = x[u];
+        else if (base + at < total) out[at] = x[u].v[0];
+    }
+}
+
 // lanes for a row of `items` loads: a power of two, at most a warp
 int log2_lanes(int64_t items) {
     int l = 0;
@@ -69,8 +109,13 @@ cudaError_t lookup(const LookupArgs& a, cudaStream_t s) {
     const size_t all = reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.out) |
                        (a.table_stride * e) | (a.out_stride * e) | (a.width * e);
     if (all % 16 == 0) return lookup_by<T, 16 / e, 4, 1>(a, s);
-    if (all % 4 == 0) return lookup_by<T, 4 / e, 8, 2>(a, s);
-    if constexpr (e < 4) return lookup_by<T, 1, 8, 4>(a, s);
+    if (a.width <= flat_width(e) && a.out_stride == a.width && reinterpret_cast<uintptr_t>(a.out) % 4 == 0) {
+        const uint32_t inverse = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
+        const int64_t blocks = cdiv(a.index.n * a.width, (int64_t)kThreads * kFlatSteps * (4 / e));
+        return launch_early(lookup_flat_kernel<T>, (unsigned)blocks, kThreads, 0, s, a, inverse);
+    }
+    if (all % 4 == 0) return e == 4 ? lookup_by<T, 4 / e, 16, 2>(a, s) : lookup_by<T, 4 / e, 16, 1>(a, s);
+    if constexpr (e < 4) return lookup_by<T, 1, 16, 2>(a, s);
     return cudaErrorInvalidValue;
 }
 

@@ -47,7 +47,8 @@ def tokens(gen, n, rows, skew=1.0, masked=0.05, dtype=torch.int64):
 # ---------------------------------------------------------------- lookup
 
 LOOKUPS = [(1, 1, 1), (1, 7, 2000), (2, 5, 3), (31, 40, 8), (33, 512, 64), (257, 100, 1001), (1000, 32, 17),
-           (4099, 3000, 256), (130, 9, 4096), (64, 50, 65536)]
+           (4099, 3000, 256), (130, 9, 4096), (64, 50, 65536),
+           (3001, 70, 5), (700, 90, 159), (701, 90, 161), (333, 20, 255), (555, 30, 257), (90, 8, 2), (5000, 9, 1)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
