@@ -34,12 +34,12 @@ constexpr int kUnroll = 4;                          // 16-byte vectors a thread 
 constexpr int kUnitVecs = kThreads;                 // 8 KB
 constexpr int kMaxBlocks = 2048;                    // most sums a table
 constexpr int64_t kCached = 64 << 20;               // bytes of the first read to find in L2 at the second
-constexpr int kSmallTable = 32, kLargeTable = 1024;
+constexpr int kSmallTable = 32, kMiddleTable = 400, kLargeTable = 1024;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // 29 bytes a tensor: the large table is just below the 32764 bytes that a
-// kernel's arguments can hold, the small one spares short lists its copy.
+// kernel's arguments can hold, the others spare shorter lists its copy.
 template <int N>
 struct Table {
     const void* in[N];
@@ -390,6 +390,8 @@ cudaError_t launch_grad_norm(int n, const void* const* tensors, const int64_t* n
                              cudaStream_t s) {
     if (n <= kSmallTable)
         return norm_and_clip<kSmallTable>(n, tensors, numels, types, outs, max_norm, eps, norm, ws, s);
+    if (n <= kMiddleTable)
+        return norm_and_clip<kMiddleTable>(n, tensors, numels, types, outs, max_norm, eps, norm, ws, s);
     return norm_and_clip<kLargeTable>(n, tensors, numels, types, outs, max_norm, eps, norm, ws, s);
 }
 

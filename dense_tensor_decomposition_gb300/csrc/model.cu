@@ -412,23 +412,30 @@ constexpr double kGather32 = 1.0, kGather16 = 0.75, kGather8 = 0.53;
 constexpr double kGatherCache = 4.5;
 constexpr double kSample = 1.3;
 constexpr double kStageStart = 3000.0, kStageRow = 3.0;
+constexpr double kSortAndJoin = 40000.0;        // what else the sums from tables take, where few samples go without
 
 double gather_cost(int cs) { return cs == 32 ? kGather32 : cs == 16 ? kGather16 : kGather8; }
 
+// An SM's work on tables: cycles to build them, and for a sample.
+struct Work {
+    double build = -1.0, sample = 0.0;      // build < 0: there are no such tables
+    double of(double samples) const { return build + samples * sample; }
+};
+
 // The tables with the least work for `samples` samples an SM among the ways to split
-// the d modes but `skip` into at most max_groups consecutive groups; returns that work (a
-// negative number where no way fits max_rows rows).
-double plan_tables(const IndexArgs& x, int skip, int cs, int64_t max_rows, int max_groups, double samples,
-                   Tables& best) {
+// the d modes but `skip` into at most max_groups consecutive groups of max_rows rows in all.
+Work plan_tables(const IndexArgs& x, int skip, int cs, int64_t max_rows, int max_groups, double samples,
+                 Tables& best) {
     int mode[MTTKRP_MAX_ORDER], modes = 0;
     for (int m = 0; m < x.d; ++m)
         if (m != skip) mode[modes++] = m;
-    double least = -1.0;
+    Work least;
     for (int cuts = 0; cuts < (modes > 0 ? 1 << (modes - 1) : 1); ++cuts) {
         Tables t;
         t.groups = 0;
         int64_t rows = 0;
-        double work = kStageStart;
+        Work work;
+        work.build = kStageStart;
         bool fits = true;
         for (int k = 0; k < modes && fits;) {
             if (t.groups == max_groups) {
@@ -445,12 +452,12 @@ double plan_tables(const IndexArgs& x, int skip, int cs, int64_t max_rows, int m
                 fits = fits && size <= max_rows;
             } while (fits && k < modes && (cuts >> (k - 1) & 1) == 0);
             rows += size;
-            work += (double)size * g.modes * kStageRow * cs / 32;
+            work.build += (double)size * g.modes * kStageRow * cs / 32;
         }
         if (!fits || rows > max_rows) continue;
         t.rows = (int)rows;
-        work += samples * (t.groups * gather_cost(cs) + kSample);
-        if (least < 0.0 || work < least) {
+        work.sample = t.groups * gather_cost(cs) + kSample;
+        if (least.build < 0.0 || work.of(samples) < least.of(samples)) {
             least = work;
             best = t;
         }
@@ -580,10 +587,10 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
             const int64_t rounds = cdiv(n, kSms * most);
             const int64_t part = cdiv(cdiv(n, kSms * rounds), 32) * 32;
             Tables t;
-            const double slice = plan_tables(a.index, -1, c, table_rows(sample_bytes(groups) * part / 32, c), groups,
-                                             (double)part, t);
-            const double work = slice * cdiv(a.width, c) * rounds;
-            if (slice >= 0.0 && work < least) {
+            const Work slice = plan_tables(a.index, -1, c, table_rows(sample_bytes(groups) * part / 32, c), groups,
+                                           (double)part, t);
+            const double work = slice.of((double)part) * cdiv(a.width, c) * rounds;
+            if (slice.build >= 0.0 && work < least) {
                 least = work;
                 tables = t;
                 share = part;
@@ -599,9 +606,25 @@ cudaError_t launch_entries(const EntriesArgs& a, cudaStream_t s) {
     return entries_cached<__half>(a, s);
 }
 
+namespace {
+
+// cycles an SM for the sums with rows from the caches; single columns a lane take about
+// as long for a load as quads, and few tokens have few warps to wait for them
+double cached_grad_work(const IndexArgs& x, int64_t width, int vec) {
+    const double slow = vec == 4 ? 1.0 : x.n <= kOwnTokens ? 4.0 : 2.0;
+    return slow * kGatherCache * x.d * (x.d - 1) * cdiv(width, 32) * (double)x.n / kSms;
+}
+
+// more than the fixed part of sums from tables
+bool tables_may_pay(const IndexArgs& x, int64_t width, int vec) {
+    return cached_grad_work(x, width, vec) > kStageStart + (x.n <= kOwnTokens ? kSortAndJoin : 0.0);
+}
+
+}  // namespace
+
 // for the largest entries that the sums from shared memory can sort
 size_t entries_grad_workspace_bytes(const IndexArgs& index, int64_t width) {
-    if (always_owned(index, width)) return 0;
+    if (always_owned(index, width) && !tables_may_pay(index, width, 1)) return 0;
     return plan_sort(index, index.d - 1 > kFewGroups ? 32 : 16).total() + part_bytes(index, width);
 }
 
@@ -611,27 +634,31 @@ cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
     bool quads = a.width % 4 == 0;
     for (int m = 0; m < d; ++m) quads = quads && reinterpret_cast<uintptr_t>(a.out[m]) % 16 == 0;
     const int vec = quads ? 4 : 1;
-    double least = kGatherCache * d * (d - 1) * cdiv(a.width, 32) * (double)n / kSms;
+    double least = cached_grad_work(a.index, a.width, vec);
     int cs = 0;
     StagedArgs st;
-    for (int c = 32; c >= 8 && n > kOwnTokens; c /= 2) {
+    for (int c = 32; c >= 8 && tables_may_pay(a.index, a.width, vec); c /= 2) {
         const int64_t combos = cdiv(a.width, c) * d;
-        int64_t tiles = combos < kSms ? kSms / combos : 1;
-        tiles = tiles < cdiv(n, tile_tokens(n)) ? tiles : cdiv(n, tile_tokens(n));     // part_bytes()
-        const int64_t waves = cdiv(combos * tiles, kSms);
-        double work = 0.0;
         Tables t[MTTKRP_MAX_ORDER];
-        for (int m = 0; m < d && work >= 0.0; ++m) {
-            const double slice = plan_tables(a.index, m, c, table_rows(sizeof(float) * kStageThreads * vec, c) - kMaxGroups,
-                                             kMaxGroups, (double)n / tiles, t[m]);
-            work = slice < 0.0 ? -1.0 : (slice > work ? slice : work);
+        Work work[MTTKRP_MAX_ORDER];
+        bool fits = true;
+        for (int m = 0; m < d && fits; ++m) {
+            work[m] = plan_tables(a.index, m, c, table_rows(sizeof(float) * kStageThreads * vec, c) - kMaxGroups,
+                                  kMaxGroups, (double)n * combos / kSms, t[m]);
+            fits = work[m].build >= 0.0;
         }
-        if (work >= 0.0 && work * waves < least) {
-            least = work * waves;
-            cs = c;
-            for (int m = 0; m < d; ++m) st.tables[m] = t[m];
-            st.s.tile = cdiv(n, tiles);
-            st.s.tiles = cdiv(n, st.s.tile);
+        // in how many tiles: the last round of CTAs over the SMs should not leave many without
+        const int64_t most = cdiv(n, tile_tokens(n)) < kSms ? cdiv(n, tile_tokens(n)) : kSms;     // part_bytes()
+        for (int64_t tiles = 1; tiles <= most && fits; tiles += tiles < 16 ? 1 : tiles / 4) {
+            double all = n <= kOwnTokens ? kSortAndJoin : 0.0;
+            for (int m = 0; m < d; ++m) all += work[m].of((double)n / tiles) * cdiv(combos * tiles, kSms) / d;
+            if (all < least) {
+                least = all;
+                cs = c;
+                for (int m = 0; m < d; ++m) st.tables[m] = t[m];
+                st.s.tile = cdiv(n, tiles);
+                st.s.tiles = cdiv(n, st.s.tile);
+            }
         }
     }
     if (cs != 0) {

@@ -551,7 +551,7 @@ inline bool always_owned(const IndexArgs& index, int64_t width) {
     dim3 grid;
     bool all = index.d > 1 || index.rows[0] * width * 4 <= kFillBytes;
     for (int type : {MTTKRP_F32, MTTKRP_F16})
-        for (int vec : {1, 4, 8}) all = all && plan_own(index, width, type, vec, o, grid);
+        for (int vec : {1, 2, 4, 8}) all = all && plan_own(index, width, type, vec, o, grid);
     return all;
 }
 

@@ -119,7 +119,8 @@ GRADS = [  # tokens, rows, width, skew
     (0, 5, 3, 1), (1, 1, 1, 1), (1, 700, 2000, 1), (2, 3, 8, 1), (7, 5, 100, 1), (8, 4, 33, 1), (9, 1, 64, 1),
     (31, 40, 17, 1), (48, 512, 256, 1), (257, 2, 40, 1), (1000, 1, 24, 1), (1025, 1023, 12, 1), (1500, 1024, 8, 1),
     (5003, 300, 65, 2), (8191, 70000, 16, 1), (8192, 50, 128, 3), (8193, 50, 72, 3), (20011, 3, 40, 1),
-    (33000, 33000, 9, 1), (70001, 1 << 20, 4, 2), (100003, 513, 32, 4), (300007, 5000, 8, 3), (40, 9, 65536, 1)]
+    (33000, 33000, 9, 1), (70001, 1 << 20, 4, 2), (100003, 513, 32, 4), (300007, 5000, 8, 3), (40, 9, 65536, 1),
+    (30000, 700, 38, 2), (777, 50, 90, 1)]
 
 
 @pytest.mark.parametrize("n,rows,width,skew", GRADS)
