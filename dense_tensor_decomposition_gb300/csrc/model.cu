@@ -100,16 +100,16 @@ struct alignas(G > kFewGroups ? 16 : 8) Rows {
     __device__ __forceinline__ uint32_t row(int k) const { return k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xFFFFu; }
 };
 
-// the product of the rows at VEC columns from tab on
-template <int CS, int VEC, int G>
-__device__ __forceinline__ Pack<float, VEC> product(const float* tab, const Rows<G>& r) {
-    using P = Pack<float, VEC>;
+// the product of the rows at the four columns from tab on
+template <int CS, int G>
+__device__ __forceinline__ Pack<float, 4> product(const float* tab, const Rows<G>& r) {
+    using P = Pack<float, 4>;
     P p = *reinterpret_cast<const P*>(tab + r.row(0) * CS);
 #pragma unroll
     for (int k = 1; k < G; ++k) {
         const P x = *reinterpret_cast<const P*>(tab + r.row(k) * CS);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) p.v[e] *= x.v[e];
+        for (int e = 0; e < 4; ++e) p.v[e] *= x.v[e];
     }
     return p;
 }
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kStageThreads, 1) entries_staged_kernel(const 
             float acc[L];
 #pragma unroll
             for (int k = 0; k < L; ++k) {
-                const Pack<float, 4> p = product<CS, 4, G>(mine, rows[base + (lane & ~(L - 1)) + k]);
+                const Pack<float, 4> p = product<CS, G>(mine, rows[base + (lane & ~(L - 1)) + k]);
                 acc[k] = (p.v[0] + p.v[1]) + (p.v[2] + p.v[3]);
             }
 #pragma unroll
@@ -289,11 +289,11 @@ __device__ __forceinline__ Entry<G> entry_at(const char* list, int64_t p) {
     return e;
 }
 
-template <int CS, int VEC, int G>
+template <int CS, int G>
 struct Staged {
     template <typename List>
     struct Terms {
-        static constexpr int L = CS / VEC, kB = L < 4 ? L : 4;
+        static constexpr int L = CS / 4, kB = L < 4 ? L : 4;
         static constexpr bool kAllLanes = true;
         const StagedOf& of;
         const List& list;
@@ -323,9 +323,9 @@ struct Staged {
             Rows<G> r;
 #pragma unroll
             for (int w = 0; w < (G + 1) / 2; ++w) r.w[w] = __shfl_sync(lanes, held.rows.w[w], at + j, L);
-            const Pack<float, VEC> p = product<CS, VEC, G>(of.tab, r);
+            const Pack<float, 4> p = product<CS, G>(of.tab, r);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] = fmaf(g, p.v[e], acc[e]);
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(g, p.v[e], acc[e]);
         }
     };
 };
@@ -338,13 +338,13 @@ struct StagedArgs {
 
 // A CTA (blockIdx.x) has a slice of CS columns and s.tile sorted samples of one mode
 // (blockIdx.y); those behind the slices' and tiles' write zeros, 32 rows a warp.
-template <int CS, int VEC, bool kMany>
+template <int CS, bool kRagged, bool kMany>
 __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __grid_constant__ StagedArgs a) {
     extern __shared__ float4 stage_smem[];
-    constexpr int L = CS / VEC, kLog2L = L == 32 ? 5 : L == 16 ? 4 : L == 8 ? 3 : L == 4 ? 2 : 1;
+    constexpr int L = CS / 4, kLog2L = L == 8 ? 3 : L == 4 ? 2 : 1;
     static_assert(1 << kLog2L == L, "lanes of a sample");
-    float* heads = reinterpret_cast<float*>(stage_smem);        // kStageThreads * VEC
-    float* tab = heads + kStageThreads * VEC;
+    float* heads = reinterpret_cast<float*>(stage_smem);        // kStageThreads * 4
+    float* tab = heads + kStageThreads * 4;
     const SumArgs& s = a.s;
     const int m = blockIdx.y;
     const int64_t n = s.a.index.n;
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     after_previous();
     if (col0 >= s.a.width) {
         const int64_t warp = (blockIdx.x - cdiv(s.a.width, CS) * s.tiles) * (kStageThreads / 32) + (threadIdx.x >> 5);
-        zero_unsorted_rows<float, VEC>(s.a, m, warp * 32, [&](int64_t p) { return key_at(s, m, p); });
+        zero_unsorted_rows<float, kRagged ? 1 : 4>(s.a, m, warp * 32, [&](int64_t p) { return key_at(s, m, p); });
         return;
     }
     const int64_t p0 = tile * s.tile, p1 = p0 + s.tile < n ? p0 + s.tile : n;
@@ -382,10 +382,10 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
     around.after = p0 + count < n && key_at(s, m, p0 + count) == key_at(s, m, p0 + count - 1);
     around.head = part;
     around.tail = part + s.a.width;
-    const StagedOf of{tab + (threadIdx.x & (L - 1)) * VEC};
+    const StagedOf of{tab + (threadIdx.x & (L - 1)) * 4};
     auto sum = [&](auto g) {
         constexpr int G = decltype(g)::value;
-        sum_list<float, VEC, Staged<CS, VEC, G>::template Terms, kStageThreads>(
+        sum_list<float, 4, Staged<CS, G>::template Terms, kStageThreads, kRagged>(
             s.a, m, of, [&](int p) { return entry_at<G>(list, p); }, [](uint32_t v) { return v; }, count, kLog2L, col0,
             heads, around, [] { __syncthreads(); });
     };
@@ -534,30 +534,30 @@ cudaError_t grad_cached(const RowSumArgs& a, cudaStream_t s) {
     return sums_by<float, 1, Model<T, 1>::template Terms, 0, Model<T, 1>::template Terms, 0>(a, s);
 }
 
-template <int CS, int VEC, bool kMany>
+template <int CS, bool kRagged, bool kMany>
 cudaError_t grad_staged(StagedArgs& a, cudaStream_t st) {
     const RowSumArgs& r = a.s.a;
     const SortPlan p = plan_sort(r.index, kMany ? 32 : 16);
     a.s.part = reinterpret_cast<float*>(static_cast<char*>(r.ws) + p.total());
     int rows = 0;
     for (int m = 0; m < r.index.d; ++m) rows = a.tables[m].rows > rows ? a.tables[m].rows : rows;
-    constexpr auto kernel = staged_sum_kernel<CS, VEC, kMany>;
+    constexpr auto kernel = staged_sum_kernel<CS, kRagged, kMany>;
     cudaError_t e = allow_smem<kernel>();
     if (e == cudaSuccess) e = sort_tokens(r.index, p, r.ws, a.tables, r.g, a.s.sorted, st);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(cdiv(r.width, CS) * a.s.tiles + cdiv(most_rows(r.index), kStageThreads)), r.index.d);
-    const size_t smem = sizeof(float) * (kStageThreads * VEC + (size_t)rows * CS);
+    const size_t smem = sizeof(float) * (kStageThreads * 4 + (size_t)rows * CS);
     e = launch_early(kernel, grid, kStageThreads, smem, st, a);
     if (e != cudaSuccess) return e;
-    return join<float, VEC>(a.s, st);
+    return join<float, kRagged ? 1 : 4>(a.s, st);
 }
 
-// vec: 4 where results are written in vectors, else 1
+// ragged: results are not written in vectors of four columns
 template <int CS>
-cudaError_t grad_staged(StagedArgs& a, int vec, cudaStream_t st) {
+cudaError_t grad_staged(StagedArgs& a, bool ragged, cudaStream_t st) {
     bool many = false;
     for (int m = 0; m < a.s.a.index.d; ++m) many = many || a.tables[m].groups > kFewGroups;
-    if (!many) return vec == 4 ? grad_staged<CS, 4, false>(a, st) : grad_staged<CS, 1, false>(a, st);
+    if (!many) return ragged ? grad_staged<CS, true, false>(a, st) : grad_staged<CS, false, false>(a, st);
     // every mode gets more than kFewGroups groups: those that lack some, tables of a row of ones
     for (int m = 0; m < a.s.a.index.d; ++m) {
         Tables& t = a.tables[m];
@@ -566,7 +566,7 @@ cudaError_t grad_staged(StagedArgs& a, int vec, cudaStream_t st) {
             t.group[t.groups++].first = t.rows++;
         }
     }
-    return vec == 4 ? grad_staged<CS, 4, true>(a, st) : grad_staged<CS, 1, true>(a, st);
+    return ragged ? grad_staged<CS, true, true>(a, st) : grad_staged<CS, false, true>(a, st);
 }
 
 }  // namespace
@@ -643,7 +643,7 @@ cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
         Work work[MTTKRP_MAX_ORDER];
         bool fits = true;
         for (int m = 0; m < d && fits; ++m) {
-            work[m] = plan_tables(a.index, m, c, table_rows(sizeof(float) * kStageThreads * vec, c) - kMaxGroups,
+            work[m] = plan_tables(a.index, m, c, table_rows(sizeof(float) * kStageThreads * 4, c) - kMaxGroups,
                                   kMaxGroups, (double)n * combos / kSms, t[m]);
             fits = work[m].build >= 0.0;
         }
@@ -664,9 +664,9 @@ cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {
     if (cs != 0) {
         st.s.a = a;
         st.stage = stage_args(a.index, a.factor, a.type, a.width);
-        if (cs == 32) return grad_staged<32>(st, vec, s);
-        if (cs == 16) return grad_staged<16>(st, vec, s);
-        return grad_staged<8>(st, vec, s);
+        if (cs == 32) return grad_staged<32>(st, !quads, s);
+        if (cs == 16) return grad_staged<16>(st, !quads, s);
+        return grad_staged<8>(st, !quads, s);
     }
     if (a.type == MTTKRP_F32) return grad_cached<float>(a, s);
     if (a.type == MTTKRP_BF16) return grad_cached<__nv_bfloat16>(a, s);

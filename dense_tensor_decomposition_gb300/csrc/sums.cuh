@@ -52,8 +52,11 @@ struct Around {
 // kB at a time: after load(p), key(j) is the row of token p + j and add(j, acc) adds its
 // term; behind p1 these repeat some token of the list.  Lanes behind the last column
 // take part only where the terms need all lanes of a group (kAllLanes).
-template <typename TO, int VEC, template <typename> typename Terms, int kN, typename Context, typename List,
-          typename Row, typename Sync>
+//
+// kRagged: a lane's last columns may lie behind the width, and rows start anywhere, so
+// that results are written one column at a time.
+template <typename TO, int VEC, template <typename> typename Terms, int kN, bool kRagged = false, typename Context,
+          typename List, typename Row, typename Sync>
 __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Context& context, const List& list,
                                          const Row& row_of, int count, int log2L, int64_t col0, float* heads,
                                          const Around& around, const Sync& sync) {
@@ -79,7 +82,18 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
     uint32_t cur = 0;
     bool open = false;          // the run at the end began in this group and goes on
     auto finish = [&]() {
-        if (on) write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+        if constexpr (kRagged) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (col + e < a.width) write_row<TO, 1>(a, m, row_of(cur), col + e, acc + e);
+        } else {
+            if (on) write_row<TO, VEC>(a, m, row_of(cur), col, acc);
+        }
+    };
+    auto put_part = [&](float* row) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (!kRagged || col + e < a.width) row[col + e] = acc[e];
     };
     if (p0 < p1 && part) {
         cur = list(p0).x;
@@ -119,7 +133,7 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
     if (open) {
         int g = group + 1;
         for (; g * share < count && list(g * share).x == cur; ++g) add(heads + ((size_t)(g << log2L) + lane) * VEC);
-        if (g * share >= count && around.after && list(count - 1).x == cur) put(around.tail + col);
+        if (g * share >= count && around.after && list(count - 1).x == cur) put_part(around.tail);
         else finish();
     }
     if (group == 0 && around.before) {
@@ -128,7 +142,7 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
         for (int e = 0; e < VEC; ++e) acc[e] = own_head[e];
         for (int g = 1; g * share < count && list(g * share).x == first; ++g)
             add(heads + ((size_t)(g << log2L) + lane) * VEC);
-        put(around.head + col);
+        put_part(around.head);
     }
 }
 
