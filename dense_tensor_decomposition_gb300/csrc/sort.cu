@@ -32,17 +32,45 @@ struct SortArgs {
     Tables tables[MTTKRP_MAX_ORDER];
 };
 
-// writes the entry of 16 or 32 bytes for a token of column m
-__device__ __noinline__ void write_entry(const SortArgs& a, uint2 kt, int m, char* to) {
-    uint32_t g = 0, rows[kMaxGroups / 2] = {};
-    if (kt.x != kNone) {
-        g = __float_as_uint(a.g[kt.y]);
+// Writes the entries of 16 or 32 bytes of N tokens (row, token) of column m to entry
+// numbers to[] (kNone: nowhere).  What it reads of the tokens' indices is used only where
+// they take part.
+template <int N>
+__device__ __forceinline__ void write_entries(const SortArgs& a, const uint2* kt, const uint32_t* to, int m) {
+    uint32_t g[N], rows[N][kMaxGroups / 2];
 #pragma unroll
-        for (int k = 0; k < kMaxGroups; ++k)
-            if (k < a.tables[m].groups) rows[k / 2] |= table_row(a.index, a.tables[m].group[k], kt.y) << (k & 1) * 16;
+    for (int u = 0; u < N; ++u) {
+        g[u] = to[u] != kNone ? __float_as_uint(a.g[kt[u].y]) : 0u;
+#pragma unroll
+        for (int w = 0; w < kMaxGroups / 2; ++w) rows[u][w] = 0;
     }
-    *reinterpret_cast<uint4*>(to) = make_uint4(kt.x, g, rows[0], rows[1]);
-    if (a.entry_bytes > 16) *reinterpret_cast<uint2*>(to + 16) = make_uint2(rows[2], rows[3]);
+    const int groups = a.tables[m].groups;
+    for (int k = 0; k < groups; ++k) {
+        const Tables::Group& group = a.tables[m].group[k];
+        uint32_t row[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) row[u] = 0;
+        for (int i = 0; i < group.modes; ++i) {
+            const int mode = group.mode[i];
+            const uint32_t size = (uint32_t)a.index.rows[mode];
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (to[u] != kNone) row[u] = row[u] * size + (uint32_t)index_at(a.index, kt[u].y, mode);
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint32_t x = (group.first + row[u] & 0xFFFFu) << (k & 1) * 16;
+#pragma unroll
+            for (int w = 0; w < kMaxGroups / 2; ++w) rows[u][w] |= k / 2 == w ? x : 0u;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        if (to[u] == kNone) continue;
+        char* e = a.entries + ((int64_t)m * a.index.n + to[u]) * a.entry_bytes;
+        *reinterpret_cast<uint4*>(e) = make_uint4(kt[u].x, g[u], rows[u][0], rows[u][1]);
+        if (a.entry_bytes > 16) *reinterpret_cast<uint2*>(e + 16) = make_uint2(rows[u][2], rows[u][3]);
+    }
 }
 
 // lanes of the warp with this lane's digit, which has at most `bits` bits or is kNone
@@ -190,21 +218,17 @@ __device__ __forceinline__ void sort_column(const SortArgs& a, int m, int cta, i
                 first[b] = next;
             }
             __syncthreads();
-#pragma unroll 1
-            for (int i = 0; i < kSortItems; ++i) {
-                uint2 x = kt[0];
-                uint32_t where = place[0];
 #pragma unroll
-                for (int k = 1; k < kSortItems; ++k) {
-                    if (i == k) {
-                        x = kt[k];
-                        where = place[k];
-                    }
-                }
-                if (where == kNone) continue;
-                const uint32_t to = wh[where & 0xFFFFu] + (where >> 16);
-                if (last && a.entries) write_entry(a, x, m, a.entries + (m * n + to) * a.entry_bytes);
-                else __stcg(dst + to, x);
+            for (int i = 0; i < kSortItems; ++i)
+                if (place[i] != kNone) place[i] = wh[place[i] & 0xFFFFu] + (place[i] >> 16);
+            if (last && a.entries) {
+                constexpr int kTogether = kSortItems < 4 ? kSortItems : 4;
+#pragma unroll
+                for (int i = 0; i < kSortItems; i += kTogether) write_entries<kTogether>(a, kt + i, place + i, m);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSortItems; ++i)
+                    if (place[i] != kNone) __stcg(dst + place[i], kt[i]);
             }
         }
         if (!last) wait();

@@ -402,7 +402,7 @@ int mttkrp_cp_entries(int d, const int64_t* dims, int64_t R, const void* const* 
  * the entries (an MTTKRP of the sparse tensor that holds g at the coordinates):
  *     outs[n](i, :) = sum over s with c_sn = i of g[s] * prod over m != n of A_m(c_sm, :)
  * outs      HOST array of d device pointers, outs[n] dims[n] x R fp32, overwritten.
- * Samples with a coordinate out of range take no part (their g is not read).
+ * Samples with a coordinate out of range take no part, whatever their g.
  * The workspace is needed as for mttkrp_embedding_grad.
  */
 size_t mttkrp_cp_entries_grad_workspace_bytes(int d, const int64_t* dims, int64_t R, int64_t n_samples);
