@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t sort_key_of(const IndexArgs& a, int64_t t, i
 
 template <typename I, int kCols>
 struct KeyOf {
-    static constexpr int kLook = kCols == 1 ? 8 : kCols == 4 ? 4 : 2;       // tokens whose loads fit the registers
+    static constexpr int kLook = kCols == 1 ? 8 : kCols <= 5 ? 4 : 2;       // tokens whose loads fit the registers
     __device__ __forceinline__ uint32_t operator()(const IndexArgs& a, int64_t t, int m) const {
         return sort_key_of<I, kCols>(a, t, m);
     }
@@ -74,7 +74,8 @@ struct KeyOf {
 template <typename F>
 __device__ __forceinline__ void with_key(const IndexArgs& a, const F& f) {
     if (a.d == 1) a.bytes == 8 ? f(KeyOf<int64_t, 1>()) : f(KeyOf<int32_t, 1>());
-    else if (a.d <= 4) a.bytes == 8 ? f(KeyOf<int64_t, 4>()) : f(KeyOf<int32_t, 4>());
+    else if (a.d <= 3) a.bytes == 8 ? f(KeyOf<int64_t, 3>()) : f(KeyOf<int32_t, 3>());
+    else if (a.d <= 5) a.bytes == 8 ? f(KeyOf<int64_t, 5>()) : f(KeyOf<int32_t, 5>());
     else a.bytes == 8 ? f(KeyOf<int64_t, MTTKRP_MAX_ORDER>()) : f(KeyOf<int32_t, MTTKRP_MAX_ORDER>());
 }
 
