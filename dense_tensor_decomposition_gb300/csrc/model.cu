@@ -116,7 +116,8 @@ __device__ __forceinline__ Pack<float, 4> product(const float* tab, const Rows<G
 
 // ---------------------------------------------------------------- entries
 
-// L lanes a sample, gathering from the caches.
+// L lanes a sample (up to a CTA's where samples are few and the rank is large), gathering
+// from the caches.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant__ EntriesArgs a, int log2L) {
     after_previous();
@@ -139,7 +140,14 @@ __global__ void __launch_bounds__(kThreads) entries_kernel(const __grid_constant
             for (int e = 0; e < VEC; ++e) sum += v[e];
         }
     }
-    for (int o = L >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    for (int o = L < 32 ? L >> 1 : 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (L > 32) {
+        __shared__ float warps[kThreads / 32];
+        if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+        __syncthreads();
+        if (lane == 0)
+            for (int w = 1; w < L >> 5; ++w) sum += warps[(threadIdx.x >> 5) + w];
+    }
     if (any && lane == 0) a.out[t] = sum;
 }
 
@@ -481,7 +489,7 @@ cudaError_t entries_cached(const EntriesArgs& a, cudaStream_t s) {
     bool w = true;
     for (int m = 0; m < a.index.d; ++m) w = w && wide_rows<T>(a.factor[m], a.width);
     int l = 0;
-    while (l < 5 && ((int64_t)(w ? kVec : 1) << l) < a.width) ++l;
+    while (((int64_t)(w ? kVec : 1) << l) < a.width && (l < 5 || (l < 8 && a.index.n << l < kSms * 1024))) ++l;
     const unsigned blocks = (unsigned)cdiv(a.index.n << l, kThreads);
     return launch_early(w ? entries_kernel<T, kVec> : entries_kernel<T, 1>, blocks, kThreads, 0, s, a, l);
 }
