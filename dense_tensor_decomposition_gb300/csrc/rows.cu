@@ -94,12 +94,43 @@ int log2_lanes(int64_t items) {
     return l;
 }
 
+// `lanes` (a power of two's logarithm) for a part of a row
 template <typename T, int VEC, int U, int K>
-cudaError_t lookup_by(const LookupArgs& a, cudaStream_t s) {
-    const int l = log2_lanes(cdiv(a.width, VEC));
-    const dim3 grid((unsigned)cdiv(cdiv(a.index.n, K) << l, kThreads),
-                    (unsigned)cdiv(a.width, (int64_t)(VEC * U) << l));
-    return launch_early(lookup_kernel<T, VEC, U, K>, grid, kThreads, 0, s, a, l);
+cudaError_t lookup_by(const LookupArgs& a, int lanes, cudaStream_t s) {
+    const dim3 grid((unsigned)cdiv(cdiv(a.index.n, K) << lanes, kThreads),
+                    (unsigned)cdiv(a.width, (int64_t)(VEC * U) << lanes));
+    return launch_early(lookup_kernel<T, VEC, U, K>, grid, kThreads, 0, s, a, lanes);
+}
+
+// Rows of 16-byte vectors, about 64 bytes of them a thread; longer ones in parts of 512
+// bytes.  The grid takes all tokens' first parts, then the next: of a table larger than L2
+// a part's columns stay there for the rows met again (read and write, two tokens a row of
+// 400 MB: 2048 fp32 columns 9.1 TB/s in parts of 512 bytes, 8.0 in parts of 2 KB, 7.2 in
+// one; 64 columns in 16 lanes of one load each 4.4, in 4 of four loads 7.2).
+template <typename T>
+cudaError_t lookup_vectors(const LookupArgs& a, cudaStream_t s) {
+    constexpr int kVec = 16 / sizeof(T);
+    const int64_t vecs = cdiv(a.width, kVec);
+    if (vecs <= 4) return lookup_by<T, kVec, 1, 4>(a, log2_lanes(vecs), s);
+    if (vecs <= 8) return lookup_by<T, kVec, 2, 2>(a, 2, s);
+    return lookup_by<T, kVec, 4, 1>(a, vecs <= 16 ? 2 : 3, s);
+}
+
+// Rows at other offsets, where a part's ends share their 32 bytes with the next part's, a
+// write of its own: in one part where 128 lanes can have it, else in parts of 32 lanes
+// (read and write, two tokens a row of 400 MB: 515 fp32 columns 5.0 TB/s in parts of 512
+// columns, 5.9 in one; 1001 columns 6.7 and 7.1; 9001 columns 7.6 in parts of 512
+// columns, 6.5 in parts of 4096).
+template <typename T, int VEC, int K>
+cudaError_t lookup_pieces(const LookupArgs& a, cudaStream_t s) {
+    constexpr int U = 16;
+    int lanes = log2_lanes(cdiv(a.width, VEC));
+    for (int l = lanes; l <= 7; ++l)
+        if (((int64_t)(VEC * U) << l) >= a.width) {
+            lanes = l;
+            break;
+        }
+    return lookup_by<T, VEC, U, K>(a, lanes, s);
 }
 
 // the widest vectors that the rows' starts and width allow
@@ -108,14 +139,14 @@ cudaError_t lookup(const LookupArgs& a, cudaStream_t s) {
     constexpr int e = sizeof(T);
     const size_t all = reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.out) |
                        (a.table_stride * e) | (a.out_stride * e) | (a.width * e);
-    if (all % 16 == 0) return lookup_by<T, 16 / e, 4, 1>(a, s);
+    if (all % 16 == 0) return lookup_vectors<T>(a, s);
     if (a.width <= flat_width(e) && a.out_stride == a.width && reinterpret_cast<uintptr_t>(a.out) % 4 == 0) {
         const uint32_t inverse = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
         const int64_t blocks = cdiv(a.index.n * a.width, (int64_t)kThreads * kFlatSteps * (4 / e));
         return launch_early(lookup_flat_kernel<T>, (unsigned)blocks, kThreads, 0, s, a, inverse);
     }
-    if (all % 4 == 0) return e == 4 ? lookup_by<T, 4 / e, 16, 2>(a, s) : lookup_by<T, 4 / e, 16, 1>(a, s);
-    if constexpr (e < 4) return lookup_by<T, 1, 16, 2>(a, s);
+    if (all % 4 == 0) return lookup_pieces<T, 4 / e, e == 4 ? 2 : 1>(a, s);
+    if constexpr (e < 4) return lookup_pieces<T, 1, 2>(a, s);
     return cudaErrorInvalidValue;
 }
 
