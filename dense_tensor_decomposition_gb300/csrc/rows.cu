@@ -14,6 +14,7 @@ namespace {
 template <typename T, int VEC, int U, int K>
 __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant__ LookupArgs a, int log2L) {
     using P = Pack<T, VEC>;
+    using B = typename Bits<sizeof(P)>::type;
     after_previous();
     const int lane = threadIdx.x & ((1 << log2L) - 1);
     const int64_t t0 = (((int64_t)blockIdx.x * kThreads + threadIdx.x) >> log2L) * K;
@@ -21,7 +22,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     const int c0 = (int)blockIdx.y * U * step + lane * VEC;
     const int width = (int)a.width;
     int64_t v[K];
-    P x[K][U];
+    B x[K][U];
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = t0 + k < a.index.n ? index_at(a.index, t0 + k, 0) : -1;
 #pragma unroll
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
         const T* src = static_cast<const T*>(a.table) + v[k] * a.table_stride;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (v[k] >= 0 && c0 + u * step < width) x[k][u] = *reinterpret_cast<const P*>(src + c0 + u * step);
+            if (v[k] >= 0 && c0 + u * step < width) x[k][u] = *reinterpret_cast<const B*>(src + c0 + u * step);
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -39,10 +40,10 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (c0 + u * step >= width) break;
+            P p = as_pack<P>(x[k][u]);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                x[k][u].v[e] = from_f32<T>(v[k] >= 0 ? a.scale * to_f32(x[k][u].v[e]) : 0.f);
-            *reinterpret_cast<P*>(dst + c0 + u * step) = x[k][u];
+            for (int e = 0; e < VEC; ++e) p.v[e] = from_f32<T>(v[k] >= 0 ? a.scale * to_f32(p.v[e]) : 0.f);
+            *reinterpret_cast<B*>(dst + c0 + u * step) = as_pack<B>(p);
         }
     }
 }
@@ -121,7 +122,7 @@ cudaError_t lookup_vectors(const LookupArgs& a, cudaStream_t s) {
 // (read and write, two tokens a row of 400 MB: 515 fp32 columns 5.0 TB/s in parts of 512
 // columns, 5.9 in one; 1001 columns 6.7 and 7.1; 9001 columns 7.6 in parts of 512
 // columns, 6.5 in parts of 4096).
-template <typename T, int VEC, int K>
+template <typename T, int VEC>
 cudaError_t lookup_pieces(const LookupArgs& a, cudaStream_t s) {
     constexpr int U = 16;
     int lanes = log2_lanes(cdiv(a.width, VEC));
@@ -130,7 +131,7 @@ cudaError_t lookup_pieces(const LookupArgs& a, cudaStream_t s) {
             lanes = l;
             break;
         }
-    return lookup_by<T, VEC, U, K>(a, lanes, s);
+    return lookup_by<T, VEC, U, 2>(a, lanes, s);
 }
 
 // the widest vectors that the rows' starts and width allow
@@ -145,8 +146,8 @@ cudaError_t lookup(const LookupArgs& a, cudaStream_t s) {
         const int64_t blocks = cdiv(a.index.n * a.width, (int64_t)kThreads * kFlatSteps * (4 / e));
         return launch_early(lookup_flat_kernel<T>, (unsigned)blocks, kThreads, 0, s, a, inverse);
     }
-    if (all % 4 == 0) return lookup_pieces<T, 4 / e, e == 4 ? 2 : 1>(a, s);
-    if constexpr (e < 4) return lookup_pieces<T, 1, 2>(a, s);
+    if (all % 4 == 0) return lookup_pieces<T, 4 / e>(a, s);
+    if constexpr (e < 4) return lookup_pieces<T, 1>(a, s);
     return cudaErrorInvalidValue;
 }
 

@@ -27,4 +27,24 @@ struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
 };
 
+// the same as bits in as few registers: 16-bit elements held as a Pack take one each
+template <int kBytes>
+struct Bits;
+template <>
+struct Bits<2> { using type = unsigned short; };
+template <>
+struct Bits<4> { using type = uint32_t; };
+template <>
+struct Bits<8> { using type = uint2; };
+template <>
+struct Bits<16> { using type = uint4; };
+
+template <typename P, typename B>
+__device__ __forceinline__ P as_pack(const B& bits) {
+    static_assert(sizeof(P) == sizeof(B));
+    P p;
+    memcpy(&p, &bits, sizeof(p));
+    return p;
+}
+
 }  // namespace mk
