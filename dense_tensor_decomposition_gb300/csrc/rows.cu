@@ -48,42 +48,48 @@ __global__ void __launch_bounds__(kThreads) lookup_kernel(const __grid_constant_
     }
 }
 
-// Narrow rows at any offset: the result as one array, 4 bytes of it a thread and step,
-// whatever rows they are of (read and write 4.8 TB/s in fp32 and 2.6 in 16 bits at every
-// width; by rows, 17 fp32 columns 0.6, 65 2.2, 333 6.9; 17 columns of 16 bits 0.3, 65 1.1,
-// 333 3.9).  The result's rows have no gaps, and it starts at a multiple of 4 bytes.
+// Narrow rows at other offsets, in pieces of VEC elements: the result as one array, 4
+// bytes of it a thread and step, whatever rows they are of.  Its rows have no gaps, and it
+// starts at a multiple of 4 bytes.  (Read and write, two tokens a row of 400 MB, this way
+// and by lookup_pieces: 17 fp32 columns 3.6 and 2.0 TB/s, 33 4.2 and 3.6, 65 4.8 and 4.9,
+// 162 5.0 and 6.1; of 16 bits 17 columns 2.0 and 1.0, 65 2.5 and 2.6, 162 3.2 and 5.2.)
 constexpr int kFlatSteps = 8;
-constexpr int64_t flat_width(int elem) { return elem == 4 ? 255 : 159; }     // at most
+constexpr int64_t kFlatPieces = 64;         // at most
 
-template <typename T>
+template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) lookup_flat_kernel(const __grid_constant__ LookupArgs a, uint32_t inverse) {
-    constexpr int P = 4 / sizeof(T), kSpan = kThreads * kFlatSteps * P;
+    constexpr int S = 4 / sizeof(T) / VEC, kSpan = kThreads * kFlatSteps * S;     // pieces of a store, of a CTA
+    using P = Pack<T, VEC>;
     after_previous();
-    const uint32_t width = (uint32_t)a.width;
-    const int64_t total = a.index.n * a.width, base = (int64_t)blockIdx.x * kSpan;
-    const int64_t t0 = base / a.width;
-    const uint32_t rest = (uint32_t)(base - t0 * a.width);
-    Pack<T, P> x[kFlatSteps];
+    const uint32_t width = (uint32_t)(a.width / VEC);
+    const int64_t total = a.index.n * width, base = (int64_t)blockIdx.x * kSpan;
+    const int64_t t0 = base / width;
+    const uint32_t rest = (uint32_t)(base - t0 * width);
+    Pack<P, S> x[kFlatSteps];
 #pragma unroll
     for (int u = 0; u < kFlatSteps; ++u) {
-        const uint32_t at = (u * kThreads + threadIdx.x) * P;
+        const uint32_t at = (u * kThreads + threadIdx.x) * S;
 #pragma unroll
-        for (int e = 0; e < P; ++e) {
+        for (int e = 0; e < S; ++e) {
             // both are below 2^13, so the quotient is exact: inverse is 2^32 / width rounded up
             const uint32_t i = rest + at + e, r = width == 1 ? i : __umulhi(i, inverse);
             const int64_t v = base + at + e < total ? index_at(a.index, t0 + r, 0) : -1;
-            x[u].v[e] = from_f32<T>(0.f);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) x[u].v[e].v[k] = from_f32<T>(0.f);
             if (v >= 0 && v < a.index.rows[0])
-                x[u].v[e] = static_cast<const T*>(a.table)[v * a.table_stride + (i - r * width)];
+                x[u].v[e] = *reinterpret_cast<const P*>(static_cast<const T*>(a.table) + v * a.table_stride +
+                                                        (i - r * width) * VEC);
         }
     }
-    T* out = static_cast<T*>(a.out) + base;
+    P* out = static_cast<P*>(a.out) + base;
 #pragma unroll
     for (int u = 0; u < kFlatSteps; ++u) {
-        const uint32_t at = (u * kThreads + threadIdx.x) * P;
+        const uint32_t at = (u * kThreads + threadIdx.x) * S;
 #pragma unroll
-        for (int e = 0; e < P; ++e) x[u].v[e] = from_f32<T>(a.scale * to_f32(x[u].v[e]));
-        if (base + at + P <= total) *reinterpret_cast<Pack<T, P>*>(out + at) = x[u];
+        for (int e = 0; e < S; ++e)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) x[u].v[e].v[k] = from_f32<T>(a.scale * to_f32(x[u].v[e].v[k]));
+        if (base + at + S <= total) *reinterpret_cast<Pack<P, S>*>(out + at) = x[u];
         else if (base + at < total) out[at] = x[u].v[0];
     }
 }
@@ -117,20 +123,24 @@ cudaError_t lookup_vectors(const LookupArgs& a, cudaStream_t s) {
     return lookup_by<T, kVec, 4, 1>(a, vecs <= 16 ? 2 : 3, s);
 }
 
-// Rows at other offsets, where a part's ends share their 32 bytes with the next part's, a
-// write of its own: in one part where 128 lanes can have it, else in parts of 32 lanes
-// (read and write, two tokens a row of 400 MB: 515 fp32 columns 5.0 TB/s in parts of 512
-// columns, 5.9 in one; 1001 columns 6.7 and 7.1; 9001 columns 7.6 in parts of 512
-// columns, 6.5 in parts of 4096).
+// Rows at other offsets, in pieces of VEC elements: 16 of them a thread, by 8 lanes at
+// least.  A part's ends share their 32 bytes with the next part's, a write of its own: so in
+// one part where 128 lanes can have it, else in parts of 32 lanes (read and write, two
+// tokens a row of 400 MB: 515 fp32 columns 5.0 TB/s in parts of 512 columns, 5.9 in one;
+// 1001 columns 6.7 and 7.1; 9001 columns 7.6 in parts of 512 columns, 6.5 in parts of 4096).
 template <typename T, int VEC>
 cudaError_t lookup_pieces(const LookupArgs& a, cudaStream_t s) {
-    constexpr int U = 16;
-    int lanes = log2_lanes(cdiv(a.width, VEC));
-    for (int l = lanes; l <= 7; ++l)
-        if (((int64_t)(VEC * U) << l) >= a.width) {
-            lanes = l;
-            break;
-        }
+    constexpr int U = 16, kMost = 7;
+    const int64_t width = a.width / VEC;
+    if (width <= kFlatPieces && a.out_stride == a.width && reinterpret_cast<uintptr_t>(a.out) % 4 == 0) {
+        constexpr int64_t kSpan = kThreads * kFlatSteps * (4 / sizeof(T) / VEC);
+        const uint32_t inverse = (uint32_t)((((uint64_t)1 << 32) + width - 1) / width);
+        return launch_early(lookup_flat_kernel<T, VEC>, (unsigned)cdiv(a.index.n * width, kSpan), kThreads, 0, s, a,
+                            inverse);
+    }
+    int lanes = width > 4 ? 3 : log2_lanes(width);
+    while (lanes < kMost && ((int64_t)U << lanes) < width) ++lanes;
+    if (((int64_t)U << lanes) < width) lanes = 5;
     return lookup_by<T, VEC, U, 2>(a, lanes, s);
 }
 
@@ -141,14 +151,8 @@ cudaError_t lookup(const LookupArgs& a, cudaStream_t s) {
     const size_t all = reinterpret_cast<uintptr_t>(a.table) | reinterpret_cast<uintptr_t>(a.out) |
                        (a.table_stride * e) | (a.out_stride * e) | (a.width * e);
     if (all % 16 == 0) return lookup_vectors<T>(a, s);
-    if (a.width <= flat_width(e) && a.out_stride == a.width && reinterpret_cast<uintptr_t>(a.out) % 4 == 0) {
-        const uint32_t inverse = (uint32_t)((((uint64_t)1 << 32) + a.width - 1) / a.width);
-        const int64_t blocks = cdiv(a.index.n * a.width, (int64_t)kThreads * kFlatSteps * (4 / e));
-        return launch_early(lookup_flat_kernel<T>, (unsigned)blocks, kThreads, 0, s, a, inverse);
-    }
     if (all % 4 == 0) return lookup_pieces<T, 4 / e>(a, s);
-    if constexpr (e < 4) return lookup_pieces<T, 1>(a, s);
-    return cudaErrorInvalidValue;
+    return lookup_pieces<T, 1>(a, s);
 }
 
 // ---------------------------------------------------------------- gradient
