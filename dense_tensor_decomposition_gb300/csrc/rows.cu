@@ -109,18 +109,25 @@ cudaError_t lookup_by(const LookupArgs& a, int lanes, cudaStream_t s) {
     return launch_early(lookup_kernel<T, VEC, U, K>, grid, kThreads, 0, s, a, lanes);
 }
 
-// Rows of 16-byte vectors, about 64 bytes of them a thread; longer ones in parts of 512
-// bytes.  The grid takes all tokens' first parts, then the next: of a table larger than L2
-// a part's columns stay there for the rows met again (read and write, two tokens a row of
-// 400 MB: 2048 fp32 columns 9.1 TB/s in parts of 512 bytes, 8.0 in parts of 2 KB, 7.2 in
-// one; 64 columns in 16 lanes of one load each 4.4, in 4 of four loads 7.2).
+// Rows of 16-byte vectors, 64 bytes of them a thread.  Rows of 1 KB and more go in parts
+// of 512 bytes: the grid takes all tokens' first parts, then the next, so that of a table
+// larger than L2 a part's columns stay there for the rows met again.  But a part's ends
+// must not share their 32 bytes with the next part's, a write of its own: such rows go in
+// one part where 128 lanes can have it.  (Read and write, two tokens a row of 400 MB: 2048
+// fp32 columns 9.1 TB/s in parts of 512 bytes, 8.0 of 2 KB, 7.2 in one; 1004 columns 6.0
+// in parts, 7.1 in one; 200 columns 6.2 and 6.9; 64 columns in 16 lanes of one load each
+// 4.4, in 4 of four loads 7.2.)
 template <typename T>
 cudaError_t lookup_vectors(const LookupArgs& a, cudaStream_t s) {
-    constexpr int kVec = 16 / sizeof(T);
+    constexpr int kVec = 16 / sizeof(T), U = 4, kMost = 7;
     const int64_t vecs = cdiv(a.width, kVec);
     if (vecs <= 4) return lookup_by<T, kVec, 1, 4>(a, log2_lanes(vecs), s);
     if (vecs <= 8) return lookup_by<T, kVec, 2, 2>(a, 2, s);
-    return lookup_by<T, kVec, 4, 1>(a, vecs <= 16 ? 2 : 3, s);
+    int lanes = 2;
+    while (lanes < kMost && ((int64_t)U << lanes) < vecs) ++lanes;
+    const bool apart = (vecs | a.out_stride / kVec) % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+    if (((int64_t)U << lanes) < vecs || (apart && vecs >= 64)) lanes = 3;
+    return lookup_by<T, kVec, U, 1>(a, lanes, s);
 }
 
 // Rows at other offsets, in pieces of VEC elements: 16 of them a thread, by 8 lanes at
