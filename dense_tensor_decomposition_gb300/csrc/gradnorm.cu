@@ -66,33 +66,26 @@ struct Vecs {
     __device__ bool holds(int64_t e) const { return e >= 0 && e < n; }
     __device__ const uint4* at(int64_t i) const { return reinterpret_cast<const uint4*>(x - shift) + i; }
     // zeros for elements that are not the tensor's
-    __device__ P load(int64_t i) const {
-        if (whole(i)) return *reinterpret_cast<const P*>(at(i));
+    __device__ uint4 load(int64_t i) const {
+        if (whole(i)) return *at(i);
         P v;
 #pragma unroll
         for (int e = 0; e < kVec; ++e) v.v[e] = holds(i * kVec - shift + e) ? x[i * kVec - shift + e] : from_f32<T>(0.f);
-        return v;
+        return as_pack<uint4>(v);
     }
     // vectors i, i + kUnitVecs, ... of `units` <= kUnroll units; keep: for the cache to keep
-    __device__ void load_units(int64_t i, int units, bool keep, P* v) const {
+    __device__ void load_units(int64_t i, int units, bool keep, uint4* v) const {
         if (units == kUnroll && whole(i - threadIdx.x) && whole(i - threadIdx.x + (int64_t)kUnroll * kUnitVecs - 1)) {
-            uint4 w[kUnroll];
             if (keep) {
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) w[u] = *at(i + u * kUnitVecs);
+                for (int u = 0; u < kUnroll; ++u) v[u] = *at(i + u * kUnitVecs);
             } else {
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) w[u] = __ldcs(at(i + u * kUnitVecs));
+                for (int u = 0; u < kUnroll; ++u) v[u] = __ldcs(at(i + u * kUnitVecs));
             }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) v[u] = *reinterpret_cast<const P*>(&w[u]);
         } else {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[u].v[e] = from_f32<T>(0.f);
-                if (u < units) v[u] = load(i + u * kUnitVecs);
-            }
+            for (int u = 0; u < kUnroll; ++u) v[u] = u < units ? load(i + u * kUnitVecs) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
 };
@@ -158,13 +151,17 @@ template <typename T>
 __device__ __forceinline__ void add_squares(const void* p, int64_t numel, int64_t unit, int units, bool keep, Sum& sum) {
     constexpr int kVec = Vecs<T>::kVec;
     const Vecs<T> x(p, numel);
-    Pack<T, kVec> v[kUnroll];
+    uint4 v[kUnroll];
     x.load_units(unit * kUnitVecs + threadIdx.x, units, keep, v);
 #pragma unroll
     for (int u = 0; u < kUnroll; u += 16 / kVec) {
         float f[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[e] = to_f32(v[u + e / kVec].v[e % kVec]);
+        for (int w = 0; w < 16 / kVec; ++w) {
+            const Pack<T, kVec> p = as_pack<Pack<T, kVec>>(v[u + w]);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) f[w * kVec + e] = to_f32(p.v[e]);
+        }
         sum.squares16(f);
     }
 }
@@ -176,20 +173,21 @@ __device__ __forceinline__ void scale(const void* p, void* q, int64_t numel, int
     T* y = static_cast<T*>(q);
     const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
     const int64_t i = unit * kUnitVecs + threadIdx.x;
-    Pack<T, kVec> v[kUnroll];
+    uint4 v[kUnroll];
     x.load_units(i, units, false, v);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         if (u >= units) break;
         const int64_t at = i + u * kUnitVecs, e0 = at * kVec - x.shift;
+        auto w = as_pack<Pack<T, kVec>>(v[u]);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[u].v[e] = from_f32<T>(coef * to_f32(v[u].v[e]));
+        for (int e = 0; e < kVec; ++e) w.v[e] = from_f32<T>(coef * to_f32(w.v[e]));
         if (same && x.whole(at)) {
-            __stcs(reinterpret_cast<uint4*>(y + e0), *reinterpret_cast<const uint4*>(&v[u]));
+            __stcs(reinterpret_cast<uint4*>(y + e0), as_pack<uint4>(w));
         } else {
 #pragma unroll
             for (int e = 0; e < kVec; ++e)
-                if (x.holds(e0 + e)) y[e0 + e] = v[u].v[e];
+                if (x.holds(e0 + e)) y[e0 + e] = w.v[e];
         }
     }
 }

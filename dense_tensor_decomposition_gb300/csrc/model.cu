@@ -245,15 +245,19 @@ struct Model {
             }
             for (int l = 0; l < a.index.d; ++l) {
                 if (l == of.m) continue;
-                Pack<T, VEC> x[kB];
+                using P = Pack<T, VEC>;
+                using Raw = typename Bits<sizeof(P)>::type;
+                Raw x[kB];
 #pragma unroll
                 for (int j = 0; j < kB; ++j)
-                    x[j] = *reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(a.factor[l]) +
-                                                                  index_at(a.index, tok[j], l) * a.width + col);
+                    x[j] = *reinterpret_cast<const Raw*>(static_cast<const T*>(a.factor[l]) +
+                                                         index_at(a.index, tok[j], l) * a.width + col);
 #pragma unroll
-                for (int j = 0; j < kB; ++j)
+                for (int j = 0; j < kB; ++j) {
+                    const P p = as_pack<P>(x[j]);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[j][e] *= to_f32(x[j].v[e]);
+                    for (int e = 0; e < VEC; ++e) v[j][e] *= to_f32(p.v[e]);
+                }
             }
         }
         __device__ __forceinline__ uint32_t key(int j) const { return keys[j]; }

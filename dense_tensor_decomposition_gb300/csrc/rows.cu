@@ -176,7 +176,9 @@ struct Grad {
         const int p1;
         const int64_t col;
         uint32_t keys[B];
-        Pack<T, VEC> x[B];
+        using P = Pack<T, VEC>;
+        using Raw = typename Bits<sizeof(P)>::type;
+        Raw x[B];
         __device__ __forceinline__ Terms(const TermsOf& of, const List& list, int, int p1, int64_t col)
             : of(of), list(list), p1(p1), col(col) {}
         __device__ __forceinline__ void load(int p) {
@@ -184,14 +186,15 @@ struct Grad {
             for (int j = 0; j < B; ++j) {
                 const uint2 entry = list(p + j < p1 ? p + j : p);
                 keys[j] = entry.x;
-                x[j] = *reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(of.a.grad) +
-                                                              (int64_t)entry.y * of.a.grad_stride + col);
+                x[j] = *reinterpret_cast<const Raw*>(static_cast<const T*>(of.a.grad) +
+                                                     (int64_t)entry.y * of.a.grad_stride + col);
             }
         }
         __device__ __forceinline__ uint32_t key(int j) const { return keys[j]; }
         __device__ __forceinline__ void add(int j, float* acc) const {
+            const P v = as_pack<P>(x[j]);
     #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += to_f32(x[j].v[e]);
+            for (int e = 0; e < VEC; ++e) acc[e] += to_f32(v.v[e]);
         }
     };
 };
@@ -269,8 +272,8 @@ cudaError_t lookup_grad(const RowSumArgs& a, cudaStream_t s) {
         return sums_by<TO, kVec, Ring<T, kSumThreads, 8>::template Terms, Ring<T, kSumThreads, 8>::kBytes,
                        Ring<T, kThreads, 16>::template Terms, Ring<T, kThreads, 16>::kBytes>(a, s);
     if (vectors_of(2))
-        return sums_by<TO, 2, Grad<T, 2, 4>::template Terms, 0, Grad<T, 2, 8>::template Terms, 0>(a, s);
-    return sums_by<TO, 1, Grad<T, 1, 4>::template Terms, 0, Grad<T, 1, 8>::template Terms, 0>(a, s);
+        return sums_by<TO, 2, Grad<T, 2, 8>::template Terms, 0, Grad<T, 2, 8>::template Terms, 0>(a, s);
+    return sums_by<TO, 1, Grad<T, 1, 8>::template Terms, 0, Grad<T, 1, 12>::template Terms, 0>(a, s);
 }
 
 }  // namespace
