@@ -4,9 +4,9 @@
 //   * few tokens (own_kernel): one launch.  Every CTA owns some of the rows, finds the
 //     tokens that point to them, groups them by row and writes its rows, zeros included.
 //   * many tokens: the tokens are sorted by row (sort.cu), and CTAs walk the sorted
-//     tokens in tiles of equal length, however long a row's run of tokens is
-//     (row_sum_kernel); runs that cross tile borders are joined, and rows without
-//     tokens set to zero, by a last launch (finish_kernel).
+//     tokens in tiles of equal length, however long a row's run of tokens is, and set
+//     rows without tokens to zero (row_sum_kernel); runs that cross tile borders are
+//     joined by a last launch (join_kernel).
 // Both add with sum_list(), which splits a list of sorted tokens over groups of lanes
 // and joins the runs that cross the groups' borders.
 #pragma once
@@ -147,7 +147,9 @@ __device__ __forceinline__ void sum_list(const RowSumArgs& a, int m, const Conte
 }
 
 // Zeros for those of `rows` local rows, from local row r0 on, that no token points
-// to, by one warp; row_of gives a local row's number in the table (kNone: none).
+// to, by one warp; row_of gives a local row's number in the table (kNone: none).  Rows at
+// any offset are written in 16-byte vectors but for their ends (3000 tokens into 200000
+// rows of 33 16-bit columns: 38 us by single columns, 12 so).
 template <typename TO, int VEC, typename Touched, typename Row>
 __device__ __forceinline__ void zero_rows(const RowSumArgs& a, int m, uint32_t r0, uint32_t rows, int64_t col0,
                                           uint32_t vecs, const Touched& touched, const Row& row_of) {
@@ -158,13 +160,22 @@ __device__ __forceinline__ void zero_rows(const RowSumArgs& a, int m, uint32_t r
     auto at = [&](uint32_t v) {
         return reinterpret_cast<Pack<TO, VEC>*>(static_cast<TO*>(a.out[m]) + (int64_t)v * a.out_stride + col0);
     };
-    if (vecs >= 32) {
-        for (uint32_t r = r0; r < r0 + rows; ++r) {
+    if (vecs >= 8) {
+        // by as many lanes as a row has of them
+        constexpr uint32_t kPer = sizeof(zero) < 16 ? 16 / sizeof(zero) : 1, kWide = sizeof(zero) * kPer / 16;
+        const uint32_t wide = vecs / kPer * kWide, lanes = wide > 16 ? 32 : wide > 8 ? 16 : 8;
+        const uint32_t l = lane & (lanes - 1);
+        for (uint32_t r = r0 + lane / lanes; r < r0 + rows; r += 32 / lanes) {
             const uint32_t v = touched(r) ? kNone : row_of(r);
             if (v == kNone) continue;
             Pack<TO, VEC>* dst = at(v);
+            const uint32_t skew = (uint32_t)(reinterpret_cast<uintptr_t>(dst) / sizeof(zero)) % kPer;
+            const uint32_t head = (kPer - skew) % kPer, body = (vecs - head) / kPer, tail = (vecs - head) % kPer;
+            if (l < head) dst[l] = zero;
+            if (l < tail) dst[vecs - tail + l] = zero;
+            uint4* mid = reinterpret_cast<uint4*>(dst + head);
 #pragma unroll 4
-            for (uint32_t c = lane; c < vecs; c += 32) dst[c] = zero;
+            for (uint32_t c = l; c < body * kWide; c += lanes) mid[c] = make_uint4(0u, 0u, 0u, 0u);
         }
     } else {
         for (uint32_t i = lane; i < rows * vecs; i += 32) {
@@ -524,11 +535,14 @@ inline int64_t most_rows(const IndexArgs& x) {
 inline bool plan_own(const IndexArgs& index, int64_t width, int out_type, int vec, OwnArgs& o, dim3& grid) {
     if (index.n > kOwnTokens) return false;
     const int64_t rows = most_rows(index);
-    // A row by as many lanes as it has vectors, in one part; with more tokens at most a warp
-    // a part, so that a frequent row's are shared by more CTAs (16384 tokens, u^3 over 1024
-    // rows of 1024: 34 us, against 69 us in one part; 48 tokens over 512 rows of 256: 6.0 us
-    // in two parts, 5.5 us in one).
-    const int most = index.n < 1024 ? 9 : 5;
+    // A row by as many lanes as it has vectors, in one part; with more tokens in parts of a
+    // warp or 128 columns, so that a frequent row's are shared by more CTAs (16384 tokens, u^3
+    // over 1024 rows of 1024 bf16: 35 us, against 69 us in one part; 4034 fp32 columns at odd
+    // offsets, 12000 tokens over 2048 rows: 117 us by a warp, 93 in parts of 128 columns, 76
+    // of 256, but 16000 u^3 over 200 rows of 513: 39, 52 and 78; 48 tokens over 512 rows of
+    // 256: 6.0 us in two parts, 5.5 us in one).
+    int most = index.n < 1024 ? 9 : 5;
+    while ((vec << most) < 128) ++most;
     o.log2L = 0;
     while (o.log2L < most && ((int64_t)vec << o.log2L) < width) ++o.log2L;
     o.part = (int64_t)vec << o.log2L;
