@@ -13,7 +13,7 @@
 // launch with a barrier over the grid instead takes 12.3 us for 3 x 512 x 2000 fp32,
 // the two, of which the second is set up while the first runs, 10.3 us; more blocks than
 // are resident at once, for the SMs to take as they get free, lose the cache's order
-// (192 MB of bf16: 112 us against 96).  More tensors than a table holds take both
+// (192 MB of bf16: 112 us against 93).  More tensors than a table holds take both
 // launches for each table.
 //
 // The squares of 16 elements are added in fp32, the sums of 16 in pairs of fp32 numbers
