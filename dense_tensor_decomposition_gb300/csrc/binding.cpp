@@ -43,12 +43,16 @@ void check_device(const at::Tensor& t, const at::Tensor& like, const char* name)
     TORCH_CHECK_VALUE(t.get_device() == like.get_device(), name, " must be on the other tensors' device");
 }
 
-// the stream of a call, and the guard that makes PyTorch allocate for it
+// the stream of a call; for as long as this lives the tensors' device is the current one
+// (a null handle means the current device's default stream), and PyTorch allocates for
+// the stream
 struct Stream {
     std::optional<c10::cuda::CUDAStreamGuard> guard;
+    c10::cuda::OptionalCUDAGuard device;
     void* handle;
     Stream(PyObject* o, const at::Tensor& t) {
         if (o == Py_None) {
+            device.set_device(t.device());
             handle = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
         } else {
             handle = PyLong_AsVoidPtr(o);
