@@ -586,7 +586,7 @@ inline bool always_owned(const IndexArgs& index, int64_t width) {
 // joins the tiles' crossing runs
 template <typename TO, int VEC>
 cudaError_t join(const SumArgs& s, cudaStream_t st) {
-    if (s.tiles < 2) return cudaGetLastError();
+    if (s.tiles < 2) return cudaSuccess;
     const dim3 grid((unsigned)cdiv(s.tiles, kThreads / 32), (unsigned)cdiv(s.a.width, 32 * VEC), s.a.index.d);
     return launch_early(join_kernel<TO, VEC>, grid, kThreads, 0, st, s);
 }
