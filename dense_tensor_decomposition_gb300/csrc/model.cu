@@ -283,18 +283,20 @@ struct Entry {
     Rows<G> rows;
 };
 
-// entry p of a list of entries of 16 or 32 bytes
+// Entry p of a list of entries of 16 or 32 bytes.  By plain loads: the sort before this
+// launch writes the list, and loads by the read-only path need not stay behind
+// after_previous().
 template <int G>
 __device__ __forceinline__ Entry<G> entry_at(const char* list, int64_t p) {
     constexpr int kBytes = G > kFewGroups ? 32 : 16;
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(list + p * kBytes));
+    const uint4 a = *reinterpret_cast<const uint4*>(list + p * kBytes);
     Entry<G> e;
     e.x = a.x;
     e.g = __uint_as_float(a.y);
     e.rows.w[0] = a.z;
     e.rows.w[1] = a.w;
     if constexpr (G > kFewGroups) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(list + p * kBytes + 16));
+        const uint2 b = *reinterpret_cast<const uint2*>(list + p * kBytes + 16);
         e.rows.w[2] = b.x;
         e.rows.w[3] = b.y;
     }

@@ -1,7 +1,10 @@
 """Host code of the sampled operators that no entry point shows by itself, in small
 programs that are compiled here and run on the CPU."""
 import os
+import re
 import subprocess
+
+import pytest
 
 from dense_tensor_decomposition_gb300 import _build
 
@@ -30,3 +33,11 @@ int main() {
 }
 """)
     assert out == ["1", "1"]
+
+
+@pytest.mark.parametrize("name", ["rows.cu", "sort.cu", "model.cu", "gradnorm.cu", "rows.cuh", "sums.cuh", "types.cuh"])
+def test_no_loads_by_the_read_only_path(name):
+    """These kernels begin before the kernel that writes what they read is done: such loads
+    are not kept behind their wait for it."""
+    with open(os.path.join(_build.CSRC, name)) as f:
+        assert not re.search(r"__ldg|\.nc\b|__restrict__", f.read())
