@@ -551,7 +551,7 @@ cudaError_t grad_cached(const RowSumArgs& a, cudaStream_t s) {
 template <int CS, bool kRagged, bool kMany>
 cudaError_t grad_staged(StagedArgs& a, cudaStream_t st) {
     const RowSumArgs& r = a.s.a;
-    const SortPlan p = plan_sort(r.index, kMany ? 32 : 16);
+    const SortPlan p = plan_sort(r.index, kMany ? 32 : 16, sort_sms());
     a.s.part = reinterpret_cast<float*>(static_cast<char*>(r.ws) + p.total());
     int rows = 0;
     for (int m = 0; m < r.index.d; ++m) rows = a.tables[m].rows > rows ? a.tables[m].rows : rows;
@@ -639,7 +639,7 @@ bool tables_may_pay(const IndexArgs& x, int64_t width, int vec) {
 // for the largest entries that the sums from shared memory can sort
 size_t entries_grad_workspace_bytes(const IndexArgs& index, int64_t width) {
     if (always_owned(index, width) && !tables_may_pay(index, width, 1)) return 0;
-    return plan_sort(index, index.d - 1 > kFewGroups ? 32 : 16).total() + part_bytes(index, width);
+    return plan_sort(index, index.d - 1 > kFewGroups ? 32 : 16, kSms).total() + part_bytes(index, width);
 }
 
 cudaError_t launch_entries_grad(const RowSumArgs& a, cudaStream_t s) {

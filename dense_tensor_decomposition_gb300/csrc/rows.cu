@@ -297,7 +297,7 @@ cudaError_t launch_lookup(const LookupArgs& a, int type, cudaStream_t s) {
 
 size_t lookup_grad_workspace_bytes(const IndexArgs& index, int64_t width) {
     if (always_owned(index, width)) return 0;
-    return plan_sort(index, sizeof(uint2)).total() + part_bytes(index, width);
+    return plan_sort(index, sizeof(uint2), kSms).total() + part_bytes(index, width);
 }
 
 cudaError_t launch_lookup_grad(const RowSumArgs& a, cudaStream_t s) {

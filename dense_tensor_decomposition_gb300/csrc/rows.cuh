@@ -16,7 +16,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 constexpr size_t elem_bytes(int type) { return type == MTTKRP_F32 ? 4 : 2; }
 
-constexpr int kSms = 152;
+constexpr int kSms = 152;       // of a GB300; what a process is given may be fewer
 
 // Dynamic shared memory that a CTA may ask for, of the 227 KB that it can have.
 constexpr size_t kMaxSmem = 226 * 1024;

@@ -263,7 +263,19 @@ __global__ void __cluster_dims__(kFillCluster, 1, 1) __launch_bounds__(kSortThre
 
 }  // namespace
 
-SortPlan plan_sort(const IndexArgs& x, int entry_bytes) {
+int sort_sms() {
+    static std::atomic<int> cached[64];     // by device; setting it twice is harmless
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && cached[dev] > 0) return cached[dev];
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return kSms;      // the launch will tell
+    if (sms > kSms) sms = kSms;
+    if (dev < 64) cached[dev] = sms;
+    return sms;
+}
+
+SortPlan plan_sort(const IndexArgs& x, int entry_bytes, int sms) {
     SortPlan p;
     // digits cover the rows and, above them, one value for tokens that take no part
     int64_t most = 0;
@@ -278,7 +290,7 @@ SortPlan plan_sort(const IndexArgs& x, int entry_bytes) {
     // (20000 tokens in two passes: 19 us in tiles of 1024, 26 us in tiles of 4096; 524288: 29
     // us in tiles of 4096, 33 us in tiles of 8192).
     const int64_t n = x.n > 0 ? x.n : 1;
-    const int64_t most_ctas = kSms / x.d;
+    const int64_t most_ctas = sms > x.d ? sms / x.d : 1;
     const int64_t few = most_ctas < 64 ? most_ctas : 64;
     p.items = n <= few * kSortThreads ? 1 : n <= most_ctas * kSortThreads * 4 ? 4 : 8;
     const int64_t tile = kSortThreads * p.items;

@@ -41,7 +41,11 @@ struct SortPlan {
     size_t total() const { return 2 * pairs + counts; }
 };
 
-SortPlan plan_sort(const IndexArgs& index, int entry_bytes);
+// The sort's CTAs wait for one another, so there are at most `sms` of them: kSms for the
+// workspace, which fewer never outgrow, sort_sms() for a launch.
+SortPlan plan_sort(const IndexArgs& index, int entry_bytes, int sms);
+// SMs of the current device, at most kSms
+int sort_sms();
 // tables: nullptr, or one for each index column, for entries of 16 or 32 bytes
 cudaError_t sort_tokens(const IndexArgs& index, const SortPlan& p, void* ws, const Tables* tables, const float* g,
                         Sorted& sorted, cudaStream_t s);

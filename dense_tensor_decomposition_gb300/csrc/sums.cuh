@@ -613,7 +613,7 @@ cudaError_t sums_by(const RowSumArgs& a, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         return launch_early(kernel, grid, kOwnThreads, smem, st, o);
     }
-    const SortPlan p = plan_sort(a.index, sizeof(uint2));
+    const SortPlan p = plan_sort(a.index, sizeof(uint2), sort_sms());
     SumArgs s;
     s.a = a;
     s.part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + p.total());

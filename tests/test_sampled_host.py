@@ -41,3 +41,26 @@ def test_no_loads_by_the_read_only_path(name):
     are not kept behind their wait for it."""
     with open(os.path.join(_build.CSRC, name)) as f:
         assert not re.search(r"__ldg|\.nc\b|__restrict__", f.read())
+
+
+def test_the_sort_fits_the_sms_there_are(tmp_path):
+    """Its CTAs wait for one another: no more of them than SMs, together with all tokens, in no
+    larger a workspace than the one asked for."""
+    out = run(tmp_path, r"""
+#include <cstdio>
+#include "sort.cu"
+int main() {
+    for (int sms : {8, 20, 66, 132, 148, 152})
+        for (int d : {1, 2, 3, 6, 8})
+            for (int64_t n : {1, 1023, 20000, 70001, 262144, 622593, 1300003, 40000000})
+                for (int64_t rows : {1, 900, 1 << 20}) {
+                    mk::IndexArgs x{nullptr, 4, d, n, d, {}};
+                    for (int m = 0; m < d; ++m) x.rows[m] = rows;
+                    const mk::SortPlan p = mk::plan_sort(x, 16, sms), most = mk::plan_sort(x, 16, mk::kSms);
+                    if (p.ctas < 1 || p.ctas * d > sms || p.ctas * p.per_cta < n || p.total() > most.total())
+                        printf("%d_%d_%lld ", sms, d, (long long)n);
+                }
+    printf("done");
+}
+""")
+    assert out == ["done"]
