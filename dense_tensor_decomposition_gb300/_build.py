@@ -4,15 +4,18 @@ module _binding.so with the host compiler.
 Every source under csrc/ is compiled in parallel into _build/, then the .cu
 files are linked into a shared library next to this file, and binding.cpp,
 which calls that library, into a module next to it.  Rebuilds only when a
-source or header is newer than what it goes into.
+source or header is newer than what it goes into; the module also when it was
+built for another Python or PyTorch.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -42,16 +45,43 @@ def _binding_source():
     return os.path.join(CSRC, "binding.cpp")
 
 
-def _deps():
-    return _sources() + [_binding_source()] + sorted(glob.glob(os.path.join(CSRC, "*.h"))) + \
-        sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "mttkrp.h")]
+def _headers():
+    return sorted(glob.glob(os.path.join(CSRC, "*.h"))) + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+        [os.path.join(INCLUDE, "mttkrp.h")]
+
+
+def _newer(built: str, sources) -> bool:
+    """Whether `built` exists and no source is newer."""
+    return os.path.exists(built) and all(os.path.getmtime(p) <= os.path.getmtime(built) for p in sources)
+
+
+def _fits() -> str:
+    """The Python and PyTorch that a binding built now fits."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:     # not installed as a package
+        import torch
+        version = torch.__version__
+    return f"{sys.implementation.cache_tag} {sysconfig.get_platform()} torch {version}"
+
+
+def _fits_file() -> str:
+    return os.path.join(BUILD, "binding.fits")
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, _sources() + _headers())
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer(BINDING, [_binding_source()] + _headers()) or not os.path.exists(_fits_file()):
+        return False
+    with open(_fits_file()) as f:
+        return f.read() == _fits()
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _library_up_to_date() and _binding_up_to_date()
 
 
 def _torch_flags():
@@ -75,12 +105,12 @@ def _run(cmd, what):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
+    library, module = force or not _library_up_to_date(), force or not _binding_up_to_date()
+    if not library and not module:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
-
-    flags, links = _torch_flags()
+    flags, links = _torch_flags() if module else ([], [])
 
     def compile_one(src):
         name = os.path.basename(src)
@@ -94,16 +124,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(res.stderr)
         return obj
 
-    srcs = _sources() + [_binding_source()]
+    srcs = ([_binding_source()] if module else []) + (_sources() if library else [])
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, len(srcs))) as ex:
-        *objs, binding = list(ex.map(compile_one, srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    _run([cc] + ARCH + ["-shared", "-o", tmp] + objs, "linking the library")
-    os.replace(tmp, LIB)
-    tmp = BINDING + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, binding, f"-L{HERE}", "-lmttkrp", "-Wl,-rpath,$ORIGIN"] + links,
-         "linking the binding")
-    os.replace(tmp, BINDING)
+        objs = list(ex.map(compile_one, srcs))
+    binding = objs.pop(0) if module else None
+    if library:
+        tmp = LIB + f".tmp{os.getpid()}"
+        _run([cc] + ARCH + ["-shared", "-o", tmp] + objs, "linking the library")
+        os.replace(tmp, LIB)
+    if module:
+        tmp = BINDING + f".tmp{os.getpid()}"
+        _run(["g++", "-shared", "-o", tmp, binding, f"-L{HERE}", "-lmttkrp", "-Wl,-rpath,$ORIGIN"] + links,
+             "linking the binding")
+        os.replace(tmp, BINDING)
+        with open(_fits_file(), "w") as f:
+            f.write(_fits())
     return LIB
 
 
