@@ -5,13 +5,14 @@ Every source under csrc/ is compiled in parallel into _build/, then the .cu
 files are linked into a shared library next to this file, and binding.cpp,
 which calls that library, into a module next to it.  Rebuilds only when a
 source or header is newer than what it goes into; the module also when it was
-built for another Python or PyTorch.
+built for another Python or PyTorch.  Without PyTorch there is only the library.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
 import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -55,8 +56,10 @@ def _newer(built: str, sources) -> bool:
     return os.path.exists(built) and all(os.path.getmtime(p) <= os.path.getmtime(built) for p in sources)
 
 
-def _fits() -> str:
-    """The Python and PyTorch that a binding built now fits."""
+def _fits() -> str | None:
+    """The Python and PyTorch that a binding built now fits; None without PyTorch."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     try:
         version = importlib.metadata.version("torch")
     except importlib.metadata.PackageNotFoundError:     # not installed as a package
@@ -74,10 +77,13 @@ def _library_up_to_date() -> bool:
 
 
 def _binding_up_to_date() -> bool:
+    fits = _fits()
+    if fits is None:
+        return True                 # cannot be built
     if not _newer(BINDING, [_binding_source()] + _headers()) or not os.path.exists(_fits_file()):
         return False
     with open(_fits_file()) as f:
-        return f.read() == _fits()
+        return f.read() == fits
 
 
 def up_to_date() -> bool:
@@ -105,7 +111,8 @@ def _run(cmd, what):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    library, module = force or not _library_up_to_date(), force or not _binding_up_to_date()
+    library, fits = force or not _library_up_to_date(), _fits()
+    module = fits is not None and (force or not _binding_up_to_date())
     if not library and not module:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -138,7 +145,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
              "linking the binding")
         os.replace(tmp, BINDING)
         with open(_fits_file(), "w") as f:
-            f.write(_fits())
+            f.write(fits)
     return LIB
 
 

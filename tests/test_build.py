@@ -1,7 +1,8 @@
-"""What build() does again (nothing is compiled here: the commands are noted and leave empty
-files)."""
+"""What build() does again, and what it does without PyTorch (nothing is compiled here: the
+commands are noted and leave empty files)."""
 import importlib.metadata
 import os
+import sys
 
 import pytest
 
@@ -44,4 +45,16 @@ def test_another_pytorch(commands, monkeypatch):
     assert not _build.up_to_date()
     _build.build()
     assert commands == [f"compiling {_build._binding_source()}", "linking the binding"]
+    assert _build.up_to_date()
+
+
+def test_without_pytorch(commands, monkeypatch):
+    """The C library needs no PyTorch, and neither does building it."""
+    def missing(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(importlib.metadata, "version", missing)
+    monkeypatch.setitem(sys.modules, "torch", None)             # import torch raises
+    _build.build()
+    assert "linking the library" in commands and "linking the binding" not in commands
     assert _build.up_to_date()
