@@ -81,6 +81,11 @@ at::Tensor workspace(size_t bytes, const at::Tensor& like) {
 
 void* pointer(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
+// tells autograd that a caller's tensor holds something else now
+void written(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* result(int rc, const at::Tensor& t) { return rc == MTTKRP_OK ? THPVariable_Wrap(t) : PyLong_FromLong(rc); }
 
 // int32 or int64 indices: contiguous of any shape, or one-dimensional with any stride
@@ -139,6 +144,7 @@ PyObject* embedding(PyObject*, PyObject* const* args, Py_ssize_t) {
     }
     const int rc = mttkrp_embedding(table.data_ptr(), rows, width, stride, code, x.ptr, x.n, x.stride, x.bytes,
                                     (float)number(args[2]), out.data_ptr(), out_stride, stream.handle);
+    if (rc == MTTKRP_OK && args[3] != Py_None) written(out);
     return result(rc, out);
     END_HANDLE_TH_ERRORS
 }
@@ -179,6 +185,7 @@ PyObject* embedding_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
     const int rc = mttkrp_embedding_grad(x.ptr, x.n, x.stride, x.bytes, grad.data_ptr(), code, stride, rows, width,
                                          (float)number(args[3]), accumulate, out.data_ptr(), out_code, out_stride,
                                          pointer(ws), need, stream.handle);
+    if (rc == MTTKRP_OK && args[4] != Py_None) written(out);
     return result(rc, out);
     END_HANDLE_TH_ERRORS
 }
@@ -249,6 +256,7 @@ PyObject* cp_entries(PyObject*, PyObject* const* args, Py_ssize_t) {
     }
     const int rc = mttkrp_cp_entries(f.d, f.dims.data(), f.R, f.ptrs.data(), f.code, c.data_ptr(), n,
                                      (int)c.element_size(), static_cast<float*>(out.data_ptr()), stream.handle);
+    if (rc == MTTKRP_OK && args[2] != Py_None) written(out);
     return result(rc, out);
     END_HANDLE_TH_ERRORS
 }
@@ -288,6 +296,8 @@ PyObject* cp_entries_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
                                           (int)c.element_size(), static_cast<const float*>(g.data_ptr()), ptrs.data(),
                                           pointer(ws), need, stream.handle);
     if (rc != MTTKRP_OK) return PyLong_FromLong(rc);
+    if (args[3] != Py_None)
+        for (const at::Tensor& o : outs) written(o);
     PyObject* list = PyList_New(f.d);
     if (list == nullptr) throw python_error();
     for (int m = 0; m < f.d; ++m) {
@@ -322,12 +332,13 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t) {
         numels[k] = t.numel();
     }
     const bool clip = args[1] != Py_None;
+    std::optional<List> outs;
     if (args[3] != Py_None) {
-        const List outs(args[3], "outs must be a sequence");
-        TORCH_CHECK_VALUE(outs.n == n, "outs must hold one tensor per input");
+        outs.emplace(args[3], "outs must be a sequence");
+        TORCH_CHECK_VALUE(outs->n == n, "outs must hold one tensor per input");
         optrs.resize(n);
         for (int k = 0; k < n; ++k) {
-            const at::Tensor& o = tensor(outs[k], "outs");
+            const at::Tensor& o = tensor((*outs)[k], "outs");
             check_device(o, first, "outs");
             TORCH_CHECK_VALUE(o.scalar_type() == THPVariable_Unpack(list[k]).scalar_type() && o.numel() == numels[k] &&
                                   o.is_contiguous(),
@@ -345,6 +356,8 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t) {
                                                 (float)number(args[2]), to, pointer(ws), need, stream.handle)
                         : mttkrp_grad_norm(n, ptrs.data(), numels.data(), codes.data(), to, pointer(ws), need,
                                            stream.handle);
+    if (rc == MTTKRP_OK && clip)
+        for (int k = 0; k < n; ++k) written(THPVariable_Unpack(outs ? (*outs)[k] : list[k]));
     return result(rc, norm);
     END_HANDLE_TH_ERRORS
 }

@@ -59,3 +59,34 @@ def test_masked_rows_are_zero_whatever_the_scale(width, dtype, scale):
     assert torch.all(bits == 0)                                          # +0
     want = (table[idx[inside]].float() * scale).to(table.dtype)
     assert torch.equal(out[inside].nan_to_num(nan=7.0), want.nan_to_num(nan=7.0))
+
+
+def test_results_written_in_place_are_seen_by_autograd():
+    gen = generator(2)
+    table, idx = whole(gen, (9, 12), torch.float32), torch.tensor([1, 2, 8], device="cuda")
+    A, c = [whole(gen, (n, 12), torch.float32) for n in (5, 6)], torch.zeros((3, 2), device="cuda", dtype=torch.int32)
+    g = torch.ones(3, device="cuda")
+    rows, sums, x = torch.empty((3, 12), device="cuda"), torch.empty((9, 12), device="cuda"), torch.empty(3, device="cuda")
+    outs, scaled = [torch.empty_like(a) for a in A], torch.empty_like(table)
+    for call, written, read in (
+            (lambda: mk.embedding(table, idx, out=rows), [rows], [table, idx]),
+            (lambda: mk.embedding_grad(idx, rows, 9, out=sums), [sums], [idx, rows]),
+            (lambda: mk.embedding_grad(idx, rows, 9, out=sums, accumulate=True), [sums], [idx, rows]),
+            (lambda: mk.cp_entries(A, c, out=x), [x], A),
+            (lambda: mk.cp_entries_grad(A, c, g, outs=outs), outs, A + [g]),
+            (lambda: mk.clip_grad_norm([table], 1.0, outs=[scaled]), [scaled], [table]),
+            (lambda: mk.clip_grad_norm([table, sums], 1.0), [table, sums], []),
+            (lambda: mk.grad_norm([table]), [], [table])):
+        before = [t._version for t in written], [t._version for t in read]
+        call()
+        assert [t._version for t in written] == [v + 1 for v in before[0]]
+        assert [t._version for t in read] == before[1]
+    w = torch.ones(12, device="cuda", requires_grad=True)
+    y = (w * table).sum()
+    mk.clip_grad_norm([table], 0.5)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        free = torch.ones((3, 12), device="cuda")
+    mk.embedding(table, idx, out=free)                                    # has no version
+    assert torch.equal(free, table[idx])
