@@ -32,6 +32,8 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;                          // 16-byte vectors a thread has in flight, a unit each
 constexpr int kUnitVecs = kThreads;                 // 8 KB
+constexpr int kLog2UnitBytes = 13;
+static_assert(kUnitVecs * 16 == 1 << kLog2UnitBytes);
 constexpr int kMaxBlocks = 2048;                    // most sums a table
 constexpr int64_t kCached = 64 << 20;               // bytes of the first read to find in L2 at the second
 constexpr int kSmallTable = 32, kMiddleTable = 400, kLargeTable = 1024;
@@ -342,8 +344,11 @@ int fill(Table<N>& t, int n, int k, const void* const* tensors, const int64_t* n
         t.numel[t.n] = numels[i];
         t.type[t.n] = (uint8_t)types[i];
         t.first[t.n] = (uint32_t)units;
-        const int e = types[i] == MTTKRP_F32 ? 4 : 2;
-        units += cdiv(numels[i] + (int64_t)(reinterpret_cast<uintptr_t>(tensors[i]) & 15) / e, kUnitVecs * 16 / e);
+        // elements from the first vector's start, in units (by shifts: about 200 tensors a call)
+        const int shift = types[i] == MTTKRP_F32 ? 2 : 1;
+        const int64_t to = numels[i] + (int64_t)((reinterpret_cast<uintptr_t>(tensors[i]) & 15) >> shift);
+        const int64_t unit = kUnitVecs * 16 >> shift;
+        units += (to + unit - 1) >> (kLog2UnitBytes - shift);
         ++t.n;
     }
     t.units = (uint32_t)units;

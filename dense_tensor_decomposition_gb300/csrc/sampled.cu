@@ -1,5 +1,9 @@
 // Entry points of the operators of a sampled fit (include/mttkrp.h): checks on the host,
 // then the launches of rows.cu, model.cu and gradnorm.cu.
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "api.h"
 #include "rows.h"
 
@@ -11,7 +15,8 @@ constexpr int64_t kMaxWidth = 65536;
 
 size_t type_bytes(int type) { return type == MTTKRP_F32 ? 4 : 2; }
 bool type_ok(int type) { return type == MTTKRP_F32 || type == MTTKRP_BF16 || type == MTTKRP_F16; }
-bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+// a: a power of two
+bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // bytes from the first to behind the last element of rows x width, rows `stride` apart
 size_t span_bytes(int64_t rows, int64_t width, int64_t stride, size_t elem) {
@@ -70,6 +75,43 @@ int check_model(int d, const int64_t* dims, int64_t R, const void* const* factor
     return MTTKRP_OK;
 }
 
+// A result that overlaps another one, or a tensor that is not its own, would be written or
+// read while another CTA writes it.  The results are put in order of their addresses, then
+// every tensor looks among them; a result has its tensor's size, so that one that is its
+// tensor cannot meet another result's (in_place: all are).
+int check_disjoint(int n, const void* const* tensors, const int64_t* numels, const int* types, void* const* outs,
+                   bool in_place) {
+    struct Span {
+        uintptr_t begin, end;
+        int k;
+    };
+    constexpr int kFew = 512;
+    Span few[kFew];
+    std::unique_ptr<Span[]> many;
+    if (n > kFew && !(many = std::unique_ptr<Span[]>(new (std::nothrow) Span[n])))
+        return fail(MTTKRP_ERR_HOST_ALLOC, "no host memory to look at %d tensors", n);
+    Span* const spans = many ? many.get() : few;
+    int used = 0;
+    for (int k = 0; k < n; ++k) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(outs[k]);
+        if (numels[k] != 0) spans[used++] = Span{at, at + numels[k] * type_bytes(types[k]), k};
+    }
+    std::sort(spans, spans + used, [](const Span& a, const Span& b) { return a.begin < b.begin; });
+    for (int i = 1; i < used; ++i)
+        if (spans[i].begin < spans[i - 1].end)
+            return fail(MTTKRP_ERR_INVALID, "results %d and %d overlap", std::min(spans[i - 1].k, spans[i].k),
+                        std::max(spans[i - 1].k, spans[i].k));
+    for (int k = 0; k < n && !in_place; ++k) {
+        if (numels[k] == 0) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(tensors[k]), end = at + numels[k] * type_bytes(types[k]);
+        // the last result that begins before the tensor's end
+        const Span* s = std::lower_bound(spans, spans + used, end, [](const Span& a, uintptr_t x) { return a.begin < x; });
+        if (s != spans && (--s)->end > at && s->k != k)
+            return fail(MTTKRP_ERR_INVALID, "result %d overlaps tensor %d", s->k, k);
+    }
+    return MTTKRP_OK;
+}
+
 int check_tensors(int n, const void* const* tensors, const int64_t* numels, const int* types, void* const* outs,
                   const float* norm, const void* ws, size_t ws_bytes) {
     if (n < 0 || n > (1 << 20)) return fail(MTTKRP_ERR_INVALID, "n=%d tensors outside [0, 2^20]", n);
@@ -77,6 +119,10 @@ int check_tensors(int n, const void* const* tensors, const int64_t* numels, cons
         return fail(MTTKRP_ERR_INVALID, "NULL tensors, numels or types");
     if (norm == nullptr || !aligned_to(norm, 4)) return fail(MTTKRP_ERR_INVALID, "norm must be a 4-byte aligned pointer");
     int64_t total = 0;
+    // Whether the results, and those tensors that are not their own results, are apart as most
+    // lists are: the results one behind the other, the tensors outside of all they span.
+    bool ascending = true, in_place = true;
+    uintptr_t first = 0, behind = 0;
     for (int k = 0; k < n; ++k) {
         if (!type_ok(types[k])) return fail(MTTKRP_ERR_INVALID, "tensor %d: unknown type %d", k, types[k]);
         if (numels[k] < 0 || numels[k] > kMaxNumel - total)
@@ -91,7 +137,17 @@ int check_tensors(int n, const void* const* tensors, const int64_t* numels, cons
             return fail(MTTKRP_ERR_INVALID, "result %d: NULL or not %zu-byte aligned", k, e);
         if (outs[k] != tensors[k] && overlap(outs[k], numels[k] * e, tensors[k], numels[k] * e))
             return fail(MTTKRP_ERR_INVALID, "result %d overlaps its tensor without being it", k);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(outs[k]);
+        first = behind == 0 ? at : first;
+        ascending = ascending && at >= behind;
+        behind = at + numels[k] * e;
+        in_place = in_place && outs[k] == tensors[k];
     }
+    bool outside = true;
+    for (int k = 0; k < n && !in_place && ascending && outside; ++k)
+        outside = !overlap(tensors[k], numels[k] * type_bytes(types[k]), reinterpret_cast<const void*>(first), behind - first);
+    if (!ascending || !outside)
+        if (int rc = check_disjoint(n, tensors, numels, types, outs, in_place)) return rc;
     return check_workspace(ws, ws_bytes, grad_norm_workspace_bytes(n));
 }
 
