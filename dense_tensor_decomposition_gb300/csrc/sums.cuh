@@ -569,8 +569,11 @@ inline size_t part_bytes(const IndexArgs& x, int64_t width) {
 }
 
 // Zeros of more than this many bytes are worth a launch in which the SMs share them as
-// they get free, for few tokens too.
-constexpr int64_t kFillBytes = 96 << 20;
+// they get free, for few tokens too.  (4000 tokens into fp32 rows of 256 columns, by
+// own_kernel and so: 64 MB 15 and 26 us, 96 MB 20 and 29, 128 MB 25 and 29, 192 MB 36 and
+// 35, 400 MB 69 and 63; 16384 tokens: 96 MB 24 and 32, 128 MB 31 and 33, 192 MB 41 and 38;
+// 4000 tokens, 33 columns: 96 MB 25 and 31, 128 MB 32 and 32, 192 MB 72 and 36.)
+constexpr int64_t kFillBytes = 128 << 20;
 
 // whether own_kernel takes the sums whatever the alignment of the rows (one launch that
 // needs no workspace)

@@ -149,12 +149,14 @@ def test_entries_of_many_samples(dims, R, S):
 
 # ---------------------------------------------------------------- large results of few tokens
 
-# results of more than 96 MB: zeros by many CTAs while a cluster sorts (a tile of 4096 tokens
-# a CTA), also where the bytes are no multiple of 16; at an odd offset the rows have owners,
-# or where they are too many the tokens are sorted by the whole GPU
+# results of more than 128 MB: zeros by many CTAs while a cluster sorts (a tile of 4096 tokens
+# a CTA), also where the bytes are no multiple of 16; smaller ones, and at an odd offset, the
+# rows have owners, or where they are too many the tokens are sorted by the whole GPU
 @pytest.mark.parametrize("offset", [0, 1])
 @pytest.mark.parametrize("rows,width,dtype", [(200003, 127, "float32"), (400001, 127, "float16"), (200000, 128, "float32"),
-                                              (800001, 65, "bfloat16"), (2000000, 16, "float32")])
+                                              (800001, 65, "bfloat16"), (2000000, 16, "float32"),
+                                              (270001, 127, "float32"), (540001, 127, "float16"), (270000, 128, "float32"),
+                                              (1100001, 65, "bfloat16"), (2200000, 16, "float32")])
 @pytest.mark.parametrize("n,skew", [(5000, 3), (16384, 1), (16384, 40), (16383, 2), (4097, 1)])
 def test_gradient_of_few_tokens_into_a_large_table(n, skew, rows, width, dtype, offset):
     gen = generator(n + rows)
