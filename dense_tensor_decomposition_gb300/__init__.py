@@ -557,6 +557,11 @@ def ttm_multi(X, modes, Ms, outs=None, stream=None, path: str = "auto", workspac
 
 # ---------------------------------------------------------------------------
 # Operators of a sampled fit
+#
+# None of them records a gradient: what they return requires none, whatever their
+# inputs do (the gradients are operators of their own).  Tensors that they are given to
+# write into (`out`, `outs`, those that clipping scales) have their version raised, as
+# after any operation in place.
 # ---------------------------------------------------------------------------
 
 _sampled = None             # the module that checks, allocates and calls for these operators
@@ -588,7 +593,8 @@ def embedding(table, idx, scale: float = 1.0, out=None, stream=None):
     (rows x width, float32, bfloat16 or float16, rows any distance apart) for int32
     or int64 indices of any shape (contiguous, or one-dimensional with any stride).
     An index outside the table, e.g. a negative mask, gives a row of zeros.  Returns
-    idx.shape + (width,) of the table's type, written into `out` when given."""
+    idx.shape + (width,) of the table's type, written into `out` when given.  The
+    result is detached from the table: its gradient is `embedding_grad`."""
     r = (_sampled or load_binding()).embedding(table, idx, scale, out, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_embedding")
@@ -617,7 +623,8 @@ def cp_entries(factors, coords, out=None, stream=None):
     (mttkrp_cp_entries): factors I_n x R of one type (float32, bfloat16 or
     float16), coords samples x d (int32 or int64).  Returns `samples` float32 values;
     0 where a coordinate is out of range.  Component weights go into a factor, or in
-    as a factor with one row."""
+    as a factor with one row.  The result is detached from the factors: their
+    gradients are `cp_entries_grad`."""
     r = (_sampled or load_binding()).cp_entries(factors, coords, out, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_cp_entries")
@@ -648,8 +655,10 @@ def grad_norm(tensors, stream=None):
 def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, stream=None):
     """Multiplies every tensor of a list by min(1, max_norm / (norm + eps)), norm
     being `grad_norm` of the list (mttkrp_clip_grad_norm), in place or, when `outs` is
-    given, into its tensors (each of its input's size and type).  Returns the norm
-    before clipping as a float32 scalar on the device."""
+    given, into its tensors (each of its input's size and type).  What is written may
+    not overlap: a tensor that is twice in the list is refused, and so is a result in
+    another tensor's place.  Returns the norm before clipping as a float32 scalar on the
+    device."""
     r = (_sampled or load_binding()).clip_grad_norm(tensors, float(max_norm), eps, outs, _handle(stream))
     if type(r) is int:
         _check(r, "mttkrp_clip_grad_norm")

@@ -41,7 +41,10 @@ constexpr int kSmallTable = 32, kMiddleTable = 400, kLargeTable = 1024;
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // 29 bytes a tensor: the large table is just below the 32764 bytes that a
-// kernel's arguments can hold, the others spare shorter lists its copy.
+// kernel's arguments can hold, the others spare shorter lists its copy.  (By the middle
+// table and by the large one: 100 tensors 10.5 and 11.6 us, 400 tensors of 64 elements
+// 19.0 and 21.0, of 250000 65.6 and 69.9; by the small one and by the middle one, 32
+// tensors 8.1 and 8.2 us.)
 template <int N>
 struct Table {
     const void* in[N];

@@ -421,7 +421,9 @@ __global__ void __launch_bounds__(kStageThreads, 1) staged_sum_kernel(const __gr
 // What a step costs an SM, in cycles, by measurement on GB300: a gathered row slice of
 // CS columns from shared memory (bank conflicts between rows of less than 128 bytes
 // included) and from the L2 cache (32 columns of fp32), the rest of a sample and slice,
-// and the start of a slice's tables with the load of a row.
+// and the start of a slice's tables with the load of a row.  Factors of 16 bits, and in
+// launch_entries() ranks that are read one column a load, are planned with the same
+// figures (tables hold fp32 whatever the factors' type).
 constexpr double kGather32 = 1.0, kGather16 = 0.75, kGather8 = 0.53;
 constexpr double kGatherCache = 4.5;
 constexpr double kSample = 1.3;

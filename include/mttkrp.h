@@ -338,10 +338,14 @@ int mttkrp_ttm_multi(int d, const int64_t* dims, const float* X, int nmodes, con
  * with clipping.  (No counterpart on the pages: they fit with full sweeps.)
  *
  * Types: MTTKRP_F32, MTTKRP_BF16, MTTKRP_F16 for tables, factors and gradients;
- * products and sums are fp32 (the norm's: fp32 over 16 elements, then fp64), each
- * result is rounded once.  Pointers need the alignment of their element; rows that
- * start at multiples of 16 bytes (fp32 results of 16-bit gradients: 32) are read
- * and written in vectors, others one element at a time.
+ * products and sums are fp32 (the norm's: fp32 over 16 elements, these sums as pairs
+ * of fp32 numbers, and fp64 for squares that leave fp32's range), each result is
+ * rounded once.  The factors of a product of several rows are taken in an order that
+ * may change with the number of samples.  Pointers need the alignment of their
+ * element.  Rows that start at multiples of 16 bytes (fp32 results of 16-bit
+ * gradients: 32; factors in tables of a gradient: 8 or 16) are read and written in
+ * vectors; others, for lookups by 4 bytes and for their gradients by two elements
+ * where all rows start so, else one element at a time.
  * Indices: int32 or int64 (idx_bytes 4 or 8) on the device, and so checked there:
  * a token (or sample) with an index outside [0, rows) takes no part, which makes
  * any negative index a mask.  At most 2^31 - 1 tokens or samples and rows.
@@ -349,7 +353,8 @@ int mttkrp_ttm_multi(int d, const int64_t* dims, const float* X, int nmodes, con
  * Every call enqueues on `stream` and returns without synchronising; results are
  * bitwise reproducible (no floating-point atomics, every sum in a fixed order).
  * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_WORKSPACE (a workspace missing, too small
- * or not 256-byte aligned), MTTKRP_ERR_CUDA.
+ * or not 256-byte aligned), MTTKRP_ERR_CUDA, and MTTKRP_ERR_HOST_ALLOC for clipping
+ * more than 512 tensors.
  */
 enum mttkrp_type { MTTKRP_F32 = 0, MTTKRP_BF16 = 1, MTTKRP_F16 = 2 };
 
@@ -376,7 +381,8 @@ int mttkrp_embedding(const void* table, int64_t rows, int64_t width, int64_t tab
  * grad      n x width of `type`, rows grad_stride >= width elements apart.
  * out       rows x width of out_type (MTTKRP_F32 or `type`), out_stride >= width.
  * workspace device, 256-byte aligned, mttkrp_embedding_grad_workspace_bytes() bytes;
- *           that is 0, and NULL is taken, for few tokens (and for invalid arguments).
+ *           that is 0, and NULL is taken, for few tokens into a table that is not
+ *           large (and for invalid arguments).
  */
 size_t mttkrp_embedding_grad_workspace_bytes(int64_t n, int64_t rows, int64_t width);
 int mttkrp_embedding_grad(const void* idx, int64_t n, int64_t idx_stride, int idx_bytes, const void* grad, int type,
@@ -403,7 +409,10 @@ int mttkrp_cp_entries(int d, const int64_t* dims, int64_t R, const void* const* 
  *     outs[n](i, :) = sum over s with c_sn = i of g[s] * prod over m != n of A_m(c_sm, :)
  * outs      HOST array of d device pointers, outs[n] dims[n] x R fp32, overwritten.
  * Samples with a coordinate out of range take no part, whatever their g.
- * The workspace is needed as for mttkrp_embedding_grad.
+ * workspace device, 256-byte aligned, mttkrp_cp_entries_grad_workspace_bytes() bytes,
+ *           which follow from d, dims, R and n_samples: 0, and NULL is taken, where
+ *           the samples are few and tables of the factors would not pay (and for
+ *           invalid arguments).
  */
 size_t mttkrp_cp_entries_grad_workspace_bytes(int d, const int64_t* dims, int64_t R, int64_t n_samples);
 int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* const* factors, int type,
@@ -421,8 +430,9 @@ int mttkrp_cp_entries_grad(int d, const int64_t* dims, int64_t R, const void* co
  *           numels[k] is 0), numels[k] elements of types[k] each (HOST arrays).
  * outs      HOST array of n device pointers that receive y, each of its tensor's
  *           type; outs[k] == tensors[k] clips in place (and writes nothing when the
- *           coefficient is 1).  No result may overlap another one or another tensor.  mttkrp_clip_grad_norm with outs == NULL clips every
- *           tensor in place.
+ *           coefficient is 1).  No result may overlap another one or another
+ *           tensor (which is refused, a tensor twice in a list clipped in place too).
+ *           outs == NULL clips every tensor in place.
  * norm      device, one float (output).
  * workspace device, 256-byte aligned, mttkrp_grad_norm_workspace_bytes(n) bytes.
  */
