@@ -343,9 +343,9 @@ int mttkrp_ttm_multi(int d, const int64_t* dims, const float* X, int nmodes, con
  * rounded once.  The factors of a product of several rows are taken in an order that
  * may change with the number of samples.  Pointers need the alignment of their
  * element.  Rows that start at multiples of 16 bytes (fp32 results of 16-bit
- * gradients: 32; factors in tables of a gradient: 8 or 16) are read and written in
- * vectors; others, for lookups by 4 bytes and for their gradients by two elements
- * where all rows start so, else one element at a time.
+ * gradients: 32; 16-bit factors of a CP gradient: 8) are read and written in vectors;
+ * others of a lookup by 4 bytes, of its gradient by two elements, where all rows start
+ * so, else one element at a time.
  * Indices: int32 or int64 (idx_bytes 4 or 8) on the device, and so checked there:
  * a token (or sample) with an index outside [0, rows) takes no part, which makes
  * any negative index a mask.  At most 2^31 - 1 tokens or samples and rows.
