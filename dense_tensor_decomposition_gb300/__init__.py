@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib
+import math
 import os
 import re
 import threading
@@ -24,7 +25,7 @@ from ._build import LIB as LIB_PATH, build  # noqa: F401
 
 __all__ = ["Plan", "mttkrp", "all_modes", "apply_rotations", "ttm", "ttm_workspace_bytes", "ttm_multi",
            "ttm_multi_workspace_bytes", "embedding", "embedding_grad", "cp_entries", "cp_entries_grad",
-           "grad_norm", "clip_grad_norm", "probe_fma", "probe_mma",
+           "grad_norm", "clip_grad_norm", "rotary", "rotary_grad", "rotary_frequencies", "probe_fma", "probe_mma",
            "MttkrpError",
            "build", "load_library",
            "exported_symbols", "PATH_AUTO", "PATH_SIMT", "PATH_TC", "PATH_TC_TF32", "PATH_TC_EXPLICIT_KRP"]
@@ -121,6 +122,8 @@ def load_library():
         lib.mttkrp_grad_norm.restype = ci
         lib.mttkrp_clip_grad_norm.argtypes = [ci, vp, vp, vp, vp, cf, cf, vp, vp, sz, vp]
         lib.mttkrp_clip_grad_norm.restype = ci
+        lib.mttkrp_rotary.argtypes = [ci, vp, ci, i64, i64, i64, vp, ci, i64, i64, vp, ci, ci, cf, ci, vp]
+        lib.mttkrp_rotary.restype = ci
         lib.mttkrp_probe_fma.argtypes = [ci, ci, vp, vp]
         lib.mttkrp_probe_fma.restype = ci
         lib.mttkrp_probe_mma.argtypes = [ci, ci, ci, vp]
@@ -663,6 +666,88 @@ def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, outs=None, strea
     if type(r) is int:
         _check(r, "mttkrp_clip_grad_norm")
     return r
+
+
+# ---------------------------------------------------------------------------
+# Orthogonal maps: rotation of rows by their position.  As above, nothing records a
+# gradient, and tensors that are written into have their version raised.
+# ---------------------------------------------------------------------------
+
+def rotary_frequencies(dims: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       length: int = 0, low: float = 1.0, high: float = 32.0):
+    """Frequencies of `rotary` for rows of which `dims` columns are rotated: base^(-2i / dims)
+    radians a position, i < dims / 2, as a float64 tensor on the host.  scaling, for contexts
+    `factor` times longer than the `length` that a table was fitted for:
+    "linear" divides all by factor (positions are squeezed);
+    "base" raises the base to base * factor^(dims / (dims - 2)), which divides the lowest
+    by factor and leaves the highest;
+    "parts" divides those that turn less than `low` times in `length` positions, leaves those
+    that turn more than `high` times, and in between mixes both by a share that is linear in
+    the pair's number (from where `high` turns fall, rounded down, to where `low` do, rounded
+    up); "turns" does the same with a share linear in the number of turns."""
+    import torch
+    dims = int(dims)
+    if dims < 2 or dims % 2:
+        raise ValueError("dims must be even and positive")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    i = torch.arange(0, dims, 2, dtype=torch.float64) / dims
+    if scaling == "base":
+        if dims == 2:
+            raise ValueError("scaling \"base\" needs more than one pair")
+        return (base * factor ** (dims / (dims - 2))) ** -i
+    f = base ** -i
+    if scaling is None:
+        return f
+    if scaling == "linear":
+        return f / factor
+    if scaling not in ("parts", "turns"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not length > 0 or not 0 < low < high:
+        raise ValueError(f"scaling {scaling!r} needs length > 0 and 0 < low < high")
+    if scaling == "turns":
+        kept = (f * (length / (2 * math.pi)) - low) / (high - low)
+    else:
+        def pair(turns):            # where the waves turn that often in `length` positions
+            return dims * math.log(length / (2 * math.pi * turns)) / (2 * math.log(base))
+        first = max(math.floor(pair(high)), 0)
+        last = min(math.ceil(pair(low)), dims - 1)
+        kept = 1.0 - (torch.arange(dims // 2, dtype=torch.float64) - first) / max(last - first, 1e-3)
+    kept = kept.clamp(0.0, 1.0)
+    return f * (kept + (1.0 - kept) / factor)
+
+
+def rotary(tensors, positions, frequencies, interleaved: bool = False, scale: float = 1.0, inverse: bool = False,
+           outs=None, stream=None):
+    """Rows rotated by their token's position p (mttkrp_rotary): pair i of a row's first
+    2 * len(frequencies) columns, columns i and i + len(frequencies) or (interleaved) 2i and
+    2i + 1, turns by p * frequencies[i] and is multiplied by `scale`; the other columns are
+    copied.  inverse turns back.
+
+    tensors: a CUDA tensor, or a list of up to 8 of one type and width (queries and keys),
+    float32, bfloat16 or float16: length x width, length x heads x width or batch x length x
+    heads x width, with any strides but those of a row (heads outside the tokens are a
+    transposed view).  positions: int32 or int64, length or batch x length (then a
+    tensor without heads is batch x length x width; a batch of 1 is shared); any value is
+    one.  frequencies: float64 on the host (`rotary_frequencies`).  Returns a tensor or a
+    list, of the inputs' layout, written into `outs` when given; outs that are the tensors
+    themselves rotate in place.  The results are detached: their gradient is `rotary_grad`."""
+    import torch
+    one = isinstance(tensors, torch.Tensor)
+    if one:
+        tensors = (tensors,)
+        outs = None if outs is None else (outs,)
+    r = (_sampled or load_binding()).rotary(tensors, positions, frequencies, interleaved, scale, inverse, outs,
+                                            _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_rotary")
+    return r[0] if one else r
+
+
+def rotary_grad(grads, positions, frequencies, interleaved: bool = False, scale: float = 1.0, outs=None, stream=None):
+    """Gradient of `rotary` with respect to its tensors, given that of its results: the
+    rotation back, multiplied by the same scale.  Arguments and results as `rotary`'s."""
+    return rotary(grads, positions, frequencies, interleaved, scale, True, outs, stream)
 
 
 def probe_fma(blocks: int, iters: int, out, stream=None):

@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -87,6 +88,20 @@ void written(const at::Tensor& t) {
 }
 
 PyObject* result(int rc, const at::Tensor& t) { return rc == MTTKRP_OK ? THPVariable_Wrap(t) : PyLong_FromLong(rc); }
+
+PyObject* as_list(const std::vector<at::Tensor>& tensors) {
+    PyObject* list = PyList_New((Py_ssize_t)tensors.size());
+    if (list == nullptr) throw python_error();
+    for (size_t k = 0; k < tensors.size(); ++k) {
+        PyObject* o = THPVariable_Wrap(tensors[k]);
+        if (o == nullptr) {
+            Py_DECREF(list);
+            throw python_error();
+        }
+        PyList_SET_ITEM(list, (Py_ssize_t)k, o);
+    }
+    return list;
+}
 
 // int32 or int64 indices: contiguous of any shape, or one-dimensional with any stride
 struct Index {
@@ -298,17 +313,7 @@ PyObject* cp_entries_grad(PyObject*, PyObject* const* args, Py_ssize_t) {
     if (rc != MTTKRP_OK) return PyLong_FromLong(rc);
     if (args[3] != Py_None)
         for (const at::Tensor& o : outs) written(o);
-    PyObject* list = PyList_New(f.d);
-    if (list == nullptr) throw python_error();
-    for (int m = 0; m < f.d; ++m) {
-        PyObject* o = THPVariable_Wrap(outs[m]);
-        if (o == nullptr) {
-            Py_DECREF(list);
-            throw python_error();
-        }
-        PyList_SET_ITEM(list, m, o);
-    }
-    return list;
+    return as_list(outs);
     END_HANDLE_TH_ERRORS
 }
 
@@ -362,6 +367,101 @@ PyObject* clip_grad_norm(PyObject*, PyObject* const* args, Py_ssize_t) {
     END_HANDLE_TH_ERRORS
 }
 
+// elements between rows of batch x length x heads, from a tensor's leading dimensions
+struct Rows {
+    int64_t batch = 1, length = 1, heads = 1, width = 0;
+    int64_t strides[3] = {0, 0, 0};
+    Rows(const at::Tensor& t, int64_t pos_dim, const char* name, Py_ssize_t k) {
+        const int64_t d = t.dim();
+        TORCH_CHECK_VALUE(d == pos_dim + 1 || d == pos_dim + 2 || (d == 4 && pos_dim == 1), name, "[", k, "] has ", d,
+                          " dimensions: one or two more than the positions are taken, or four for shared positions");
+        const bool has_heads = d == 4 || d == pos_dim + 2, has_batch = d == 4 || pos_dim == 2;
+        int64_t m = 0;
+        if (has_batch) {
+            batch = t.size(m);
+            strides[0] = t.stride(m++);
+        }
+        length = t.size(m);
+        strides[1] = t.stride(m++);
+        if (has_heads) {
+            heads = t.size(m);
+            strides[2] = t.stride(m++);
+        }
+        width = t.size(m);
+        TORCH_CHECK_VALUE(width <= 1 || t.stride(m) == 1, name, "[", k, "]: the elements of a row must be consecutive");
+    }
+};
+
+// (tensors, positions, frequencies, interleaved, scale, inverse, outs or None, stream or None): a list
+PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const List list(args[0], "tensors must be a sequence");
+    const int n = (int)list.n;
+    TORCH_CHECK_VALUE(n >= 1 && list.n <= MTTKRP_MAX_ROTARY, "1 to ", MTTKRP_MAX_ROTARY, " tensors are taken");
+    const at::Tensor& first = tensor(list[0], "tensors");
+    const int code = type_code(first, "tensors");
+    const at::Tensor& pos = tensor(args[1], "positions");
+    check_device(pos, first, "positions");
+    TORCH_CHECK_TYPE(pos.scalar_type() == at::kInt || pos.scalar_type() == at::kLong, "positions must be int32 or int64");
+    TORCH_CHECK_VALUE(pos.dim() == 1 || pos.dim() == 2, "positions must have one or two dimensions");
+    TORCH_CHECK_TYPE(THPVariable_Check(args[2]), "frequencies must be a tensor on the host");
+    const at::Tensor& freq = THPVariable_Unpack(args[2]);
+    TORCH_CHECK_TYPE(freq.device().is_cpu() && freq.scalar_type() == at::kDouble,
+                     "frequencies must be a float64 tensor on the host");
+    TORCH_CHECK_VALUE(freq.dim() == 1 && freq.is_contiguous() && freq.numel() >= 1 &&
+                          freq.numel() <= MTTKRP_MAX_ROTARY_DIMS / 2,
+                      "frequencies must be contiguous, 1 to ", MTTKRP_MAX_ROTARY_DIMS / 2, " of them");
+    std::optional<List> outs;
+    if (args[6] != Py_None) {
+        outs.emplace(args[6], "outs must be a sequence");
+        TORCH_CHECK_VALUE(outs->n == n, "outs must hold one tensor per input");
+    }
+    const Stream stream(args[7], first);
+    mttkrp_rotary_tensor rows[MTTKRP_MAX_ROTARY];
+    std::vector<at::Tensor> results;
+    int64_t batch = 0, length = 0, width = 0;
+    for (int k = 0; k < n; ++k) {
+        const at::Tensor& t = tensor(list[k], "tensors");
+        check_device(t, first, "tensors");
+        TORCH_CHECK_VALUE(t.scalar_type() == first.scalar_type(), "tensors must have one type");
+        const Rows r(t, pos.dim(), "tensors", k);
+        if (k == 0) {
+            batch = r.batch;
+            length = r.length;
+            width = r.width;
+        }
+        TORCH_CHECK_VALUE(r.batch == batch && r.length == length && r.width == width,
+                          "tensors must have the same tokens and width");
+        at::Tensor out;
+        if (outs) {
+            out = tensor((*outs)[k], "outs");
+            TORCH_CHECK_VALUE(out.get_device() == first.get_device() && out.scalar_type() == first.scalar_type() &&
+                                  out.sizes() == t.sizes(),
+                              "outs[", k, "] must have its input's type, device and shape");
+        } else if (t.is_non_overlapping_and_dense()) {
+            out = at::empty_strided(t.sizes(), t.strides(), t.options());
+        } else {
+            out = at::empty(t.sizes(), t.options());
+        }
+        const Rows o(out, pos.dim(), "outs", k);
+        rows[k] = {t.data_ptr(), out.data_ptr(), r.heads, {r.strides[0], r.strides[1], r.strides[2]},
+                   {o.strides[0], o.strides[1], o.strides[2]}};
+        results.push_back(std::move(out));
+    }
+    const bool shared = pos.dim() == 1 || pos.size(0) == 1;
+    TORCH_CHECK_VALUE(pos.size(-1) == length && (shared || pos.size(0) == batch), "positions must be of ", length,
+                      " tokens, or ", batch, " x ", length);
+    const int rc = mttkrp_rotary(n, rows, code, batch, length, width, pos.data_ptr(), (int)pos.element_size(),
+                                 shared ? 0 : pos.stride(0), pos.stride(-1), freq.const_data_ptr<double>(),
+                                 2 * (int)freq.numel(), PyObject_IsTrue(args[3]) == 1, (float)number(args[4]),
+                                 PyObject_IsTrue(args[5]) == 1, stream.handle);
+    if (rc != MTTKRP_OK) return PyLong_FromLong(rc);
+    if (outs)
+        for (const at::Tensor& o : results) written(o);
+    return as_list(results);
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t), int kArgs>
 PyObject* checked(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     if (n != kArgs) {
@@ -382,6 +482,7 @@ PyMethodDef methods[] = {method<embedding, 5>("embedding"),
                          method<cp_entries, 4>("cp_entries"),
                          method<cp_entries_grad, 5>("cp_entries_grad"),
                          method<clip_grad_norm, 5>("clip_grad_norm"),
+                         method<rotary, 8>("rotary"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

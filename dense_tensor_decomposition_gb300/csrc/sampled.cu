@@ -4,7 +4,7 @@
 #include <memory>
 #include <new>
 
-#include "api.h"
+#include "checks.h"
 #include "rows.h"
 
 namespace mk {
@@ -12,21 +12,6 @@ namespace {
 
 constexpr int64_t kMaxTokens = INT32_MAX;
 constexpr int64_t kMaxWidth = 65536;
-
-size_t type_bytes(int type) { return type == MTTKRP_F32 ? 4 : 2; }
-bool type_ok(int type) { return type == MTTKRP_F32 || type == MTTKRP_BF16 || type == MTTKRP_F16; }
-// a: a power of two
-bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// bytes from the first to behind the last element of rows x width, rows `stride` apart
-size_t span_bytes(int64_t rows, int64_t width, int64_t stride, size_t elem) {
-    return rows == 0 ? 0 : ((size_t)(rows - 1) * stride + width) * elem;
-}
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na != 0 && nb != 0 && x < y + nb && y < x + na;
-}
 
 int check_index(const void* idx, int64_t n, int64_t stride, int bytes) {
     if (bytes != 4 && bytes != 8) return fail(MTTKRP_ERR_INVALID, "indices of %d bytes: 4 or 8 are taken", bytes);
@@ -47,14 +32,6 @@ int check_rows(const char* what, const void* p, int64_t rows, int64_t width, int
     if (rows > 0 && p == nullptr) return fail(MTTKRP_ERR_INVALID, "NULL %s", what);
     if (!aligned_to(p, type_bytes(type)))
         return fail(MTTKRP_ERR_INVALID, "%s must be %zu-byte aligned", what, type_bytes(type));
-    return MTTKRP_OK;
-}
-
-int check_workspace(const void* ws, size_t bytes, size_t need) {
-    if (need == 0) return MTTKRP_OK;
-    if (ws == nullptr || bytes < need)
-        return fail(MTTKRP_ERR_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? bytes : (size_t)0, need);
-    if (!aligned_to(ws, 256)) return fail(MTTKRP_ERR_WORKSPACE, "workspace must be 256-byte aligned");
     return MTTKRP_OK;
 }
 

@@ -444,6 +444,54 @@ int mttkrp_clip_grad_norm(int n, const void* const* tensors, const int64_t* nume
                           size_t workspace_bytes, void* stream);
 
 /*
+ * Orthogonal maps next to the sampled fit: rows rotated by their position with the
+ * gradient, and matrices orthogonalised by Newton-Schulz products, alone or as the update
+ * of a training step.  (No counterpart on the pages, whose rotations are of pairs of indices
+ * along a mode: mttkrp_apply_rotations.)  Types, streams and errors as above.
+ */
+
+/* Tensors of one call, and columns that are rotated, at most. */
+#define MTTKRP_MAX_ROTARY 8
+#define MTTKRP_MAX_ROTARY_DIMS 1024
+
+/*
+ * One tensor of a call: batch x length tokens of `heads` rows each, row (b, t, h) at
+ * element b * x_strides[0] + t * x_strides[1] + h * x_strides[2], its elements consecutive.
+ * out may be x itself (with the same strides: in place) and may not overlap x otherwise, nor
+ * any other tensor of the call, nor the positions.
+ */
+typedef struct mttkrp_rotary_tensor {
+    const void* x;
+    void* out;
+    int64_t heads;
+    int64_t x_strides[3];
+    int64_t out_strides[3];
+} mttkrp_rotary_tensor;
+
+/*
+ * Rotation of rows by their token's position p: with a = p * frequencies[i],
+ *     (u, v) -> scale * (u cos a - v sin a, u sin a + v cos a)
+ * for pair i of the first `dims` columns: columns i and i + dims / 2, or (interleaved != 0)
+ * 2 i and 2 i + 1.  Columns from dims on are copied.  inverse != 0 rotates by -a, which is
+ * the gradient with respect to x.
+ *
+ * n           number of tensors, at most MTTKRP_MAX_ROTARY; tensors: HOST array.  All of
+ *             `type`, with the same batch, length and width; heads may differ.
+ * width       elements of a row (at most 65536), dims of them rotated: even, between 2 and
+ *             MTTKRP_MAX_ROTARY_DIMS.
+ * positions   device, int32 or int64 (pos_bytes 4 or 8): of token (b, t) at element
+ *             b * pos_batch_stride + t * pos_stride (strides of 0 share positions).  Any value
+ *             is a position; negative ones turn back.
+ * frequencies HOST, dims / 2 values in radians a position, finite.  The angle is taken modulo
+ *             a whole turn in 64-bit fixed point, and so holds for positions of any size.
+ * Tokens and vectors of their rows: at most 2^31 - 1 tokens, and rows that the grid can hold.
+ * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_CUDA.
+ */
+int mttkrp_rotary(int n, const mttkrp_rotary_tensor* tensors, int type, int64_t batch, int64_t length, int64_t width,
+                  const void* positions, int pos_bytes, int64_t pos_batch_stride, int64_t pos_stride,
+                  const double* frequencies, int dims, int interleaved, float scale, int inverse, void* stream);
+
+/*
  * Peak probes for the roofline of a benchmark (measurement only; the pages have
  * no counterpart).  Both enqueue one kernel on `stream` and return; the caller
  * times it with events.
