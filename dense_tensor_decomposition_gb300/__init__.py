@@ -732,8 +732,7 @@ def rotary(tensors, positions, frequencies, interleaved: bool = False, scale: fl
     one.  frequencies: float64 on the host (`rotary_frequencies`).  Returns a tensor or a
     list, of the inputs' layout, written into `outs` when given; outs that are the tensors
     themselves rotate in place.  The results are detached: their gradient is `rotary_grad`."""
-    import torch
-    one = isinstance(tensors, torch.Tensor)
+    one = not isinstance(tensors, (list, tuple))
     if one:
         tensors = (tensors,)
         outs = None if outs is None else (outs,)
