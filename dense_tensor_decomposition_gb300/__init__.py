@@ -25,7 +25,8 @@ from ._build import LIB as LIB_PATH, build  # noqa: F401
 
 __all__ = ["Plan", "mttkrp", "all_modes", "apply_rotations", "ttm", "ttm_workspace_bytes", "ttm_multi",
            "ttm_multi_workspace_bytes", "embedding", "embedding_grad", "cp_entries", "cp_entries_grad",
-           "grad_norm", "clip_grad_norm", "rotary", "rotary_grad", "rotary_frequencies", "probe_fma", "probe_mma",
+           "grad_norm", "clip_grad_norm", "rotary", "rotary_grad", "rotary_frequencies",
+           "orthogonalize", "orthogonal_step", "probe_fma", "probe_mma",
            "MttkrpError",
            "build", "load_library",
            "exported_symbols", "PATH_AUTO", "PATH_SIMT", "PATH_TC", "PATH_TC_TF32", "PATH_TC_EXPLICIT_KRP"]
@@ -124,6 +125,13 @@ def load_library():
         lib.mttkrp_clip_grad_norm.restype = ci
         lib.mttkrp_rotary.argtypes = [ci, vp, ci, i64, i64, i64, vp, ci, i64, i64, vp, ci, ci, cf, ci, vp]
         lib.mttkrp_rotary.restype = ci
+        cd = ctypes.c_double
+        lib.mttkrp_orthogonalize_workspace_bytes.argtypes = [ci, vp]
+        lib.mttkrp_orthogonalize_workspace_bytes.restype = sz
+        lib.mttkrp_orthogonalize.argtypes = [ci, vp, vp, ci, vp, cd, vp, vp, sz, vp]
+        lib.mttkrp_orthogonalize.restype = ci
+        lib.mttkrp_orthogonal_step.argtypes = [ci, vp, vp, vp, vp, vp, cd, cd, ci, cd, ci, vp, cd, vp, vp, sz, vp]
+        lib.mttkrp_orthogonal_step.restype = ci
         lib.mttkrp_probe_fma.argtypes = [ci, ci, vp, vp]
         lib.mttkrp_probe_fma.restype = ci
         lib.mttkrp_probe_mma.argtypes = [ci, ci, ci, vp]
@@ -747,6 +755,70 @@ def rotary_grad(grads, positions, frequencies, interleaved: bool = False, scale:
     """Gradient of `rotary` with respect to its tensors, given that of its results: the
     rotation back, multiplied by the same scale.  Arguments and results as `rotary`'s."""
     return rotary(grads, positions, frequencies, interleaved, scale, True, outs, stream)
+
+
+QUINTIC = (3.4445, -4.775, 2.0315)      # brings singular values between 1e-3 and 1 near 1 in five steps
+
+
+def _step_coefficients(steps, coefficients):
+    """3 numbers a step, one behind the other."""
+    if len(coefficients) == 3 and not hasattr(coefficients[0], "__len__"):
+        return tuple(coefficients) * int(steps)
+    if len(coefficients) != steps or any(len(c) != 3 for c in coefficients):
+        raise ValueError("coefficients must be a triple, or one for every step")
+    return tuple(x for c in coefficients for x in c)
+
+
+def orthogonalize(matrices, steps: int = 5, coefficients=QUINTIC, eps: float = 1e-7, scale=1.0, outs=None, dtype=None,
+                  stream=None):
+    """Matrices brought near to the orthogonal ones closest to them, by Newton-Schulz products
+    (mttkrp_orthogonalize): X = G / (|G|_F + eps), then `steps` times X <- (a I + b S + c S^2) X
+    with S = X X^T (or, with more rows than columns, from the right), times `scale`.  Singular
+    values s become s (a + b s^2 + c s^4) a step; coefficients: (a, b, c), or one such triple for
+    every step.  QUINTIC brings them to between 0.7 and 1.2 in five steps; (15/8, -10/8, 3/8)
+    goes to 1 as the steps increase.
+
+    matrices: a CUDA tensor, or a list of them, rows x cols or with batch dimensions in
+    front, float32, bfloat16 or float16 in any mix; rows any distance apart, or columns (a
+    transposed view).  Returns a tensor or a list of the same shapes, of `dtype` (each input's own
+    by default), written into `outs` when given (which may be the matrices themselves).
+    The precision follows the results' type: bfloat16 is about three times as fast.  scale: a
+    number, or one for every element of the list.  The results are detached."""
+    module = _sampled or load_binding()
+    code = -1 if dtype is None else _type_codes.get(dtype)
+    if code is None:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    one = not isinstance(matrices, (list, tuple))
+    if one:
+        matrices, outs = (matrices,), None if outs is None else (outs,)
+    r = module.orthogonalize(matrices, _step_coefficients(steps, coefficients), eps, scale, outs, code, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_orthogonalize")
+    return r[0] if one else r
+
+
+def orthogonal_step(weights, grads, momenta, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                    weight_decay: float = 0.0, steps: int = 5, coefficients=QUINTIC, eps: float = 1e-7, scale=None,
+                    outs=None, momenta_outs=None, stream=None):
+    """A training step of a list of matrices with the orthogonalised momentum as update
+    (mttkrp_orthogonal_step):
+        M' = momentum * M + G,  U = G + momentum * M' (nesterov) or M',
+        W' = (1 - lr * weight_decay) * W - lr * scale * orthogonalize(U)
+    weights, grads, momenta: lists of CUDA tensors of the same shapes (or one tensor each), with
+    types and strides as `orthogonalize`'s.  W' and M' are written in place, or into `outs` and
+    `momenta_outs` (of their types and shapes).  scale: a number, one for every matrix, or None:
+    sqrt(max(1, rows / cols)), which makes updates of tall and wide matrices alike in size.
+    Returns the list of new weights (the tensors that were written)."""
+    if not isinstance(weights, (list, tuple)):
+        weights, grads, momenta = (weights,), (grads,), (momenta,)
+        outs = None if outs is None else (outs,)
+        momenta_outs = None if momenta_outs is None else (momenta_outs,)
+    r = (_sampled or load_binding()).orthogonal_step(weights, grads, momenta, lr, momentum, nesterov, weight_decay,
+                                                     _step_coefficients(steps, coefficients), eps, scale, outs,
+                                                     momenta_outs, _handle(stream))
+    if type(r) is int:
+        _check(r, "mttkrp_orthogonal_step")
+    return r
 
 
 def probe_fma(blocks: int, iters: int, out, stream=None):

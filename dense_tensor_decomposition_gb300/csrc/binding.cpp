@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <optional>
 #include <vector>
 
@@ -463,6 +464,164 @@ PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t) {
     END_HANDLE_TH_ERRORS
 }
 
+// Whether a tensor's matrices lie with the elements of a column consecutive.
+bool turned(const at::Tensor& t) {
+    return t.size(-1) > 1 && t.stride(-1) != 1 && (t.stride(-2) == 1 || t.size(-2) <= 1);
+}
+
+// a tensor (at least two-dimensional) as matrices; turn: rows and columns change places
+mttkrp_matrices matrices_of(const at::Tensor& t, bool turn, const char* name, Py_ssize_t k) {
+    mttkrp_matrices m;
+    const int64_t d = t.dim(), r = turn ? d - 1 : d - 2, c = turn ? d - 2 : d - 1;
+    m.data = t.data_ptr();
+    m.rows = t.size(r);
+    m.cols = t.size(c);
+    m.row_stride = m.rows > 1 ? t.stride(r) : m.cols;
+    m.type = type_code(t, name);
+    TORCH_CHECK_VALUE(m.cols <= 1 || t.stride(c) == 1, name, "[", k, "]: the elements of a row (or, in all tensors of a "
+                      "matrix, of a column) must be consecutive");
+    m.batch = 1;
+    m.batch_stride = m.rows * m.row_stride;
+    bool first = true;
+    int64_t next = 0;           // stride that the dimension before has to have
+    for (int64_t i = d - 3; i >= 0; --i) {
+        m.batch *= t.size(i);
+        if (t.size(i) == 1) continue;
+        if (first) m.batch_stride = t.stride(i);
+        TORCH_CHECK_VALUE(first || t.stride(i) == next, name, "[", k, "]: matrices must lie at equal distances");
+        first = false;
+        next = t.stride(i) * t.size(i);
+    }
+    return m;
+}
+
+// tensors of the matrices of a call, and their list for the library
+struct Matrices {
+    const List list;
+    const char* name;
+    std::vector<mttkrp_matrices> m;
+    Matrices(PyObject* o, const char* what) : list(o, what), name(what) {}
+    const at::Tensor& operator[](Py_ssize_t k) const { return tensor(list[k], name); }
+    // like: the call's first list, whose tensors have been checked
+    void fill(const Matrices& like) {
+        TORCH_CHECK_VALUE(list.n == like.list.n, name, " must hold one tensor per matrix");
+        for (Py_ssize_t k = 0; k < list.n; ++k) {
+            const at::Tensor& t = (*this)[k];
+            check_device(t, like[0], name);
+            TORCH_CHECK_VALUE(t.dim() >= 2 && t.sizes() == like[k].sizes(), name, "[", k, "] must be of its matrix's shape");
+            m.push_back(matrices_of(t, turned(like[k]), name, k));
+        }
+    }
+};
+
+std::vector<double> numbers(PyObject* o, const char* what) {
+    const List list(o, what);
+    std::vector<double> v(list.n);
+    for (Py_ssize_t k = 0; k < list.n; ++k) v[k] = number(list[k]);
+    return v;
+}
+
+// scales of the list elements: None for `one`, a number, or a sequence
+template <typename F>
+std::vector<float> scales(PyObject* o, Py_ssize_t n, F one) {
+    std::vector<float> v(n);
+    if (o == Py_None) {
+        for (Py_ssize_t k = 0; k < n; ++k) v[k] = one(k);
+    } else if (PyNumber_Check(o) && !PySequence_Check(o)) {
+        std::fill(v.begin(), v.end(), (float)number(o));
+    } else {
+        const std::vector<double> all = numbers(o, "scale must be a number or a sequence");
+        TORCH_CHECK_VALUE((Py_ssize_t)all.size() == n, "scale must hold one number per matrix");
+        for (Py_ssize_t k = 0; k < n; ++k) v[k] = (float)all[k];
+    }
+    return v;
+}
+
+// (matrices, coefficients, eps, scale, outs or None, dtype code of new results or -1, stream or None): a list
+PyObject* orthogonalize(PyObject*, PyObject* const* args, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    Matrices in(args[0], "matrices");
+    TORCH_CHECK_VALUE(in.list.n >= 1 && in.list.n <= (1 << 20), "1 to 2^20 matrices are taken");
+    const at::Tensor& first = in[0];
+    in.fill(in);
+    const std::vector<double> abc = numbers(args[1], "coefficients must be a sequence");
+    const std::vector<float> by = scales(args[3], in.list.n, [](Py_ssize_t) { return 1.f; });
+    const Stream stream(args[6], first);
+    std::vector<at::Tensor> results;
+    std::vector<mttkrp_matrices> to;
+    const int code = (int)whole(args[5]);
+    if (args[4] == Py_None) {
+        const at::ScalarType types[] = {at::kFloat, at::kBFloat16, at::kHalf};
+        for (Py_ssize_t k = 0; k < in.list.n; ++k) {
+            const at::Tensor& t = in[k];
+            const auto options = t.options().dtype(code < 0 ? t.scalar_type() : types[code]);
+            if (turned(t)) {
+                at::DimVector shape(t.sizes().begin(), t.sizes().end());
+                std::swap(shape[t.dim() - 1], shape[t.dim() - 2]);
+                results.push_back(at::empty(shape, options).transpose(-1, -2));
+            } else {
+                results.push_back(at::empty(t.sizes(), options));
+            }
+            to.push_back(matrices_of(results.back(), turned(t), "outs", k));
+        }
+    } else {
+        Matrices out(args[4], "outs");
+        out.fill(in);
+        for (Py_ssize_t k = 0; k < in.list.n; ++k) {
+            TORCH_CHECK_VALUE(code < 0 || out.m[k].type == code, "outs must be of dtype if that is given");
+            results.push_back(out[k]);
+        }
+        to = std::move(out.m);
+    }
+    const int n = (int)in.list.n;
+    const size_t need = mttkrp_orthogonalize_workspace_bytes(n, in.m.data());
+    const at::Tensor ws = workspace(need, first);
+    const int rc = mttkrp_orthogonalize(n, in.m.data(), to.data(), (int)(abc.size() / 3), abc.data(), number(args[2]),
+                                        by.data(), pointer(ws), need, stream.handle);
+    if (rc != MTTKRP_OK) return PyLong_FromLong(rc);
+    if (args[4] != Py_None)
+        for (const at::Tensor& o : results) written(o);
+    return as_list(results);
+    END_HANDLE_TH_ERRORS
+}
+
+// (weights, grads, momenta, lr, momentum, nesterov, weight_decay, coefficients, eps, scale, outs or None,
+//  momenta_outs or None, stream or None): the new weights, a list
+PyObject* orthogonal_step(PyObject*, PyObject* const* args, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    Matrices w(args[0], "weights"), g(args[1], "grads"), m(args[2], "momenta");
+    TORCH_CHECK_VALUE(w.list.n >= 1 && w.list.n <= (1 << 20), "1 to 2^20 matrices are taken");
+    const at::Tensor& first = w[0];
+    w.fill(w);
+    g.fill(w);
+    m.fill(w);
+    Matrices wo(args[10] == Py_None ? args[0] : args[10], "outs"), mo(args[11] == Py_None ? args[2] : args[11], "momenta_outs");
+    wo.fill(w);
+    mo.fill(w);
+    const std::vector<double> abc = numbers(args[7], "coefficients must be a sequence");
+    const std::vector<float> by = scales(args[9], w.list.n, [&](Py_ssize_t k) {
+        const at::Tensor& t = w[k];
+        return t.size(-2) > t.size(-1) && t.size(-1) > 0 ? (float)std::sqrt((double)t.size(-2) / (double)t.size(-1)) : 1.f;
+    });
+    const Stream stream(args[12], first);
+    const int n = (int)w.list.n;
+    const size_t need = mttkrp_orthogonalize_workspace_bytes(n, g.m.data());
+    const at::Tensor ws = workspace(need, first);
+    const int rc = mttkrp_orthogonal_step(n, w.m.data(), g.m.data(), m.m.data(), wo.m.data(), mo.m.data(),
+                                          number(args[3]), number(args[4]), PyObject_IsTrue(args[5]) == 1,
+                                          number(args[6]), (int)(abc.size() / 3), abc.data(), number(args[8]),
+                                          by.data(), pointer(ws), need, stream.handle);
+    if (rc != MTTKRP_OK) return PyLong_FromLong(rc);
+    std::vector<at::Tensor> results;
+    for (Py_ssize_t k = 0; k < w.list.n; ++k) {
+        results.push_back(wo[k]);
+        written(wo[k]);
+        written(mo[k]);
+    }
+    return as_list(results);
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*f)(PyObject*, PyObject* const*, Py_ssize_t), int kArgs>
 PyObject* checked(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     if (n != kArgs) {
@@ -484,6 +643,8 @@ PyMethodDef methods[] = {method<embedding, 5>("embedding"),
                          method<cp_entries_grad, 5>("cp_entries_grad"),
                          method<clip_grad_norm, 5>("clip_grad_norm"),
                          method<rotary, 8>("rotary"),
+                         method<orthogonalize, 7>("orthogonalize"),
+                         method<orthogonal_step, 13>("orthogonal_step"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -492,6 +492,67 @@ int mttkrp_rotary(int n, const mttkrp_rotary_tensor* tensors, int type, int64_t 
                   const double* frequencies, int dims, int interleaved, float scale, int inverse, void* stream);
 
 /*
+ * `batch` matrices of rows x cols elements: element (b, r, c) at
+ * b * batch_stride + r * row_stride + c.  batch, rows and cols may be 0 (nothing is done for
+ * the element then); row_stride >= cols, batch_stride >= (rows - 1) * row_stride + cols.
+ */
+typedef struct mttkrp_matrices {
+    void* data;
+    int64_t batch, rows, cols;
+    int64_t batch_stride, row_stride;
+    int type;
+} mttkrp_matrices;
+
+/* Steps of one call, and rows or columns of a matrix, at most. */
+#define MTTKRP_MAX_NEWTON_STEPS 64
+#define MTTKRP_MAX_NEWTON_SIDE 262144
+
+/*
+ * Orthogonalisation by Newton-Schulz products, of every matrix G of a list:
+ *     X = G / (|G|_F + eps);  `steps` times  X <- (a I + b S + c S^2) X,  S = X X^T;
+ *     out = scale * X
+ * (S = X^T X and X on the left where G has more rows than columns).  (a, b, c) are the step's;
+ * each step maps every singular value s to s (a + b s^2 + c s^4).
+ *
+ * n            elements of the list, at most 2^20; in, out, scales: HOST arrays of n.
+ * in           the matrices G, of any type; out: where the results go, of the same batch, rows
+ *              and cols, of any type.  out[k] may be in[k] itself (same data and strides and
+ *              type); no result may overlap another or another input otherwise.
+ * steps        in [1, MTTKRP_MAX_NEWTON_STEPS]; coefficients: HOST, 3 a step.  Refused where they
+ *              let a singular value grow beyond 3.9, or a + b s^2 + c s^4 beyond 15.9: the
+ *              products run on fp16 images (twice 11 bits) with a fixed scale.
+ * scales       one a list element, or NULL: 1.
+ * Results in fp32 and fp16 are computed from products that are exact to about 2^-22 of their
+ * terms; those in bf16 from products of the 11 leading bits but for X's: relative errors (in
+ * the Frobenius norm) of about 1e-6 and 1.5e-3 at five steps of (3.4445, -4.775, 2.0315).
+ * A matrix with an infinite or NaN element becomes NaN; one of zeros stays zero.
+ * workspace    device, 256-byte aligned, mttkrp_orthogonalize_workspace_bytes(n, in) bytes: 16
+ *              to 32 bytes an element of up to 4 GB worth of matrices at a time.  0 for lists
+ *              without elements and invalid ones.
+ * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_WORKSPACE, MTTKRP_ERR_HOST_ALLOC, MTTKRP_ERR_CUDA.
+ */
+size_t mttkrp_orthogonalize_workspace_bytes(int n, const mttkrp_matrices* in);
+int mttkrp_orthogonalize(int n, const mttkrp_matrices* in, const mttkrp_matrices* out, int steps,
+                         const double* coefficients, double eps, const float* scales, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * A training step with the orthogonalised update, of every matrix W of a list:
+ *     M' = momentum * M + G;  U = G + momentum * M' (nesterov != 0) or M';
+ *     W' = (1 - lr * weight_decay) * W - lr * scale * O(U)
+ * with O as above.  weights_out may be `weights` and momenta_out `momenta` (element by element,
+ * same data and strides: in place).  No result may overlap another one or another tensor.  All
+ * lists have the same shapes; types are each tensor's own, but a weight's result has its type,
+ * and a momentum's its.  The precision is that of weights_out's type, as above.  Workspace and
+ * limits as mttkrp_orthogonalize.
+ */
+int mttkrp_orthogonal_step(int n, const mttkrp_matrices* weights, const mttkrp_matrices* grads,
+                           const mttkrp_matrices* momenta, const mttkrp_matrices* weights_out,
+                           const mttkrp_matrices* momenta_out, double lr, double momentum, int nesterov,
+                           double weight_decay, int steps, const double* coefficients, double eps,
+                           const float* scales, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Peak probes for the roofline of a benchmark (measurement only; the pages have
  * no counterpart).  Both enqueue one kernel on `stream` and return; the caller
  * times it with events.

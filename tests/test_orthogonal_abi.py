@@ -99,3 +99,99 @@ def test_cpu_tensors_are_refused():
     for bad in (lambda: mk.rotary(x, p, f), lambda: mk.rotary_grad([x], p, f)):
         with pytest.raises(TypeError):
             bad()
+
+
+class Matrices(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("batch_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
+def matrix(data=0x1000000, batch=2, rows=6, cols=5, batch_stride=40, row_stride=6, type=F32):
+    return Matrices(data, batch, rows, cols, batch_stride, row_stride, type)
+
+
+def listed(ms):
+    return None if ms is None else (Matrices * max(len(ms), 1))(*ms)
+
+
+QUINTIC = (3.4445, -4.775, 2.0315)
+
+
+def orthogonalize(lib, ins=(matrix(),), outs=(matrix(0x2000000),), n=None, steps=5, abc=QUINTIC * 5, eps=1e-7,
+                  scales=None, ws=0x4000000, ws_bytes=1 << 30):
+    n = len(ins) if n is None else n
+    c = None if abc is None else (ctypes.c_double * max(len(abc), 3))(*abc)
+    return lib.mttkrp_orthogonalize(n, listed(ins), listed(outs), steps, c, eps, scales, ws, ws_bytes, None)
+
+
+HERE = 0x1000000
+
+
+@pytest.mark.parametrize("change,why,code", [
+    ({"n": -1}, "n=", 1), ({"n": (1 << 20) + 1}, "n=", 1), ({"ins": None, "n": 1}, "NULL", 1), ({"outs": None}, "NULL", 1),
+    ({"ins": [matrix(rows=-1)]}, "range", 1), ({"ins": [matrix(cols=1 << 19)]}, "range", 1),
+    ({"ins": [matrix(batch=1 << 31)]}, "range", 1), ({"ins": [matrix(rows=1 << 18, cols=1 << 18)]}, "128 GB", 1),
+    ({"ins": [matrix(type=7)]}, "type", 1), ({"outs": [matrix(0x2000000, type=-1)]}, "type", 1),
+    ({"ins": [matrix(0)]}, "NULL", 1), ({"outs": [matrix(0)]}, "NULL", 1), ({"ins": [matrix(HERE + 2)]}, "aligned", 1),
+    ({"ins": [matrix(row_stride=4)]}, "closer", 1), ({"ins": [matrix(batch_stride=34)]}, "overlap", 1),
+    ({"ins": [matrix(row_stride=-6)]}, "negative", 1), ({"ins": [matrix(row_stride=1 << 40)]}, "2^40", 1),
+    ({"outs": [matrix(0x2000000, rows=5)]}, "shape", 1), ({"outs": [matrix(0x2000000, batch=1)]}, "shape", 1),
+    ({"outs": [matrix(HERE + 4)]}, "overlaps", 1), ({"outs": [matrix(HERE, row_stride=7)]}, "overlaps", 1),
+    ({"outs": [matrix(HERE, type=BF16, row_stride=6)]}, "overlaps", 1),
+    ({"ins": [matrix(), matrix(0x3000000)], "outs": [matrix(0x2000000), matrix(0x2000010)]}, "overlaps", 1),
+    ({"ins": [matrix(), matrix(0x3000000)], "outs": [matrix(0x2000000), matrix(HERE)]}, "overlaps", 1),
+    ({"ins": [matrix(), matrix()], "outs": [matrix(HERE), matrix(0x2000000)]}, "overlaps", 1),
+    ({"steps": 0}, "steps", 1), ({"steps": 65}, "steps", 1), ({"abc": None}, "NULL", 1), ({"eps": -1.0}, "eps", 1),
+    ({"eps": float("nan")}, "eps", 1), ({"eps": float("inf")}, "eps", 1),
+    ({"abc": QUINTIC * 4 + (float("nan"), 0, 0)}, "finite", 1), ({"abc": (16.0, 0, 0) * 5}, "15.9", 1),
+    ({"abc": (2.0, 0, 0) * 5}, "3.9", 1), ({"abc": (4.0, 0, 0) + QUINTIC * 4}, "3.9", 1),
+    ({"abc": (1.0, 14.95, -13.0) + QUINTIC * 4}, "3.9", 1),     # 4.26 at s^2 = 0.79 (-14 reaches 3.87: taken)
+    ({"ws": 0}, "workspace", 3), ({"ws_bytes": 100}, "workspace", 3), ({"ws": 0x4000080}, "256-byte", 3)])
+def test_orthogonalisation_refuses(lib, change, why, code):
+    refused(lib, orthogonalize(lib, **change), why, code)
+
+
+def test_orthogonalisation_takes_what_fits(lib):
+    """Up to the status word, which a machine without a GPU does not have: in place, columns of
+    one buffer, coefficients whose last step grows, no matrices."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("made-up pointers are not for a GPU")
+    assert orthogonalize(lib, outs=[matrix(HERE)]) == 4
+    left, right = matrix(HERE, 1, 6, 5, 0, 12), matrix(HERE + 24, 1, 6, 5, 0, 12)
+    assert orthogonalize(lib, ins=[left, right], outs=[left, right]) == 4
+    assert orthogonalize(lib, ins=[right, left], outs=[right, left]) == 4
+    refused(lib, orthogonalize(lib, ins=[left, right], outs=[right, left]), "overlaps")
+    assert orthogonalize(lib, steps=1, abc=(15.0, 0.0, 0.0)) == 4
+    assert orthogonalize(lib, ins=[], outs=[]) == 0
+    assert orthogonalize(lib, ins=[matrix(0, rows=0)], outs=[matrix(0, rows=0)], ws=0, ws_bytes=0) == 0
+
+
+def test_orthogonalisation_workspace(lib):
+    size = lambda *ms: lib.mttkrp_orthogonalize_workspace_bytes(len(ms), listed(ms))
+    one = size(matrix(batch=1, rows=64, cols=64, batch_stride=0, row_stride=64))
+    assert 8 * 8192 <= one < 8 * 8192 + 4096
+    assert size(matrix(batch=3, rows=100, cols=500, row_stride=500, batch_stride=50000)) >= 3 * 4 * (2 * 8 + 4) * 8192
+    # a list beyond 4 GB goes in parts
+    big = matrix(batch=100, rows=4096, cols=4096, row_stride=4096, batch_stride=1 << 24)
+    assert size(big) <= (4 << 30) + (1 << 20) and size(big, big) <= (4 << 30) + (1 << 20)
+    assert size(matrix(rows=-1)) == 0 and size(matrix(batch=0)) == 0 and lib.mttkrp_orthogonalize_workspace_bytes(0, None) == 0
+
+
+def step(lib, weights=None, grads=None, momenta=None, weights_out=None, momenta_out=None, lr=0.1, momentum=0.9, wd=0.0,
+         steps=5, ws=0x40000000):
+    at = lambda k, ms: listed(ms if ms is not None else [matrix(0x1000000 * (k + 1))])
+    c = (ctypes.c_double * 15)(*(QUINTIC * 5))
+    return lib.mttkrp_orthogonal_step(1, at(0, weights), at(1, grads), at(2, momenta), at(3, weights_out), at(4, momenta_out),
+                                      lr, momentum, 1, wd, steps, c, 1e-7, None, ws, 1 << 30, None)
+
+
+@pytest.mark.parametrize("change,why", [
+    ({"weights": [matrix(rows=7, batch_stride=60)]}, "shape"), ({"momenta": [matrix(0)]}, "NULL"),
+    ({"weights_out": [matrix(0x4000000, type=BF16)]}, "type"), ({"momenta_out": [matrix(0x5000000, type=F16)]}, "type"),
+    ({"weights_out": [matrix(0x2000000)]}, "overlaps"), ({"momenta_out": [matrix(0x1000000)]}, "overlaps"),
+    ({"momenta_out": [matrix(0x4000000)]}, "overlaps"), ({"weights_out": [matrix(0x1000004)]}, "overlaps"),
+    ({"lr": float("nan")}, "finite"), ({"momentum": float("inf")}, "finite"), ({"wd": float("nan")}, "finite"),
+    ({"steps": 0}, "steps")])
+def test_step_refuses(lib, change, why):
+    refused(lib, step(lib, **change), why)
