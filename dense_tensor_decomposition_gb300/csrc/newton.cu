@@ -33,7 +33,7 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstring>
+#include <cmath>
 
 #include "launch.cuh"
 #include "newton.h"
@@ -50,11 +50,12 @@ constexpr uint32_t kTileBytes = 8192;
 constexpr int64_t kGroupTiles = (int64_t)4 << 17;   // 4 GB of images a group (one matrix at least)
 constexpr float kScale = 4096.f, kUnscale = 1.f / 4096.f;   // of the images
 
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
-constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;      // 384
+constexpr int kEpiWarp0 = 4;
 constexpr int kPassThreads = 256;
 
-enum Phase { kGram, kSquare, kUpdate };
+// what a launch computes: S, P (from S S), P X, and the last P X, whose result goes to the caller
+enum Phase { kGram, kSquare, kUpdate, kResult };
+__host__ __device__ constexpr bool is_update(int phase) { return phase >= kUpdate; }
 
 // Matrices of one list element.  Tiles of one matrix, hi and lo of each: X twice (a step
 // reads one and writes the other), S, P.
@@ -92,7 +93,8 @@ __device__ __forceinline__ void get8_of(const Store& s, int64_t at, int valid, f
         constexpr int kVec = 16 / sizeof(T);
 #pragma unroll
         for (int k = 0; k < 8 / kVec; ++k) {
-            const auto w = as_pack<Pack<T, kVec>>(reinterpret_cast<const uint4*>(p)[k]);
+            const uint4 bits = reinterpret_cast<const uint4*>(p)[k];    // (a reference to memory would be copied by bytes)
+            const auto w = as_pack<Pack<T, kVec>>(bits);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) v[k * kVec + e] = to_f32(w.v[e]);
         }
@@ -165,9 +167,15 @@ __device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * 
 
 struct Source {
     Store g, m, out;            // m.data NULL: no momentum
-    uint32_t first;             // number of the element's first slice
-    int slices;                 // of a matrix
-    int at;                     // number of its first partial sum
+    uint32_t first[2];          // number of the element's first work item: sums, images
+    int slices;                 // sums of a matrix
+    int at;                     // number of its first sum
+};
+
+// a sum of squares as fp32 pair, and in fp64 what does not fit
+struct Partial {
+    float hi, lo;
+    double wide;
 };
 
 struct PassArgs {
@@ -175,7 +183,7 @@ struct PassArgs {
     float mu;
     bool nesterov;
     double eps;
-    double* partial;
+    Partial* partial;
     uint8_t* tiles;
     Shape shape[kTable];
     Source source[kTable];
@@ -193,22 +201,6 @@ __device__ __forceinline__ int element_of(int n, uint32_t x, F first) {
     return lo;
 }
 
-struct Slice {
-    int k, b, slice;            // element, matrix, slice of it
-    int t0, t1;                 // its tiles
-    __device__ explicit Slice(const PassArgs& a) {
-        k = element_of(a.n, blockIdx.x, [&](int i) { return a.source[i].first; });
-        const Source& s = a.source[k];
-        const uint32_t at = blockIdx.x - s.first;
-        b = (int)(at / s.slices);
-        slice = (int)(at - (uint32_t)b * s.slices);
-        const Grid g(a.shape[k]);
-        const int64_t tiles = (int64_t)g.rt * g.ct;
-        t0 = (int)(tiles * slice / s.slices);
-        t1 = (int)(tiles * (slice + 1) / s.slices);
-    }
-};
-
 // U of eight elements and, where there is momentum, what it becomes
 __device__ __forceinline__ void update8(const PassArgs& a, const Source& s, int b, int r, int c, int cols, float* u,
                                         float* kept) {
@@ -223,76 +215,110 @@ __device__ __forceinline__ void update8(const PassArgs& a, const Source& s, int 
     }
 }
 
-// partial sums of squares, a slice each
+// Sums of squares: a matrix in slices of consecutive groups of 8 columns, row by row, a slice
+// a CTA.
 __global__ void __launch_bounds__(kPassThreads) squares_kernel(const __grid_constant__ PassArgs a) {
     after_previous();
-    const Slice w(a);
-    const Source& s = a.source[w.k];
-    const Shape& shape = a.shape[w.k];
-    const int ct = tiles_of(shape.cols);
-    const int tr = threadIdx.x >> 3, tc = (threadIdx.x & 7) * 8;
+    const int k = element_of(a.n, blockIdx.x, [&](int i) { return a.source[i].first[0]; });
+    const Source s = a.source[k];
+    const int cols = a.shape[k].cols, per = (cols + 7) / 8;
+    const uint32_t at = blockIdx.x - s.first[0];
+    const int b = (int)(at / (uint32_t)s.slices), slice = (int)(at - (uint32_t)b * s.slices);
+    const int64_t groups = (int64_t)a.shape[k].rows * per;
+    const bool narrow = groups < INT32_MAX;
+    const int64_t g0 = groups * slice / s.slices, g1 = groups * (slice + 1) / s.slices;
     Sum sum;
-    for (int t = w.t0; t < w.t1; ++t) {
-        const int ti = t / ct, c = (t - ti * ct) * 64 + tc;
-        float v[16], kept[8];
+    constexpr int kAhead = 4;
+    for (int64_t g = g0 + threadIdx.x; g < g1; g += kAhead * kPassThreads) {
+        float v[kAhead][8], kept[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = ti * 64 + 32 * h + tr;
-            if (r < shape.rows && c < shape.cols) {
-                update8(a, s, w.b, r, c, shape.cols, v + 8 * h, kept);
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t x = g + i * kPassThreads;
+            if (x < g1) {
+                const int r = narrow ? (int)((uint32_t)x / (uint32_t)per) : (int)(x / per);
+                const int c = (int)(x - (int64_t)r * per) * 8;
+                update8(a, s, b, r, c, cols, v[i], kept);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * h + e] = 0.f;
+                for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
             }
         }
-        sum.squares16(v);
+#pragma unroll
+        for (int i = 0; i < kAhead; i += 2) sum.squares16(v[i]);
     }
-    const double total = block_sum<kPassThreads / 32>(sum);
-    if (threadIdx.x == 0) a.partial[s.at + w.b * s.slices + w.slice] = total;
+    const Sum total = block_total<kPassThreads / 32>(sum);
+    if (threadIdx.x == 0) a.partial[s.at + b * s.slices + slice] = Partial{total.hi, total.lo, total.wide};
 }
 
-// the images of X = U / (|U| + eps), zeros behind the last row and column; momentum written
+// The images of X = U / (|U| + eps), zeros behind the last row and column; momentum written.
+// A CTA takes 64 rows of four column tiles: a warp reads and writes one row of them at a time.
+constexpr int kStrip = 4;
+
 __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_constant__ PassArgs a) {
-    __shared__ double warp_sum[kPassThreads / 32];
     after_previous();
-    const Slice w(a);
-    const Source& s = a.source[w.k];
-    const Shape& shape = a.shape[w.k];
+    const int k = element_of(a.n, blockIdx.x, [&](int i) { return a.source[i].first[1]; });
+    const Source s = a.source[k];
+    const Shape shape = a.shape[k];
     const Grid g(shape);
+    const int strips = (g.ct + kStrip - 1) / kStrip;
+    const uint32_t at = blockIdx.x - s.first[1];
+    const int b = (int)(at / (uint32_t)(g.rt * strips)), rest = (int)(at - (uint32_t)b * (g.rt * strips));
+    const int ti = rest / strips, strip = rest - ti * strips;
+
     static_assert(kMaxSlices <= kPassThreads, "a partial sum a thread");
-    double norm = threadIdx.x < s.slices ? a.partial[s.at + w.b * s.slices + threadIdx.x] : 0.0;
-    for (int o = 16; o > 0; o >>= 1) norm += __shfl_xor_sync(0xFFFFFFFFu, norm, o);
-    if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = norm;
+    Sum sum;
+    if (threadIdx.x < s.slices) {
+        const Partial p = a.partial[s.at + b * s.slices + threadIdx.x];
+        sum.hi = p.hi;
+        sum.lo = p.lo;
+        sum.wide = p.wide;
+    }
+    __shared__ float2 found;
+    const Sum total = block_total<kPassThreads / 32>(sum);
+    if (threadIdx.x == 0) {
+        // factors whose product is 2^12 / (|U| + eps); two, as one may leave fp32's range
+        const float square = total.hi + total.lo;
+        if (total.wide == 0.0 && square >= 0x1p-100f && square <= 0x1p100f) {
+            found = make_float2(1.f, kScale / (sqrtf(square) + (float)a.eps));
+        } else {
+            const double f = (double)kScale / (sqrt((double)total.hi + (double)total.lo + total.wide) + a.eps);
+            const double by = f > 0x1p60 ? 0x1p100 : f < 0x1p-60 ? 0x1p-100 : 1.0;
+            found = make_float2((float)by, (float)(f / by));
+        }
+    }
     __syncthreads();
-    norm = 0.0;
+    const float2 factor = found;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tj = strip * kStrip + lane / 8, c = tj * 64 + (lane & 7) * 8;
+    if (tj >= g.ct) return;
+    uint8_t* const tile = a.tiles + ((int64_t)shape.base + (int64_t)b * g.tiles() + (int64_t)ti * g.ct + tj) * kTileBytes;
+    const int64_t lo = (int64_t)g.x_lo() * kTileBytes;
+    constexpr int kAhead = 4;           // rows a thread has in flight
 #pragma unroll
-    for (int i = 0; i < kPassThreads / 32; ++i) norm += warp_sum[i];
-    const double factor = (double)kScale / (sqrt(norm) + a.eps);
-    const bool narrow = factor >= 0x1p-110 && factor <= 0x1p110;     // else (NaN too) the product in fp64
-    const float f32 = (float)factor;
-    const int tr = threadIdx.x >> 3, tc = threadIdx.x & 7;
-    uint8_t* const hi0 = a.tiles + ((int64_t)shape.base + (int64_t)w.b * g.tiles()) * kTileBytes;
-    for (int t = w.t0; t < w.t1; ++t) {
-        const int ti = t / g.ct, c = (t - ti * g.ct) * 64 + 8 * tc;
+    for (int i0 = 0; i0 < 8; i0 += kAhead) {
+        float u[kAhead][8], kept[kAhead][8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = 32 * h + tr, row = ti * 64 + r;
-            float u[8], kept[8];
+        for (int i = 0; i < kAhead; ++i) {
+            const int row = ti * 64 + warp + 8 * (i0 + i);
             if (row < shape.rows && c < shape.cols) {
-                update8(a, s, w.b, row, c, shape.cols, u, kept);
-                if (s.m.data != nullptr) put8(s.out, w.b, row, c, shape.cols, kept);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    u[e] = c + e >= shape.cols ? 0.f : narrow ? u[e] * f32 : (float)((double)u[e] * factor);
+                update8(a, s, b, row, c, shape.cols, u[i], kept[i]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = 0.f;
+                for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
             }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = warp + 8 * (i0 + i), row = ti * 64 + r;
+            if (s.m.data != nullptr && row < shape.rows && c < shape.cols)
+                put8(s.out, b, row, c, shape.cols, kept[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                u[i][e] = row < shape.rows && c + e < shape.cols ? u[i][e] * factor.x * factor.y : 0.f;
             uint4 vh, vl;
-            split8(u, vh, vl);
-            uint8_t* at = hi0 + (int64_t)t * kTileBytes + piece(r, tc);
-            *reinterpret_cast<uint4*>(at) = vh;
-            *reinterpret_cast<uint4*>(at + (int64_t)g.x_lo() * kTileBytes) = vl;
+            split8(u[i], vh, vl);
+            *reinterpret_cast<uint4*>(tile + piece(r, lane & 7)) = vh;
+            *reinterpret_cast<uint4*>(tile + lo + piece(r, lane & 7)) = vl;
         }
     }
 }
@@ -304,15 +330,18 @@ struct Result {
     float beta;
 };
 
+// Work items of a symmetric result of nb x nb blocks: rows of blocks from the block of 256 they are in on.
+__host__ __device__ inline int symmetric_items(int nb, int ctas) {
+    if (ctas == 2) return nb * (nb + 1) / 2;
+    const int pairs = nb / 2;           // rows 2 p and 2 p + 1 have nb - 2 p items each
+    return pairs * (2 * nb - 2 * pairs + 2) + (nb % 2);
+}
+
 struct ProductArgs {
     CUtensorMap map;            // the workspace's tiles as rows of 128 bytes
     int n;
     uint32_t items;             // tiles of the result, of all matrices
-    int phase;
     int from;                   // which X is read
-    bool full;                  // both parts of every operand
-    bool last;                  // of P X: results to `result`
-    int chunk;                  // steps of 64 indices between drains
     float a, b, c, alpha;
     uint8_t* tiles;
     uint32_t* status;
@@ -334,16 +363,20 @@ struct Operand {
     Major major;
 };
 
-template <int kCtas>
+// Symmetric matrices are stored on and above the diagonal in blocks of 256 (and read so whatever the
+// form of the kernel, as it may change from launch to launch).
+constexpr int kSymBlock = 4;                    // tiles of 64 a side
+
+template <int kCtas, int kPhase>
 __device__ __forceinline__ Item item_of(const ProductArgs& a, uint32_t t) {
     constexpr int kBlock = 2 * kCtas;           // tiles of 64 a side of a work item
     Item w;
-    const int f = a.phase == kUpdate ? 1 : 0;
+    constexpr int f = is_update(kPhase) ? 1 : 0;
     w.k = element_of(a.n, t, [&](int i) { return a.shape[i].first[f]; });
     const Shape& s = a.shape[w.k];
     const Grid g(s);
     const uint32_t at = t - s.first[f];
-    if (a.phase == kUpdate) {
+    if constexpr (is_update(kPhase)) {
         const int ni = (g.rt + kBlock - 1) / kBlock, nj = (g.ct + kBlock - 1) / kBlock;
         w.b = (int)(at / (uint32_t)(ni * nj));
         const int r = (int)(at - (uint32_t)w.b * (ni * nj));
@@ -352,31 +385,36 @@ __device__ __forceinline__ Item item_of(const ProductArgs& a, uint32_t t) {
         w.j = g.wide ? r / ni : r % nj;
         w.steps = g.mt;
     } else {
-        const int nb = (g.mt + kBlock - 1) / kBlock, per = nb * (nb + 1) / 2;
+        const int nb = (g.mt + kBlock - 1) / kBlock, per = symmetric_items(nb, kCtas);
         w.b = (int)(at / (uint32_t)per);
         int r = (int)(at - (uint32_t)w.b * per);
+        // block row i begins with the block of 256 that it is in
         w.i = 0;
-        for (int len = nb; r >= len; --len, ++w.i) r -= len;
-        w.j = w.i + r;
-        w.steps = a.phase == kSquare ? g.mt : g.wide ? g.ct : g.rt;
+        for (int len = nb; r >= len; len = nb - (w.i * kBlock / kSymBlock) * (kSymBlock / kBlock)) {
+            r -= len;
+            ++w.i;
+        }
+        w.j = (w.i * kBlock / kSymBlock) * (kSymBlock / kBlock) + r;
+        w.steps = kPhase == kSquare ? g.mt : g.wide ? g.ct : g.rt;
     }
     w.i *= kBlock;
     w.j *= kBlock;
     return w;
 }
 
+template <bool kFull, int kPhase>
 __device__ __forceinline__ void operands(const ProductArgs& a, const Item& w, Operand& p, Operand& q, bool& p_lo,
                                          bool& q_lo) {
     const Shape& s = a.shape[w.k];
     const Grid g(s);
     const int at = s.base + w.b * g.tiles();
     const Operand x{at + g.x(a.from), g.x_lo(), g.ct, kRowsK};
-    p_lo = q_lo = a.full;
-    if (a.phase == kGram) {
+    p_lo = q_lo = kFull;
+    if constexpr (kPhase == kGram) {
         p = x;
         p.major = g.wide ? kRowsK : kRowsMn;
         q = p;
-    } else if (a.phase == kSquare) {
+    } else if constexpr (kPhase == kSquare) {
         p = q = Operand{at + g.s(), g.s_lo(), g.mt, kSymmetric};
     } else {
         const Operand sym{at + g.p(), g.s_lo(), g.mt, kSymmetric};
@@ -389,10 +427,8 @@ __device__ __forceinline__ void operands(const ProductArgs& a, const Item& w, Op
 }
 
 // Whether the operand's 64 x 64 tiles of block row `first` are K-major at step k.
-template <int kCtas>
 __device__ __forceinline__ bool k_major(const Operand& o, int first, int k) {
-    constexpr int kBlock = 2 * kCtas;
-    return o.major == kSymmetric ? first / kBlock <= k / kBlock : o.major == kRowsK;
+    return o.major == kSymmetric ? first / kSymBlock <= k / kSymBlock : o.major == kRowsK;
 }
 
 // ---- PTX of a pair of CTAs
@@ -428,31 +464,304 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, int tile, uint
             : "memory");
 }
 
+// by the lane whose `leader` is not 0
 template <int kCtas>
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc, uint32_t leader) {
     if constexpr (kCtas == 2)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
             "mov.b64 da, {%1, %3};\n\t"
             "mov.b64 db, {%2, %3};\n\t"
             "setp.ne.b32 p, %5, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
-            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc));
+            "setp.ne.b32 e, %6, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc), "r"(leader));
     else
-        mma_f16_ss(d, a_lo, b_lo, idesc, acc);
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %3};\n\t"
+            "mov.b64 db, {%2, %3};\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "setp.ne.b32 e, %6, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc), "r"(leader));
 }
 
-// arrive on `bar` (of both CTAs) when the MMAs so far are done
+// arrive on `bar` (of both CTAs) when that lane's MMAs so far are done
 template <int kCtas>
-__device__ __forceinline__ void commit(uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
     if constexpr (kCtas == 2)
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
                 smem_u32(bar)),
-            "h"((uint16_t)3)
+            "h"((uint16_t)3), "r"(leader)
             : "memory");
     else
-        mma_commit(bar);
+        asm volatile(
+            "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+            "r"(leader)
+            : "memory");
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
+                 "r"(smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+// until what this thread's stores read (but for the last few), or all they do, is done
+template <int kPending = 0>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A warp's stage: 32 rows of kC columns (16 or 32) of fp32, 16-byte pieces in an order in which
+// neither rows nor columns meet in a bank.
+template <int kC>
+__device__ __forceinline__ uint32_t staged(int r, int q) {
+    return kC == 32 ? piece(r, q) : (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+}
+
+// Writes them (beta O(U)) to a result, after adding alpha W: whole rows of the stage at a time, or
+// where rows are not aligned a column a lane.
+template <typename T, int kC>
+__device__ __forceinline__ void write_rows_of(const ProductArgs& a, const Result& o, int b, int row0, int col0, int rows,
+                                              int cols, const uint8_t* stage, int lane) {
+    T* const out = static_cast<T*>(o.out.data) + b * o.out.batch;
+    const T* const old = o.w.data != nullptr ? static_cast<const T*>(o.w.data) + b * o.w.batch : nullptr;
+    if (o.out.whole && (old == nullptr || o.w.whole) && col0 + kC <= cols) {
+        using B = typename Bits<4 * sizeof(T)>::type;
+        using P = Pack<T, 4>;
+        constexpr int kLanes = kC / 4, kStep = 32 / kLanes;
+        const int q = lane % kLanes, col = col0 + 4 * q;
+        B had[kLanes];
+        if (old != nullptr) {
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const int row = row0 + kStep * i + lane / kLanes;
+                if (row < rows) had[i] = *reinterpret_cast<const B*>(old + row * o.w.row + col);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLanes; ++i) {
+            const int r = kStep * i + lane / kLanes, row = row0 + r;
+            if (row >= rows) continue;
+            const float4 f = *reinterpret_cast<const float4*>(stage + staged<kC>(r, q));
+            float v[4] = {f.x, f.y, f.z, f.w};
+            if (old != nullptr) {
+                const P p = as_pack<P>(had[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(a.alpha, to_f32(p.v[e]), v[e]);
+            }
+            P p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p.v[e] = from_f32<T>(v[e]);
+            *reinterpret_cast<B*>(out + row * o.out.row + col) = as_pack<B>(p);
+        }
+    } else {
+        const int c = lane % kC, col = col0 + c;
+        if (col >= cols) return;
+#pragma unroll 4
+        for (int r = lane / kC; r < 32; r += 32 / kC) {
+            if (row0 + r >= rows) break;
+            float v = *reinterpret_cast<const float*>(stage + staged<kC>(r, c >> 2) + (c & 3) * 4);
+            const int64_t row = row0 + r;
+            if (old != nullptr) v = fmaf(a.alpha, to_f32(old[row * o.w.row + col]), v);
+            out[row * o.out.row + col] = from_f32<T>(v);
+        }
+    }
+}
+template <int kC>
+__device__ __forceinline__ void write_rows(const ProductArgs& a, const Result& o, int b, int row0, int col0, int rows,
+                                           int cols, const uint8_t* stage, int lane) {
+    if (o.out.type == MTTKRP_F32) write_rows_of<float, kC>(a, o, b, row0, col0, rows, cols, stage, lane);
+    else if (o.out.type == MTTKRP_BF16) write_rows_of<__nv_bfloat16, kC>(a, o, b, row0, col0, rows, cols, stage, lane);
+    else write_rows_of<__half, kC>(a, o, b, row0, col0, rows, cols, stage, lane);
+}
+
+// Where a thread's 64-column blocks of an item go.
+struct Place {
+    int k, b;
+    int rows, cols, m;          // of the matrix, and its smaller side
+    int ti, tj, nt, mt;         // tile of the first block; tiles that there are
+    int r0, r;                  // in the tile: the warp's first row, this thread's
+    int from, to, lo;           // tiles: S, the image that is written, from hi to lo parts
+    __device__ __forceinline__ Place(const ProductArgs& a, int phase, const Item& w, int i, int j, int row0, int lane)
+        : k(w.k), b(w.b), ti(i), tj(j), r0(row0), r(row0 + lane) {
+        const Shape s = a.shape[w.k];
+        const Grid g(s);
+        const int at = s.base + w.b * g.tiles();
+        rows = s.rows;
+        cols = s.cols;
+        m = min(s.rows, s.cols);
+        nt = is_update(phase) ? g.rt : g.mt;
+        mt = is_update(phase) ? g.ct : g.mt;
+        from = at + g.s();
+        to = at + (is_update(phase) ? g.x(1 - a.from) : phase == kGram ? g.s() : g.p());
+        lo = is_update(phase) ? g.x_lo() : g.s_lo();
+    }
+};
+
+// A warp's 32 rows of a tile, as it loads them: piece 32 i + lane of their 4 KB.
+struct Lines {
+    uint4 v[8];
+    __device__ __forceinline__ void get(const uint8_t* tile, const Place& at, int lane) {
+        const uint4* p = reinterpret_cast<const uint4*>(tile + 128 * at.r0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = p[32 * i + lane];
+    }
+    __device__ __forceinline__ void put(uint8_t* stage, int lane) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(stage)[32 * i + lane] = v[i];
+    }
+};
+__device__ __forceinline__ const uint8_t* tile_of_s(const ProductArgs& a, const Place& at, int n) {
+    return a.tiles + (int64_t)(at.from + at.ti * at.mt + at.tj + n) * kTileBytes;
+}
+
+// P from S S (f, scaled): a I + b S + c S S, all scaled, with 8 elements of S.
+__device__ __forceinline__ void polynomial8(const ProductArgs& a, const Place& at, int j, int q, const float* s, float* v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[e] = fmaf(a.c, v[e], a.b * s[e]);
+        if (at.ti == j && at.r == 8 * q + e && at.ti * 64 + at.r < at.m) v[e] += a.a * kScale;
+    }
+}
+
+// From full products: S read as it lies, two pieces of hi and lo at a time.
+__device__ __forceinline__ void polynomial_full(const ProductArgs& a, const Place& at, int j, float* f) {
+    const uint8_t* row = a.tiles + (int64_t)(at.from + at.ti * at.mt + j) * kTileBytes;
+    const uint8_t* row_lo = row + (int64_t)at.lo * kTileBytes;
+    constexpr int kAhead = 2;
+#pragma unroll
+    for (int q0 = 0; q0 < 8; q0 += kAhead) {
+        uint4 hi[kAhead], lo[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            hi[q] = *reinterpret_cast<const uint4*>(row + piece(at.r, q0 + q));
+            lo[q] = *reinterpret_cast<const uint4*>(row_lo + piece(at.r, q0 + q));
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            float s[8];
+            join8(hi[q], lo[q], s);
+            polynomial8(a, at, j, q0 + q, s, f + 8 * (q0 + q));
+        }
+    }
+}
+
+// From S_hi S_hi: what the low part of S's diagonal (large beside the rest) adds to it comes
+// here.  S is loaded in whole lines (its hi part before the accumulators are there) and goes
+// through the warp's stage to the threads of its rows.
+__device__ __forceinline__ void polynomial_short(const ProductArgs& a, const Place& at, int n, Lines& s, float* f,
+                                                 uint8_t* stage, int lane) {
+    const int j = at.tj + n;
+    const int64_t to_lo = (int64_t)at.lo * kTileBytes;
+    auto diagonal = [&](int t, int i) {     // element (i, i) of the low part of diagonal tile t
+        const uint8_t* p = a.tiles + (int64_t)(at.from + t * (at.mt + 1)) * kTileBytes + to_lo + piece(i, i >> 3) + (i & 7) * 2;
+        return __half2float(*reinterpret_cast<const __half*>(p)) * kUnscale;
+    };
+    const float own = diagonal(at.ti, at.r);
+    const float low[2] = {diagonal(j, lane), diagonal(j, 32 + lane)};   // of columns lane and 32 + lane
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) bulk_wait_read();
+    __syncwarp();
+    s.put(stage, lane);
+    __syncwarp();
+    s.get(tile_of_s(a, at, n) + to_lo, at, lane);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        float x[8], *v = f + 8 * q;
+        join8(*reinterpret_cast<const uint4*>(stage + piece(lane, q)), zero, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = 8 * q + e;
+            v[e] = fmaf(own + __shfl_sync(0xffffffffu, low[c / 32], c % 32), x[e], v[e]);
+        }
+        polynomial8(a, at, j, q, x, v);
+    }
+    __syncwarp();
+    s.put(stage, lane);
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        float x[8];
+        join8(zero, *reinterpret_cast<const uint4*>(stage + piece(lane, q)), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[8 * q + e] = fmaf(a.b, x[e], f[8 * q + e]);
+    }
+    __syncwarp();
+}
+
+// Writes block n of 64 columns (accumulators, which carry 2^24) of this thread's row: to the
+// images, or to the result.  kStage: bytes of the warp's stage.
+template <bool kFull, int kPhase, int kStage>
+__device__ __forceinline__ void write_block(const ProductArgs& a, const Place& at, int n, float* f, Lines& s, int blocks,
+                                            uint8_t* stage, int lane) {
+    const int j = at.tj + n;
+    if (at.ti >= at.nt || j >= at.mt) return;
+    if constexpr (kPhase == kResult) {
+        // some columns at a time through shared memory, for whole lines
+        constexpr int kC = kStage / 128;
+        const Result& o = a.result[at.k];
+#pragma unroll
+        for (int c = 0; c < 64; c += kC) {
+            if (j * 64 + c >= at.cols) continue;
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < kC / 4; ++q) {
+                float4 v;
+                v.x = o.beta * (f[c + 4 * q] * (kUnscale * kUnscale));
+                v.y = o.beta * (f[c + 4 * q + 1] * (kUnscale * kUnscale));
+                v.z = o.beta * (f[c + 4 * q + 2] * (kUnscale * kUnscale));
+                v.w = o.beta * (f[c + 4 * q + 3] * (kUnscale * kUnscale));
+                *reinterpret_cast<float4*>(stage + staged<kC>(lane, q)) = v;
+            }
+            __syncwarp();
+            write_rows<kC>(a, o, at.b, at.ti * 64 + at.r0, j * 64 + c, at.rows, at.cols, stage, lane);
+        }
+    } else {
+#pragma unroll
+    for (int e = 0; e < 64; ++e) f[e] *= kUnscale;
+    if constexpr (kPhase == kSquare) {
+        if constexpr (kFull) {
+            polynomial_full(a, at, j, f);
+        } else {
+            polynomial_short(a, at, n, s, f, stage, lane);
+            if (n + 1 < blocks && j + 1 < at.mt) s.get(tile_of_s(a, at, n + 1), at, lane);
+        }
+    }
+    // 16 rows of a tile are 2 KB in one piece: hi and lo by way of shared memory (16-byte stores
+    // of every thread to its own row: 30 us of 138 in S of 2 x 4096 x 4096)
+    constexpr int kUnit = 2048;
+    constexpr bool kBoth = kStage >= 2 * kUnit;         // hi and lo at once
+    uint8_t* dst = a.tiles + (int64_t)(at.to + at.ti * at.mt + j) * kTileBytes + 128 * at.r0;
+#pragma unroll 1
+    for (int u = 0; u < (kBoth ? 2 : 4); ++u) {
+        const int half = kBoth ? u : u >> 1, low = kBoth ? 0 : u & 1;
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+        if (lane >> 4 == half) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint4 hi, lo;
+                split8(f + 8 * q, hi, lo);
+                *reinterpret_cast<uint4*>(stage + piece(lane & 15, q)) = low ? lo : hi;
+                if (kBoth) *reinterpret_cast<uint4*>(stage + kUnit + piece(lane & 15, q)) = lo;
+            }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            uint8_t* to = dst + half * kUnit;
+            const int64_t to_lo = (int64_t)at.lo * kTileBytes;
+            bulk_store(to + (low ? to_lo : 0), stage, kUnit);
+            if (kBoth) bulk_store(to + to_lo, stage + kUnit, kUnit);
+        }
+    }    }
 }
 
 // ---- shared memory: stages of A hi, B hi, then the low parts that are used
@@ -460,17 +769,66 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 constexpr uint32_t kPart = 2 * kTileBytes;              // 128 rows x 64 indices
 constexpr uint32_t kRing = 12 * kPart;                  // 192 KB
 constexpr int kMaxStages = 6;
+constexpr uint32_t kStages = 32768;                     // of the epilogue warps
+constexpr uint32_t kBars = kRing + kStages;
 constexpr uint32_t kBarBytes = 256;
-constexpr uint32_t kSmem = 1024 + kRing + kBarBytes;
+constexpr uint32_t kSmem = 1024 + kBars + kBarBytes;
 static_assert(kSmem <= 232448, "shared memory");
 
-template <int kCtas>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductArgs a) {
+// A warp waits together: warp-uniform control keeps descriptors in uniform registers.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
+                                          uint32_t code) {
+    if (__any_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __any_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, status, code));
+}
+
+// The tiles that one lane of the TMA warp loads for an item: at step k tile base + k * step, of
+// a symmetric operand from step `turn` on the other form of it.
+struct Stream {
+    int base, step, turn, base2, step2;
+    uint32_t dst;               // in the stage
+};
+
+// operand o, rows from tile `row` on (of the block from `first` on): its tile number `half`
+__device__ __forceinline__ Stream stream_of(const Operand& o, int first, int row, int half, int low, uint32_t dst) {
+    const int base = o.base + (low ? o.lo : 0), r = row + half;
+    Stream t;
+    t.dst = dst;
+    // K-major: tile (r, k); MN-major: (k, r); symmetric: MN-major before its own block
+    const int k_base = base + r * o.ld, mn_base = base + r;
+    t.turn = o.major == kSymmetric ? first / kSymBlock * kSymBlock : 0;
+    t.base = o.major == kRowsK ? k_base : mn_base;
+    t.step = o.major == kRowsK ? 1 : o.ld;
+    t.base2 = o.major == kRowsMn ? mn_base : k_base;
+    t.step2 = o.major == kRowsMn ? o.ld : 1;
+    return t;
+}
+
+// kFull: both parts of all operands, accumulators added up in registers every step.  Else the
+// accumulators stay in tensor memory for all steps of an item.
+//
+// Epilogue warps: eight, with 64 or 128 columns a thread and up to 168 registers; for pairs in full
+// 16 with 64 columns, as 128 running sums a thread do not fit (2780 cycles a drain, the MMAs take
+// 1536): 640 threads, whose 96 registers at launch go 56 to the control warps, 104 to the others.
+template <int kCtas, bool kFull>
+struct Roles {
+    static constexpr bool kMany = kCtas == 2 && kFull;
+    static constexpr int kEpiWarps = kMany ? 16 : 8;
+    static constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+    static constexpr int kCtl = 56, kEpi = 104, kLaunch = 96;       // registers where kMany
+    static_assert(!kMany || kEpiWarp0 * 32 * kCtl + kEpiWarps * 32 * kEpi <= kThreads * kLaunch, "register split");
+};
+
+template <int kCtas, bool kFull, int kPhase>
+__global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kernel(const __grid_constant__ ProductArgs a) {
+    using R = Roles<kCtas, kFull>;
+    constexpr int kEpiWarps = R::kEpiWarps;
     constexpr int kN = 128 * kCtas;             // columns of the accumulator
-    constexpr int kCols = kN / 2;               // of a thread
+    constexpr int kCols = kN * 4 / kEpiWarps;   // of a thread
+    constexpr int kStage = kStages / kEpiWarps; // shared memory of an epilogue warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kRing);     // [stages] of the leader: all parts landed
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);     // [stages] of the leader: all parts landed
     uint64_t* empty = full + kMaxStages;        // [stages] the MMAs that read the stage are done
     uint64_t* zfull = empty + kMaxStages;       // [2]
     uint64_t* zempty = zfull + 2;               // [2] of the leader
@@ -478,12 +836,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     static_assert((2 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barriers");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
     // parts a stage: of both operands hi, and lo of both (full) or of one (P X)
-    const int parts = a.full ? 4 : a.phase == kUpdate ? 3 : 2;
-    const int stages = 12 / parts;
-    const uint32_t stage_bytes = (uint32_t)parts * kPart;
+    constexpr int parts = kFull ? 4 : is_update(kPhase) ? 3 : 2;
+    // steps a stage: with four MMAs a step the control of each would take longer than they do
+    // (733 cycles a step for 512 of MMAs)
+    constexpr int sub = !kFull && !is_update(kPhase) ? 2 : 1;
+    constexpr int stages = 12 / (parts * sub);
+    constexpr int per_pass = kFull ? 2 : sub;   // steps between drains, or of a stage
+    constexpr uint32_t step_bytes = (uint32_t)parts * kPart, stage_bytes = step_bytes * sub;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
@@ -517,241 +879,223 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     after_previous();
 
     const uint32_t first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
-    if (warp == 0 && lane == 0) {
-        // ------------------------- TMA: this CTA's rows of both operands -------------------------
+    if (warp < kEpiWarp0) {
+    if constexpr (R::kMany) regs_dec<R::kCtl>();
+    if (warp == 0) {
+        // ------------- TMA: this CTA's rows of both operands, a lane for each tile of a stage -------------
         asm volatile("fence.proxy.async;" ::: "memory");    // what the kernel before wrote
         const uint32_t ring = smem_u32(smem);
-        int slot = 0;
-        uint32_t phase = 0;
+        const int in_step = 2 * parts, mine = lane / in_step, tile_of = lane - mine * in_step;
+        uint32_t slot = 0, phase = 0;
         bool reused = false, ok = true;
         for (uint32_t t = first; t < a.items && ok; t += stride) {
-            const Item w = item_of<kCtas>(a, t);
+            const Item w = item_of<kCtas, kPhase>(a, t);
             Operand p, q;
             bool p_lo, q_lo;
-            operands(a, w, p, q, p_lo, q_lo);
-            const int pi = w.i + 2 * (int)rank, qj = w.j + 2 * (int)rank;
-            for (int k = 0; k < w.steps; ++k) {
-                if (reused && !wait_bounded(&empty[slot], phase ^ 1u, abort_flag, a.status, kStatusTimeoutTma)) {
+            operands<kFull, kPhase>(a, w, p, q, p_lo, q_lo);
+            // tiles 0-3: both operands' hi; behind them the low parts
+            const int half = tile_of & 1, which = tile_of >> 1;
+            const bool of_p = which == 0 || (which == 2 && p_lo);
+            const Operand& o = of_p ? p : q;
+            const int block = of_p ? w.i : w.j;
+            const Stream m = stream_of(o, block, block + 2 * (int)rank, half, which >= 2,
+                                              (uint32_t)mine * step_bytes + (uint32_t)tile_of * kTileBytes);
+            for (int k0 = 0; k0 < w.steps; k0 += sub) {
+                const int k = k0 + mine, here = min(sub, w.steps - k0);
+                const int tile = k < m.turn ? m.base + k * m.step : m.base2 + k * m.step2;
+                if (reused && !warp_wait(&empty[slot], phase ^ 1u, abort_flag, a.status, kStatusTimeoutTma)) {
                     ok = false;
                     break;
                 }
-                if (rank == 0) mbar_arrive_expect_tx(&full[slot], kCtas * stage_bytes);
+                if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&full[slot], kCtas * step_bytes * here);
+                __syncwarp();
                 const uint32_t bar = kCtas == 2 ? in_leader(&full[slot]) : smem_u32(&full[slot]);
-                uint32_t dst = ring + (uint32_t)slot * stage_bytes;
-                const bool pk = k_major<kCtas>(p, w.i, k), qk = k_major<kCtas>(q, w.j, k);
-                const int p0 = p.base + (pk ? pi * p.ld + k : k * p.ld + pi), ps = pk ? p.ld : 1;
-                const int q0 = q.base + (qk ? qj * q.ld + k : k * q.ld + qj), qs = qk ? q.ld : 1;
-                load_tile<kCtas>(&a.map, p0, dst, bar);
-                load_tile<kCtas>(&a.map, p0 + ps, dst + kTileBytes, bar);
-                load_tile<kCtas>(&a.map, q0, dst + kPart, bar);
-                load_tile<kCtas>(&a.map, q0 + qs, dst + kPart + kTileBytes, bar);
-                dst += 2 * kPart;
-                if (p_lo) {
-                    load_tile<kCtas>(&a.map, p0 + p.lo, dst, bar);
-                    load_tile<kCtas>(&a.map, p0 + p.lo + ps, dst + kTileBytes, bar);
-                    dst += kPart;
-                }
-                if (q_lo) {
-                    load_tile<kCtas>(&a.map, q0 + q.lo, dst, bar);
-                    load_tile<kCtas>(&a.map, q0 + q.lo + qs, dst + kTileBytes, bar);
-                }
-                if (++slot == stages) {
+                if (mine < here) load_tile<kCtas>(&a.map, tile, ring + slot * stage_bytes + m.dst, bar);
+                if (++slot == (uint32_t)stages) {
                     slot = 0;
                     phase ^= 1u;
                     reused = true;
                 }
             }
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ------------------------- MMA: the leader, for both CTAs -------------------------
         if (rank == 0) {
             constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kN >> 3) << 17) | ((uint32_t)(128 * kCtas >> 4) << 24);
             const uint32_t ring = smem_u32(smem);
-            int slot = 0, z = 0;
-            uint32_t phase = 0, zphase = 0, zused = 0;
+            const uint32_t leader = lane == 0 ? 1u : 0u;
+            uint32_t slot = 0, phase = 0, z = 0, zphase = 0, zused = 0;
             bool ok = true;
             for (uint32_t t = first; t < a.items && ok; t += stride) {
-                const Item w = item_of<kCtas>(a, t);
+                const Item w = item_of<kCtas, kPhase>(a, t);
                 Operand p, q;
                 bool p_lo, q_lo;
-                operands(a, w, p, q, p_lo, q_lo);
-                int in_chunk = 0;
-                for (int k = 0; k < w.steps; ++k) {
-                    if (in_chunk == 0 && ((zused >> z) & 1u)) {
-                        if (!wait_bounded(&zempty[z], (zphase >> z) & 1u, abort_flag, a.status, kStatusTimeoutMma)) {
-                            ok = false;
-                            break;
-                        }
-                        zphase ^= 1u << z;
-                        tc_fence_after();
-                    }
-                    if (!wait_bounded(&full[slot], phase, abort_flag, a.status, kStatusTimeoutMma)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const bool pk = k_major<kCtas>(p, w.i, k), qk = k_major<kCtas>(q, w.j, k);
+                operands<kFull, kPhase>(a, w, p, q, p_lo, q_lo);
+                // the MMAs of step k, from the stage at shared-memory address `at`: small terms (low), or hi hi
+                auto issue = [&](int k, uint32_t at, uint32_t d, bool small, uint32_t acc) {
+                    const bool pk = k_major(p, w.i, k), qk = k_major(q, w.j, k);
                     const uint32_t idesc = kIdesc | (pk ? 0u : 1u << 15) | (qk ? 0u : 1u << 16);
-                    const uint32_t at = ring + (uint32_t)slot * stage_bytes;
                     const uint32_t p0 = pk ? sdesc128_lo(at) : sdesc128mn_lo(at);
                     const uint32_t q0 = qk ? sdesc128_lo(at + kPart) : sdesc128mn_lo(at + kPart);
-                    const uint32_t pl = p0 + ((2 * kPart) >> 4), ql = q0 + (((p_lo ? 2 : 1) * kPart) >> 4);
                     const uint32_t pstep = pk ? 2u : 128u, qstep = qk ? 2u : 128u;
-                    const uint32_t d = tmem + (uint32_t)(z * kN);
-                    // the small terms first: a sum loses by its size at every addition
-                    uint32_t acc = in_chunk == 0 ? 0u : 1u;
-                    if (q_lo) {
+                    if (!small) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk, acc = 1u) mma<kCtas>(d, p0 + kk * pstep, ql + kk * qstep, idesc, acc);
+                        for (uint32_t kk = 0; kk < 4; ++kk, acc = 1u)
+                            mma<kCtas>(d, p0 + kk * pstep, q0 + kk * qstep, idesc, acc, leader);
+                        return;
                     }
-                    if (p_lo) {
+                    if (kFull || q_lo) {
+                        const uint32_t ql = q0 + (((kFull || p_lo ? 2 : 1) * kPart) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk, acc = 1u) mma<kCtas>(d, pl + kk * pstep, q0 + kk * qstep, idesc, acc);
+                        for (uint32_t kk = 0; kk < 4; ++kk, acc = 1u)
+                            mma<kCtas>(d, p0 + kk * pstep, ql + kk * qstep, idesc, acc, leader);
                     }
+                    if (kFull || p_lo) {
+                        const uint32_t pl = p0 + ((2 * kPart) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk, acc = 1u) mma<kCtas>(d, p0 + kk * pstep, q0 + kk * qstep, idesc, acc);
-                    commit<kCtas>(&empty[slot]);
-                    if (++in_chunk == a.chunk || k == w.steps - 1) {
-                        commit<kCtas>(&zfull[z]);
+                        for (uint32_t kk = 0; kk < 4; ++kk, acc = 1u)
+                            mma<kCtas>(d, pl + kk * pstep, q0 + kk * qstep, idesc, acc, leader);
+                    }
+                };
+                auto landed = [&](uint32_t s, uint32_t parity) {
+                    const bool here = warp_wait(&full[s], parity, abort_flag, a.status, kStatusTimeoutMma);
+                    tc_fence_after();
+                    return here;
+                };
+                auto next = [&](uint32_t& s, uint32_t& parity) {
+                    if (++s == (uint32_t)stages) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
+                };
+                for (int k0 = 0; k0 < w.steps && ok; k0 += per_pass) {
+                    const int here = min(per_pass, w.steps - k0);
+                    if ((kFull || k0 == 0) && ((zused >> z) & 1u)) {
+                        if (!(ok = warp_wait(&zempty[z], (zphase >> z) & 1u, abort_flag, a.status, kStatusTimeoutMma))) break;
+                        zphase ^= 1u << z;
+                    }
+                    if (!(ok = landed(slot, phase))) break;
+                    const uint32_t d = tmem + z * kN, at = ring + slot * stage_bytes;
+                    if constexpr (kFull) {
+                        // the small terms of two steps first: a sum loses by its size at every addition
+                        issue(k0, at, d, true, 0u);
+                        uint32_t slot2 = slot, phase2 = phase;
+                        next(slot2, phase2);
+                        const uint32_t at2 = ring + slot2 * stage_bytes;
+                        if (here == 2) {
+                            if (!(ok = landed(slot2, phase2))) break;
+                            issue(k0 + 1, at2, d, true, 1u);
+                        }
+                        issue(k0, at, d, false, 1u);
+                        commit<kCtas>(&empty[slot], leader);
+                        if (here == 2) {
+                            issue(k0 + 1, at2, d, false, 1u);
+                            commit<kCtas>(&empty[slot2], leader);
+                            slot = slot2;
+                            phase = phase2;
+                        }
+                    } else {
+                        for (int k = k0; k < k0 + here; ++k) {
+                            const uint32_t from = at + (uint32_t)(k - k0) * step_bytes;
+                            if constexpr (is_update(kPhase)) issue(k, from, d, true, k == 0 ? 0u : 1u);
+                            issue(k, from, d, false, is_update(kPhase) || k > 0 ? 1u : 0u);
+                        }
+                        commit<kCtas>(&empty[slot], leader);
+                    }
+                    next(slot, phase);
+                    if (kFull || k0 + here == w.steps) {
+                        commit<kCtas>(&zfull[z], leader);
                         zused |= 1u << z;
-                        z ^= 1;
-                        in_chunk = 0;
-                    }
-                    if (++slot == stages) {
-                        slot = 0;
-                        phase ^= 1u;
+                        z ^= 1u;
                     }
                 }
             }
-            commit<kCtas>(done);
+            commit<kCtas>(done, leader);
         }
-        wait_drain(done, 0, a.status);
-    } else if (warp >= kEpiWarp0) {
-        // ------------------------- epilogue: eight warps -------------------------
+        if (lane == 0) wait_drain(done, 0, a.status);
+    }
+    } else {
+        if constexpr (R::kMany) regs_inc<R::kEpi>();
+        // ------------------------- epilogue -------------------------
         const int quad = warp & 3, part = (warp - kEpiWarp0) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(part * kCols);
-        int z = 0;
-        uint32_t zphase = 0;
-        bool ok = true;
-        for (uint32_t t = first; t < a.items && ok; t += stride) {
-            const Item w = item_of<kCtas>(a, t);
-            float acc[kCols];
-            const int chunks = (w.steps + a.chunk - 1) / a.chunk;
-            for (int n = 0; n < chunks; ++n) {
-                bool here = true;
-                if (lane == 0)
-                    here = wait_bounded(&zfull[z], (zphase >> z) & 1u, abort_flag, a.status, kStatusTimeoutEpi);
-                if (!__shfl_sync(0xffffffffu, here ? 1 : 0, 0)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t from = lanes + (uint32_t)(z * kN);
-#pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32(from + c, v);
-                    tmem_ld_wait();
-                    if (n == 0) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) acc[c + e] = __uint_as_float(v[e]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) acc[c + e] += __uint_as_float(v[e]);
-                    }
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (kCtas == 2)
-                        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(&zempty[z]))
-                                     : "memory");
-                    else
-                        mbar_arrive(&zempty[z]);
-                }
-                zphase ^= 1u << z;
-                z ^= 1;
+        uint8_t* const stage = smem + kRing + (warp - kEpiWarp0) * kStage;
+        uint32_t z = 0, zphase = 0;
+        auto filled = [&]() {
+            const bool here = warp_wait(&zfull[z], (zphase >> z) & 1u, abort_flag, a.status, kStatusTimeoutEpi);
+            tc_fence_after();
+            return here;
+        };
+        auto emptied = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kCtas == 2)
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_leader(&zempty[z]))
+                                 : "memory");
+                else
+                    mbar_arrive(&zempty[z]);
             }
-            if (!ok) break;
-            // this thread's row and columns of the result
-            const Shape& s = a.shape[w.k];
-            const Grid g(s);
-            const int ti = w.i + 2 * (int)rank + quad / 2, r = 32 * (quad & 1) + lane;
-            const int tj = w.j + part * (kCols / 64);
-            const int nt = a.phase == kUpdate ? g.rt : g.mt, mt = a.phase == kUpdate ? g.ct : g.mt;
-            if (ti >= nt) continue;
-            const int at = s.base + w.b * g.tiles();
-            if (a.phase == kUpdate && a.last) {
-                const Result& o = a.result[w.k];
-                const int row = ti * 64 + r;
-#pragma unroll
-                for (int c = 0; c < kCols; c += 8) {
-                    const int col = tj * 64 + c;
-                    if (row >= s.rows || col >= s.cols) continue;
-                    float v[8];
-                    if (o.w.data != nullptr) {
-                        get8(o.w, w.b, row, col, s.cols, v);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = fmaf(a.alpha, v[e], o.beta * (acc[c + e] * (kUnscale * kUnscale)));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = o.beta * (acc[c + e] * (kUnscale * kUnscale));
-                    }
-                    put8(o.out, w.b, row, col, s.cols, v);
-                }
-                continue;
-            }
-            // images: accumulators carry 2^24
-            const int to = at + (a.phase == kUpdate ? g.x(1 - a.from) : a.phase == kGram ? g.s() : g.p());
-            const int64_t lo = (int64_t)(a.phase == kUpdate ? g.x_lo() : g.s_lo()) * kTileBytes;
-            const int64_t back = (int64_t)(g.p() - g.s()) * kTileBytes;     // from P to S
-            const bool mend = a.phase == kSquare && !a.full;
-            // the low part of S's element (i, i), times 2^12
-            auto diagonal = [&](int i) {
-                const int at_tile = at + g.s() + g.s_lo() + (i >> 6) * (mt + 1);
-                const uint8_t* p = a.tiles + (int64_t)at_tile * kTileBytes + piece(i & 63, (i & 63) >> 3) + (i & 7) * 2;
-                return __half2float(*reinterpret_cast<const __half*>(p));
+            zphase ^= 1u << z;
+            z ^= 1u;
+        };
+        for (uint32_t t = first; t < a.items; t += stride) {
+            const Item w = item_of<kCtas, kPhase>(a, t);
+            auto place = [&](const Item& w) {
+                return Place(a, kPhase, w, w.i + 2 * (int)rank + quad / 2, w.j + part * (kCols / 64), 32 * (quad & 1), lane);
             };
-            const float own = mend ? diagonal(ti * 64 + r) * kUnscale : 0.f;
+            Lines s;
+            if constexpr (kFull) {
+                float acc[kCols];
+                bool here = true;
+                const int drains = (w.steps + per_pass - 1) / per_pass;
+                for (int n = 0; n < drains; ++n) {
+                    if (!(here = filled())) break;
+                    // columns in flight: all, or what registers there are for
+                    constexpr int kAhead = R::kMany ? 32 : 64;
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8) {
-                const int j = tj + c / 64;
-                if (j >= mt) continue;
-                uint8_t* hi_at = a.tiles + (int64_t)(to + ti * mt + j) * kTileBytes + piece(r, (c % 64) / 8);
-                float v[8];
+                    for (int c = 0; c < kCols; c += kAhead) {
+                        uint32_t v[kAhead];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = acc[c + e] * kUnscale;
-                if (a.phase == kSquare) {
-                    float sv[8];
-                    const uint4 shi = *reinterpret_cast<const uint4*>(hi_at - back);
-                    join8(shi, *reinterpret_cast<const uint4*>(hi_at - back + lo), sv);
-                    if (mend) {
-                        float lead[8];
-                        join8(shi, make_uint4(0u, 0u, 0u, 0u), lead);
+                        for (int e = 0; e < kAhead; e += 32) tmem_ld32(lanes + z * kN + c + e, v + e);
+                        tmem_ld_wait();
+                        if (c + kAhead == kCols) emptied();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = fmaf(own + diagonal(j * 64 + c % 64 + e) * kUnscale, lead[e], v[e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[e] = fmaf(a.c, v[e], a.b * sv[e]);
-                        const int row = ti * 64 + r;
-                        if (row == j * 64 + c % 64 + e && row < (g.wide ? s.rows : s.cols)) v[e] += a.a * kScale;
+                        for (int e = 0; e < kAhead; ++e)
+                            acc[c + e] = n == 0 ? __uint_as_float(v[e]) : acc[c + e] + __uint_as_float(v[e]);
                     }
                 }
-                uint4 hi, low;
-                split8(v, hi, low);
-                *reinterpret_cast<uint4*>(hi_at) = hi;
-                *reinterpret_cast<uint4*>(hi_at + lo) = low;
+                if (!here) break;
+                const Place at = place(item_of<kCtas, kPhase>(a, t));       // (again: registers are short before)
+#pragma unroll
+                for (int c = 0; c < kCols; c += 64)
+                    write_block<kFull, kPhase, kStage>(a, at, c / 64, acc + c, s, kCols / 64, stage, lane);
+            } else {
+                const Place at = place(w);
+                if (kPhase == kSquare && at.ti < at.nt && at.tj < at.mt) s.get(tile_of_s(a, at, 0), at, lane);
+                if (!filled()) break;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 64) {
+                    uint32_t v[64];
+                    tmem_ld32(lanes + z * kN + c, v);
+                    tmem_ld32(lanes + z * kN + c + 32, v + 32);
+                    tmem_ld_wait();
+                    if (c + 64 == kCols) emptied();
+                    float f[64];
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) f[e] = __uint_as_float(v[e]);
+                    write_block<kFull, kPhase, kStage>(a, at, c / 64, f, s, kCols / 64, stage, lane);
+                }
             }
         }
+        if (lane == 0) bulk_wait();
     }
 
     if (*abort_flag) {
         // given up: copies in flight land within microseconds, which nobody waits for any more
         for (int i = 0; i < 100; ++i) __nanosleep(10000);
     }
+    __syncwarp();
     tc_fence_before();
     if constexpr (kCtas == 2) cluster_sync();
     else __syncthreads();
@@ -801,16 +1145,18 @@ int next_group(int n, const mttkrp_matrices* like, int& k, int64_t& b, Part* par
     return used;
 }
 
-// CTAs of the passes over U for one matrix: a tile each, but for large ones
-int slices_of(int64_t tiles) { return (int)std::min<int64_t>(tiles, kMaxSlices); }
+// sums of a matrix: of 16 groups of eight columns a thread, more for large ones
+int slices_of(const mttkrp_matrices& m) {
+    return (int)std::min<int64_t>(cdiv(m.rows * cdiv(m.cols, 8), 16 * kPassThreads), kMaxSlices);
+}
 
 size_t partial_bytes(int used, const Part* parts, const mttkrp_matrices* like) {
     int64_t sums = 0;
     for (int i = 0; i < used; ++i) {
         const mttkrp_matrices& m = like[parts[i].k];
-        sums += parts[i].count * slices_of(cdiv(m.rows, 64) * cdiv(m.cols, 64));
+        sums += parts[i].count * slices_of(m);
     }
-    return (size_t)cdiv(sums * 8, 1024) * 1024;
+    return (size_t)cdiv(sums * (int64_t)sizeof(Partial), 1024) * 1024;
 }
 
 Store store_of(const mttkrp_matrices& m, int64_t b0) {
@@ -844,6 +1190,31 @@ cudaError_t launch(K kernel, unsigned blocks, unsigned threads, size_t smem, int
     return e;
 }
 
+template <int kCtas, bool kFull>
+cudaError_t launch_product(int phase, unsigned units, cudaStream_t s, const ProductArgs& p) {
+    const auto kernel = phase == kGram     ? product_kernel<kCtas, kFull, kGram>
+                        : phase == kSquare ? product_kernel<kCtas, kFull, kSquare>
+                        : phase == kUpdate ? product_kernel<kCtas, kFull, kUpdate>
+                                           : product_kernel<kCtas, kFull, kResult>;
+    return launch(kernel, units * kCtas, Roles<kCtas, kFull>::kThreads, kSmem, kCtas, s, p);
+}
+
+// allows a form of the kernels their shared memory
+template <int kCtas, bool kFull>
+cudaError_t allow() {
+    for (const auto kernel : {product_kernel<kCtas, kFull, kGram>, product_kernel<kCtas, kFull, kSquare>,
+                              product_kernel<kCtas, kFull, kUpdate>, product_kernel<kCtas, kFull, kResult>}) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        cudaFuncAttributes attr;
+        if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kernel);
+        // the register split that a kernel asks for waits for ever where its launch has fewer
+        if (e == cudaSuccess && Roles<kCtas, kFull>::kMany && attr.numRegs < Roles<kCtas, kFull>::kLaunch)
+            e = cudaErrorInvalidConfiguration;
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 struct Device {
     int sms = 0;
 };
@@ -859,24 +1230,38 @@ cudaError_t device(Device& d) {
         return cudaSuccess;
     }
     e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(product_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(product_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess) e = allow<1, false>();
+    if (e == cudaSuccess) e = allow<1, true>();
+    if (e == cudaSuccess) e = allow<2, false>();
+    if (e == cudaSuccess) e = allow<2, true>();
     if (e == cudaSuccess && dev < 64) known[dev] = d.sms;
     return e;
 }
 
-// Work items of the products with tiles of 64 x kBlock a side, into the shapes.
-void count_items(ProductArgs& p, int block, uint32_t* items) {
-    items[0] = items[1] = 0;
+// Numbers the work items of a product whose CTAs (or pairs) take blocks of 128 (256) a side, and
+// says how long it takes, in microseconds without the launch: waves of items, whose epilogues run
+// beside the next one's MMAs.  Steps of 64 indices and epilogues as measured on 12 x 1024 x 4096,
+// 2 x 4096 x 4096 and 3 x 512 x 2000; a pair's items are four times a CTA's.
+float number_items(ProductArgs& p, int phase, int ctas, bool full, int sms) {
+    const int f = is_update(phase) ? 1 : 0, block = 2 * ctas;
+    const float step = full ? (ctas == 2 ? 1.02f : 0.72f) : f ? (ctas == 2 ? 0.61f : 0.52f) : (ctas == 2 ? 0.33f : 0.26f);
+    const float end = (phase == kSquare ? (ctas == 2 ? 8.f : 4.f) : (ctas == 2 ? 4.f : 2.f));
+    float work = 0.f, longest = 0.f;
+    p.items = 0;
     for (int i = 0; i < p.n; ++i) {
         Shape& s = p.shape[i];
         const Grid g(s);
-        const int64_t nb = cdiv(g.mt, block);
-        s.first[0] = items[0];
-        s.first[1] = items[1];
-        items[0] += (uint32_t)(s.count * (nb * (nb + 1) / 2));
-        items[1] += (uint32_t)(s.count * cdiv(g.rt, block) * cdiv(g.ct, block));
+        s.first[f] = p.items;
+        const int64_t items = f ? s.count * cdiv(g.rt, block) * cdiv(g.ct, block)
+                                : s.count * (int64_t)symmetric_items((int)cdiv(g.mt, block), ctas);
+        const float steps = (float)(phase == kGram ? (g.wide ? g.ct : g.rt) : g.mt);
+        const float one = std::max(steps * step, end);
+        work += (float)items * one;
+        longest = std::max(longest, one);
+        p.items += (uint32_t)items;
     }
+    const float units = (float)(sms / ctas), waves = std::ceil((float)p.items / units);
+    return std::max(longest, waves * work / (float)p.items) + end;
 }
 
 // Tensor map of the images: rows of 128 bytes, loaded 64 at a time as they are.
@@ -905,12 +1290,12 @@ cudaError_t run_group(const NewtonArgs& a, int used, const Part* parts, int64_t 
     pass.mu = a.mu;
     pass.nesterov = a.nesterov;
     pass.eps = a.eps;
-    pass.partial = static_cast<double*>(a.ws);
+    pass.partial = static_cast<Partial*>(a.ws);
     pass.tiles = p.tiles = static_cast<uint8_t*>(a.ws) + partial_bytes(used, parts, a.grad);
     p.status = a.status;
     p.alpha = a.alpha;
-    p.full = false;
-    uint32_t blocks = 0;
+    bool full = false;          // both parts of every operand
+    uint32_t strips = 0;
     int base = 0, sums = 0;
     for (int i = 0; i < used; ++i) {
         const Part& w = parts[i];
@@ -925,37 +1310,35 @@ cudaError_t run_group(const NewtonArgs& a, int used, const Part* parts, int64_t 
             u.m = store_of(a.momentum[w.k], w.b0);
             u.out = store_of(a.momentum_out[w.k], w.b0);
         }
-        u.first = blocks;
-        u.slices = slices_of((int64_t)g.rt * g.ct);
+        u.slices = slices_of(m);
+        u.first[0] = (uint32_t)sums;
+        u.first[1] = strips;
         u.at = sums;
-        blocks += (uint32_t)(u.slices * w.count);
         sums += (int)(u.slices * w.count);
+        strips += (uint32_t)(w.count * g.rt * cdiv(g.ct, kStrip));
         base += (int)(g.tiles() * w.count);
         Result& r = p.result[i];
         r.out = store_of(a.out[w.k], w.b0);
         r.w = a.weight != nullptr ? store_of(a.weight[w.k], w.b0) : Store{nullptr, 0, 0, 0, 0};
         r.beta = a.beta[w.k];
-        if (r.out.type != MTTKRP_BF16) p.full = true;
+        if (r.out.type != MTTKRP_BF16) full = true;
     }
     if (!tile_map(&p.map, p.tiles, (uint64_t)tiles * 64)) return cudaErrorUnknown;
-    cudaError_t e = launch(squares_kernel, blocks, kPassThreads, 0, 1, s, pass);
-    if (e == cudaSuccess) e = launch(images_kernel, blocks, kPassThreads, 0, 1, s, pass);
-    const int ctas = 1;
-    uint32_t items[2];
-    count_items(p, 2 * ctas, items);
+    cudaError_t e = launch(squares_kernel, (unsigned)sums, kPassThreads, 0, 1, s, pass);
+    if (e == cudaSuccess) e = launch(images_kernel, strips, kPassThreads, 0, 1, s, pass);
     for (int step = 0; step < a.steps && e == cudaSuccess; ++step) {
         p.from = step & 1;
-        p.last = step == a.steps - 1;
         p.a = a.coefficients[3 * step];
         p.b = a.coefficients[3 * step + 1];
         p.c = a.coefficients[3 * step + 2];
-        p.chunk = p.full ? 1 : 8;
-        for (int phase = kGram; phase <= kUpdate && e == cudaSuccess; ++phase) {
-            p.phase = phase;
-            p.items = items[phase == kUpdate ? 1 : 0];
+        for (int at = kGram; at <= kUpdate && e == cudaSuccess; ++at) {
+            const int phase = at == kUpdate && step == a.steps - 1 ? kResult : at;
+            const float pair = number_items(p, phase, 2, full, d.sms);
+            const int ctas = number_items(p, phase, 1, full, d.sms) <= pair ? 1 : 2;
+            if (ctas == 2) number_items(p, phase, 2, full, d.sms);
             const unsigned units = std::min<unsigned>(p.items, (unsigned)(d.sms / ctas));
-            e = ctas == 2 ? launch(product_kernel<2>, units * 2, kThreads, kSmem, 2, s, p)
-                          : launch(product_kernel<1>, units, kThreads, kSmem, 1, s, p);
+            e = ctas == 2 ? full ? launch_product<2, true>(phase, units, s, p) : launch_product<2, false>(phase, units, s, p)
+                          : full ? launch_product<1, true>(phase, units, s, p) : launch_product<1, false>(phase, units, s, p);
         }
     }
     return e;

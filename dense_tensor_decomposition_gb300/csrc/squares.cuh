@@ -34,7 +34,7 @@ struct Sum {
 
 // over the block; the result in thread 0
 template <int kWarps>
-__device__ __forceinline__ double block_sum(Sum s) {
+__device__ __forceinline__ Sum block_total(Sum s) {
     __shared__ float hi[kWarps], lo[kWarps];
     __shared__ double wide[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -51,17 +51,21 @@ __device__ __forceinline__ double block_sum(Sum s) {
         wide[warp] = s.wide;
     }
     __syncthreads();
-    double sum = 0.0;
+    Sum t;
     if (threadIdx.x == 0) {
-        Sum t;
         for (int w = 0; w < kWarps; ++w) {
             t.add(hi[w]);
             t.lo += lo[w];
             if (any) t.wide += wide[w];
         }
-        sum = (double)t.hi + (double)t.lo + t.wide;
     }
-    return sum;
+    return t;
+}
+
+template <int kWarps>
+__device__ __forceinline__ double block_sum(Sum s) {
+    const Sum t = block_total<kWarps>(s);
+    return threadIdx.x == 0 ? (double)t.hi + (double)t.lo + t.wide : 0.0;
 }
 
 }  // namespace mk
