@@ -36,19 +36,14 @@
 #include <cmath>
 
 #include "launch.cuh"
+#include "newton.cuh"
 #include "newton.h"
-#include "ptx.cuh"
-#include "squares.cuh"
-#include "types.cuh"
 
 namespace mk {
 namespace {
 
-constexpr int kTable = 32;                  // list elements a group of launches
 constexpr int kMaxSlices = 256;             // CTAs a matrix in the passes over U
-constexpr uint32_t kTileBytes = 8192;
 constexpr int64_t kGroupTiles = (int64_t)4 << 17;   // 4 GB of images a group (one matrix at least)
-constexpr float kScale = 4096.f, kUnscale = 1.f / 4096.f;   // of the images
 
 constexpr int kEpiWarp0 = 4;
 constexpr int kPassThreads = 256;
@@ -56,15 +51,6 @@ constexpr int kPassThreads = 256;
 // what a launch computes: S, P (from S S), P X, and the last P X, whose result goes to the caller
 enum Phase { kGram, kSquare, kUpdate, kResult };
 __host__ __device__ constexpr bool is_update(int phase) { return phase >= kUpdate; }
-
-// Matrices of one list element.  Tiles of one matrix, hi and lo of each: X twice (a step
-// reads one and writes the other), S, P.
-struct Shape {
-    int base;                   // first tile
-    int rows, cols, count;
-    uint32_t first[2];          // number of the first work item: of S and S S, of P X
-};
-__host__ __device__ inline int tiles_of(int n) { return (n + 63) / 64; }
 
 struct Grid {
     int rt, ct, mt;             // tiles of 64 along rows, columns and the smaller side
@@ -79,98 +65,7 @@ struct Grid {
     __host__ __device__ int tiles() const { return 4 * (rt * ct + mt * mt); }
 };
 
-// Rows of a matrix in its own memory.
-struct Store {
-    void* data;
-    int64_t row, batch;         // strides
-    uint8_t type, whole;        // whole: eight elements from a multiple of eight on are aligned to 16 bytes
-};
-
-template <typename T>
-__device__ __forceinline__ void get8_of(const Store& s, int64_t at, int valid, float* v) {
-    const T* p = static_cast<const T*>(s.data) + at;
-    if (s.whole && valid >= 8) {
-        constexpr int kVec = 16 / sizeof(T);
-#pragma unroll
-        for (int k = 0; k < 8 / kVec; ++k) {
-            const uint4 bits = reinterpret_cast<const uint4*>(p)[k];    // (a reference to memory would be copied by bytes)
-            const auto w = as_pack<Pack<T, kVec>>(bits);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) v[k * kVec + e] = to_f32(w.v[e]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < valid ? to_f32(p[e]) : 0.f;
-    }
-}
-// eight elements of row r from column c on, zeros from `cols` on
-__device__ __forceinline__ void get8(const Store& s, int64_t b, int r, int c, int cols, float* v) {
-    const int64_t at = b * s.batch + r * s.row + c;
-    if (s.type == MTTKRP_F32) get8_of<float>(s, at, cols - c, v);
-    else if (s.type == MTTKRP_BF16) get8_of<__nv_bfloat16>(s, at, cols - c, v);
-    else get8_of<__half>(s, at, cols - c, v);
-}
-template <typename T>
-__device__ __forceinline__ void put8_of(const Store& s, int64_t at, int valid, const float* v) {
-    T* p = static_cast<T*>(s.data) + at;
-    if (s.whole && valid >= 8) {
-        constexpr int kVec = 16 / sizeof(T);
-#pragma unroll
-        for (int k = 0; k < 8 / kVec; ++k) {
-            Pack<T, kVec> w;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) w.v[e] = from_f32<T>(v[k * kVec + e]);
-            reinterpret_cast<uint4*>(p)[k] = as_pack<uint4>(w);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < valid) p[e] = from_f32<T>(v[e]);
-    }
-}
-__device__ __forceinline__ void put8(const Store& s, int64_t b, int r, int c, int cols, const float* v) {
-    const int64_t at = b * s.batch + r * s.row + c;
-    if (s.type == MTTKRP_F32) put8_of<float>(s, at, cols - c, v);
-    else if (s.type == MTTKRP_BF16) put8_of<__nv_bfloat16>(s, at, cols - c, v);
-    else put8_of<__half>(s, at, cols - c, v);
-}
-
-// eight scaled values as hi and lo
-__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __half2 p = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-        const float2 f = __half22float2(p);
-        const __half2 q = __floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y);
-        h[e] = *reinterpret_cast<const uint32_t*>(&p);
-        l[e] = *reinterpret_cast<const uint32_t*>(&q);
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-__device__ __forceinline__ void join8(const uint4& hi, const uint4& lo, float* v) {
-    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[e]));
-        v[2 * e] = a.x + b.x;
-        v[2 * e + 1] = a.y + b.y;
-    }
-}
-
-// byte offset of 16-byte piece c (0-7) of row r in a tile
-__device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
 // ---------------------------------------------------------------- the passes over U
-
-struct Source {
-    Store g, m, out;            // m.data NULL: no momentum
-    uint32_t first[2];          // number of the element's first work item: sums, images
-    int slices;                 // sums of a matrix
-    int at;                     // number of its first sum
-};
 
 // a sum of squares as fp32 pair, and in fp64 what does not fit
 struct Partial {
@@ -188,32 +83,6 @@ struct PassArgs {
     Shape shape[kTable];
     Source source[kTable];
 };
-
-// the last of n increasing numbers that is not above x
-template <typename F>
-__device__ __forceinline__ int element_of(int n, uint32_t x, F first) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first(mid) <= x) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
-}
-
-// U of eight elements and, where there is momentum, what it becomes
-__device__ __forceinline__ void update8(const PassArgs& a, const Source& s, int b, int r, int c, int cols, float* u,
-                                        float* kept) {
-    get8(s.g, b, r, c, cols, u);
-    if (s.m.data != nullptr) {
-        get8(s.m, b, r, c, cols, kept);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            kept[e] = fmaf(a.mu, kept[e], u[e]);
-            u[e] = a.nesterov ? fmaf(a.mu, kept[e], u[e]) : kept[e];
-        }
-    }
-}
 
 // Sums of squares: a matrix in slices of consecutive groups of 8 columns, row by row, a slice
 // a CTA.
@@ -237,7 +106,7 @@ __global__ void __launch_bounds__(kPassThreads) squares_kernel(const __grid_cons
             if (x < g1) {
                 const int r = narrow ? (int)((uint32_t)x / (uint32_t)per) : (int)(x / per);
                 const int c = (int)(x - (int64_t)r * per) * 8;
-                update8(a, s, b, r, c, cols, v[i], kept);
+                update8(a.mu, a.nesterov, s, b, r, c, cols, v[i], kept);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
@@ -276,15 +145,7 @@ __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_const
     __shared__ float2 found;
     const Sum total = block_total<kPassThreads / 32>(sum);
     if (threadIdx.x == 0) {
-        // factors whose product is 2^12 / (|U| + eps); two, as one may leave fp32's range
-        const float square = total.hi + total.lo;
-        if (total.wide == 0.0 && square >= 0x1p-100f && square <= 0x1p100f) {
-            found = make_float2(1.f, kScale / (sqrtf(square) + (float)a.eps));
-        } else {
-            const double f = (double)kScale / (sqrt((double)total.hi + (double)total.lo + total.wide) + a.eps);
-            const double by = f > 0x1p60 ? 0x1p100 : f < 0x1p-60 ? 0x1p-100 : 1.0;
-            found = make_float2((float)by, (float)(f / by));
-        }
+        found = factors(total, a.eps);
     }
     __syncthreads();
     const float2 factor = found;
@@ -301,7 +162,7 @@ __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_const
         for (int i = 0; i < kAhead; ++i) {
             const int row = ti * 64 + warp + 8 * (i0 + i);
             if (row < shape.rows && c < shape.cols) {
-                update8(a, s, b, row, c, shape.cols, u[i], kept[i]);
+                update8(a.mu, a.nesterov, s, b, row, c, shape.cols, u[i], kept[i]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
@@ -324,11 +185,6 @@ __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------- the products
-
-struct Result {
-    Store out, w;               // w.data NULL: alpha is not used
-    float beta;
-};
 
 // Work items of a symmetric result of nb x nb blocks: rows of blocks from the block of 256 they are in on.
 __host__ __device__ inline int symmetric_items(int nb, int ctas) {
@@ -464,47 +320,6 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, int tile, uint
             : "memory");
 }
 
-// by the lane whose `leader` is not 0
-template <int kCtas>
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc, uint32_t leader) {
-    if constexpr (kCtas == 2)
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-            "mov.b64 da, {%1, %3};\n\t"
-            "mov.b64 db, {%2, %3};\n\t"
-            "setp.ne.b32 p, %5, 0;\n\t"
-            "setp.ne.b32 e, %6, 0;\n\t"
-            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
-            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc), "r"(leader));
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-            "mov.b64 da, {%1, %3};\n\t"
-            "mov.b64 db, {%2, %3};\n\t"
-            "setp.ne.b32 p, %5, 0;\n\t"
-            "setp.ne.b32 e, %6, 0;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
-            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc), "r"(leader));
-}
-
-// arrive on `bar` (of both CTAs) when that lane's MMAs so far are done
-template <int kCtas>
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
-    if constexpr (kCtas == 2)
-        asm volatile(
-            "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
-            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
-                smem_u32(bar)),
-            "h"((uint16_t)3), "r"(leader)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
-            "r"(leader)
-            : "memory");
-}
-
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(dst),
                  "r"(smem_u32(src)), "r"(bytes)
@@ -517,70 +332,6 @@ __device__ __forceinline__ void bulk_wait_read() {
 }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// A warp's stage: 32 rows of kC columns (16 or 32) of fp32, 16-byte pieces in an order in which
-// neither rows nor columns meet in a bank.
-template <int kC>
-__device__ __forceinline__ uint32_t staged(int r, int q) {
-    return kC == 32 ? piece(r, q) : (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
-}
-
-// Writes them (beta O(U)) to a result, after adding alpha W: whole rows of the stage at a time, or
-// where rows are not aligned a column a lane.
-template <typename T, int kC>
-__device__ __forceinline__ void write_rows_of(const ProductArgs& a, const Result& o, int b, int row0, int col0, int rows,
-                                              int cols, const uint8_t* stage, int lane) {
-    T* const out = static_cast<T*>(o.out.data) + b * o.out.batch;
-    const T* const old = o.w.data != nullptr ? static_cast<const T*>(o.w.data) + b * o.w.batch : nullptr;
-    if (o.out.whole && (old == nullptr || o.w.whole) && col0 + kC <= cols) {
-        using B = typename Bits<4 * sizeof(T)>::type;
-        using P = Pack<T, 4>;
-        constexpr int kLanes = kC / 4, kStep = 32 / kLanes;
-        const int q = lane % kLanes, col = col0 + 4 * q;
-        B had[kLanes];
-        if (old != nullptr) {
-#pragma unroll
-            for (int i = 0; i < kLanes; ++i) {
-                const int row = row0 + kStep * i + lane / kLanes;
-                if (row < rows) had[i] = *reinterpret_cast<const B*>(old + row * o.w.row + col);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kLanes; ++i) {
-            const int r = kStep * i + lane / kLanes, row = row0 + r;
-            if (row >= rows) continue;
-            const float4 f = *reinterpret_cast<const float4*>(stage + staged<kC>(r, q));
-            float v[4] = {f.x, f.y, f.z, f.w};
-            if (old != nullptr) {
-                const P p = as_pack<P>(had[i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaf(a.alpha, to_f32(p.v[e]), v[e]);
-            }
-            P p;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p.v[e] = from_f32<T>(v[e]);
-            *reinterpret_cast<B*>(out + row * o.out.row + col) = as_pack<B>(p);
-        }
-    } else {
-        const int c = lane % kC, col = col0 + c;
-        if (col >= cols) return;
-#pragma unroll 4
-        for (int r = lane / kC; r < 32; r += 32 / kC) {
-            if (row0 + r >= rows) break;
-            float v = *reinterpret_cast<const float*>(stage + staged<kC>(r, c >> 2) + (c & 3) * 4);
-            const int64_t row = row0 + r;
-            if (old != nullptr) v = fmaf(a.alpha, to_f32(old[row * o.w.row + col]), v);
-            out[row * o.out.row + col] = from_f32<T>(v);
-        }
-    }
-}
-template <int kC>
-__device__ __forceinline__ void write_rows(const ProductArgs& a, const Result& o, int b, int row0, int col0, int rows,
-                                           int cols, const uint8_t* stage, int lane) {
-    if (o.out.type == MTTKRP_F32) write_rows_of<float, kC>(a, o, b, row0, col0, rows, cols, stage, lane);
-    else if (o.out.type == MTTKRP_BF16) write_rows_of<__nv_bfloat16, kC>(a, o, b, row0, col0, rows, cols, stage, lane);
-    else write_rows_of<__half, kC>(a, o, b, row0, col0, rows, cols, stage, lane);
-}
 
 // Where a thread's 64-column blocks of an item go.
 struct Place {
@@ -721,7 +472,7 @@ __device__ __forceinline__ void write_block(const ProductArgs& a, const Place& a
                 *reinterpret_cast<float4*>(stage + staged<kC>(lane, q)) = v;
             }
             __syncwarp();
-            write_rows<kC>(a, o, at.b, at.ti * 64 + at.r0, j * 64 + c, at.rows, at.cols, stage, lane);
+            write_rows<kC>(a.alpha, o, at.b, at.ti * 64 + at.r0, j * 64 + c, at.rows, at.cols, stage, lane);
         }
     } else {
 #pragma unroll
@@ -1066,6 +817,8 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                     }
                 }
                 if (!here) break;
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) acc[e] = uncut(acc[e], short_of(8));
                 const Place at = place(item_of<kCtas, kPhase>(a, t));       // (again: registers are short before)
 #pragma unroll
                 for (int c = 0; c < kCols; c += 64)
@@ -1124,7 +877,7 @@ int next_group(int n, const mttkrp_matrices* like, int& k, int64_t& b, Part* par
     tiles = 0;
     while (k < n && used < kTable) {
         const mttkrp_matrices& m = like[k];
-        if (m.batch - b <= 0 || m.rows == 0 || m.cols == 0) {
+        if (m.batch - b <= 0 || !newton_some(m) || newton_is_small(m)) {
             ++k;
             b = 0;
             continue;
@@ -1159,44 +912,13 @@ size_t partial_bytes(int used, const Part* parts, const mttkrp_matrices* like) {
     return (size_t)cdiv(sums * (int64_t)sizeof(Partial), 1024) * 1024;
 }
 
-Store store_of(const mttkrp_matrices& m, int64_t b0) {
-    const int64_t elem = m.type == MTTKRP_F32 ? 4 : 2, row = m.rows > 1 ? m.row_stride : 0, batch = m.batch > 1 ? m.batch_stride : 0;
-    Store s;
-    s.data = static_cast<uint8_t*>(m.data) + b0 * batch * elem;
-    s.row = row;
-    s.batch = batch;
-    s.type = (uint8_t)m.type;
-    s.whole = (reinterpret_cast<uintptr_t>(m.data) % 16 == 0 && row * elem % 16 == 0 && batch * elem % 16 == 0) ? 1 : 0;
-    return s;
-}
-
-template <typename K, typename A>
-cudaError_t launch(K kernel, unsigned blocks, unsigned threads, size_t smem, int cluster, cudaStream_t s, const A& args) {
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(blocks);
-    config.blockDim = dim3(threads);
-    config.dynamicSmemBytes = smem;
-    config.stream = s;
-    config.attrs = attr;
-    config.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args);
-    if (e != cudaSuccess) cudaGetLastError();       // the error is told by this call alone
-    return e;
-}
-
 template <int kCtas, bool kFull>
 cudaError_t launch_product(int phase, unsigned units, cudaStream_t s, const ProductArgs& p) {
     const auto kernel = phase == kGram     ? product_kernel<kCtas, kFull, kGram>
                         : phase == kSquare ? product_kernel<kCtas, kFull, kSquare>
                         : phase == kUpdate ? product_kernel<kCtas, kFull, kUpdate>
                                            : product_kernel<kCtas, kFull, kResult>;
-    return launch(kernel, units * kCtas, Roles<kCtas, kFull>::kThreads, kSmem, kCtas, s, p);
+    return launch_clusters(kernel, units * kCtas, Roles<kCtas, kFull>::kThreads, kSmem, kCtas, s, p);
 }
 
 // allows a form of the kernels their shared memory
@@ -1324,8 +1046,8 @@ cudaError_t run_group(const NewtonArgs& a, int used, const Part* parts, int64_t 
         if (r.out.type != MTTKRP_BF16) full = true;
     }
     if (!tile_map(&p.map, p.tiles, (uint64_t)tiles * 64)) return cudaErrorUnknown;
-    cudaError_t e = launch(squares_kernel, (unsigned)sums, kPassThreads, 0, 1, s, pass);
-    if (e == cudaSuccess) e = launch(images_kernel, strips, kPassThreads, 0, 1, s, pass);
+    cudaError_t e = launch_clusters(squares_kernel, (unsigned)sums, kPassThreads, 0, 1, s, pass);
+    if (e == cudaSuccess) e = launch_clusters(images_kernel, strips, kPassThreads, 0, 1, s, pass);
     for (int step = 0; step < a.steps && e == cudaSuccess; ++step) {
         p.from = step & 1;
         p.a = a.coefficients[3 * step];
@@ -1359,6 +1081,7 @@ size_t newton_workspace_bytes(int n, const mttkrp_matrices* like) {
 cudaError_t launch_newton(const NewtonArgs& a, cudaStream_t s) {
     Device d;
     cudaError_t e = device(d);
+    if (e == cudaSuccess) e = launch_newton_small(a, d.sms, s);
     Part parts[kTable];
     int k = 0;
     int64_t b = 0, tiles = 0;

@@ -1,0 +1,272 @@
+// What the kernels of the orthogonalisation share: lists of matrices, their elements, images
+// (see newton.cu), U and its norm, and results.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "mttkrp.h"
+#include "ptx.cuh"
+#include "squares.cuh"
+#include "types.cuh"
+
+namespace mk {
+
+constexpr int kTable = 32;                  // list elements a group of launches
+constexpr uint32_t kTileBytes = 8192;
+constexpr float kScale = 4096.f, kUnscale = 1.f / 4096.f;   // of the images
+
+// Matrices of one list element.  Tiles of one matrix, hi and lo of each: X twice (a step
+// reads one and writes the other), S, P.
+struct Shape {
+    int base;                   // first tile
+    int rows, cols, count;
+    uint32_t first[2];          // number of the first work item: of S and S S, of P X
+};
+__host__ __device__ inline int tiles_of(int n) { return (n + 63) / 64; }
+
+// Rows of a matrix in its own memory.
+struct Store {
+    void* data;
+    int64_t row, batch;         // strides
+    uint8_t type, whole;        // whole: eight elements from a multiple of eight on are aligned to 16 bytes
+};
+
+template <typename T>
+__device__ __forceinline__ void get8_of(const Store& s, int64_t at, int valid, float* v) {
+    const T* p = static_cast<const T*>(s.data) + at;
+    if (s.whole && valid >= 8) {
+        constexpr int kVec = 16 / sizeof(T);
+#pragma unroll
+        for (int k = 0; k < 8 / kVec; ++k) {
+            const uint4 bits = reinterpret_cast<const uint4*>(p)[k];    // (a reference to memory would be copied by bytes)
+            const auto w = as_pack<Pack<T, kVec>>(bits);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) v[k * kVec + e] = to_f32(w.v[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < valid ? to_f32(p[e]) : 0.f;
+    }
+}
+// eight elements of row r from column c on, zeros from `cols` on
+__device__ __forceinline__ void get8(const Store& s, int64_t b, int r, int c, int cols, float* v) {
+    const int64_t at = b * s.batch + r * s.row + c;
+    if (s.type == MTTKRP_F32) get8_of<float>(s, at, cols - c, v);
+    else if (s.type == MTTKRP_BF16) get8_of<__nv_bfloat16>(s, at, cols - c, v);
+    else get8_of<__half>(s, at, cols - c, v);
+}
+template <typename T>
+__device__ __forceinline__ void put8_of(const Store& s, int64_t at, int valid, const float* v) {
+    T* p = static_cast<T*>(s.data) + at;
+    if (s.whole && valid >= 8) {
+        constexpr int kVec = 16 / sizeof(T);
+#pragma unroll
+        for (int k = 0; k < 8 / kVec; ++k) {
+            Pack<T, kVec> w;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) w.v[e] = from_f32<T>(v[k * kVec + e]);
+            reinterpret_cast<uint4*>(p)[k] = as_pack<uint4>(w);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < valid) p[e] = from_f32<T>(v[e]);
+    }
+}
+__device__ __forceinline__ void put8(const Store& s, int64_t b, int r, int c, int cols, const float* v) {
+    const int64_t at = b * s.batch + r * s.row + c;
+    if (s.type == MTTKRP_F32) put8_of<float>(s, at, cols - c, v);
+    else if (s.type == MTTKRP_BF16) put8_of<__nv_bfloat16>(s, at, cols - c, v);
+    else put8_of<__half>(s, at, cols - c, v);
+}
+
+// eight scaled values as hi and lo
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __half2 p = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+        const float2 f = __half22float2(p);
+        const __half2 q = __floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y);
+        h[e] = *reinterpret_cast<const uint32_t*>(&p);
+        l[e] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ void join8(const uint4& hi, const uint4& lo, float* v) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[e]));
+        v[2 * e] = a.x + b.x;
+        v[2 * e + 1] = a.y + b.y;
+    }
+}
+
+// Sums in tensor memory are cut off towards zero at each addition while they grow to their size.
+// What one is short of, as a share of it, after n additions of equal parts: 1.4e-7 for four
+// (measured on S X and S S X of 256 x 64: 2.8e-7 and 5.5e-7 short of the exact ones, all of it along the
+// result), else by n + 1.
+__host__ __device__ constexpr float short_of(int n) { return 0x1.2p-23f / 5.f * (float)(n + 1); }
+
+// That put back, where the sum's last three bits show that it was rounded at all, so that sums of
+// few bits stay exact.  What five steps leave is then within 1.4 of the error of fp32 products, else up
+// to twice.
+__device__ __forceinline__ float uncut(float v, float share) {
+    return (__float_as_uint(v) & 7u) != 0u ? fmaf(v, share, v) : v;
+}
+
+// byte offset of 16-byte piece c (0-7) of row r in a tile
+__device__ __forceinline__ uint32_t piece(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+struct Source {
+    Store g, m, out;            // m.data NULL: no momentum
+    uint32_t first[2];          // number of the element's first work item: sums, images
+    int slices;                 // sums of a matrix
+    int at;                     // number of its first sum
+};
+
+// the last of n increasing numbers that is not above x
+template <typename F>
+__device__ __forceinline__ int element_of(int n, uint32_t x, F first) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first(mid) <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// U of eight elements and, where there is momentum, what it becomes
+__device__ __forceinline__ void update8(float mu, bool nesterov, const Source& s, int b, int r, int c, int cols, float* u,
+                                        float* kept) {
+    get8(s.g, b, r, c, cols, u);
+    if (s.m.data != nullptr) {
+        get8(s.m, b, r, c, cols, kept);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            kept[e] = fmaf(mu, kept[e], u[e]);
+            u[e] = nesterov ? fmaf(mu, kept[e], u[e]) : kept[e];
+        }
+    }
+}
+
+// factors whose product is 2^12 / (|U| + eps); two, as one may leave fp32's range
+__device__ __forceinline__ float2 factors(const Sum& total, double eps) {
+    const float square = total.hi + total.lo;
+    if (total.wide == 0.0 && square >= 0x1p-100f && square <= 0x1p100f)
+        return make_float2(1.f, kScale / (sqrtf(square) + (float)eps));
+    const double f = (double)kScale / (sqrt((double)total.hi + (double)total.lo + total.wide) + eps);
+    const double by = f > 0x1p60 ? 0x1p100 : f < 0x1p-60 ? 0x1p-100 : 1.0;
+    return make_float2((float)by, (float)(f / by));
+}
+
+struct Result {
+    Store out, w;               // w.data NULL: alpha is not used
+    float beta;
+};
+
+// A warp's stage: 32 rows of kC columns (16 or 32) of fp32, 16-byte pieces in an order in which
+// neither rows nor columns meet in a bank.
+template <int kC>
+__device__ __forceinline__ uint32_t staged(int r, int q) {
+    return kC == 32 ? piece(r, q) : (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+}
+
+// Writes them (beta O(U)) to a result, after adding alpha W: whole rows of the stage at a time, or
+// where rows are not aligned a column a lane.
+template <typename T, int kC>
+__device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int b, int row0, int col0, int rows,
+                                              int cols, const uint8_t* stage, int lane) {
+    T* const out = static_cast<T*>(o.out.data) + b * o.out.batch;
+    const T* const old = o.w.data != nullptr ? static_cast<const T*>(o.w.data) + b * o.w.batch : nullptr;
+    if (o.out.whole && (old == nullptr || o.w.whole) && col0 + kC <= cols) {
+        using B = typename Bits<4 * sizeof(T)>::type;
+        using P = Pack<T, 4>;
+        constexpr int kLanes = kC / 4, kStep = 32 / kLanes;
+        const int q = lane % kLanes, col = col0 + 4 * q;
+        B had[kLanes];
+        if (old != nullptr) {
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const int row = row0 + kStep * i + lane / kLanes;
+                if (row < rows) had[i] = *reinterpret_cast<const B*>(old + row * o.w.row + col);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kLanes; ++i) {
+            const int r = kStep * i + lane / kLanes, row = row0 + r;
+            if (row >= rows) continue;
+            const float4 f = *reinterpret_cast<const float4*>(stage + staged<kC>(r, q));
+            float v[4] = {f.x, f.y, f.z, f.w};
+            if (old != nullptr) {
+                const P p = as_pack<P>(had[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(alpha, to_f32(p.v[e]), v[e]);
+            }
+            P p;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p.v[e] = from_f32<T>(v[e]);
+            *reinterpret_cast<B*>(out + row * o.out.row + col) = as_pack<B>(p);
+        }
+    } else {
+        const int c = lane % kC, col = col0 + c;
+        if (col >= cols) return;
+#pragma unroll 4
+        for (int r = lane / kC; r < 32; r += 32 / kC) {
+            if (row0 + r >= rows) break;
+            float v = *reinterpret_cast<const float*>(stage + staged<kC>(r, c >> 2) + (c & 3) * 4);
+            const int64_t row = row0 + r;
+            if (old != nullptr) v = fmaf(alpha, to_f32(old[row * o.w.row + col]), v);
+            out[row * o.out.row + col] = from_f32<T>(v);
+        }
+    }
+}
+template <int kC>
+__device__ __forceinline__ void write_rows(float alpha, const Result& o, int b, int row0, int col0, int rows,
+                                           int cols, const uint8_t* stage, int lane) {
+    if (o.out.type == MTTKRP_F32) write_rows_of<float, kC>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    else if (o.out.type == MTTKRP_BF16) write_rows_of<__nv_bfloat16, kC>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    else write_rows_of<__half, kC>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+}
+
+// ---- host
+
+// the matrices of m from number b0 on
+inline Store store_of(const mttkrp_matrices& m, int64_t b0) {
+    const int64_t elem = m.type == MTTKRP_F32 ? 4 : 2, row = m.rows > 1 ? m.row_stride : 0, batch = m.batch > 1 ? m.batch_stride : 0;
+    Store s;
+    s.data = static_cast<uint8_t*>(m.data) + b0 * batch * elem;
+    s.row = row;
+    s.batch = batch;
+    s.type = (uint8_t)m.type;
+    s.whole = (reinterpret_cast<uintptr_t>(m.data) % 16 == 0 && row * elem % 16 == 0 && batch * elem % 16 == 0) ? 1 : 0;
+    return s;
+}
+
+// A launch of clusters whose start overlaps the end of the kernel before it (see launch.cuh).
+template <typename K, typename A> cudaError_t launch_clusters(K kernel, unsigned blocks, unsigned threads, size_t smem, int cluster, cudaStream_t s, const A& args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(blocks);
+    config.blockDim = dim3(threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    config.attrs = attr;
+    config.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args);
+    if (e != cudaSuccess) cudaGetLastError();       // the error is told by this call alone
+    return e;
+}
+
+}  // namespace mk

@@ -29,7 +29,12 @@ struct NewtonArgs {
     uint32_t* status;           // the device's error word
 };
 
-// bytes for matrices of these shapes; 0 where they cannot be taken
+inline bool newton_some(const mttkrp_matrices& m) { return m.batch > 0 && m.rows > 0 && m.cols > 0; }
+// whether newton_small.cu takes it: a short side of at most 128, and a long one that fits a cluster
+bool newton_is_small(const mttkrp_matrices& m);
+cudaError_t launch_newton_small(const NewtonArgs& a, int sms, cudaStream_t s);
+
+// bytes for matrices of these shapes; 0 where none needs any
 size_t newton_workspace_bytes(int n, const mttkrp_matrices* like);
 cudaError_t launch_newton(const NewtonArgs& a, cudaStream_t s);
 

@@ -1,0 +1,859 @@
+// Orthogonalisation of matrices of which one side is at most 128, in one launch: a cluster of
+// CTAs keeps the matrix in shared memory through all steps.  (The arithmetic and the images are
+// those of newton.cu, with both parts of every operand; its launches, 17 for five steps, take
+// 90 us for a 256 x 64 matrix, of which next to nothing is work.)
+//
+// Every CTA holds a slab of X: all of the short side, some tiles of 64 along the long one.
+// A step: the slab's part of S = X X^T (every 64 indices from tensor memory into registers); the
+// parts added up over the cluster, each CTA some rows, and spread again; P, by every CTA; its
+// slab of P X, written over X.  S and P are whole (up to 128 x 128).  What a step costs is mostly
+// latency: XX us a step for 256 x 64.
+//
+// One CTA an SM whatever the size (the launch asks for most of the shared memory): a second
+// one would wait for the tensor memory of the first, which may wait for its cluster.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "launch.cuh"
+#include "newton.cuh"
+#include "newton.h"
+
+namespace mk {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr uint32_t kHeader = 1024;              // barriers, sums, flags
+constexpr uint32_t kSmem = 232448 - 512;        // all but what is static: one CTA an SM
+constexpr uint32_t kTiles = (kSmem - 1024 - kHeader) / kTileBytes;      // 28
+constexpr uint32_t kHalfTmem = 256;             // columns of one of two buffers of accumulators
+
+struct Partial {
+    float hi, lo;
+    double wide;
+};
+
+struct SmallArgs {
+    int n, steps;
+    float mu, alpha;
+    bool nesterov;
+    double eps;
+    uint32_t* status;
+    Shape shape[kTable];
+    Source source[kTable];
+    Result result[kTable];
+    float abc[3 * kNewtonMaxSteps];
+};
+
+// tiles of 64 along the long side that a CTA of a cluster of c can hold, with the short side of b
+// tiles: beside X (hi and lo) lie S, the sums that the cluster exchanges and (b = 1) those that halves of a CTA do
+int most_tiles(int b, int c) {
+    const int s = 2 * b * b, exchange = c > 1 ? 2 * b * b : 0, halves = b == 1 ? 2 : 0;
+    return ((int)kTiles - s - exchange - halves) / (2 * b);
+}
+
+__device__ __forceinline__ uint32_t rank_in_cluster() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void put_in_cluster(uint32_t addr, uint4 v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+template <int kC>
+__device__ __forceinline__ void all_sync() {
+    __syncwarp();
+    if constexpr (kC > 1)
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+// generic writes to shared memory (of any CTA of the cluster), before the tensor core reads them
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// descriptor low word of an MN-major operand whose 64-row parts of M lie `apart` bytes from one another
+__device__ __forceinline__ uint32_t mn_desc(uint32_t addr, uint32_t apart) {
+    return ((apart >> 4) << 16) | ((addr & 0x3FFFFu) >> 4);
+}
+
+// An operand of 64 contraction indices: descriptors of its parts, and what a slice of 16 advances them.
+struct Op {
+    uint32_t hi, lo, step;
+};
+
+// Up to 64 indices in slices of 16, by a whole warp: small terms (lo lo too: 2.0e-6 instead of 2.2e-6
+// off for 256 x 64), then hi hi, into an accumulator of its own.
+__device__ __forceinline__ void issue(uint32_t d, const Op& p, const Op& q, int slices, uint32_t idesc, uint32_t leader) {
+    uint32_t acc = 0u;
+    for (int kk = 0; kk < slices; ++kk, acc = 1u) mma<1>(d, p.lo + kk * p.step, q.lo + kk * q.step, idesc, acc, leader);
+    for (int kk = 0; kk < slices; ++kk) mma<1>(d, p.hi + kk * p.step, q.lo + kk * q.step, idesc, 1u, leader);
+    for (int kk = 0; kk < slices; ++kk) mma<1>(d, p.lo + kk * p.step, q.hi + kk * q.step, idesc, 1u, leader);
+    for (int kk = 0; kk < slices; ++kk) mma<1>(d, p.hi + kk * p.step, q.hi + kk * q.step, idesc, 1u, leader);
+}
+// slices that indices [64 t, n) of a tile have
+__device__ __forceinline__ int slices_of(int n, int t) { return min(4, (n - 64 * t + 15) / 16); }
+
+// U of this CTA's tiles, its norm over the cluster, and their images.  place(tile, row, col, at): the
+// tile's first row and column, and where it lies behind x_hi (its low part x_lo bytes further).
+template <int kC, typename A, typename F>
+__device__ __forceinline__ void load_slab(const A& a, const Shape& shape, const Source& src, int b, int tiles,
+                                          Partial* sums, float2* found, F place, uint8_t* x_hi, uint32_t x_lo) {
+    const int groups = tiles * 512;             // of eight columns
+    auto locate = [&](int g, int& row, int& col, uint32_t& at) {
+        const int r = (g >> 3) & 63, q = g & 7;
+        place(g >> 9, row, col, at);
+        row += r;
+        col += 8 * q;
+        at += piece(r, q);
+    };
+    // kAhead groups of a thread at a time; where that is all, U stays in registers
+    constexpr int kAhead = 4;
+    float u[kAhead][8], kept[kAhead][8];
+    auto read = [&](int g0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            int row = 0, col = 0;
+            uint32_t at;
+            const int g = g0 + i * kThreads;
+            if (g < groups) locate(g, row, col, at);
+            if (g < groups && row < shape.rows && col < shape.cols) {
+                update8(a.mu, a.nesterov, src, b, row, col, shape.cols, u[i], kept[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
+            }
+        }
+    };
+    Sum sum;
+    for (int g0 = threadIdx.x; g0 < groups; g0 += kAhead * kThreads) {
+        read(g0);
+#pragma unroll
+        for (int i = 0; i < kAhead; i += 2) sum.squares16(u[i]);
+    }
+    Sum total = block_total<kWarps>(sum);
+    if constexpr (kC > 1) {
+        if (threadIdx.x == 0) {
+            const Partial mine{total.hi, total.lo, total.wide};
+            uint4 bits;
+            memcpy(&bits, &mine, sizeof(bits));
+            for (uint32_t c = 0; c < kC; ++c) put_in_cluster(in_cta(smem_u32(&sums[rank_in_cluster()]), c), bits);
+        }
+        all_sync<kC>();
+        total = Sum();
+        if (threadIdx.x == 0)
+            for (int c = 0; c < kC; ++c) {
+                total.add(sums[c].hi);
+                total.lo += sums[c].lo;
+                total.wide += sums[c].wide;
+            }
+    }
+    if (threadIdx.x == 0) *found = factors(total, a.eps);
+    __syncthreads();
+    const float2 factor = *found;
+    for (int g0 = threadIdx.x; g0 < groups; g0 += kAhead * kThreads) {
+        if (groups > kAhead * kThreads) read(g0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int g = g0 + i * kThreads;
+            if (g >= groups) continue;
+            int row, col;
+            uint32_t at;
+            locate(g, row, col, at);
+            const bool inside = row < shape.rows && col < shape.cols;
+            if (inside && src.m.data != nullptr) put8(src.out, b, row, col, shape.cols, kept[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[i][e] = inside && col + e < shape.cols ? u[i][e] * factor.x * factor.y : 0.f;
+            uint4 hi, lo;
+            split8(u[i], hi, lo);
+            *reinterpret_cast<uint4*>(x_hi + at) = hi;
+            *reinterpret_cast<uint4*>(x_hi + x_lo + at) = lo;
+        }
+    }
+    fence_async();
+    __syncthreads();
+}
+
+// kC: CTAs a cluster; kB: tiles of 64 of the short side (2; narrow_kernel below is for 1)
+template <int kC, int kB>
+__global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constant__ SmallArgs a) {
+    constexpr int kM = 64 * kB;                 // rows of S
+    constexpr int kCols = 16 * kB;              // of a thread, in S
+    constexpr int kOwn = kM / kC;               // rows of S that a CTA adds up
+    constexpr int kGroup = 4 / kB;              // tiles of a wide slab (or, times 2 / kB, of a tall one) at once in P X
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [2] of the accumulators' buffers
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 16);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + 20);
+    float2* const found = reinterpret_cast<float2*>(smem + 24);
+    Partial* const sums = reinterpret_cast<Partial*>(smem + 64);                // [kC]
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = kC > 1 ? rank_in_cluster() : 0u;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(2 * kHalfTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    all_sync<kC>();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    after_previous();
+
+    // this cluster's matrix and this CTA's slab
+    const uint32_t matrix = blockIdx.x / kC;
+    const int k = element_of(a.n, matrix, [&](int i) { return a.shape[i].first[0]; });
+    const Shape shape = a.shape[k];
+    const Source src = a.source[k];
+    const int b = (int)(matrix - shape.first[0]);
+    const bool wide = shape.rows <= shape.cols;
+    const int m = min(shape.rows, shape.cols), tiles = tiles_of(max(shape.rows, shape.cols));
+    const int nt_most = (tiles + kC - 1) / kC;
+    const int t0 = tiles * (int)rank / kC, nt = tiles * ((int)rank + 1) / kC - t0;
+    // tile (along the short side s, along the long one t): rows of K-major operands follow one another
+    const uint32_t t_step = (wide ? kB : 1) * kTileBytes, s_step = (wide ? 1 : nt_most) * kTileBytes;
+    uint8_t* const x_hi = smem + kHeader;
+    uint8_t* const s_hi = x_hi + (size_t)2 * nt_most * kB * kTileBytes;
+    uint8_t* const exchange = s_hi + 2 * kB * kB * kTileBytes;
+    const uint32_t x_lo = (uint32_t)(nt_most * kB) * kTileBytes, s_lo = kB * kB * kTileBytes;    // from hi to lo
+    const uint32_t xa = smem_u32(x_hi), sa = smem_u32(s_hi);
+    auto tile_at = [&](int s, int t) { return (uint32_t)s * s_step + (uint32_t)t * t_step; };
+
+    load_slab<kC>(a, shape, src, b, nt * kB, sums, found,
+                      [&](int tile, int& row, int& col, uint32_t& at) {
+                          const int sh = tile % kB, t = tile / kB;
+                          row = (wide ? sh : t0 + t) * 64;
+                          col = (wide ? t0 + t : sh) * 64;
+                          at = tile_at(sh, t);
+                      },
+                      x_hi, x_lo);
+
+    // ---- the steps
+    const uint32_t leader = lane == 0 ? 1u : 0u;
+    const int quad = warp & 3, part_of = warp >> 2, r = 32 * quad + lane;  // row of the accumulators, quarter of their columns
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    uint32_t parity = 0;                        // a bit for each buffer
+    auto wait = [&](int z) {
+        wait_bounded(&bars[z], (parity >> z) & 1u, abort_flag, a.status, kStatusTimeoutMma);
+        parity ^= 1u << z;
+        tc_fence_after();
+    };
+    constexpr uint32_t kF32 = 1u << 4, kM128 = (uint32_t)(128 >> 4) << 24;
+    const uint32_t square_desc = kF32 | kM128 | ((uint32_t)(kM >> 3) << 17);
+    const uint32_t gram_desc = square_desc | (wide ? 0u : (1u << 15) | (1u << 16));
+    // S's rows by 64 columns from column tile t on
+    auto sym = [&](int t) {
+        const uint32_t at = sa + (uint32_t)(t * kB) * kTileBytes;
+        return Op{sdesc128_lo(at), sdesc128_lo(at + s_lo), 2u};
+    };
+    // a thread's columns of S from accumulators, added to v or put there
+    auto drain = [&](uint32_t from, float* v, bool add) {
+        uint32_t bits[kCols];
+        if constexpr (kB == 2) tmem_ld32(from, bits);
+        else tmem_ld16(from, bits);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) v[e] = add ? v[e] + __uint_as_float(bits[e]) : __uint_as_float(bits[e]);
+    };
+    // what sums over the long and the short side are short of (see uncut())
+    const int n_slices = slices_of(max(shape.rows, shape.cols), 0), m_slices = slices_of(m, 0);
+    const float n_short = short_of(n_slices), m_short = short_of(m_slices);
+    const int col0 = part_of * kCols;           // of S
+
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.abc[3 * step], cb = a.abc[3 * step + 1], cc = a.abc[3 * step + 2];
+        // S: this slab's part, a tile of the long side at a time
+        float part[kCols];
+#pragma unroll
+        for (int e = 0; e < kCols; ++e) part[e] = 0.f;
+        auto gram = [&](int t) {
+            const uint32_t at = xa + (uint32_t)t * t_step;
+            Op o;
+            if (wide) o = Op{sdesc128_lo(at), sdesc128_lo(at + x_lo), 2u};
+            else o = Op{mn_desc(at, kB > 1 ? s_step : kTileBytes), mn_desc(at + x_lo, kB > 1 ? s_step : kTileBytes), 128u};
+            issue(tmem + (uint32_t)(t & 1) * kHalfTmem, o, o, slices_of(max(shape.rows, shape.cols), t0 + t), gram_desc, leader);
+            commit<1>(&bars[t & 1], leader);
+        };
+        if (warp == 0) {
+            tc_fence_after();
+            for (int t = 0; t < min(nt, 2); ++t) gram(t);
+        }
+        for (int t = 0; t < nt; ++t) {
+            wait(t & 1);
+            drain(lanes + (uint32_t)(t & 1) * kHalfTmem + (uint32_t)col0, part, true);
+            tc_fence_before();
+            __syncthreads();
+            if (warp == 0 && t + 2 < nt) {
+                tc_fence_after();
+                gram(t + 2);
+            }
+        }
+        if constexpr (kC > 1) {
+            // to the CTA that adds up the row
+            if (r < kM) {
+                const uint32_t to = in_cta(smem_u32(exchange), (uint32_t)(r / kOwn)) +
+                                    (uint32_t)(((int)rank * kOwn + r % kOwn) * kM + col0) * 4u;
+#pragma unroll
+                for (int c = 0; c < kCols; c += 4)
+                    put_in_cluster(to + 4u * c, make_uint4(__float_as_uint(part[c]), __float_as_uint(part[c + 1]),
+                                                           __float_as_uint(part[c + 2]), __float_as_uint(part[c + 3])));
+            }
+            all_sync<kC>();
+            for (int v = threadIdx.x; v < kOwn * kM / 8; v += kThreads) {
+                const int own = v / (kM / 8), col = v % (kM / 8) * 8, row = (int)rank * kOwn + own;
+                float s[8];
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const float4* f = reinterpret_cast<const float4*>(exchange) + ((c * kOwn + own) * kM + col) / 4;
+                    const float4 x = f[0], y = f[1];
+                    const float p[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] = c == 0 ? p[e] : s[e] + p[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = uncut(s[e], n_short) * kUnscale;
+                uint4 hi, lo;
+                split8(s, hi, lo);
+                const uint32_t at = sa + (uint32_t)(col / 64 * kB + row / 64) * kTileBytes + piece(row & 63, (col & 63) >> 3);
+#pragma unroll
+                for (uint32_t c = 0; c < kC; ++c) {
+                    const uint32_t to = in_cta(at, c);
+                    put_in_cluster(to, hi);
+                    put_in_cluster(to + s_lo, lo);
+                }
+            }
+            fence_async();
+            all_sync<kC>();
+            fence_async();
+        } else {
+            if (r < kM) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 8) {
+                    const int col = col0 + c;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) part[c + e] = uncut(part[c + e], n_short) * kUnscale;
+                    uint4 hi, lo;
+                    split8(part + c, hi, lo);
+                    uint8_t* at = s_hi + (col / 64 * kB + r / 64) * kTileBytes + piece(r & 63, (col & 63) >> 3);
+                    *reinterpret_cast<uint4*>(at) = hi;
+                    *reinterpret_cast<uint4*>(at + s_lo) = lo;
+                }
+            }
+            fence_async();
+            __syncthreads();
+        }
+
+        // P = a I + b S + c S S, over S
+        if (warp == 0) {
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < kB; ++t) issue(tmem + (uint32_t)t * kHalfTmem, sym(t), sym(t), slices_of(m, t), square_desc, leader);
+            commit<1>(&bars[0], leader);
+        }
+        wait(0);
+        drain(lanes + (uint32_t)col0, part, false);
+        if constexpr (kB == 2) drain(lanes + kHalfTmem + (uint32_t)col0, part, true);
+        tc_fence_before();
+        if (r < kM) {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 8) {
+                const int col = col0 + c;
+                uint8_t* at = s_hi + (col / 64 * kB + r / 64) * kTileBytes + piece(r & 63, (col & 63) >> 3);
+                float s[8];
+                join8(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + s_lo), s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s[e] = fmaf(cc, uncut(part[c + e], m_short) * kUnscale, cb * s[e]);
+                    if (r == col + e && r < m) s[e] += ca * kScale;
+                }
+                uint4 hi, lo;
+                split8(s, hi, lo);
+                *reinterpret_cast<uint4*>(at) = hi;
+                *reinterpret_cast<uint4*>(at + s_lo) = lo;
+            }
+        }
+        fence_async();
+        __syncthreads();
+
+        // P X over X, some tiles of the long side at a time: 64 x 64 blocks of the result, each
+        // from kB slices of 64 indices in accumulators of their own
+        const bool last = step == a.steps - 1;
+        const int at_once = wide ? kGroup : 8 / (kB * kB);          // tiles of the long side
+        const int passes = (nt + at_once - 1) / at_once;
+        auto update = [&](int n) {
+            const uint32_t d = tmem + (uint32_t)(n & 1) * kHalfTmem;
+            const int first = n * at_once, count = min(at_once, nt - first);
+            for (int s = 0; s < kB; ++s) {
+                if (wide) {
+                    const uint32_t at = xa + tile_at(s, first);
+                    const Op q{mn_desc(at, t_step), mn_desc(at + x_lo, t_step), 128u};
+                    issue(d + (uint32_t)s * 128u, sym(s), q, slices_of(m, s), kF32 | kM128 | (1u << 16) | ((uint32_t)(8 * count) << 17), leader);
+                } else {
+                    for (int t = 0; t < count; t += 2) {
+                        const uint32_t at = xa + tile_at(s, first + t);
+                        const Op p{sdesc128_lo(at), sdesc128_lo(at + x_lo), 2u};
+                        issue(d + (uint32_t)s * 128u + (uint32_t)(t / 2 * kM), p, sym(s), slices_of(m, s), square_desc, leader);
+                    }
+                }
+            }
+            commit<1>(&bars[n & 1], leader);
+        };
+        if (warp == 0) {
+            tc_fence_after();
+            for (int n = 0; n < min(passes, 2); ++n) update(n);
+        }
+        for (int n = 0; n < passes; ++n) {
+            wait(n & 1);
+            const int first = n * at_once;
+            // a thread's columns of its row: a quarter of the accumulators', in one tile
+            constexpr int kWidth = 64 / kB;
+            const int block = part_of / kB, c0 = part_of % kB * kWidth;     // of 64 columns; first one in it
+            const uint32_t from = lanes + (uint32_t)(n & 1) * kHalfTmem + (uint32_t)(block * 64 + c0);
+            float f[kWidth];
+            {
+                uint32_t bits[64];
+                tmem_ld32(from, bits);
+                tmem_ld32(kB == 2 ? from + 128u : from + 32u, bits + 32);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < kWidth; ++e)
+                    f[e] = uncut(kB == 2 ? __uint_as_float(bits[e]) + __uint_as_float(bits[32 + e % 32]) : __uint_as_float(bits[e]), m_short);
+            }
+            const int s = wide ? r / 64 : kB == 2 ? block : 0;
+            const int t = wide ? first + block : first + (kB == 2 ? 0 : 2 * block) + r / 64;
+            if (s < kB && t < nt) {                         // (the same for a warp)
+                uint8_t* const tile = x_hi + tile_at(s, t);
+                if (last) {
+                    // by way of what these 32 rows of X were (hi or lo part, as two warps have a tile's
+                    // rows): nobody reads them any more
+                    const Result& o = a.result[k];
+                    uint8_t* const stage = tile + 4096 * (quad & 1) + (kB == 2 && c0 != 0 ? x_lo : 0u);
+                    const int row0 = (wide ? s : t0 + t) * 64 + 32 * (quad & 1), first_col = (wide ? t0 + t : s) * 64 + c0;
+#pragma unroll
+                    for (int c = 0; c < kWidth; c += 32) {
+                        if (first_col + c >= shape.cols) continue;
+                        __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const float* v = f + c + 4 * q;
+                            const float by = kUnscale * kUnscale;
+                            *reinterpret_cast<float4*>(stage + staged<32>(lane, q)) =
+                                make_float4(o.beta * (v[0] * by), o.beta * (v[1] * by), o.beta * (v[2] * by), o.beta * (v[3] * by));
+                        }
+                        __syncwarp();
+                        write_rows<32>(a.alpha, o, b, row0, first_col + c, shape.rows, shape.cols, stage, lane);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kWidth / 8; ++q) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[8 * q + e] *= kUnscale;
+                        uint4 hi, lo;
+                        split8(f + 8 * q, hi, lo);
+                        uint8_t* at = tile + piece(r & 63, c0 / 8 + q);
+                        *reinterpret_cast<uint4*>(at) = hi;
+                        *reinterpret_cast<uint4*>(at + x_lo) = lo;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (n == passes - 1) fence_async();
+            __syncthreads();
+            if (warp == 0 && n + 2 < passes) {
+                tc_fence_after();
+                update(n + 2);
+            }
+        }
+    }
+
+    all_sync<kC>();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kHalfTmem));
+    }
+}
+
+// The short side at most 64.  A tile's hi and lo lie behind one another and are one operand of 128
+// rows: one MMA gives hi hi, hi lo, lo hi and lo lo in the quarters of its accumulators (rows 0-63
+// and 64-127, columns 0-63 and 64-127), which are added up outside: a quarter of the MMAs, and the
+// small terms by themselves.  Warps of rows r and 64 + r change halves of what they have: a thread
+// ends up with 8 elements of one row, a piece of an image.
+template <int kC>
+__global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_constant__ SmallArgs a) {
+    constexpr uint32_t kPair = 2 * kTileBytes;
+    constexpr int kOwn = 64 / kC;               // rows of S that a CTA adds up
+    constexpr int kAtOnce = 2;                  // tiles of P X at once, in each of two buffers
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [2] of the accumulators' buffers
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 16);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + 20);
+    float2* const found = reinterpret_cast<float2*>(smem + 24);
+    Partial* const sums = reinterpret_cast<Partial*>(smem + 64);                // [kC]
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = kC > 1 ? rank_in_cluster() : 0u;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(2 * kHalfTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    all_sync<kC>();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    after_previous();
+
+    const uint32_t matrix = blockIdx.x / kC;
+    const int k = element_of(a.n, matrix, [&](int i) { return a.shape[i].first[0]; });
+    const Shape shape = a.shape[k];
+    const Source src = a.source[k];
+    const int b = (int)(matrix - shape.first[0]);
+    const bool wide = shape.rows <= shape.cols;
+    const int m = min(shape.rows, shape.cols), n = max(shape.rows, shape.cols), tiles = tiles_of(n);
+    const int nt_most = (tiles + kC - 1) / kC;
+    const int t0 = tiles * (int)rank / kC, nt = tiles * ((int)rank + 1) / kC - t0;
+    uint8_t* const x = smem + kHeader;          // pairs of tiles along the long side
+    uint8_t* const sp = x + (size_t)nt_most * kPair;
+    float4* const halves = reinterpret_cast<float4*>(sp + kPair);               // [2][kThreads]
+    uint8_t* const exchange = sp + 2 * kPair;
+    const uint32_t xa = smem_u32(x), sa = smem_u32(sp);
+
+    load_slab<kC>(a, shape, src, b, nt, sums, found,
+                  [&](int t, int& row, int& col, uint32_t& at) {
+                      row = wide ? 0 : (t0 + t) * 64;
+                      col = wide ? (t0 + t) * 64 : 0;
+                      at = (uint32_t)t * kPair;
+                  },
+                  x, kTileBytes);
+
+    const uint32_t leader = lane == 0 ? 1u : 0u;
+    const int quad = warp & 3, part = warp >> 2, low = quad >> 1;
+    const int r = 32 * (quad & 1) + lane;       // this thread's row
+    const int q = 2 * part + low;               // and piece of it: columns 8 q to 8 q + 7
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    const uint32_t own_piece = piece(r, q);
+    uint32_t parity = 0;                        // a bit for each buffer
+    auto wait = [&](int z) {
+        wait_bounded(&bars[z], (parity >> z) & 1u, abort_flag, a.status, kStatusTimeoutMma);
+        parity ^= 1u << z;
+        tc_fence_after();
+    };
+    // the four quarters' terms of this thread's 8 elements, from accumulators at `from`, and from
+    // as many more buffers of 128 columns as `buffers` says
+    auto gather = [&](uint32_t from, int buffers, float* v) {
+        float all[16];
+        for (int i = 0; i < buffers; ++i) {
+            uint32_t lead[16], rest[16];
+            tmem_ld16(from + (uint32_t)(128 * i + 16 * part), lead);
+            tmem_ld16(from + (uint32_t)(128 * i + 64 + 16 * part), rest);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float f = __uint_as_float(lead[e]) + __uint_as_float(rest[e]);
+                all[e] = i == 0 ? f : all[e] + f;
+            }
+        }
+        // rows r give away columns 8-15 of the 16 they have, rows 64 + r columns 0-7
+        const int mine = threadIdx.x, other = threadIdx.x ^ 64;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float4 f;
+            f.x = low ? all[4 * h] : all[8 + 4 * h];
+            f.y = low ? all[4 * h + 1] : all[8 + 4 * h + 1];
+            f.z = low ? all[4 * h + 2] : all[8 + 4 * h + 2];
+            f.w = low ? all[4 * h + 3] : all[8 + 4 * h + 3];
+            halves[h * kThreads + mine] = f;
+        }
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + 2 * part + (quad & 1)) : "memory");
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 f = halves[h * kThreads + other];
+            const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * h + e] = g[e] + (low ? all[8 + 4 * h + e] : all[4 * h + e]);
+        }
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + 2 * part + (quad & 1)) : "memory");
+    };
+    auto put8_pair = [&](uint8_t* pair, const float* v) {
+        uint4 hi, lo;
+        split8(v, hi, lo);
+        *reinterpret_cast<uint4*>(pair + own_piece) = hi;
+        *reinterpret_cast<uint4*>(pair + kTileBytes + own_piece) = lo;
+    };
+    constexpr uint32_t kDesc = (1u << 4) | ((uint32_t)(128 >> 4) << 24);        // fp32 accumulators, M = 128
+    constexpr uint32_t kN128 = (uint32_t)(128 >> 3) << 17, kAMn = 1u << 15, kBMn = 1u << 16;
+    // products of pairs, in slices of 16 indices
+    auto multiply = [&](uint32_t d, uint32_t p, uint32_t p_step, uint32_t q0, uint32_t q_step, int slices, uint32_t idesc,
+                        uint32_t acc) {
+        for (int kk = 0; kk < slices; ++kk, acc = 1u) mma<1>(d, p + kk * p_step, q0 + kk * q_step, idesc, acc, leader);
+    };
+    const int m_slices = slices_of(m, 0);
+    const float m_short = short_of(m_slices);
+    // tiles of the slab into one buffer of accumulators of S: additions
+    const float n_short = short_of(max(slices_of(n, 0), 4 * ((nt_most + 3) / 4) * (nt_most > 1)));
+
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.abc[3 * step], cb = a.abc[3 * step + 1], cc = a.abc[3 * step + 2];
+        // S: this slab's part, its tiles in turn into four buffers of accumulators
+        if (warp == 0) {
+            tc_fence_after();
+            for (int t = 0; t < nt; ++t) {
+                const uint32_t at = xa + (uint32_t)t * kPair;
+                const uint32_t o = wide ? sdesc128_lo(at) : sdesc128mn_lo(at);
+                multiply(tmem + (uint32_t)(t & 3) * 128u, o, wide ? 2u : 128u, o, wide ? 2u : 128u, slices_of(n, t0 + t),
+                         kDesc | kN128 | (wide ? 0u : kAMn | kBMn), t < 4 ? 0u : 1u);
+            }
+            commit<1>(&bars[0], leader);
+        }
+        float s[8];
+        if (nt > 0) {
+            wait(0);
+            gather(lanes, min(nt, 4), s);
+        } else {
+            wait(0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = 0.f;
+        }
+        tc_fence_before();
+        if constexpr (kC > 1) {
+            // to the CTA that adds up the row
+            const uint32_t to = in_cta(smem_u32(exchange), (uint32_t)(r / kOwn)) + (uint32_t)(((int)rank * kOwn + r % kOwn) * 64 + 8 * q) * 4u;
+            put_in_cluster(to, make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])));
+            put_in_cluster(to + 16u, make_uint4(__float_as_uint(s[4]), __float_as_uint(s[5]), __float_as_uint(s[6]), __float_as_uint(s[7])));
+            all_sync<kC>();
+            if ((int)threadIdx.x < kOwn * 8) {
+                const int own = threadIdx.x >> 3, piece_of = threadIdx.x & 7, row = (int)rank * kOwn + own;
+                float f[8];
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const float4* from = reinterpret_cast<const float4*>(exchange) + ((c * kOwn + own) * 64 + 8 * piece_of) / 4;
+                    const float4 y = from[0], z = from[1];
+                    const float g[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) f[e] = c == 0 ? g[e] : f[e] + g[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = uncut(f[e], n_short) * kUnscale;
+                uint4 hi, lo;
+                split8(f, hi, lo);
+#pragma unroll
+                for (uint32_t c = 0; c < kC; ++c) {
+                    const uint32_t to_s = in_cta(sa + piece(row, piece_of), c);
+                    put_in_cluster(to_s, hi);
+                    put_in_cluster(to_s + kTileBytes, lo);
+                }
+            }
+            fence_async();
+            all_sync<kC>();
+            fence_async();
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = uncut(s[e], n_short) * kUnscale;
+            put8_pair(sp, s);
+            fence_async();
+            __syncthreads();
+        }
+
+        // P = a I + b S + c S S, over S
+        const uint32_t sd = sdesc128_lo(sa);
+        if (warp == 0) {
+            tc_fence_after();
+            multiply(tmem, sd, 2u, sd, 2u, m_slices, kDesc | kN128, 0u);
+            commit<1>(&bars[0], leader);
+        }
+        wait(0);
+        float p[8];
+        gather(lanes, 1, p);
+        tc_fence_before();
+        join8(*reinterpret_cast<const uint4*>(sp + own_piece), *reinterpret_cast<const uint4*>(sp + kTileBytes + own_piece), s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            p[e] = fmaf(cc, uncut(p[e], m_short) * kUnscale, cb * s[e]);
+            if (r == 8 * q + e && r < m) p[e] += ca * kScale;
+        }
+        put8_pair(sp, p);
+        fence_async();
+        __syncthreads();
+
+        // P X over X
+        const bool last = step == a.steps - 1;
+        const int passes = (nt + kAtOnce - 1) / kAtOnce;
+        auto update = [&](int pass) {
+            for (int i = 0; i < kAtOnce && pass * kAtOnce + i < nt; ++i) {
+                const uint32_t at = xa + (uint32_t)(pass * kAtOnce + i) * kPair;
+                const uint32_t d = tmem + (uint32_t)(pass & 1) * kHalfTmem + 128u * i;
+                if (wide) multiply(d, sd, 2u, sdesc128mn_lo(at), 128u, m_slices, kDesc | kN128 | kBMn, 0u);
+                else multiply(d, sdesc128_lo(at), 2u, sd, 2u, m_slices, kDesc | kN128, 0u);
+            }
+            commit<1>(&bars[pass & 1], leader);
+        };
+        if (warp == 0) {
+            tc_fence_after();
+            for (int pass = 0; pass < min(passes, 2); ++pass) update(pass);
+        }
+        for (int pass = 0; pass < passes; ++pass) {
+            wait(pass & 1);
+            const int first = pass * kAtOnce, count = min(kAtOnce, nt - first);
+            for (int i = 0; i < count; ++i) {
+                uint8_t* const pair = x + (size_t)(first + i) * kPair;
+                float v[8];
+                gather(lanes + (uint32_t)(pass & 1) * kHalfTmem + 128u * i, 1, v);
+                if (!last) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = uncut(v[e], m_short) * kUnscale;
+                    put8_pair(pair, v);
+                } else {
+                    // fp32 in the place of the pair, as two blocks of 32 columns
+                    const float by = a.result[k].beta;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = by * (uncut(v[e], m_short) * (kUnscale * kUnscale));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<float4*>(pair + (q >> 2) * kTileBytes + staged<32>(r, 2 * (q & 3) + h)) =
+                            make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+                }
+            }
+            tc_fence_before();
+            if (pass == passes - 1) fence_async();
+            __syncthreads();
+            if (warp == 0 && pass + 2 < passes) {
+                tc_fence_after();
+                update(pass + 2);
+            }
+            if (last && warp < 4 * count) {
+                // a warp for 32 rows of 32 columns
+                const Result& o = a.result[k];
+                const int i = warp >> 2, rows = warp & 1, cols = (warp >> 1) & 1;
+                const int row0 = (wide ? 0 : (t0 + first + i) * 64) + 32 * rows, col0 = (wide ? (t0 + first + i) * 64 : 0) + 32 * cols;
+                if (col0 < shape.cols && row0 < shape.rows)
+                    write_rows<32>(a.alpha, o, b, row0, col0, shape.rows, shape.cols,
+                                   x + (size_t)(first + i) * kPair + cols * kTileBytes + 4096 * rows, lane);
+            }
+        }
+    }
+
+    all_sync<kC>();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kHalfTmem));
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+template <int kC, int kB>
+cudaError_t run(unsigned matrices, cudaStream_t s, const SmallArgs& args) {
+    void (*kernel)(SmallArgs) = nullptr;
+    if constexpr (kB == 1) kernel = narrow_kernel<kC>;
+    else kernel = small_kernel<kC, kB>;
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !allowed[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) allowed[dev] = true;
+    }
+    return launch_clusters(kernel, matrices * kC, kThreads, kSmem, kC, s, args);
+}
+
+template <int kB>
+cudaError_t run(int c, unsigned matrices, cudaStream_t s, const SmallArgs& args) {
+    switch (c) {
+        case 1: return run<1, kB>(matrices, s, args);
+        case 2: return run<2, kB>(matrices, s, args);
+        case 4: return run<4, kB>(matrices, s, args);
+        default: return run<8, kB>(matrices, s, args);
+    }
+}
+
+int short_tiles(const mttkrp_matrices& m) { return tiles_of((int)std::min(m.rows, m.cols)); }
+int long_tiles(const mttkrp_matrices& m) { return tiles_of((int)std::max(m.rows, m.cols)); }
+
+// CTAs for a matrix: as many as it takes to hold it, and up to one for every two tiles of 128
+// while there are SMs for all
+int cluster_of(const mttkrp_matrices& m, int64_t matrices, int sms) {
+    const int b = short_tiles(m), t = long_tiles(m);
+    int c = 1;
+    while (c < 8 && (long long)most_tiles(b, c) * c < t) c *= 2;
+    while (c < 8 && t >= (b == 1 ? 8 : 4) * c && matrices * c * 2 <= sms) c *= 2;
+    return c;
+}
+
+}  // namespace
+
+bool newton_is_small(const mttkrp_matrices& m) {
+    const int b = short_tiles(m);
+    return b <= 2 && long_tiles(m) <= 8 * most_tiles(b, 8);
+}
+
+cudaError_t launch_newton_small(const NewtonArgs& a, int sms, cudaStream_t s) {
+    int64_t matrices = 0;
+    for (int k = 0; k < a.n; ++k)
+        if (newton_some(a.grad[k]) && newton_is_small(a.grad[k])) matrices += a.grad[k].batch;
+    cudaError_t e = cudaSuccess;
+    if (matrices == 0) return e;
+    SmallArgs p;
+    p.steps = a.steps;
+    p.mu = a.mu;
+    p.alpha = a.alpha;
+    p.nesterov = a.nesterov;
+    p.eps = a.eps;
+    p.status = a.status;
+    for (int i = 0; i < 3 * a.steps; ++i) p.abc[i] = a.coefficients[i];
+    // a launch for every size of cluster and short side, of as many elements as a table holds
+    for (int b = 1; b <= 2; ++b)
+        for (int c = 1; c <= 8; c *= 2) {
+            p.n = 0;
+            unsigned used = 0;
+            for (int k = 0; k <= a.n && e == cudaSuccess; ++k) {
+                if (p.n == kTable || (k == a.n && p.n > 0)) {
+                    e = b == 1 ? run<1>(c, used, s, p) : run<2>(c, used, s, p);
+                    p.n = 0;
+                    used = 0;
+                }
+                if (k == a.n) break;
+                const mttkrp_matrices& m = a.grad[k];
+                if (!newton_some(m) || !newton_is_small(m) || short_tiles(m) != b || cluster_of(m, matrices, sms) != c) continue;
+                p.shape[p.n] = Shape{0, (int)m.rows, (int)m.cols, (int)m.batch, {used, 0}};
+                Source& u = p.source[p.n];
+                u.g = store_of(m, 0);
+                u.m = u.out = Store{nullptr, 0, 0, 0, 0};
+                if (a.momentum != nullptr) {
+                    u.m = store_of(a.momentum[k], 0);
+                    u.out = store_of(a.momentum_out[k], 0);
+                }
+                Result& r = p.result[p.n];
+                r.out = store_of(a.out[k], 0);
+                r.w = a.weight != nullptr ? store_of(a.weight[k], 0) : Store{nullptr, 0, 0, 0, 0};
+                r.beta = a.beta[k];
+                used += (unsigned)m.batch;
+                ++p.n;
+            }
+        }
+    return e;
+}
+
+}  // namespace mk

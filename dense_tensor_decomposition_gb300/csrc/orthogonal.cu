@@ -90,7 +90,7 @@ bool same_place(const mttkrp_matrices& a, const mttkrp_matrices& b) {
            (a.rows <= 1 || a.row_stride == b.row_stride);
 }
 
-bool none(const mttkrp_matrices& m) { return m.batch == 0 || m.rows == 0 || m.cols == 0; }
+bool none(const mttkrp_matrices& m) { return !newton_some(m); }
 
 Rows rows_of(const mttkrp_matrices& m) {
     const int64_t strides[3] = {m.batch_stride, m.row_stride, 0};
@@ -228,7 +228,9 @@ int check_steps(int steps, const double* coefficients, double eps, float* rounde
 
 int run_newton(NewtonArgs& a, const float* scales, double factor, void* ws, size_t ws_bytes, void* stream) {
     if (int rc = check_workspace(ws, ws_bytes, newton_workspace_bytes(a.n, a.grad))) return rc;
-    if (newton_workspace_bytes(a.n, a.grad) == 0) return MTTKRP_OK;     // no element
+    int some = 0;
+    for (int k = 0; k < a.n; ++k) some += newton_some(a.grad[k]);
+    if (some == 0) return MTTKRP_OK;
     std::unique_ptr<float[]> beta(new (std::nothrow) float[a.n]);
     if (!beta) return fail(MTTKRP_ERR_HOST_ALLOC, "no host memory for %d scales", a.n);
     for (int k = 0; k < a.n; ++k) beta[k] = (float)(factor * (scales ? (double)scales[k] : 1.0));

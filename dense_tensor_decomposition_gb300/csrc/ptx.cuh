@@ -159,6 +159,48 @@ constexpr uint32_t kDescMnLo = (uint32_t)((8192 >> 4) << 16);   // leading byte 
 
 __device__ __forceinline__ uint32_t sdesc128mn_lo(uint32_t saddr) { return kDescMnLo | ((saddr & 0x3FFFFu) >> 4); }
 
+// D (+)= A B of fp16 operands by the low words of their descriptors, on one CTA or a pair; issued
+// by the lane whose `leader` is not 0
+template <int kCtas>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc, uint32_t leader) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %3};\n\t"
+            "mov.b64 db, {%2, %3};\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "setp.ne.b32 e, %6, 0;\n\t"
+            "@e tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc), "r"(leader));
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+            "mov.b64 da, {%1, %3};\n\t"
+            "mov.b64 db, {%2, %3};\n\t"
+            "setp.ne.b32 p, %5, 0;\n\t"
+            "setp.ne.b32 e, %6, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}\n" ::"r"(d),
+            "r"(a_lo), "r"(b_lo), "r"((uint32_t)(kDescSw128Hi >> 32)), "r"(idesc), "r"(acc), "r"(leader));
+}
+
+// arrive on `bar` (of both CTAs) when that lane's MMAs so far are done
+template <int kCtas>
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t leader) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %2, 0;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+                smem_u32(bar)),
+            "h"((uint16_t)3), "r"(leader)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+            "r"(leader)
+            : "memory");
+}
+
 // Registers of the warpgroup's threads: up only within what the block was launched with.
 template <int N>
 __device__ __forceinline__ void regs_dec() {

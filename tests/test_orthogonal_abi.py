@@ -125,6 +125,9 @@ def orthogonalize(lib, ins=(matrix(),), outs=(matrix(0x2000000),), n=None, steps
 
 
 HERE = 0x1000000
+# a matrix of which no side is short: it needs a workspace
+BIG_SHAPE = dict(batch=1, rows=130, cols=200, batch_stride=0, row_stride=200)
+LARGE = dict(ins=[matrix(HERE, **BIG_SHAPE)], outs=[matrix(0x2000000, **BIG_SHAPE)])
 
 
 @pytest.mark.parametrize("change,why,code", [
@@ -146,7 +149,8 @@ HERE = 0x1000000
     ({"abc": QUINTIC * 4 + (float("nan"), 0, 0)}, "finite", 1), ({"abc": (16.0, 0, 0) * 5}, "15.9", 1),
     ({"abc": (2.0, 0, 0) * 5}, "3.9", 1), ({"abc": (4.0, 0, 0) + QUINTIC * 4}, "3.9", 1),
     ({"abc": (1.0, 14.95, -13.0) + QUINTIC * 4}, "3.9", 1),     # 4.26 at s^2 = 0.79 (-14 reaches 3.87: taken)
-    ({"ws": 0}, "workspace", 3), ({"ws_bytes": 100}, "workspace", 3), ({"ws": 0x4000080}, "256-byte", 3)])
+    ({**LARGE, "ws": 0}, "workspace", 3), ({**LARGE, "ws_bytes": 100}, "workspace", 3),
+    ({**LARGE, "ws": 0x4000080}, "256-byte", 3)])
 def test_orthogonalisation_refuses(lib, change, why, code):
     refused(lib, orthogonalize(lib, **change), why, code)
 
@@ -169,9 +173,12 @@ def test_orthogonalisation_takes_what_fits(lib):
 
 def test_orthogonalisation_workspace(lib):
     size = lambda *ms: lib.mttkrp_orthogonalize_workspace_bytes(len(ms), listed(ms))
-    one = size(matrix(batch=1, rows=64, cols=64, batch_stride=0, row_stride=64))
-    assert 8 * 8192 <= one < 8 * 8192 + 4096
-    assert size(matrix(batch=3, rows=100, cols=500, row_stride=500, batch_stride=50000)) >= 3 * 4 * (2 * 8 + 4) * 8192
+    one = size(matrix(batch=1, rows=192, cols=192, batch_stride=0, row_stride=192))
+    assert 72 * 8192 <= one < 72 * 8192 + 4096
+    assert size(matrix(batch=3, rows=200, cols=500, row_stride=500, batch_stride=100000)) >= 3 * 4 * (4 * 8 + 16) * 8192
+    assert size(matrix(batch=3, rows=100, cols=1500, row_stride=1500, batch_stride=150000)) == 0      # one launch, no workspace
+    assert size(matrix(batch=1, rows=100, cols=1600, batch_stride=0, row_stride=1600)) > 0            # beyond a cluster
+    assert size(matrix(batch=1, rows=7000, cols=64, batch_stride=0, row_stride=64)) > 0
     # a list beyond 4 GB goes in parts
     big = matrix(batch=100, rows=4096, cols=4096, row_stride=4096, batch_stride=1 << 24)
     assert size(big) <= (4 << 30) + (1 << 20) and size(big, big) <= (4 << 30) + (1 << 20)
