@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "newton.cuh"
@@ -34,22 +35,24 @@ struct Partial {
     double wide;
 };
 
+constexpr int kElements = 64;       // list elements a launch: 14 KB of arguments
+
 struct SmallArgs {
     int n, steps;
     float mu, alpha;
     bool nesterov;
     double eps;
     uint32_t* status;
-    Shape shape[kTable];
-    Source source[kTable];
-    Result result[kTable];
+    Shape shape[kElements];
+    Source source[kElements];
+    Result result[kElements];
     float abc[3 * kNewtonMaxSteps];
 };
 
 // tiles of 64 along the long side that a CTA of a cluster of c can hold, with the short side of b
 // tiles: beside X (hi and lo) lie S, the sums that the cluster exchanges and (b = 1) those that halves of a CTA do
 int most_tiles(int b, int c) {
-    const int s = 2 * b * b, exchange = c > 1 ? 2 * b * b : 0, halves = b == 1 ? 2 : 0;
+    const int s = 2 * b * b, exchange = c > 1 ? 2 * b * b : 0, halves = b == 1 ? 4 : 0;
     return ((int)kTiles - s - exchange - halves) / (2 * b);
 }
 
@@ -75,8 +78,9 @@ __device__ __forceinline__ void all_sync() {
     else
         __syncthreads();
 }
-// generic writes to shared memory (of any CTA of the cluster), before the tensor core reads them
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// generic writes to shared memory, of this CTA or of any of the cluster, before the tensor core reads them
+__device__ __forceinline__ void fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.proxy.async.shared::cluster;" ::: "memory"); }
 
 // descriptor low word of an MN-major operand whose 64-row parts of M lie `apart` bytes from one another
 __device__ __forceinline__ uint32_t mn_desc(uint32_t addr, uint32_t apart) {
@@ -91,14 +95,35 @@ struct Op {
 // Up to 64 indices in slices of 16, by a whole warp: small terms (lo lo too: 2.0e-6 instead of 2.2e-6
 // off for 256 x 64), then hi hi, into an accumulator of its own.
 __device__ __forceinline__ void issue(uint32_t d, const Op& p, const Op& q, int slices, uint32_t idesc, uint32_t leader) {
+    if (slices == 4) {
+        uint32_t acc = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk, acc = 1u)
+                mma<1>(d, (i == 1 || i == 3 ? p.hi : p.lo) + kk * p.step, (i >= 2 ? q.hi : q.lo) + kk * q.step, idesc, acc, leader);
+        return;
+    }
     uint32_t acc = 0u;
-    for (int kk = 0; kk < slices; ++kk, acc = 1u) mma<1>(d, p.lo + kk * p.step, q.lo + kk * q.step, idesc, acc, leader);
-    for (int kk = 0; kk < slices; ++kk) mma<1>(d, p.hi + kk * p.step, q.lo + kk * q.step, idesc, 1u, leader);
-    for (int kk = 0; kk < slices; ++kk) mma<1>(d, p.lo + kk * p.step, q.hi + kk * q.step, idesc, 1u, leader);
-    for (int kk = 0; kk < slices; ++kk) mma<1>(d, p.hi + kk * p.step, q.hi + kk * q.step, idesc, 1u, leader);
+    for (int i = 0; i < 4; ++i)
+        for (int kk = 0; kk < slices; ++kk, acc = 1u)
+            mma<1>(d, (i == 1 || i == 3 ? p.hi : p.lo) + kk * p.step, (i >= 2 ? q.hi : q.lo) + kk * q.step, idesc, acc, leader);
 }
 // slices that indices [64 t, n) of a tile have
 __device__ __forceinline__ int slices_of(int n, int t) { return min(4, (n - 64 * t + 15) / 16); }
+
+// a warp's sum, in all its lanes
+__device__ __forceinline__ Sum warp_total(Sum s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float l = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
+        s.add(__shfl_xor_sync(0xFFFFFFFFu, s.hi, o));
+        s.lo += l;
+    }
+    if (__any_sync(0xFFFFFFFFu, s.wide != 0.0))         // NaN too
+        for (int o = 16; o > 0; o >>= 1) s.wide += __shfl_xor_sync(0xFFFFFFFFu, s.wide, o);
+    return s;
+}
 
 // U of this CTA's tiles, its norm over the cluster, and their images.  place(tile, row, col, at): the
 // tile's first row and column, and where it lies behind x_hi (its low part x_lo bytes further).
@@ -137,13 +162,26 @@ __device__ __forceinline__ void load_slab(const A& a, const Shape& shape, const 
 #pragma unroll
         for (int i = 0; i < kAhead; i += 2) sum.squares16(u[i]);
     }
-    Sum total = block_total<kWarps>(sum);
+    __shared__ Partial of_warp[kWarps];
+    const int lane = threadIdx.x & 31;
+    sum = warp_total(sum);
+    if (lane == 0) of_warp[threadIdx.x >> 5] = Partial{sum.hi, sum.lo, sum.wide};
+    __syncthreads();
+    Sum total;
+    if (threadIdx.x < 32) {
+        if (lane < kWarps) {
+            total.hi = of_warp[lane].hi;
+            total.lo = of_warp[lane].lo;
+            total.wide = of_warp[lane].wide;
+        }
+        total = warp_total(total);
+    }
     if constexpr (kC > 1) {
-        if (threadIdx.x == 0) {
+        if (threadIdx.x < kC) {
             const Partial mine{total.hi, total.lo, total.wide};
             uint4 bits;
             memcpy(&bits, &mine, sizeof(bits));
-            for (uint32_t c = 0; c < kC; ++c) put_in_cluster(in_cta(smem_u32(&sums[rank_in_cluster()]), c), bits);
+            put_in_cluster(in_cta(smem_u32(&sums[rank_in_cluster()]), threadIdx.x), bits);
         }
         all_sync<kC>();
         total = Sum();
@@ -176,7 +214,7 @@ __device__ __forceinline__ void load_slab(const A& a, const Shape& shape, const 
             *reinterpret_cast<uint4*>(x_hi + x_lo + at) = lo;
         }
     }
-    fence_async();
+    fence_shared();
     __syncthreads();
 }
 
@@ -336,9 +374,9 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                     put_in_cluster(to + s_lo, lo);
                 }
             }
-            fence_async();
+            fence_cluster();
             all_sync<kC>();
-            fence_async();
+            fence_cluster();
         } else {
             if (r < kM) {
 #pragma unroll
@@ -353,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                     *reinterpret_cast<uint4*>(at + s_lo) = lo;
                 }
             }
-            fence_async();
+            fence_shared();
             __syncthreads();
         }
 
@@ -386,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                 *reinterpret_cast<uint4*>(at + s_lo) = lo;
             }
         }
-        fence_async();
+        fence_shared();
         __syncthreads();
 
         // P X over X, some tiles of the long side at a time: 64 x 64 blocks of the result, each
@@ -471,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                 }
             }
             tc_fence_before();
-            if (n == passes - 1) fence_async();
+            if (n == passes - 1) fence_shared();
             __syncthreads();
             if (warp == 0 && n + 2 < passes) {
                 tc_fence_after();
@@ -491,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
 // rows: one MMA gives hi hi, hi lo, lo hi and lo lo in the quarters of its accumulators (rows 0-63
 // and 64-127, columns 0-63 and 64-127), which are added up outside: a quarter of the MMAs, and the
 // small terms by themselves.  Warps of rows r and 64 + r change halves of what they have: a thread
-// ends up with 8 elements of one row, a piece of an image.
+// ends up with 8 elements of one row, a piece of an image.  (A warp of its own for the MMAs leaves
+// 96 registers a thread: 51 us instead of XX for 256 x 64.)
 template <int kC>
 __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_constant__ SmallArgs a) {
     constexpr uint32_t kPair = 2 * kTileBytes;
@@ -535,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
     const int t0 = tiles * (int)rank / kC, nt = tiles * ((int)rank + 1) / kC - t0;
     uint8_t* const x = smem + kHeader;          // pairs of tiles along the long side
     uint8_t* const sp = x + (size_t)nt_most * kPair;
-    float4* const halves = reinterpret_cast<float4*>(sp + kPair);               // [2][kThreads]
-    uint8_t* const exchange = sp + 2 * kPair;
+    float4* const halves = reinterpret_cast<float4*>(sp + kPair);               // [4][kThreads]
+    uint8_t* const exchange = sp + 3 * kPair;
     const uint32_t xa = smem_u32(x), sa = smem_u32(sp);
 
     load_slab<kC>(a, shape, src, b, nt, sums, found,
@@ -559,42 +598,56 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         parity ^= 1u << z;
         tc_fence_after();
     };
-    // the four quarters' terms of this thread's 8 elements, from accumulators at `from`, and from
-    // as many more buffers of 128 columns as `buffers` says
-    auto gather = [&](uint32_t from, int buffers, float* v) {
-        float all[16];
-        for (int i = 0; i < buffers; ++i) {
-            uint32_t lead[16], rest[16];
-            tmem_ld16(from + (uint32_t)(128 * i + 16 * part), lead);
-            tmem_ld16(from + (uint32_t)(128 * i + 64 + 16 * part), rest);
+    // the four quarters' terms of this thread's 8 elements (v), of kTiles tiles whose accumulators lie
+    // 128 columns apart, or of the sum over two tiles
+    auto gather = [&](uint32_t from, auto tiles_of_it, bool added, float* v) {
+        constexpr int kT = decltype(tiles_of_it)::value;
+        float all[kT][16];
+        {
+            uint32_t lead[kT][16], rest[kT][16];
+#pragma unroll
+            for (int i = 0; i < kT; ++i) {
+                tmem_ld16(from + (uint32_t)(128 * i + 16 * part), lead[i]);
+                tmem_ld16(from + (uint32_t)(128 * i + 64 + 16 * part), rest[i]);
+            }
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float f = __uint_as_float(lead[e]) + __uint_as_float(rest[e]);
-                all[e] = i == 0 ? f : all[e] + f;
-            }
+            for (int i = 0; i < kT; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) all[i][e] = __uint_as_float(lead[i][e]) + __uint_as_float(rest[i][e]);
+        }
+        const bool both = kT == 2 && added;
+        if (both) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) all[0][e] += all[kT - 1][e];
         }
         // rows r give away columns 8-15 of the 16 they have, rows 64 + r columns 0-7
-        const int mine = threadIdx.x, other = threadIdx.x ^ 64;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float4 f;
-            f.x = low ? all[4 * h] : all[8 + 4 * h];
-            f.y = low ? all[4 * h + 1] : all[8 + 4 * h + 1];
-            f.z = low ? all[4 * h + 2] : all[8 + 4 * h + 2];
-            f.w = low ? all[4 * h + 3] : all[8 + 4 * h + 3];
-            halves[h * kThreads + mine] = f;
+        for (int i = 0; i < kT; ++i) {
+            if (i > 0 && both) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float* lower = all[i] + 4 * h;
+                halves[(2 * i + h) * kThreads + threadIdx.x] =
+                    make_float4(low ? lower[0] : lower[8], low ? lower[1] : lower[9], low ? lower[2] : lower[10], low ? lower[3] : lower[11]);
+            }
         }
         asm volatile("bar.sync %0, 64;" ::"r"(1 + 2 * part + (quad & 1)) : "memory");
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 f = halves[h * kThreads + other];
-            const float g[4] = {f.x, f.y, f.z, f.w};
+        for (int i = 0; i < kT; ++i) {
+            if (i > 0 && both) break;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * h + e] = g[e] + (low ? all[8 + 4 * h + e] : all[4 * h + e]);
+            for (int h = 0; h < 2; ++h) {
+                const float4 f = halves[(2 * i + h) * kThreads + (threadIdx.x ^ 64)];
+                const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[8 * i + 4 * h + e] = g[e] + (low ? all[i][8 + 4 * h + e] : all[i][4 * h + e]);
+            }
         }
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + 2 * part + (quad & 1)) : "memory");
+        // (the exchange may be written again behind the next barrier of the CTA only)
     };
+    constexpr std::integral_constant<int, 1> kOne{};
+    constexpr std::integral_constant<int, 2> kTwo{};
     auto put8_pair = [&](uint8_t* pair, const float* v) {
         uint4 hi, lo;
         split8(v, hi, lo);
@@ -606,34 +659,42 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
     // products of pairs, in slices of 16 indices
     auto multiply = [&](uint32_t d, uint32_t p, uint32_t p_step, uint32_t q0, uint32_t q_step, int slices, uint32_t idesc,
                         uint32_t acc) {
+        if (slices == 4) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk, acc = 1u) mma<1>(d, p + kk * p_step, q0 + kk * q_step, idesc, acc, leader);
+            return;
+        }
         for (int kk = 0; kk < slices; ++kk, acc = 1u) mma<1>(d, p + kk * p_step, q0 + kk * q_step, idesc, acc, leader);
     };
     const int m_slices = slices_of(m, 0);
     const float m_short = short_of(m_slices);
     // tiles of the slab into one buffer of accumulators of S: additions
-    const float n_short = short_of(max(slices_of(n, 0), 4 * ((nt_most + 3) / 4) * (nt_most > 1)));
+    const float n_short = short_of(max(slices_of(n, 0), 4 * ((nt_most + 1) / 2) * (nt_most > 1)));
 
     for (int step = 0; step < a.steps; ++step) {
         const float ca = a.abc[3 * step], cb = a.abc[3 * step + 1], cc = a.abc[3 * step + 2];
-        // S: this slab's part, its tiles in turn into four buffers of accumulators
+        // S: this slab's part, its tiles in turn into two buffers of accumulators
         if (warp == 0) {
             tc_fence_after();
             for (int t = 0; t < nt; ++t) {
                 const uint32_t at = xa + (uint32_t)t * kPair;
                 const uint32_t o = wide ? sdesc128_lo(at) : sdesc128mn_lo(at);
-                multiply(tmem + (uint32_t)(t & 3) * 128u, o, wide ? 2u : 128u, o, wide ? 2u : 128u, slices_of(n, t0 + t),
-                         kDesc | kN128 | (wide ? 0u : kAMn | kBMn), t < 4 ? 0u : 1u);
+                multiply(tmem + (uint32_t)(t & 1) * 128u, o, wide ? 2u : 128u, o, wide ? 2u : 128u, slices_of(n, t0 + t),
+                         kDesc | kN128 | (wide ? 0u : kAMn | kBMn), t < 2 ? 0u : 1u);
             }
             commit<1>(&bars[0], leader);
         }
         float s[8];
-        if (nt > 0) {
-            wait(0);
-            gather(lanes, min(nt, 4), s);
-        } else {
-            wait(0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = 0.f;
+        for (int e = 0; e < 8; ++e) s[e] = 0.f;
+        wait(0);
+        if (nt > 1) {
+            float v[16];
+            gather(lanes, kTwo, true, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = v[e];
+        } else if (nt == 1) {
+            gather(lanes, kOne, false, s);
         }
         tc_fence_before();
         if constexpr (kC > 1) {
@@ -664,14 +725,14 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
                     put_in_cluster(to_s + kTileBytes, lo);
                 }
             }
-            fence_async();
+            fence_cluster();
             all_sync<kC>();
-            fence_async();
+            fence_cluster();
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = uncut(s[e], n_short) * kUnscale;
             put8_pair(sp, s);
-            fence_async();
+            fence_shared();
             __syncthreads();
         }
 
@@ -684,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         }
         wait(0);
         float p[8];
-        gather(lanes, 1, p);
+        gather(lanes, kOne, false, p);
         tc_fence_before();
         join8(*reinterpret_cast<const uint4*>(sp + own_piece), *reinterpret_cast<const uint4*>(sp + kTileBytes + own_piece), s);
 #pragma unroll
@@ -693,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
             if (r == 8 * q + e && r < m) p[e] += ca * kScale;
         }
         put8_pair(sp, p);
-        fence_async();
+        fence_shared();
         __syncthreads();
 
         // P X over X
@@ -715,27 +776,32 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         for (int pass = 0; pass < passes; ++pass) {
             wait(pass & 1);
             const int first = pass * kAtOnce, count = min(kAtOnce, nt - first);
-            for (int i = 0; i < count; ++i) {
+            const uint32_t from = lanes + (uint32_t)(pass & 1) * kHalfTmem;
+            float v[16];
+            if (count == 2) gather(from, kTwo, false, v);
+            else gather(from, kOne, false, v);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (i >= count) break;
                 uint8_t* const pair = x + (size_t)(first + i) * kPair;
-                float v[8];
-                gather(lanes + (uint32_t)(pass & 1) * kHalfTmem + 128u * i, 1, v);
+                float* f = v + 8 * i;
                 if (!last) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = uncut(v[e], m_short) * kUnscale;
-                    put8_pair(pair, v);
+                    for (int e = 0; e < 8; ++e) f[e] = uncut(f[e], m_short) * kUnscale;
+                    put8_pair(pair, f);
                 } else {
                     // fp32 in the place of the pair, as two blocks of 32 columns
                     const float by = a.result[k].beta;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = by * (uncut(v[e], m_short) * (kUnscale * kUnscale));
+                    for (int e = 0; e < 8; ++e) f[e] = by * (uncut(f[e], m_short) * (kUnscale * kUnscale));
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         *reinterpret_cast<float4*>(pair + (q >> 2) * kTileBytes + staged<32>(r, 2 * (q & 3) + h)) =
-                            make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+                            make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
                 }
             }
             tc_fence_before();
-            if (pass == passes - 1) fence_async();
+            if (pass == passes - 1) fence_shared();
             __syncthreads();
             if (warp == 0 && pass + 2 < passes) {
                 tc_fence_after();
@@ -792,29 +858,18 @@ cudaError_t run(int c, unsigned matrices, cudaStream_t s, const SmallArgs& args)
 int short_tiles(const mttkrp_matrices& m) { return tiles_of((int)std::min(m.rows, m.cols)); }
 int long_tiles(const mttkrp_matrices& m) { return tiles_of((int)std::max(m.rows, m.cols)); }
 
-// CTAs for a matrix: as many as it takes to hold it, and up to one for every two tiles of 128
-// while there are SMs for all
+// CTAs for a matrix: one where it does with few tiles (an exchange over a cluster is as long as
+// the work on four or eight), else as many as leave each two or four while there are SMs for all, and
+// as hold it in any case.
 int cluster_of(const mttkrp_matrices& m, int64_t matrices, int sms) {
-    const int b = short_tiles(m), t = long_tiles(m);
+    const int b = short_tiles(m), t = long_tiles(m), alone = b == 1 ? 8 : 3, each = b == 1 ? 4 : 2;
     int c = 1;
-    while (c < 8 && (long long)most_tiles(b, c) * c < t) c *= 2;
-    while (c < 8 && t >= (b == 1 ? 8 : 4) * c && matrices * c * 2 <= sms) c *= 2;
+    while (c < 8 && most_tiles(b, c) * c < t) c *= 2;
+    while (c < 8 && t > alone && t > each * c && matrices * c * 2 <= sms) c *= 2;
     return c;
 }
 
-}  // namespace
-
-bool newton_is_small(const mttkrp_matrices& m) {
-    const int b = short_tiles(m);
-    return b <= 2 && long_tiles(m) <= 8 * most_tiles(b, 8);
-}
-
-cudaError_t launch_newton_small(const NewtonArgs& a, int sms, cudaStream_t s) {
-    int64_t matrices = 0;
-    for (int k = 0; k < a.n; ++k)
-        if (newton_some(a.grad[k]) && newton_is_small(a.grad[k])) matrices += a.grad[k].batch;
-    cudaError_t e = cudaSuccess;
-    if (matrices == 0) return e;
+cudaError_t run_list(const NewtonArgs& a, int64_t matrices, int sms, cudaStream_t s) {
     SmallArgs p;
     p.steps = a.steps;
     p.mu = a.mu;
@@ -823,13 +878,14 @@ cudaError_t launch_newton_small(const NewtonArgs& a, int sms, cudaStream_t s) {
     p.eps = a.eps;
     p.status = a.status;
     for (int i = 0; i < 3 * a.steps; ++i) p.abc[i] = a.coefficients[i];
+    cudaError_t e = cudaSuccess;
     // a launch for every size of cluster and short side, of as many elements as a table holds
     for (int b = 1; b <= 2; ++b)
         for (int c = 1; c <= 8; c *= 2) {
             p.n = 0;
             unsigned used = 0;
             for (int k = 0; k <= a.n && e == cudaSuccess; ++k) {
-                if (p.n == kTable || (k == a.n && p.n > 0)) {
+                if (p.n == kElements || (k == a.n && p.n > 0)) {
                     e = b == 1 ? run<1>(c, used, s, p) : run<2>(c, used, s, p);
                     p.n = 0;
                     used = 0;
@@ -854,6 +910,20 @@ cudaError_t launch_newton_small(const NewtonArgs& a, int sms, cudaStream_t s) {
             }
         }
     return e;
+}
+
+}  // namespace
+
+bool newton_is_small(const mttkrp_matrices& m) {
+    const int b = short_tiles(m);
+    return b <= 2 && long_tiles(m) <= 8 * most_tiles(b, 8);
+}
+
+cudaError_t launch_newton_small(const NewtonArgs& a, int sms, cudaStream_t s) {
+    int64_t matrices = 0;
+    for (int k = 0; k < a.n; ++k)
+        if (newton_some(a.grad[k]) && newton_is_small(a.grad[k])) matrices += a.grad[k].batch;
+    return matrices > 0 ? run_list(a, matrices, sms, s) : cudaSuccess;
 }
 
 }  // namespace mk
