@@ -7,11 +7,14 @@ entry in every sweep): each step takes a batch of (coordinates, value) pairs and
     cp_entries_grad   the squared error's gradient for every factor,
     embedding         the rows of a factor that the batch touched, scaled by a penalty,
     embedding_grad    which are added to that factor's gradient, row by row,
-    clip_grad_norm    all gradients, scaled so that their common norm is at most a limit.
+    clip_grad_norm    all gradients, scaled so that their common norm is at most a limit,
+    orthogonal_step   (--orthogonal) momentum and the update along the orthogonal matrix
+                      nearest to it, instead of along the momentum itself.
 
 Nothing in a step waits for the GPU.
 
     python examples/sampled_cp_fit.py --dims 60 50 40 --rank 8 --steps 1500
+    python examples/sampled_cp_fit.py --orthogonal
 """
 from __future__ import annotations
 
@@ -41,9 +44,10 @@ def gradients(factors, coords, values, penalty: float = 0.0, max_norm: float | N
 
 
 def fit(coords, values, dims, rank: int, steps: int, batch: int, rate: float = 0.3, momentum: float = 0.9,
-        penalty: float = 1e-4, max_norm: float = 1.0, seed: int = 0):
+        penalty: float = 1e-4, max_norm: float = 1.0, seed: int = 0, orthogonal: bool = False):
     """Factors (list of dims[n] x rank, float32) after `steps` steps over random batches of
-    the samples, and the batches' mean squared errors."""
+    the samples, and the batches' mean squared errors.  orthogonal: every factor moves along its
+    orthogonalised momentum, all singular directions alike, by `rate`."""
     gen = torch.Generator(device=coords.device).manual_seed(seed)
     factors = [torch.randn(n, rank, generator=gen, device=coords.device).mul_(0.3) for n in dims]
     velocity = [torch.zeros_like(a) for a in factors]
@@ -51,9 +55,12 @@ def fit(coords, values, dims, rank: int, steps: int, batch: int, rate: float = 0
     for _ in range(steps):
         pick = torch.randint(coords.shape[0], (batch,), generator=gen, device=coords.device)
         loss, grads, _ = gradients(factors, coords[pick], values[pick], penalty, max_norm)
-        for A, V, G in zip(factors, velocity, grads):
-            V.mul_(momentum).add_(G)
-            A.sub_(V, alpha=rate)
+        if orthogonal:
+            mk.orthogonal_step(factors, grads, velocity, rate, momentum=momentum, scale=1.0)
+        else:
+            for A, V, G in zip(factors, velocity, grads):
+                V.mul_(momentum).add_(G)
+                A.sub_(V, alpha=rate)
         losses.append(loss)
     return factors, torch.stack(losses)
 
@@ -76,9 +83,11 @@ def main():
     ap.add_argument("--samples", type=int, default=60000)
     ap.add_argument("--batch", type=int, default=8192)
     ap.add_argument("--steps", type=int, default=1500)
+    ap.add_argument("--orthogonal", action="store_true")
     args = ap.parse_args()
     coords, values = samples(args.dims, args.rank, args.samples)
-    _, losses = fit(coords, values, args.dims, 2 * args.rank, args.steps, args.batch, rate=1.0)
+    _, losses = fit(coords, values, args.dims, 2 * args.rank, args.steps, args.batch,
+                    rate=0.02 if args.orthogonal else 1.0, orthogonal=args.orthogonal)
     every = max(1, args.steps // 10)
     for k in range(0, args.steps, every):
         print(f"step {k:5d}: mean squared error {float(losses[k]):.5f}")

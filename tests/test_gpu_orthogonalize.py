@@ -88,6 +88,58 @@ def test_two_steps_of_whole_numbers(dtype):
         assert torch.equal(out, cuda(want).to(TYPES[dtype])), (rows, cols)
 
 
+CLUSTERS = [  # short side, long side, q: a CTA, clusters of 2, 4 and 8 of either kind of kernel, and beyond
+    (64, 512, 5), (64, 513, 5), (33, 1000, 5), (1, 2500, 5), (64, 5000, 6), (17, 5120, 6), (17, 5121, 6), (65, 65, 4),
+    (128, 192, 5), (100, 193, 5), (128, 500, 5), (65, 1000, 5), (127, 1536, 6), (127, 1537, 6)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tall", [False, True])
+@pytest.mark.parametrize("short,long,q", CLUSTERS)
+def test_short_sides(short, long, q, tall, dtype):
+    """S X, and S of that, in whole numbers; the same for every matrix of a list and a batch."""
+    g = signs(short + long, (3, long, short) if tall else (3, short, long), q)
+    out = mk.orthogonalize(cuda(g), 1, (0.0, 1.0, 0.0), eps=0.0, dtype=TYPES[dtype])
+    want = cuda(oo.orthogonalize(g, 1, (0.0, 1.0, 0.0), 0.0)).to(TYPES[dtype])
+    assert torch.equal(out, want)
+    each = [cuda(m) for m in g]
+    for got, one in zip(mk.orthogonalize(each, 1, (0.0, 1.0, 0.0), eps=0.0, dtype=TYPES[dtype]), want):
+        assert torch.equal(got, one)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("abc", [(1.0, 0.0, 0.0), (0.0, 1.0, 0.0), (0.0, 0.0, 1.0)])
+@pytest.mark.parametrize("count,rows,cols", [(24, 1024, 768), (24, 600, 1100), (24, 1100, 600), (2, 4096, 4033), (5, 3971, 2050)])
+def test_pairs_of_ctas(count, rows, cols, abc, dtype):
+    """Sizes from which pairs take some or all of the products, in whole numbers: one to three entries
+    a row of the smaller side, so that all are small."""
+    gen = generator(rows)
+    g = torch.zeros(count, rows, cols, device="cuda", dtype=torch.float64)
+    at = torch.stack([torch.randperm(rows * cols, generator=gen, device="cuda")[:1024] for _ in range(count)])
+    sign = torch.randint(0, 2, at.shape, generator=gen, device="cuda").double() * 2 - 1
+    g.view(count, -1).scatter_(1, at, sign)
+    out = mk.orthogonalize(g.to(torch.float32), 1, abc, eps=0.0, dtype=TYPES[dtype])
+    x = g / 32.0
+    x = x.mT if rows > cols else x
+    s = x @ x.mT
+    want = abc[0] * x + (abc[1] * s + abc[2] * (s @ s)) @ x
+    want = want.mT if rows > cols else want
+    assert torch.equal(out, want.to(TYPES[dtype]))
+
+
+def test_long_lists_of_small_matrices():
+    """More elements than a launch takes, of both kinds of kernel and several clusters, and large ones between."""
+    gen = generator(11)
+    shapes = [(8, 8), (20, 128), (128, 20), (64, 700), (100, 100), (128, 400), (300, 200), (1, 1), (70, 900)] * 20
+    gs = [gradient(gen, s) for s in shapes]
+    got = mk.orthogonalize(gs)
+    for s, g, x in zip(shapes, gs, got):
+        want = mk.orthogonalize(g)
+        # a cluster's size follows the number of matrices: sums are added in another order
+        assert float((x - want).norm()) <= 1e-5 * float(want.norm()), s
+    assert all(torch.equal(a, b) for a, b in zip(got, mk.orthogonalize(gs)))
+
+
 def trajectory_bound(g, steps, coefficients, eta):
     """Bound of the error's Frobenius norm, and the oracle's result."""
     total, before = 0.0, oo.orthogonalize(g, 0, coefficients)
