@@ -198,6 +198,7 @@ struct ProductArgs {
     int n;
     uint32_t items;             // tiles of the result, of all matrices
     int from;                   // which X is read
+    int split;                  // of S, by single CTAs: CTAs (a cluster) an item, each with some of its steps
     float a, b, c, alpha;
     uint8_t* tiles;
     uint32_t* status;
@@ -555,6 +556,46 @@ __device__ __forceinline__ Stream stream_of(const Operand& o, int first, int row
     return t;
 }
 
+// The parts that a cluster's CTAs have of one 128 x 128 block of S (f: 64 columns of a row), added up
+// by way of the ring, which is idle then: every CTA gets some rows of all parts, adds them in the order of
+// the CTAs and writes them.  128 rows of 512 bytes in all, pieces of 16 bytes in an order that spreads banks.
+__device__ __forceinline__ void add_up_split(const ProductArgs& a, const Place& at, uint8_t* ring, int share, int split,
+                                             int quad, int part, int lane, const float* f) {
+    auto where = [](int row, int q) { return (uint32_t)(row * 512 + ((q ^ (row & 7)) << 4)); };
+    const int own = 128 / split, row = 32 * quad + lane;        // rows a CTA; of the block
+    cluster_sync();             // every CTA's MMAs are done
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(ring)), "r"(row / own));
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + where(share * own + row % own, 16 * part + q)),
+                     "f"(f[4 * q]), "f"(f[4 * q + 1]), "f"(f[4 * q + 2]), "f"(f[4 * q + 3])
+                     : "memory");
+    cluster_sync();
+    // pieces of 8 columns: 16 a row
+    const int ti0 = at.ti - quad / 2, tj0 = at.tj - part;
+    for (int p = (4 * part + quad) * 32 + lane; p < own * 16; p += 256) {
+        const int r = p >> 4, c = p & 15;
+        float v[8];
+        for (int s = 0; s < split; ++s) {
+            const float4 x = *reinterpret_cast<const float4*>(ring + where(s * own + r, 2 * c));
+            const float4 y = *reinterpret_cast<const float4*>(ring + where(s * own + r, 2 * c + 1));
+            const float g[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = s == 0 ? g[e] : v[e] + g[e];
+        }
+        const int row_of = share * own + r, ti = ti0 + row_of / 64, tj = tj0 + c / 8;
+        if (ti >= at.nt || tj >= at.mt) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= kUnscale;
+        uint4 hi, lo;
+        split8(v, hi, lo);
+        uint8_t* dst = a.tiles + (int64_t)(at.to + ti * at.mt + tj) * kTileBytes + piece(row_of & 63, c & 7);
+        *reinterpret_cast<uint4*>(dst) = hi;
+        *reinterpret_cast<uint4*>(dst + (int64_t)at.lo * kTileBytes) = lo;
+    }
+}
+
 // kFull: both parts of all operands, accumulators added up in registers every step.  Else the
 // accumulators stay in tensor memory for all steps of an item.
 //
@@ -589,6 +630,9 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
     static_assert((2 * kMaxStages + 5) * 8 + 8 <= kBarBytes, "barriers");
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = kCtas == 2 ? cluster_rank() : 0;
+    // one of `split` CTAs that share an item's steps
+    constexpr bool kSplits = kCtas == 1 && kPhase == kGram;
+    const int split = kSplits ? a.split : 1, share = kSplits && split > 1 ? (int)cluster_rank() : 0;
     // parts a stage: of both operands hi, and lo of both (full) or of one (P X)
     constexpr int parts = kFull ? 4 : is_update(kPhase) ? 3 : 2;
     // steps a stage: with four MMAs a step the control of each would take longer than they do
@@ -629,7 +673,9 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
     const uint32_t tmem = *tmem_slot;
     after_previous();
 
-    const uint32_t first = blockIdx.x / kCtas, stride = gridDim.x / kCtas;
+    const uint32_t first = blockIdx.x / (uint32_t)(kCtas * split), stride = gridDim.x / (uint32_t)(kCtas * split);
+    auto from_step = [&](const Item& w) { return kSplits ? w.steps * share / split : 0; };
+    auto to_step = [&](const Item& w) { return kSplits ? w.steps * (share + 1) / split : w.steps; };
     if (warp < kEpiWarp0) {
     if constexpr (R::kMany) regs_dec<R::kCtl>();
     if (warp == 0) {
@@ -651,8 +697,9 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
             const int block = of_p ? w.i : w.j;
             const Stream m = stream_of(o, block, block + 2 * (int)rank, half, which >= 2,
                                               (uint32_t)mine * step_bytes + (uint32_t)tile_of * kTileBytes);
-            for (int k0 = 0; k0 < w.steps; k0 += sub) {
-                const int k = k0 + mine, here = min(sub, w.steps - k0);
+            const int ke = to_step(w);
+            for (int k0 = from_step(w); k0 < ke; k0 += sub) {
+                const int k = k0 + mine, here = min(sub, ke - k0);
                 const int tile = k < m.turn ? m.base + k * m.step : m.base2 + k * m.step2;
                 if (reused && !warp_wait(&empty[slot], phase ^ 1u, abort_flag, a.status, kStatusTimeoutTma)) {
                     ok = false;
@@ -719,9 +766,10 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                         parity ^= 1u;
                     }
                 };
-                for (int k0 = 0; k0 < w.steps && ok; k0 += per_pass) {
-                    const int here = min(per_pass, w.steps - k0);
-                    if ((kFull || k0 == 0) && ((zused >> z) & 1u)) {
+                const int kb = from_step(w), ke = to_step(w);
+                for (int k0 = kb; k0 < ke && ok; k0 += per_pass) {
+                    const int here = min(per_pass, ke - k0);
+                    if ((kFull || k0 == kb) && ((zused >> z) & 1u)) {
                         if (!(ok = warp_wait(&zempty[z], (zphase >> z) & 1u, abort_flag, a.status, kStatusTimeoutMma))) break;
                         zphase ^= 1u << z;
                     }
@@ -748,13 +796,13 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                     } else {
                         for (int k = k0; k < k0 + here; ++k) {
                             const uint32_t from = at + (uint32_t)(k - k0) * step_bytes;
-                            if constexpr (is_update(kPhase)) issue(k, from, d, true, k == 0 ? 0u : 1u);
-                            issue(k, from, d, false, is_update(kPhase) || k > 0 ? 1u : 0u);
+                            if constexpr (is_update(kPhase)) issue(k, from, d, true, k == kb ? 0u : 1u);
+                            issue(k, from, d, false, is_update(kPhase) || k > kb ? 1u : 0u);
                         }
                         commit<kCtas>(&empty[slot], leader);
                     }
                     next(slot, phase);
-                    if (kFull || k0 + here == w.steps) {
+                    if (kFull || k0 + here == ke) {
                         commit<kCtas>(&zfull[z], leader);
                         zused |= 1u << z;
                         z ^= 1u;
@@ -764,6 +812,11 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
             commit<kCtas>(done, leader);
         }
         if (lane == 0) wait_drain(done, 0, a.status);
+    }
+    if (split > 1) {        // beside the epilogue's
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     } else {
         if constexpr (R::kMany) regs_inc<R::kEpi>();
@@ -799,7 +852,7 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
             if constexpr (kFull) {
                 float acc[kCols];
                 bool here = true;
-                const int drains = (w.steps + per_pass - 1) / per_pass;
+                const int drains = (to_step(w) - from_step(w) + per_pass - 1) / per_pass;
                 for (int n = 0; n < drains; ++n) {
                     if (!(here = filled())) break;
                     // columns in flight: all, or what registers there are for
@@ -816,9 +869,15 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                             acc[c + e] = n == 0 ? __uint_as_float(v[e]) : acc[c + e] + __uint_as_float(v[e]);
                     }
                 }
-                if (!here) break;
+                if (!here && split == 1) break;         // (a cluster's barriers wait for all)
 #pragma unroll
                 for (int e = 0; e < kCols; ++e) acc[e] = uncut(acc[e], short_of(8));
+                if constexpr (kSplits) {
+                    if (split > 1) {
+                        add_up_split(a, place(item_of<kCtas, kPhase>(a, t)), smem, share, split, quad, part, lane, acc);
+                        continue;
+                    }
+                }
                 const Place at = place(item_of<kCtas, kPhase>(a, t));       // (again: registers are short before)
 #pragma unroll
                 for (int c = 0; c < kCols; c += 64)
@@ -826,7 +885,7 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
             } else {
                 const Place at = place(w);
                 if (kPhase == kSquare && at.ti < at.nt && at.tj < at.mt) s.get(tile_of_s(a, at, 0), at, lane);
-                if (!filled()) break;
+                if (!filled() && split == 1) break;
 #pragma unroll
                 for (int c = 0; c < kCols; c += 64) {
                     uint32_t v[64];
@@ -837,6 +896,12 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                     float f[64];
 #pragma unroll
                     for (int e = 0; e < 64; ++e) f[e] = __uint_as_float(v[e]);
+                    if constexpr (kSplits) {
+                        if (split > 1) {
+                            add_up_split(a, at, smem, share, split, quad, part, lane, f);
+                            continue;
+                        }
+                    }
                     write_block<kFull, kPhase, kStage>(a, at, c / 64, f, s, kCols / 64, stage, lane);
                 }
             }
@@ -913,12 +978,13 @@ size_t partial_bytes(int used, const Part* parts, const mttkrp_matrices* like) {
 }
 
 template <int kCtas, bool kFull>
-cudaError_t launch_product(int phase, unsigned units, cudaStream_t s, const ProductArgs& p) {
+cudaError_t launch_product(int phase, unsigned units, cudaStream_t s, const ProductArgs& p) {     // units: of CTAs or pairs
     const auto kernel = phase == kGram     ? product_kernel<kCtas, kFull, kGram>
                         : phase == kSquare ? product_kernel<kCtas, kFull, kSquare>
                         : phase == kUpdate ? product_kernel<kCtas, kFull, kUpdate>
                                            : product_kernel<kCtas, kFull, kResult>;
-    return launch_clusters(kernel, units * kCtas, Roles<kCtas, kFull>::kThreads, kSmem, kCtas, s, p);
+    const int cluster = kCtas * (phase == kGram && kCtas == 1 ? p.split : 1);
+    return launch_clusters(kernel, units * kCtas, Roles<kCtas, kFull>::kThreads, kSmem, cluster, s, p);
 }
 
 // allows a form of the kernels their shared memory
@@ -964,6 +1030,8 @@ cudaError_t device(Device& d) {
 // says how long it takes, in microseconds without the launch: waves of items, whose epilogues run
 // beside the next one's MMAs.  Steps of 64 indices and epilogues as measured on 12 x 1024 x 4096,
 // 2 x 4096 x 4096 and 3 x 512 x 2000; a pair's items are four times a CTA's.
+constexpr float kExchange = 2.5f;       // microseconds that a cluster takes to add up its parts of S
+
 float number_items(ProductArgs& p, int phase, int ctas, bool full, int sms) {
     const int f = is_update(phase) ? 1 : 0, block = 2 * ctas;
     const float step = full ? (ctas == 2 ? 1.02f : 0.72f) : f ? (ctas == 2 ? 0.61f : 0.52f) : (ctas == 2 ? 0.33f : 0.26f);
@@ -982,7 +1050,12 @@ float number_items(ProductArgs& p, int phase, int ctas, bool full, int sms) {
         longest = std::max(longest, one);
         p.items += (uint32_t)items;
     }
+    // S by single CTAs, where they are fewer than half of the SMs: two or four an item, with steps enough each
+    p.split = 1;
+    if (phase == kGram && ctas == 1)
+        while (p.split < 4 && p.items * p.split * 2 <= (uint32_t)sms && longest / (2 * p.split) > kExchange) p.split *= 2;
     const float units = (float)(sms / ctas), waves = std::ceil((float)p.items / units);
+    if (p.split > 1) return longest / (float)p.split + kExchange + end;
     return std::max(longest, waves * work / (float)p.items) + end;
 }
 
@@ -1058,7 +1131,7 @@ cudaError_t run_group(const NewtonArgs& a, int used, const Part* parts, int64_t 
             const float pair = number_items(p, phase, 2, full, d.sms);
             const int ctas = number_items(p, phase, 1, full, d.sms) <= pair ? 1 : 2;
             if (ctas == 2) number_items(p, phase, 2, full, d.sms);
-            const unsigned units = std::min<unsigned>(p.items, (unsigned)(d.sms / ctas));
+            const unsigned units = p.split > 1 ? p.items * p.split : std::min<unsigned>(p.items, (unsigned)(d.sms / ctas));
             e = ctas == 2 ? full ? launch_product<2, true>(phase, units, s, p) : launch_product<2, false>(phase, units, s, p)
                           : full ? launch_product<1, true>(phase, units, s, p) : launch_product<1, false>(phase, units, s, p);
         }
