@@ -269,6 +269,96 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     }
 }
 
+// Dense tensors whose rows start at any element.  A CTA takes some rows, which lie in one piece of
+// memory: loads and stores are whole aligned 16-byte vectors of it (its ends element by element), and
+// the rows are turned in shared memory at the same offset.  What bounds it is the wait for the loads
+// of a CTA, which nothing of its own covers: 24 KB a CTA keep eight of them on a multiprocessor.
+// (84M bf16 in rows of 171: 24 heads 76 us, element by element from memory 77 in halves and 140 for
+// neighbours; 10 heads 78, 113 and 137 in rows of 83; one head 171, 286 and 209.)
+constexpr int kStageBytes = 24576;      // of rows, at most, but for one token that takes more
+constexpr int kMostStage = 98304;
+constexpr int kFewest = 608;            // CTAs before they take more than one token: four a multiprocessor
+
+struct Dense {
+    const void* x;
+    void* y;
+    uint64_t rows;                      // all of them: fewer than 2^32
+    uint32_t per_cta;                   // rows: whole tokens where heads follow one another
+    uint32_t heads;                     // rows in a token that follow one another, or 1
+    uint32_t outside;                   // else heads that lie outside of the tokens
+};
+
+template <int kPairs>
+struct DenseArgs {
+    Dense t[kMaxTensors];
+    const void* positions;
+    int64_t pb, pt;
+    uint32_t length;
+    int dims, half, width;
+    float scale;
+    bool wide, inverse;
+    uint64_t turns[kPairs];
+};
+
+template <typename T, bool kNeighbours, int kPairs>
+__global__ void __launch_bounds__(kThreads) dense_kernel(const __grid_constant__ DenseArgs<kPairs> a) {
+    extern __shared__ __align__(16) uint8_t room[];
+    after_previous();
+    const Dense d = a.t[blockIdx.y];
+    const uint64_t row0 = (uint64_t)blockIdx.x * d.per_cta;
+    if (row0 >= d.rows) return;
+    const uint32_t rows = (uint32_t)min(d.rows - row0, (uint64_t)d.per_cta);
+    const T* const from = static_cast<const T*>(d.x) + row0 * a.width;
+    T* const to = static_cast<T*>(d.y) + row0 * a.width;
+    constexpr uint32_t kVec = 16 / sizeof(T);
+    // elements before the first one in its vector; vectors that are whole
+    const uint32_t shift = (uint32_t)((reinterpret_cast<uintptr_t>(from) & 15) / sizeof(T)), n = rows * (uint32_t)a.width;
+    T* const s = reinterpret_cast<T*>(room) + shift;
+    const uint32_t v0 = shift == 0 ? 0 : 1, v1 = (shift + n) / kVec;
+    const uint32_t head = v1 >= v0 && v0 * kVec >= shift ? min(v0 * kVec - shift, n) : n;      // elements before the first whole one
+    const uint32_t tail = v1 > v0 ? v1 * kVec - shift : head;                                   // first one behind the last
+    for (uint32_t v = v0 + threadIdx.x; v < v1; v += kThreads)
+        reinterpret_cast<uint4*>(room)[v] = __ldcs(reinterpret_cast<const uint4*>(from - shift) + v);
+    for (uint32_t e = threadIdx.x; e < head; e += kThreads) s[e] = from[e];
+    for (uint32_t e = tail + threadIdx.x; e < n; e += kThreads) s[e] = from[e];
+    __syncthreads();
+    // a thread's pairs: number i of a token's rows
+    const uint32_t tokens = rows / d.heads, first = (uint32_t)row0 / d.heads;
+    uint32_t token = threadIdx.x / (uint32_t)a.half, i = threadIdx.x - token * (uint32_t)a.half;
+    const uint32_t token_step = kThreads / (uint32_t)a.half, i_step = kThreads - token_step * (uint32_t)a.half;
+    const uint64_t* turns = a.turns;
+    asm volatile("" : "+l"(turns));         // (see Unit::frequencies)
+    while (token < tokens) {
+        const uint32_t at = first + token, group = at / a.length, t = at - group * a.length;
+        const uint32_t b = d.outside > 0 ? group / d.outside : group;
+        const int64_t where = (int64_t)b * a.pb + (int64_t)t * a.pt;
+        uint64_t p = a.wide ? (uint64_t)static_cast<const int64_t*>(a.positions)[where]
+                            : (uint64_t)(int64_t)static_cast<const int32_t*>(a.positions)[where];
+        if (a.inverse) p = 0 - p;
+        float c, sn;
+        cos_sin(p * turns[i], a.scale, c, sn);
+        T* u = s + token * d.heads * (uint32_t)a.width + (kNeighbours ? 2 * i : i);
+        const int other = kNeighbours ? 1 : a.half;
+#pragma unroll 4
+        for (uint32_t h = 0; h < d.heads; ++h, u += a.width) {
+            const float m = to_f32(u[0]), q = to_f32(u[other]);
+            u[0] = from_f32<T>(m * c - q * sn);
+            u[other] = from_f32<T>(m * sn + q * c);
+        }
+        token += token_step;
+        i += i_step;
+        if (i >= (uint32_t)a.half) {
+            i -= (uint32_t)a.half;
+            ++token;
+        }
+    }
+    __syncthreads();
+    for (uint32_t v = v0 + threadIdx.x; v < v1; v += kThreads)
+        __stcs(reinterpret_cast<uint4*>(to - shift) + v, reinterpret_cast<const uint4*>(room)[v]);
+    for (uint32_t e = threadIdx.x; e < head; e += kThreads) to[e] = s[e];
+    for (uint32_t e = tail + threadIdx.x; e < n; e += kThreads) to[e] = s[e];
+}
+
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The largest number of elements, a power of two up to 16 bytes, that divides everything a
@@ -307,6 +397,68 @@ cudaError_t launch(Args<kPairs>& a, cudaStream_t s) {
     return launch_early(heads_kernel<T, V, kWhole, kLayout, kPairs>, dim3((unsigned)blocks, chunks), kThreads, 0, s, a);
 }
 
+// Whether the rows of a tensor and of its result fill their memory in the order of tokens and heads
+// (heads = 0) or of heads and tokens in every batch (their number in `outside`), at the same offset from
+// 16 bytes.
+bool dense(const RotaryArgs& r, const mttkrp_rotary_tensor& t, Dense& d) {
+    const int64_t w = r.width, h = t.heads, n = r.length;
+    auto is = [&](const int64_t* s, int64_t batch, int64_t token, int64_t head) {
+        return (r.batch == 1 || s[0] == batch) && (n == 1 || s[1] == token) && (h == 1 || s[2] == head);
+    };
+    if (((reinterpret_cast<uintptr_t>(t.x) ^ reinterpret_cast<uintptr_t>(t.out)) & 15) != 0) return false;
+    d.x = t.x;
+    d.y = t.out;
+    d.rows = (uint64_t)r.batch * n * h;
+    if (is(t.x_strides, n * h * w, h * w, w) && is(t.out_strides, n * h * w, h * w, w)) {
+        d.heads = (uint32_t)h;
+        d.outside = 0;
+    } else if (is(t.x_strides, n * h * w, w, n * w) && is(t.out_strides, n * h * w, w, n * w)) {
+        d.heads = 1;
+        d.outside = (uint32_t)h;
+    } else {
+        return false;
+    }
+    return true;
+}
+
+template <typename T, int kPairs>
+cudaError_t run_dense(const RotaryArgs& r, cudaStream_t s, bool& taken) {
+    DenseArgs<kPairs> a;
+    uint64_t blocks = 0;
+    size_t most = 0;
+    taken = false;
+    for (int k = 0; k < r.n; ++k) {
+        Dense& d = a.t[k];
+        if (!dense(r, r.tensor[k], d)) return cudaSuccess;
+        if (d.rows > UINT32_MAX || d.heads * (uint64_t)r.width > kMostStage / sizeof(T)) return cudaSuccess;
+        const size_t token = (size_t)d.heads * r.width * sizeof(T);
+        const uint64_t spread = d.rows / d.heads / kFewest;         // tokens
+        d.per_cta = d.heads * (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(kStageBytes / token, spread));
+        most = std::max(most, (size_t)d.per_cta * r.width * sizeof(T));
+        blocks = std::max(blocks, (d.rows + d.per_cta - 1) / d.per_cta);
+    }
+    if (blocks > INT32_MAX) return cudaSuccess;
+    a.positions = r.positions;
+    a.pb = r.pos_batch_stride;
+    a.pt = r.pos_stride;
+    a.length = (uint32_t)r.length;
+    a.dims = r.dims;
+    a.half = r.dims / 2;
+    a.width = (int)r.width;
+    a.scale = r.scale;
+    a.wide = r.pos_bytes == 8;
+    a.inverse = r.inverse;
+    for (int i = 0; i < r.dims / 2; ++i) a.turns[i] = r.turns[i];
+    taken = true;
+    const size_t smem = (most + 15 + 16) / 16 * 16;     // and up to a vector before the first element
+    const auto kernel = r.interleaved ? dense_kernel<T, true, kPairs> : dense_kernel<T, false, kPairs>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_early(kernel, dim3((unsigned)blocks, (unsigned)r.n), kThreads, smem, s, a);
+}
+
 template <typename T, int kPairs>
 cudaError_t run(const RotaryArgs& r, cudaStream_t s) {
     Args<kPairs> a;
@@ -334,6 +486,13 @@ cudaError_t run(const RotaryArgs& r, cudaStream_t s) {
     a.inverse = r.inverse;
     for (int i = 0; i < r.dims / 2; ++i) a.turns[i] = r.turns[i];
     const int v = vector_of(r, sizeof(T)), half = r.dims / 2;
+    // (fp32 in halves, 24 heads: 114 us element by element from memory, 130 through shared memory;
+    // one head: 284 and 188)
+    if (v == 1 && (sizeof(T) == 2 || r.interleaved || a.heads < kRows)) {
+        bool taken;
+        const cudaError_t e = run_dense<T, kPairs>(r, s, taken);
+        if (taken) return e;
+    }
     if (!r.interleaved) {
         a.units = half / v;
         a.copies = copies ? (a.width - r.dims) / v : 0;

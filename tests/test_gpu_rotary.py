@@ -213,3 +213,42 @@ def test_positions_give_lookups_their_turn():
     rhs = float((grad.double() * table.double()).sum())
     # both are sums of 200 x 24 products of normals: sqrt(4800) in size, each product within 16 U
     assert abs(lhs - rhs) <= 32 * U * float((rows.abs().double() * g.abs().double()).sum() * 2)
+
+
+DENSE = [  # batch, length, heads of each tensor, width, dims: rows at odd offsets that follow one another
+    (1, 1, (1,), 3, 2), (2, 3, (5, 1), 7, 6), (1, 700, (3,), 13, 12), (3, 1001, (1,), 9, 8), (2, 650, (8, 2), 83, 66),
+    (1, 900, (4,), 1031, 1024), (1, 5, (47,), 1045, 1000), (1, 3, (48,), 1047, 10), (4, 7, (2, 30, 1), 171, 168)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shift", [0, 1, 5])
+@pytest.mark.parametrize("batch,length,heads,width,dims", DENSE)
+def test_dense_rows_at_odd_offsets(batch, length, heads, width, dims, shift, interleaved, dtype):
+    """Tensors that fill their memory, as tokens of heads and as heads of tokens, with what lies around
+    them left as it was; the same values as from rows that do not follow one another."""
+    gen = generator(length + width + shift)
+    f = mk.rotary_frequencies(dims)
+    p = torch.randint(-1000, 1 << 20, (batch, length), generator=gen, device="cuda")
+    for outside in (False, True):
+        xs, outs, rooms = [], [], []
+        for h in heads:
+            shape = (batch, h, length, width) if outside else (batch, length, h, width)
+            n = batch * h * length * width
+            rooms.append(torch.full((n + 17,), 7.0, device="cuda", dtype=TYPES[dtype]))
+            x = torch.empty(n + 17, device="cuda", dtype=TYPES[dtype])[shift:shift + n].view(shape)
+            x.copy_(normal(gen, shape, TYPES[dtype]))
+            out = rooms[-1][shift:shift + n].view(shape)
+            xs.append(x.transpose(1, 2) if outside else x)
+            outs.append(out.transpose(1, 2) if outside else out)
+        mk.rotary(xs, p, f, interleaved, scale=1.25, outs=outs)
+        for x, out, room, h in zip(xs, outs, rooms, heads):
+            check(x, p, f, out, interleaved, 1.25)
+            n = batch * h * length * width
+            assert (room[:shift] == 7).all() and (room[shift + n:] == 7).all()
+            apart = torch.zeros(batch, length, h, width + 2, device="cuda", dtype=TYPES[dtype])
+            apart[..., :width] = x
+            assert torch.equal(mk.rotary(apart[..., :width], p, f, interleaved, scale=1.25), out)
+        again = [x.clone(memory_format=torch.preserve_format) for x in xs]
+        mk.rotary(again, p, f, interleaved, scale=1.25, outs=again)
+        assert all(torch.equal(x, y) for x, y in zip(again, outs))
