@@ -179,8 +179,10 @@ __device__ __forceinline__ uint32_t staged(int r, int q) {
 }
 
 // Writes them (beta O(U)) to a result, after adding alpha W: whole rows of the stage at a time, or
-// where rows are not aligned a column a lane.
-template <typename T, int kC>
+// where rows are not aligned a column a lane, the old values of kAtOnce rows in flight.  (Four: 64 bf16
+// steps of 501 x 333 take 463 us, one row at a time 576; but the registers cost newton_small.cu's
+// kernels 3 us whatever they write: one there.)
+template <typename T, int kC, int kAtOnce>
 __device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int b, int row0, int col0, int rows,
                                               int cols, const uint8_t* stage, int lane) {
     T* const out = static_cast<T*>(o.out.data) + b * o.out.batch;
@@ -217,22 +219,50 @@ __device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int 
     } else {
         const int c = lane % kC, col = col0 + c;
         if (col >= cols) return;
+        if constexpr (kAtOnce == 1) {
 #pragma unroll 4
-        for (int r = lane / kC; r < 32; r += 32 / kC) {
-            if (row0 + r >= rows) break;
-            float v = *reinterpret_cast<const float*>(stage + staged<kC>(r, c >> 2) + (c & 3) * 4);
-            const int64_t row = row0 + r;
-            if (old != nullptr) v = fmaf(alpha, to_f32(old[row * o.w.row + col]), v);
-            out[row * o.out.row + col] = from_f32<T>(v);
+            for (int r = lane / kC; r < 32; r += 32 / kC) {
+                if (row0 + r >= rows) break;
+                float v = *reinterpret_cast<const float*>(stage + staged<kC>(r, c >> 2) + (c & 3) * 4);
+                const int64_t row = row0 + r;
+                if (old != nullptr) v = fmaf(alpha, to_f32(old[row * o.w.row + col]), v);
+                out[row * o.out.row + col] = from_f32<T>(v);
+            }
+        } else {
+            constexpr int kStep = 32 / kC;
+            const int first = lane / kC, n = rows - row0 < 32 ? rows - row0 : 32;
+            T* to = out + (row0 + first) * o.out.row + col;
+            const T* from = old != nullptr ? old + (row0 + first) * o.w.row + col : nullptr;
+#pragma unroll 1
+            for (int r0 = first; r0 < n; r0 += kAtOnce * kStep) {
+                T had[kAtOnce];
+                float v[kAtOnce];
+                if (old != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) {
+                        if (r0 + i * kStep < n) had[i] = *from;
+                        from += kStep * o.w.row;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i)       // (the stage has 32 rows)
+                    v[i] = *reinterpret_cast<const float*>(stage + staged<kC>((r0 + i * kStep) & 31, c >> 2) + (c & 3) * 4);
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    if (old != nullptr) v[i] = fmaf(alpha, to_f32(had[i]), v[i]);
+                    if (r0 + i * kStep < n) *to = from_f32<T>(v[i]);
+                    to += kStep * o.out.row;
+                }
+            }
         }
     }
 }
-template <int kC>
+template <int kC, int kAtOnce>
 __device__ __forceinline__ void write_rows(float alpha, const Result& o, int b, int row0, int col0, int rows,
                                            int cols, const uint8_t* stage, int lane) {
-    if (o.out.type == MTTKRP_F32) write_rows_of<float, kC>(alpha, o, b, row0, col0, rows, cols, stage, lane);
-    else if (o.out.type == MTTKRP_BF16) write_rows_of<__nv_bfloat16, kC>(alpha, o, b, row0, col0, rows, cols, stage, lane);
-    else write_rows_of<__half, kC>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    if (o.out.type == MTTKRP_F32) write_rows_of<float, kC, kAtOnce>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    else if (o.out.type == MTTKRP_BF16) write_rows_of<__nv_bfloat16, kC, kAtOnce>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    else write_rows_of<__half, kC, kAtOnce>(alpha, o, b, row0, col0, rows, cols, stage, lane);
 }
 
 // ---- host

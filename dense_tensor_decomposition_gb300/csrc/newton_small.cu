@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
                                 make_float4(o.beta * (v[0] * by), o.beta * (v[1] * by), o.beta * (v[2] * by), o.beta * (v[3] * by));
                         }
                         __syncwarp();
-                        write_rows<32>(a.alpha, o, b, row0, first_col + c, shape.rows, shape.cols, stage, lane);
+                        write_rows<32, 1>(a.alpha, o, b, row0, first_col + c, shape.rows, shape.cols, stage, lane);
                     }
                 } else {
 #pragma unroll
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
                 const int i = warp >> 2, rows = warp & 1, cols = (warp >> 1) & 1;
                 const int row0 = (wide ? 0 : (t0 + first + i) * 64) + 32 * rows, col0 = (wide ? (t0 + first + i) * 64 : 0) + 32 * cols;
                 if (col0 < shape.cols && row0 < shape.rows)
-                    write_rows<32>(a.alpha, o, b, row0, col0, shape.rows, shape.cols,
+                    write_rows<32, 1>(a.alpha, o, b, row0, col0, shape.rows, shape.cols,
                                    x + (size_t)(first + i) * kPair + cols * kTileBytes + 4096 * rows, lane);
             }
         }
