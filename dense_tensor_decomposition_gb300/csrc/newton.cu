@@ -26,7 +26,15 @@
 // A launch does one product for all matrices of a list: a CTA (or a pair of CTAs that share one
 // tcgen05.mma, cta_group::2) takes tiles of the result in turn; a TMA thread fills a ring of
 // stages of 64 contraction indices, one thread issues MMAs into one of two accumulators in tensor
-// memory, eight warps drain the other one and write the result.
+// memory, eight or 16 warps drain the other one and write the result.  Which of the two forms
+// runs is the host's choice, product by product (see number_items).
+//
+// What bounds it, and measured (five steps, fp32 / bf16).  Large matrices: the tensor cores; 2 x
+// 4096 x 4096 in 5.4 / 2.6 ms, 1520 TFLOP/s of MMAs done in fp32 (three an fp32 product), 80 % of a
+// large library product's rate.  Tiles that do not fill the SMs a whole number of times:
+// 12 x 1024 x 4096 2.2 / 1.2 ms, 8 x 2048 x 1360 1.7 / 0.9 ms.  Few tiles: launches of 11 to 17 us of
+// which half is filling and draining; 3 x 512 x 2000 236 / 178 us.  Many small ones: epilogues and the
+// passes over U; 64 x 501 x 333 504 / 365 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -639,7 +647,10 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
     // (733 cycles a step for 512 of MMAs)
     constexpr int sub = !kFull && !is_update(kPhase) ? 2 : 1;
     constexpr int stages = 12 / (parts * sub);
-    constexpr int per_pass = kFull ? 2 : sub;   // steps between drains, or of a stage
+    // steps between drains, or of a stage: two in full, but one for items of few (a sum is cut off at every
+    // addition: 128 x 1833 with two 1.8 times as far off as fp32 products, with one 1.2)
+    constexpr int per_pass = kFull ? 2 : sub;
+    auto between = [&](int steps) { return kFull && steps <= 2 ? 1 : per_pass; };
     constexpr uint32_t step_bytes = (uint32_t)parts * kPart, stage_bytes = step_bytes * sub;
 
     if (threadIdx.x == 0) {
@@ -767,8 +778,9 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                     }
                 };
                 const int kb = from_step(w), ke = to_step(w);
-                for (int k0 = kb; k0 < ke && ok; k0 += per_pass) {
-                    const int here = min(per_pass, ke - k0);
+                const int per = between(ke - kb);
+                for (int k0 = kb; k0 < ke && ok; k0 += per) {
+                    const int here = min(per, ke - k0);
                     if ((kFull || k0 == kb) && ((zused >> z) & 1u)) {
                         if (!(ok = warp_wait(&zempty[z], (zphase >> z) & 1u, abort_flag, a.status, kStatusTimeoutMma))) break;
                         zphase ^= 1u << z;
@@ -852,7 +864,7 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
             if constexpr (kFull) {
                 float acc[kCols];
                 bool here = true;
-                const int drains = (to_step(w) - from_step(w) + per_pass - 1) / per_pass;
+                const int of_item = to_step(w) - from_step(w), drains = (of_item + between(of_item) - 1) / between(of_item);
                 for (int n = 0; n < drains; ++n) {
                     if (!(here = filled())) break;
                     // columns in flight: all, or what registers there are for
@@ -871,7 +883,7 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
                 }
                 if (!here && split == 1) break;         // (a cluster's barriers wait for all)
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) acc[e] = uncut(acc[e], short_of(8));
+                for (int e = 0; e < kCols; ++e) acc[e] = uncut(acc[e], of_item <= 2 ? short_of(4) : short_of(8));
                 if constexpr (kSplits) {
                     if (split > 1) {
                         add_up_split(a, place(item_of<kCtas, kPhase>(a, t)), smem, share, split, quad, part, lane, acc);

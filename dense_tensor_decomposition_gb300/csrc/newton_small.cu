@@ -7,7 +7,7 @@
 // A step: the slab's part of S = X X^T (every 64 indices from tensor memory into registers); the
 // parts added up over the cluster, each CTA some rows, and spread again; P, by every CTA; its
 // slab of P X, written over X.  S and P are whole (up to 128 x 128).  What a step costs is mostly
-// latency: XX us a step for 256 x 64.
+// latency: 33 us for five steps of 256 x 64, 5 us a step; 48 us for 128 x 128.
 //
 // One CTA an SM whatever the size (the launch asks for most of the shared memory): a second
 // one would wait for the tensor memory of the first, which may wait for its cluster.
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
 // and 64-127, columns 0-63 and 64-127), which are added up outside: a quarter of the MMAs, and the
 // small terms by themselves.  Warps of rows r and 64 + r change halves of what they have: a thread
 // ends up with 8 elements of one row, a piece of an image.  (A warp of its own for the MMAs leaves
-// 96 registers a thread: 51 us instead of XX for 256 x 64.)
+// 96 registers a thread, whose spills cost more than it gives.)
 template <int kC>
 __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_constant__ SmallArgs a) {
     constexpr uint32_t kPair = 2 * kTileBytes;
@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         parity ^= 1u << z;
         tc_fence_after();
     };
-    // the four quarters' terms of this thread's 8 elements (v), of kTiles tiles whose accumulators lie
-    // 128 columns apart, or of the sum over two tiles
-    auto gather = [&](uint32_t from, auto tiles_of_it, bool added, float* v) {
+    // the four quarters' terms of this thread's 8 elements (v), of kT tiles whose accumulators lie
+    // 128 columns apart, or (added) of the sum over two accumulators, or four
+    auto gather = [&](uint32_t from, auto tiles_of_it, int added, float* v) {
         constexpr int kT = decltype(tiles_of_it)::value;
         float all[kT][16];
         {
@@ -616,10 +616,19 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
 #pragma unroll
                 for (int e = 0; e < 16; ++e) all[i][e] = __uint_as_float(lead[i][e]) + __uint_as_float(rest[i][e]);
         }
-        const bool both = kT == 2 && added;
+        const bool both = kT == 2 && added > 0;
         if (both) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) all[0][e] += all[kT - 1][e];
+#pragma unroll 1
+            for (int i = kT; i < added; ++i) {
+                uint32_t lead[16], rest[16];
+                tmem_ld16(from + (uint32_t)(128 * i + 16 * part), lead);
+                tmem_ld16(from + (uint32_t)(128 * i + 64 + 16 * part), rest);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) all[0][e] += __uint_as_float(lead[e]) + __uint_as_float(rest[e]);
+            }
         }
         // rows r give away columns 8-15 of the 16 they have, rows 64 + r columns 0-7
 #pragma unroll
@@ -668,19 +677,21 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
     };
     const int m_slices = slices_of(m, 0);
     const float m_short = short_of(m_slices);
-    // tiles of the slab into one buffer of accumulators of S: additions
-    const float n_short = short_of(max(slices_of(n, 0), 4 * ((nt_most + 1) / 2) * (nt_most > 1)));
+    // accumulators of S, of two tiles each or few more: a sum is cut off at every addition (9 x 423 with four
+    // tiles in one: 1.5 times as far off as fp32 products, so 1.2); additions into one
+    const int apart = nt_most <= 4 ? 2 : 4;
+    const float n_short = nt_most > 1 ? short_of(4 * ((nt_most + apart - 1) / apart)) : short_of(slices_of(n, 0));
 
     for (int step = 0; step < a.steps; ++step) {
         const float ca = a.abc[3 * step], cb = a.abc[3 * step + 1], cc = a.abc[3 * step + 2];
-        // S: this slab's part, its tiles in turn into two buffers of accumulators
+        // S: this slab's part, its tiles in turn into the accumulators
         if (warp == 0) {
             tc_fence_after();
             for (int t = 0; t < nt; ++t) {
                 const uint32_t at = xa + (uint32_t)t * kPair;
                 const uint32_t o = wide ? sdesc128_lo(at) : sdesc128mn_lo(at);
-                multiply(tmem + (uint32_t)(t & 1) * 128u, o, wide ? 2u : 128u, o, wide ? 2u : 128u, slices_of(n, t0 + t),
-                         kDesc | kN128 | (wide ? 0u : kAMn | kBMn), t < 2 ? 0u : 1u);
+                multiply(tmem + (uint32_t)(t & (apart - 1)) * 128u, o, wide ? 2u : 128u, o, wide ? 2u : 128u, slices_of(n, t0 + t),
+                         kDesc | kN128 | (wide ? 0u : kAMn | kBMn), t < apart ? 0u : 1u);
             }
             commit<1>(&bars[0], leader);
         }
@@ -690,11 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         wait(0);
         if (nt > 1) {
             float v[16];
-            gather(lanes, kTwo, true, v);
+            gather(lanes, kTwo, min(apart, nt), v);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = v[e];
         } else if (nt == 1) {
-            gather(lanes, kOne, false, s);
+            gather(lanes, kOne, 0, s);
         }
         tc_fence_before();
         if constexpr (kC > 1) {
@@ -745,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         }
         wait(0);
         float p[8];
-        gather(lanes, kOne, false, p);
+        gather(lanes, kOne, 0, p);
         tc_fence_before();
         join8(*reinterpret_cast<const uint4*>(sp + own_piece), *reinterpret_cast<const uint4*>(sp + kTileBytes + own_piece), s);
 #pragma unroll
@@ -778,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
             const int first = pass * kAtOnce, count = min(kAtOnce, nt - first);
             const uint32_t from = lanes + (uint32_t)(pass & 1) * kHalfTmem;
             float v[16];
-            if (count == 2) gather(from, kTwo, false, v);
-            else gather(from, kOne, false, v);
+            if (count == 2) gather(from, kTwo, 0, v);
+            else gather(from, kOne, 0, v);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
                 if (i >= count) break;

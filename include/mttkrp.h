@@ -36,7 +36,9 @@
  * mode-n product (mttkrp_ttm) and Givens rotations along a mode
  * (mttkrp_apply_rotations).  For fitting on samples of entries instead of full
  * sweeps there are row lookups with their gradient, CP model entries with the
- * gradient of every factor, and clipping by the norm over many tensors.
+ * gradient of every factor, and clipping by the norm over many tensors; next to them orthogonal
+ * maps: rows rotated by their position (mttkrp_rotary) and matrices orthogonalised, alone or as a
+ * training step (mttkrp_orthogonalize, mttkrp_orthogonal_step).
  *
  * Errors: every int-returning call returns MTTKRP_OK (0) or one of the codes
  * below; nothing is thrown across the ABI.  mttkrp_strerror() names a code and
@@ -524,11 +526,15 @@ typedef struct mttkrp_matrices {
  * scales       one a list element, or NULL: 1.
  * Results in fp32 and fp16 are computed from products that are exact to about 2^-22 of their
  * terms; those in bf16 from products of the 11 leading bits but for X's: relative errors (in
- * the Frobenius norm) of about 1e-6 and 1.5e-3 at five steps of (3.4445, -4.775, 2.0315).
+ * the Frobenius norm) of about 2e-6 and 1.5e-3 at five steps of (3.4445, -4.775, 2.0315).
+ * Matrices with a side of at most 128 whose other side is not too long for the shared memory
+ * of eight SMs (5120 beside 64, 1536 beside 128) are done in one launch with the products of fp32
+ * whatever the result's type.  Which form of the kernels runs follows the list, so that the last
+ * bits of a result may depend on what else is in its call; a call repeats bit by bit.
  * A matrix with an infinite or NaN element becomes NaN; one of zeros stays zero.
  * workspace    device, 256-byte aligned, mttkrp_orthogonalize_workspace_bytes(n, in) bytes: 16
  *              to 32 bytes an element of up to 4 GB worth of matrices at a time.  0 for lists
- *              without elements and invalid ones.
+ *              of matrices that are done in one launch (above), without elements, or invalid.
  * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_WORKSPACE, MTTKRP_ERR_HOST_ALLOC, MTTKRP_ERR_CUDA.
  */
 size_t mttkrp_orthogonalize_workspace_bytes(int n, const mttkrp_matrices* in);
