@@ -94,6 +94,7 @@ struct PassArgs {
 
 // Sums of squares: a matrix in slices of consecutive groups of 8 columns, row by row, a slice
 // a CTA.
+template <bool kMomentum>
 __global__ void __launch_bounds__(kPassThreads) squares_kernel(const __grid_constant__ PassArgs a) {
     after_previous();
     const int k = element_of(a.n, blockIdx.x, [&](int i) { return a.source[i].first[0]; });
@@ -105,23 +106,22 @@ __global__ void __launch_bounds__(kPassThreads) squares_kernel(const __grid_cons
     const bool narrow = groups < INT32_MAX;
     const int64_t g0 = groups * slice / s.slices, g1 = groups * (slice + 1) / s.slices;
     Sum sum;
-    constexpr int kAhead = 4;
+    constexpr int kAhead = kMomentum ? 2 : 4;
     for (int64_t g = g0 + threadIdx.x; g < g1; g += kAhead * kPassThreads) {
-        float v[kAhead][8], kept[8];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
+        Raws<kAhead, kMomentum> raw;
+        raw.get(s, b, cols, [&](int i, int& r, int& c) {
             const int64_t x = g + i * kPassThreads;
-            if (x < g1) {
-                const int r = narrow ? (int)((uint32_t)x / (uint32_t)per) : (int)(x / per);
-                const int c = (int)(x - (int64_t)r * per) * 8;
-                update8(a.mu, a.nesterov, s, b, r, c, cols, v[i], kept);
-            } else {
+            r = narrow ? (int)((uint32_t)x / (uint32_t)per) : (int)(x / per);
+            c = (int)(x - (int64_t)r * per) * 8;
+            return x < g1;
+        });
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-            }
+        for (int i = 0; i < kAhead; i += 2) {
+            float v[2][8], kept[8];
+            raw.update(a.mu, a.nesterov, s, i, v[0], kept);
+            raw.update(a.mu, a.nesterov, s, i + 1, v[1], kept);
+            sum.squares16(v[0]);
         }
-#pragma unroll
-        for (int i = 0; i < kAhead; i += 2) sum.squares16(v[i]);
     }
     const Sum total = block_total<kPassThreads / 32>(sum);
     if (threadIdx.x == 0) a.partial[s.at + b * s.slices + slice] = Partial{total.hi, total.lo, total.wide};
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kPassThreads) squares_kernel(const __grid_cons
 // A CTA takes 64 rows of four column tiles: a warp reads and writes one row of them at a time.
 constexpr int kStrip = 4;
 
+template <bool kMomentum>
 __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_constant__ PassArgs a) {
     after_previous();
     const int k = element_of(a.n, blockIdx.x, [&](int i) { return a.source[i].first[1]; });
@@ -162,30 +163,30 @@ __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_const
     if (tj >= g.ct) return;
     uint8_t* const tile = a.tiles + ((int64_t)shape.base + (int64_t)b * g.tiles() + (int64_t)ti * g.ct + tj) * kTileBytes;
     const int64_t lo = (int64_t)g.x_lo() * kTileBytes;
-    constexpr int kAhead = 4;           // rows a thread has in flight
-#pragma unroll
+    constexpr int kAhead = kMomentum ? 2 : 4;       // rows a thread has in flight
+#pragma unroll 1
     for (int i0 = 0; i0 < 8; i0 += kAhead) {
-        float u[kAhead][8], kept[kAhead][8];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int row = ti * 64 + warp + 8 * (i0 + i);
-            if (row < shape.rows && c < shape.cols) {
-                update8(a.mu, a.nesterov, s, b, row, c, shape.cols, u[i], kept[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
-            }
-        }
+        Raws<kAhead, kMomentum> raw;
+        raw.get(s, b, shape.cols, [&](int i, int& r, int& col) {
+            r = ti * 64 + warp + 8 * (i0 + i);
+            col = c;
+            return r < shape.rows && c < shape.cols;
+        });
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int r = warp + 8 * (i0 + i), row = ti * 64 + r;
-            if (s.m.data != nullptr && row < shape.rows && c < shape.cols)
-                put8(s.out, b, row, c, shape.cols, kept[i]);
+            float u[8], kept[8];
+            raw.update(a.mu, a.nesterov, s, i, u, kept);
+            if (kMomentum && row < shape.rows && c < shape.cols) put8(s.out, b, row, c, shape.cols, kept);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                u[i][e] = row < shape.rows && c + e < shape.cols ? u[i][e] * factor.x * factor.y : 0.f;
+            for (int e = 0; e < 8; ++e) u[e] = u[e] * factor.x * factor.y;
+            // (a norm that is not a number spreads over the matrix, but not to what lies outside)
+            if (row >= shape.rows || c + 8 > shape.cols) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = row < shape.rows && c + e < shape.cols ? u[e] : 0.f;
+            }
             uint4 vh, vl;
-            split8(u[i], vh, vl);
+            split8(u, vh, vl);
             *reinterpret_cast<uint4*>(tile + piece(r, lane & 7)) = vh;
             *reinterpret_cast<uint4*>(tile + lo + piece(r, lane & 7)) = vl;
         }
@@ -1131,8 +1132,8 @@ cudaError_t run_group(const NewtonArgs& a, int used, const Part* parts, int64_t 
         if (r.out.type != MTTKRP_BF16) full = true;
     }
     if (!tile_map(&p.map, p.tiles, (uint64_t)tiles * 64)) return cudaErrorUnknown;
-    cudaError_t e = launch_clusters(squares_kernel, (unsigned)sums, kPassThreads, 0, 1, s, pass);
-    if (e == cudaSuccess) e = launch_clusters(images_kernel, strips, kPassThreads, 0, 1, s, pass);
+    cudaError_t e = launch_clusters(a.momentum != nullptr ? squares_kernel<true> : squares_kernel<false>, (unsigned)sums, kPassThreads, 0, 1, s, pass);
+    if (e == cudaSuccess) e = launch_clusters(a.momentum != nullptr ? images_kernel<true> : images_kernel<false>, strips, kPassThreads, 0, 1, s, pass);
     for (int step = 0; step < a.steps && e == cudaSuccess; ++step) {
         p.from = step & 1;
         p.a = a.coefficients[3 * step];

@@ -33,53 +33,93 @@ struct Store {
     uint8_t type, whole;        // whole: eight elements from a multiple of eight on are aligned to 16 bytes
 };
 
-template <typename T>
-__device__ __forceinline__ void get8_of(const Store& s, int64_t at, int valid, float* v) {
-    const T* p = static_cast<const T*>(s.data) + at;
-    if (s.whole && valid >= 8) {
-        constexpr int kVec = 16 / sizeof(T);
-#pragma unroll
-        for (int k = 0; k < 8 / kVec; ++k) {
-            const uint4 bits = reinterpret_cast<const uint4*>(p)[k];    // (a reference to memory would be copied by bytes)
-            const auto w = as_pack<Pack<T, kVec>>(bits);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) v[k * kVec + e] = to_f32(w.v[e]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < valid ? to_f32(p[e]) : 0.f;
-    }
+// Eight consecutive elements of a row as they lie in memory: 32 bytes, or 16 in x.
+struct Raw8 {
+    uint4 x, y;
+};
+// Those of row r from column c on; zeros from `cols` on.  (One piece of code for all types, which differ
+// in how much of it they use: a copy a type is more instructions than the cache holds for as long as a
+// kernel of a few microseconds runs.)  fast: all eight are there and aligned, or nothing is to be read (in).
+__device__ __forceinline__ Raw8 raw_fast(const Store& s, bool in, int64_t b, int r, int c) {
+    const bool wide = s.type == MTTKRP_F32;
+    const uint8_t* p = static_cast<const uint8_t*>(s.data) + ((b * s.batch + r * s.row + c) << (wide ? 2 : 1));
+    Raw8 w;
+    w.x = w.y = make_uint4(0u, 0u, 0u, 0u);
+    if (in) w.x = *reinterpret_cast<const uint4*>(p);
+    if (in && wide) w.y = *reinterpret_cast<const uint4*>(p + 16);
+    return w;
 }
-// eight elements of row r from column c on, zeros from `cols` on
-__device__ __forceinline__ void get8(const Store& s, int64_t b, int r, int c, int cols, float* v) {
+__device__ __forceinline__ Raw8 raw_any(const Store& s, bool in, int64_t b, int r, int c, int cols) {
+    if (s.whole && c + 8 <= cols) return raw_fast(s, in, b, r, c);
+    const int valid = in ? cols - c : 0;
     const int64_t at = b * s.batch + r * s.row + c;
-    if (s.type == MTTKRP_F32) get8_of<float>(s, at, cols - c, v);
-    else if (s.type == MTTKRP_BF16) get8_of<__nv_bfloat16>(s, at, cols - c, v);
-    else get8_of<__half>(s, at, cols - c, v);
+    uint32_t w[8];
+    if (s.type == MTTKRP_F32) {
+        const uint32_t* p = static_cast<const uint32_t*>(s.data) + at;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = e < valid ? p[e] : 0u;
+        return Raw8{make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+    }
+    const uint16_t* p = static_cast<const uint16_t*>(s.data) + at;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = e < valid ? (uint32_t)p[e] : 0u;
+    return Raw8{make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16),
+                make_uint4(0u, 0u, 0u, 0u)};
 }
-template <typename T>
-__device__ __forceinline__ void put8_of(const Store& s, int64_t at, int valid, const float* v) {
-    T* p = static_cast<T*>(s.data) + at;
-    if (s.whole && valid >= 8) {
-        constexpr int kVec = 16 / sizeof(T);
+__device__ __forceinline__ void values(uint8_t type, const Raw8& w, float* v) {
+    const uint32_t x[4] = {w.x.x, w.x.y, w.x.z, w.x.w}, y[4] = {w.y.x, w.y.y, w.y.z, w.y.w};
+    if (type == MTTKRP_F32) {
 #pragma unroll
-        for (int k = 0; k < 8 / kVec; ++k) {
-            Pack<T, kVec> w;
+        for (int e = 0; e < 4; ++e) {
+            v[e] = __uint_as_float(x[e]);
+            v[4 + e] = __uint_as_float(y[e]);
+        }
+    } else if (type == MTTKRP_BF16) {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) w.v[e] = from_f32<T>(v[k * kVec + e]);
-            reinterpret_cast<uint4*>(p)[k] = as_pack<uint4>(w);
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(x[e] << 16);
+            v[2 * e + 1] = __uint_as_float(x[e] & 0xFFFF0000u);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < valid) p[e] = from_f32<T>(v[e]);
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+        }
     }
 }
 __device__ __forceinline__ void put8(const Store& s, int64_t b, int r, int c, int cols, const float* v) {
     const int64_t at = b * s.batch + r * s.row + c;
-    if (s.type == MTTKRP_F32) put8_of<float>(s, at, cols - c, v);
-    else if (s.type == MTTKRP_BF16) put8_of<__nv_bfloat16>(s, at, cols - c, v);
-    else put8_of<__half>(s, at, cols - c, v);
+    const int valid = cols - c;
+    if (s.type == MTTKRP_F32) {
+        float* p = static_cast<float*>(s.data) + at;
+        if (s.whole && valid >= 8) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < valid) p[e] = v[e];
+        }
+        return;
+    }
+    uint32_t w[4];
+    const bool bf16 = s.type == MTTKRP_BF16;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 f = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = bf16 ? *reinterpret_cast<const uint32_t*>(&f) : *reinterpret_cast<const uint32_t*>(&h);
+    }
+    uint16_t* p = static_cast<uint16_t*>(s.data) + at;
+    if (s.whole && valid >= 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < valid) p[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+    }
 }
 
 // eight scaled values as hi and lo
@@ -142,19 +182,45 @@ __device__ __forceinline__ int element_of(int n, uint32_t x, F first) {
     return lo;
 }
 
-// U of eight elements and, where there is momentum, what it becomes
-__device__ __forceinline__ void update8(float mu, bool nesterov, const Source& s, int b, int r, int c, int cols, float* u,
-                                        float* kept) {
-    get8(s.g, b, r, c, cols, u);
-    if (s.m.data != nullptr) {
-        get8(s.m, b, r, c, cols, kept);
+// Eight elements each of the gradient and, where there is one, the momentum, of kN places: first what is in
+// memory, all of it in flight, then U and what the momentum becomes.  place(i, r, c): whether there is
+// an i-th place, and its row and column.  kMomentum: whether there may be one.
+template <int kN, bool kMomentum = true>
+struct Raws {
+    Raw8 g[kN], m[kMomentum ? kN : 1];
+    template <typename F>
+    __device__ __forceinline__ void get(const Source& s, int b, int cols, F place) {
+        const bool momentum = kMomentum && s.m.data != nullptr;
+        if (s.g.whole && (!momentum || s.m.whole) && cols % 8 == 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            kept[e] = fmaf(mu, kept[e], u[e]);
-            u[e] = nesterov ? fmaf(mu, kept[e], u[e]) : kept[e];
+            for (int i = 0; i < kN; ++i) {
+                int r = 0, c = 0;
+                const bool in = place(i, r, c);
+                g[i] = raw_fast(s.g, in, b, r, c);
+                if constexpr (kMomentum) m[i] = raw_fast(s.m, in && momentum, b, r, c);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+                int r = 0, c = 0;
+                const bool in = place(i, r, c);
+                g[i] = raw_any(s.g, in, b, r, c, cols);
+                if (kMomentum && momentum) m[kMomentum ? i : 0] = raw_any(s.m, in, b, r, c, cols);
+            }
         }
     }
-}
+    __device__ __forceinline__ void update(float mu, bool nesterov, const Source& s, int i, float* u, float* kept) const {
+        values(s.g.type, g[i], u);
+        if (kMomentum && s.m.data != nullptr) {
+            values(s.m.type, m[kMomentum ? i : 0], kept);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                kept[e] = fmaf(mu, kept[e], u[e]);
+                u[e] = nesterov ? fmaf(mu, kept[e], u[e]) : kept[e];
+            }
+        }
+    }
+};
 
 // factors whose product is 2^12 / (|U| + eps); two, as one may leave fp32's range
 __device__ __forceinline__ float2 factors(const Sum& total, double eps) {

@@ -142,19 +142,15 @@ __device__ __forceinline__ void load_slab(const A& a, const Shape& shape, const 
     constexpr int kAhead = 4;
     float u[kAhead][8], kept[kAhead][8];
     auto read = [&](int g0) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            int row = 0, col = 0;
+        Raws<kAhead> raw;
+        raw.get(src, b, shape.cols, [&](int i, int& row, int& col) {
             uint32_t at;
             const int g = g0 + i * kThreads;
             if (g < groups) locate(g, row, col, at);
-            if (g < groups && row < shape.rows && col < shape.cols) {
-                update8(a.mu, a.nesterov, src, b, row, col, shape.cols, u[i], kept[i]);
-            } else {
+            return g < groups && row < shape.rows && col < shape.cols;
+        });
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[i][e] = 0.f;
-            }
-        }
+        for (int i = 0; i < kAhead; ++i) raw.update(a.mu, a.nesterov, src, i, u[i], kept[i]);
     };
     Sum sum;
     for (int g0 = threadIdx.x; g0 < groups; g0 += kAhead * kThreads) {
