@@ -482,7 +482,7 @@ __device__ __forceinline__ void write_block(const ProductArgs& a, const Place& a
                 *reinterpret_cast<float4*>(stage + staged<kC>(lane, q)) = v;
             }
             __syncwarp();
-            write_rows<kC, 4>(a.alpha, o, at.b, at.ti * 64 + at.r0, j * 64 + c, at.rows, at.cols, stage, lane);
+            write_rows<kC, 4, !kFull>(a.alpha, o, at.b, at.ti * 64 + at.r0, j * 64 + c, at.rows, at.cols, stage, lane);
         }
     } else {
 #pragma unroll

@@ -89,6 +89,11 @@ __device__ __forceinline__ void values(uint8_t type, const Raw8& w, float* v) {
         }
     }
 }
+__device__ __forceinline__ uint32_t pair16(bool bf16, float a, float b) {
+    const __nv_bfloat162 f = __floats2bfloat162_rn(a, b);
+    const __half2 h = __floats2half2_rn(a, b);
+    return bf16 ? *reinterpret_cast<const uint32_t*>(&f) : *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ void put8(const Store& s, int64_t b, int r, int c, int cols, const float* v) {
     const int64_t at = b * s.batch + r * s.row + c;
     const int valid = cols - c;
@@ -107,11 +112,7 @@ __device__ __forceinline__ void put8(const Store& s, int64_t b, int r, int c, in
     uint32_t w[4];
     const bool bf16 = s.type == MTTKRP_BF16;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 f = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-        const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-        w[e] = bf16 ? *reinterpret_cast<const uint32_t*>(&f) : *reinterpret_cast<const uint32_t*>(&h);
-    }
+    for (int e = 0; e < 4; ++e) w[e] = pair16(bf16, v[2 * e], v[2 * e + 1]);
     uint16_t* p = static_cast<uint16_t*>(s.data) + at;
     if (s.whole && valid >= 8) {
         *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -244,18 +245,44 @@ __device__ __forceinline__ uint32_t staged(int r, int q) {
     return kC == 32 ? piece(r, q) : (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
 }
 
+// one element, and four, of a type of 32 bits or of either of 16
+__device__ __forceinline__ float get1(float x, bool) { return x; }
+__device__ __forceinline__ float get1(uint16_t x, bool bf16) {
+    return bf16 ? __uint_as_float((uint32_t)x << 16) : __half2float(__ushort_as_half(x));
+}
+__device__ __forceinline__ void put1(float* p, bool, float v) { *p = v; }
+__device__ __forceinline__ void put1(uint16_t* p, bool bf16, float v) {
+    *p = bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ void get4(const uint4& x, bool, float* v) {
+    v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y), v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
+}
+__device__ __forceinline__ void get4(const uint2& x, bool bf16, float* v) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x.x));
+    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&x.y));
+    v[0] = bf16 ? __uint_as_float(x.x << 16) : f.x, v[1] = bf16 ? __uint_as_float(x.x & 0xFFFF0000u) : f.y;
+    v[2] = bf16 ? __uint_as_float(x.y << 16) : g.x, v[3] = bf16 ? __uint_as_float(x.y & 0xFFFF0000u) : g.y;
+}
+__device__ __forceinline__ void put4(uint4* p, bool, const float* v) {
+    *p = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ void put4(uint2* p, bool bf16, const float* v) {
+    *p = make_uint2(pair16(bf16, v[0], v[1]), pair16(bf16, v[2], v[3]));
+}
+
 // Writes them (beta O(U)) to a result, after adding alpha W: whole rows of the stage at a time, or
 // where rows are not aligned a column a lane, the old values of kAtOnce rows in flight.  (Four: 64 bf16
 // steps of 501 x 333 take 463 us, one row at a time 576; but the registers cost newton_small.cu's
 // kernels 3 us whatever they write: one there.)
-template <typename T, int kC, int kAtOnce>
+// (T: float, or uint16_t for either type of 16 bits; kBf16: that it is bf16)
+template <typename T, int kC, int kAtOnce, bool kBf16>
 __device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int b, int row0, int col0, int rows,
                                               int cols, const uint8_t* stage, int lane) {
+    const bool bf16 = kBf16 || o.out.type == MTTKRP_BF16;
     T* const out = static_cast<T*>(o.out.data) + b * o.out.batch;
     const T* const old = o.w.data != nullptr ? static_cast<const T*>(o.w.data) + b * o.w.batch : nullptr;
     if (o.out.whole && (old == nullptr || o.w.whole) && col0 + kC <= cols) {
         using B = typename Bits<4 * sizeof(T)>::type;
-        using P = Pack<T, 4>;
         constexpr int kLanes = kC / 4, kStep = 32 / kLanes;
         const int q = lane % kLanes, col = col0 + 4 * q;
         B had[kLanes];
@@ -273,14 +300,12 @@ __device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int 
             const float4 f = *reinterpret_cast<const float4*>(stage + staged<kC>(r, q));
             float v[4] = {f.x, f.y, f.z, f.w};
             if (old != nullptr) {
-                const P p = as_pack<P>(had[i]);
+                float w[4];
+                get4(had[i], bf16, w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fmaf(alpha, to_f32(p.v[e]), v[e]);
+                for (int e = 0; e < 4; ++e) v[e] = fmaf(alpha, w[e], v[e]);
             }
-            P p;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) p.v[e] = from_f32<T>(v[e]);
-            *reinterpret_cast<B*>(out + row * o.out.row + col) = as_pack<B>(p);
+            put4(reinterpret_cast<B*>(out + row * o.out.row + col), bf16, v);
         }
     } else {
         const int c = lane % kC, col = col0 + c;
@@ -291,8 +316,8 @@ __device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int 
                 if (row0 + r >= rows) break;
                 float v = *reinterpret_cast<const float*>(stage + staged<kC>(r, c >> 2) + (c & 3) * 4);
                 const int64_t row = row0 + r;
-                if (old != nullptr) v = fmaf(alpha, to_f32(old[row * o.w.row + col]), v);
-                out[row * o.out.row + col] = from_f32<T>(v);
+                if (old != nullptr) v = fmaf(alpha, get1(old[row * o.w.row + col], bf16), v);
+                put1(out + row * o.out.row + col, bf16, v);
             }
         } else {
             constexpr int kStep = 32 / kC;
@@ -315,20 +340,21 @@ __device__ __forceinline__ void write_rows_of(float alpha, const Result& o, int 
                     v[i] = *reinterpret_cast<const float*>(stage + staged<kC>((r0 + i * kStep) & 31, c >> 2) + (c & 3) * 4);
 #pragma unroll
                 for (int i = 0; i < kAtOnce; ++i) {
-                    if (old != nullptr) v[i] = fmaf(alpha, to_f32(had[i]), v[i]);
-                    if (r0 + i * kStep < n) *to = from_f32<T>(v[i]);
+                    if (old != nullptr) v[i] = fmaf(alpha, get1(had[i], bf16), v[i]);
+                    if (r0 + i * kStep < n) put1(to, bf16, v[i]);
                     to += kStep * o.out.row;
                 }
             }
         }
     }
 }
-template <int kC, int kAtOnce>
+template <int kC, int kAtOnce, bool kBf16 = false>
 __device__ __forceinline__ void write_rows(float alpha, const Result& o, int b, int row0, int col0, int rows,
                                            int cols, const uint8_t* stage, int lane) {
-    if (o.out.type == MTTKRP_F32) write_rows_of<float, kC, kAtOnce>(alpha, o, b, row0, col0, rows, cols, stage, lane);
-    else if (o.out.type == MTTKRP_BF16) write_rows_of<__nv_bfloat16, kC, kAtOnce>(alpha, o, b, row0, col0, rows, cols, stage, lane);
-    else write_rows_of<__half, kC, kAtOnce>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    if (!kBf16 && o.out.type == MTTKRP_F32)
+        write_rows_of<float, kC, kAtOnce, false>(alpha, o, b, row0, col0, rows, cols, stage, lane);
+    else
+        write_rows_of<uint16_t, kC, kAtOnce, kBf16>(alpha, o, b, row0, col0, rows, cols, stage, lane);
 }
 
 // ---- host
