@@ -32,9 +32,9 @@
 // What bounds it, and measured (five steps, fp32 / bf16).  Large matrices: the tensor cores; 2 x
 // 4096 x 4096 in 5.4 / 2.6 ms, 1520 TFLOP/s of MMAs done in fp32 (three an fp32 product), 80 % of a
 // large library product's rate.  Tiles that do not fill the SMs a whole number of times:
-// 12 x 1024 x 4096 2.2 / 1.2 ms, 8 x 2048 x 1360 1.7 / 0.9 ms.  Few tiles: launches of 11 to 17 us of
-// which half is filling and draining; 3 x 512 x 2000 236 / 178 us.  Many small ones: epilogues and the
-// passes over U; 64 x 501 x 333 504 / 365 us.
+// 12 x 1024 x 4096 2.2 / 1.15 ms, 8 x 2048 x 1360 1.67 / 0.85 ms.  Few tiles: launches of 11 to 17 us of
+// which half is filling and draining; 3 x 512 x 2000 227 / 167 us.  Many small ones: epilogues and the
+// passes over U; 64 x 501 x 333 485 / 339 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>

@@ -107,3 +107,39 @@ def test_the_example_with_orthogonalised_updates_repeats():
     for a, g, b in zip(start, grads, one):
         want, _ = oo.step(a.double().cpu(), g.double().cpu(), np.zeros(g.shape), 0.02, 0.9, True, 0.0, 1.0, 5, mk.QUINTIC)
         assert np.linalg.norm(b.double().cpu().numpy() - want) <= 0.02 * 1e-4 * 6 ** 0.5 + 4 * U * np.linalg.norm(want)
+
+
+def test_two_graphs_at_once():
+    """Two captured graphs of all operators, replayed beside one another and beside eager calls, with results of
+    their own: workspaces are not shared."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    f = mk.rotary_frequencies(16)
+    shapes = [(300, 200), (64, 40), (100, 500), (257, 1033)]
+    sets = []
+    for _ in range(3):
+        x = torch.randn(2, 50, 3, 17, generator=gen, device="cuda")
+        p = torch.randint(0, 1000, (2, 50), generator=gen, device="cuda")
+        gs = [torch.randn(s, generator=gen, device="cuda") for s in shapes]
+        sets.append((x, p, gs))
+
+    def run(x, p, gs):
+        return [mk.rotary(x, p, f, True)] + mk.orthogonalize(gs) + mk.orthogonalize(gs, dtype=torch.bfloat16)
+
+    want = [run(*s) for s in sets]
+    graphs, got = [], []
+    for s in sets[:2]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(run(*s))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    eager = []
+    for _ in range(5):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager.append(run(*sets[2]))
+    torch.cuda.synchronize()
+    for a, b in zip(got + eager, want[:2] + 5 * [want[2]]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

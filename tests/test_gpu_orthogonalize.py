@@ -383,3 +383,39 @@ def test_refusals():
         with pytest.raises(kind):
             bad()
     assert torch.equal(x, torch.ones(6, 4, device="cuda"))
+
+
+@pytest.mark.parametrize("weights,grads,momenta", MOMENTA)
+@pytest.mark.parametrize("rows,cols,ahead", [(201, 333, 0), (333, 201, 3), (150, 264, 1), (264, 150, 0), (130, 136, 8)])
+def test_step_at_odd_offsets(rows, cols, ahead, weights, grads, momenta):
+    """Matrices with sides above 128 whose rows lie at any offset (and, in the last shape, aligned), in parts of
+    wider ones: the new weight is the old one and the update, each rounded as the formula says."""
+    gen = generator(rows + cols)
+
+    def part(x, dtype):
+        room = torch.full((rows, ahead + cols + 2), 3.0, device="cuda", dtype=dtype)
+        view = room[:, ahead:ahead + cols]
+        view.copy_(x)
+        return room, view
+
+    room_g, g = part(gradient(gen, (rows, cols)).mul(1e-3), TYPES[grads])
+    room_m, m = part(gradient(gen, (rows, cols)).mul(5e-3), TYPES[momenta])
+    room_w, w = part(torch.randn(rows, cols, generator=gen, device="cuda").mul(0.02), TYPES[weights])
+    before_w, before_m, before_g = f64(w), f64(m), f64(g)
+    by = max(1.0, rows / cols) ** 0.5
+    mk.orthogonal_step(w, g, m, 0.02, momentum=0.9, weight_decay=0.1)
+    want, want_m = oo.step(before_w, before_g, before_m, 0.02, 0.9, True, 0.1, by, 5, mk.QUINTIC)
+    size = 0.9 * np.abs(before_m) + np.abs(before_g)
+    assert np.all(np.abs(f64(m) - want_m) <= 2.0 ** -23 * size + UNIT[m.dtype] * 1.01 * np.abs(want_m) + 2.0 ** -25)
+    u = before_g + 0.9 * (0.9 * before_m + before_g)
+    bound, o = trajectory_bound(u, 5, mk.QUINTIC, 2.0 ** -11 if weights == "bfloat16" else 2.0 ** -20)
+    bound += 4.25 ** 5 * 2.0 ** -23
+    size = np.linalg.norm(before_w) + 0.02 * by * np.linalg.norm(o)
+    err = np.linalg.norm(f64(w) - want)
+    assert err <= 0.02 * by * bound + 2.0 ** -22 * size + UNIT[w.dtype] * np.linalg.norm(want)
+    # each element near its own, so that none is misplaced: half of what 2 % of an update's typical element is
+    typical = 0.02 * by / np.sqrt(max(rows, cols))
+    assert np.abs(f64(w) - want).max() <= 0.5 * typical + UNIT[w.dtype] * 1.01 * np.abs(want).max()
+    assert np.array_equal(f64(g), before_g)
+    for room in (room_g, room_m, room_w):
+        assert (room[:, :ahead] == 3).all() and (room[:, ahead + cols:] == 3).all()
