@@ -155,7 +155,7 @@ __device__ __forceinline__ void join8(const uint4& hi, const uint4& lo, float* v
 __host__ __device__ constexpr float short_of(int n) { return 0x1.2p-23f / 5.f * (float)(n + 1); }
 
 // That put back, where the sum's last three bits show that it was rounded at all, so that sums of
-// few bits stay exact.  What five steps leave is then within 1.4 of the error of fp32 products, else up
+// few bits stay exact.  What five steps leave is then within 1.6 of the error of fp32 products, else up
 // to twice.
 __device__ __forceinline__ float uncut(float v, float share) {
     return (__float_as_uint(v) & 7u) != 0u ? fmaf(v, share, v) : v;
