@@ -27,7 +27,7 @@
 // tcgen05.mma, cta_group::2) takes tiles of the result in turn; a TMA thread fills a ring of
 // stages of 64 contraction indices, one thread issues MMAs into one of two accumulators in tensor
 // memory, eight or 16 warps drain the other one and write the result.  Which of the two forms
-// runs is the host's choice, product by product (see number_items).
+// runs is the host's choice, product by product (number_items, newton_plan.h).
 //
 // What bounds it, and measured (five steps, fp32 / bf16).  Large matrices: the tensor cores; 2 x
 // 4096 x 4096 in 5.4 / 2.6 ms, 1520 TFLOP/s of MMAs done in fp32 (three an fp32 product), 80 % of a
@@ -41,11 +41,11 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cmath>
 
 #include "launch.cuh"
 #include "newton.cuh"
 #include "newton.h"
+#include "newton_plan.h"
 
 namespace mk {
 namespace {
@@ -55,23 +55,6 @@ constexpr int64_t kGroupTiles = (int64_t)4 << 17;   // 4 GB of images a group (o
 
 constexpr int kEpiWarp0 = 4;
 constexpr int kPassThreads = 256;
-
-// what a launch computes: S, P (from S S), P X, and the last P X, whose result goes to the caller
-enum Phase { kGram, kSquare, kUpdate, kResult };
-__host__ __device__ constexpr bool is_update(int phase) { return phase >= kUpdate; }
-
-struct Grid {
-    int rt, ct, mt;             // tiles of 64 along rows, columns and the smaller side
-    bool wide;
-    __host__ __device__ explicit Grid(const Shape& s)
-        : rt(tiles_of(s.rows)), ct(tiles_of(s.cols)), mt(s.rows <= s.cols ? rt : ct), wide(s.rows <= s.cols) {}
-    __host__ __device__ int x(int which) const { return 2 * which * rt * ct; }
-    __host__ __device__ int x_lo() const { return rt * ct; }
-    __host__ __device__ int s() const { return 4 * rt * ct; }
-    __host__ __device__ int p() const { return s() + 2 * mt * mt; }
-    __host__ __device__ int s_lo() const { return mt * mt; }
-    __host__ __device__ int tiles() const { return 4 * (rt * ct + mt * mt); }
-};
 
 // ---------------------------------------------------------------- the passes over U
 
@@ -195,13 +178,6 @@ __global__ void __launch_bounds__(kPassThreads) images_kernel(const __grid_const
 
 // ---------------------------------------------------------------- the products
 
-// Work items of a symmetric result of nb x nb blocks: rows of blocks from the block of 256 they are in on.
-__host__ __device__ inline int symmetric_items(int nb, int ctas) {
-    if (ctas == 2) return nb * (nb + 1) / 2;
-    const int pairs = nb / 2;           // rows 2 p and 2 p + 1 have nb - 2 p items each
-    return pairs * (2 * nb - 2 * pairs + 2) + (nb % 2);
-}
-
 struct ProductArgs {
     CUtensorMap map;            // the workspace's tiles as rows of 128 bytes
     int n;
@@ -261,7 +237,7 @@ __device__ __forceinline__ Item item_of(const ProductArgs& a, uint32_t t) {
             ++w.i;
         }
         w.j = (w.i * kBlock / kSymBlock) * (kSymBlock / kBlock) + r;
-        w.steps = kPhase == kSquare ? g.mt : g.wide ? g.ct : g.rt;
+        w.steps = g.steps(kPhase);
     }
     w.i *= kBlock;
     w.j *= kBlock;
@@ -686,8 +662,8 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
     after_previous();
 
     const uint32_t first = blockIdx.x / (uint32_t)(kCtas * split), stride = gridDim.x / (uint32_t)(kCtas * split);
-    auto from_step = [&](const Item& w) { return kSplits ? w.steps * share / split : 0; };
-    auto to_step = [&](const Item& w) { return kSplits ? w.steps * (share + 1) / split : w.steps; };
+    auto from_step = [&](const Item& w) { return kSplits ? share_begin(w.steps, share, split) : 0; };
+    auto to_step = [&](const Item& w) { return kSplits ? share_begin(w.steps, share + 1, split) : w.steps; };
     if (warp < kEpiWarp0) {
     if constexpr (R::kMany) regs_dec<R::kCtl>();
     if (warp == 0) {
@@ -863,7 +839,7 @@ __global__ void __launch_bounds__(Roles<kCtas, kFull>::kThreads, 1) product_kern
             };
             Lines s;
             if constexpr (kFull) {
-                float acc[kCols];
+                float acc[kCols] = {};
                 bool here = true;
                 const int of_item = to_step(w) - from_step(w), drains = (of_item + between(of_item) - 1) / between(of_item);
                 for (int n = 0; n < drains; ++n) {
@@ -1037,39 +1013,6 @@ cudaError_t device(Device& d) {
     if (e == cudaSuccess) e = allow<2, true>();
     if (e == cudaSuccess && dev < 64) known[dev] = d.sms;
     return e;
-}
-
-// Numbers the work items of a product whose CTAs (or pairs) take blocks of 128 (256) a side, and
-// says how long it takes, in microseconds without the launch: waves of items, whose epilogues run
-// beside the next one's MMAs.  Steps of 64 indices and epilogues as measured on 12 x 1024 x 4096,
-// 2 x 4096 x 4096 and 3 x 512 x 2000; a pair's items are four times a CTA's.
-constexpr float kExchange = 2.5f;       // microseconds that a cluster takes to add up its parts of S
-
-float number_items(ProductArgs& p, int phase, int ctas, bool full, int sms) {
-    const int f = is_update(phase) ? 1 : 0, block = 2 * ctas;
-    const float step = full ? (ctas == 2 ? 1.02f : 0.72f) : f ? (ctas == 2 ? 0.61f : 0.52f) : (ctas == 2 ? 0.33f : 0.26f);
-    const float end = (phase == kSquare ? (ctas == 2 ? 8.f : 4.f) : (ctas == 2 ? 4.f : 2.f));
-    float work = 0.f, longest = 0.f;
-    p.items = 0;
-    for (int i = 0; i < p.n; ++i) {
-        Shape& s = p.shape[i];
-        const Grid g(s);
-        s.first[f] = p.items;
-        const int64_t items = f ? s.count * cdiv(g.rt, block) * cdiv(g.ct, block)
-                                : s.count * (int64_t)symmetric_items((int)cdiv(g.mt, block), ctas);
-        const float steps = (float)(phase == kGram ? (g.wide ? g.ct : g.rt) : g.mt);
-        const float one = std::max(steps * step, end);
-        work += (float)items * one;
-        longest = std::max(longest, one);
-        p.items += (uint32_t)items;
-    }
-    // S by single CTAs, where they are fewer than half of the SMs: two or four an item, with steps enough each
-    p.split = 1;
-    if (phase == kGram && ctas == 1)
-        while (p.split < 4 && p.items * p.split * 2 <= (uint32_t)sms && longest / (2 * p.split) > kExchange) p.split *= 2;
-    const float units = (float)(sms / ctas), waves = std::ceil((float)p.items / units);
-    if (p.split > 1) return longest / (float)p.split + kExchange + end;
-    return std::max(longest, waves * work / (float)p.items) + end;
 }
 
 // Tensor map of the images: rows of 128 bytes, loaded 64 at a time as they are.

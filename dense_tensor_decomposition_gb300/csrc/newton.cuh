@@ -7,24 +7,15 @@
 #include <cstdint>
 
 #include "mttkrp.h"
+#include "newton_plan.h"
 #include "ptx.cuh"
 #include "squares.cuh"
 #include "types.cuh"
 
 namespace mk {
 
-constexpr int kTable = 32;                  // list elements a group of launches
 constexpr uint32_t kTileBytes = 8192;
 constexpr float kScale = 4096.f, kUnscale = 1.f / 4096.f;   // of the images
-
-// Matrices of one list element.  Tiles of one matrix, hi and lo of each: X twice (a step
-// reads one and writes the other), S, P.
-struct Shape {
-    int base;                   // first tile
-    int rows, cols, count;
-    uint32_t first[2];          // number of the first work item: of S and S S, of P X
-};
-__host__ __device__ inline int tiles_of(int n) { return (n + 63) / 64; }
 
 // Rows of a matrix in its own memory.
 struct Store {

@@ -1,0 +1,59 @@
+"""GPU orthogonalisation of lists of unlike matrices, whose products are dealt out together: every
+matrix as the formula says, whatever else is in its call.
+
+Whole numbers as in the tests of single matrices: G of 4^q entries +-1 has the norm 2^q, and S and S X are
+whole numbers over powers of two, exact in the parts' bits and in the sums, so that results are
+compared bit by bit after one rounding to their type."""
+import numpy as np
+import pytest
+
+from oracle import orthogonal as oo
+
+torch = pytest.importorskip("torch")
+import dense_tensor_decomposition_gb300 as mk  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"float32": torch.float32, "bfloat16": torch.bfloat16, "float16": torch.float16}
+
+
+def signs(seed, rows, cols, q):
+    """4^q entries +-1, the others 0."""
+    rng = np.random.default_rng(seed)
+    g = np.zeros(rows * cols)
+    g[rng.choice(rows * cols, 4 ** q, replace=False)] = rng.choice([-1.0, 1.0], 4 ** q)
+    return g.reshape(rows, cols)
+
+
+def cuda(a, dtype=torch.float32):
+    return torch.from_numpy(np.ascontiguousarray(a)).to("cuda", dtype)
+
+
+# a long matrix, whose S is split over the CTAs of a cluster, with ones of three steps
+UNLIKE = [[(512, 2000), (160, 160)], [(2000, 150), (150, 150), (150, 150)], [(768, 1024), (192, 192)],
+          [(2500, 160), (160, 160)], [(512, 4096), (150, 150)], [(256, 1000), (129, 192), (192, 130)],
+          [(192, 4097)], [(130, 2600), (257, 192), (129, 129)]]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shapes", UNLIKE)
+def test_lists_of_unlike_matrices(shapes, dtype):
+    gs = [signs(k, *s, 6) for k, s in enumerate(shapes)]
+    got = mk.orthogonalize([cuda(g) for g in gs], 1, (0.0, 1.0, 0.0), eps=0.0, dtype=TYPES[dtype])
+    assert mk.device_status() == 0
+    for g, x in zip(gs, got):
+        want = oo.orthogonalize(g, 1, (0.0, 1.0, 0.0), 0.0)
+        assert torch.equal(x, cuda(want).to(TYPES[dtype])), g.shape
+
+
+@pytest.mark.parametrize("shapes", UNLIKE)
+def test_steps_of_unlike_matrices(shapes):
+    """The training step takes the same path: weights of zero become -lr O(G), here of S X."""
+    gs = [signs(k, *s, 6) for k, s in enumerate(shapes)]
+    ws = [torch.zeros(*s, device="cuda") for s in shapes]
+    ms = [torch.zeros(*s, device="cuda") for s in shapes]
+    mk.orthogonal_step(ws, [cuda(g) for g in gs], ms, 1.0, momentum=0.5, nesterov=False, steps=1,
+                       coefficients=(0.0, 1.0, 0.0), eps=0.0, scale=1.0)
+    assert mk.device_status() == 0
+    for g, w, m in zip(gs, ws, ms):
+        assert torch.equal(w, cuda(-oo.orthogonalize(g, 1, (0.0, 1.0, 0.0), 0.0))) and torch.equal(m, cuda(g))
