@@ -93,4 +93,26 @@ float number_items(P& p, int phase, int ctas, bool full, int sms) {
     return std::max(longest, waves * work / (float)p.items) + end;
 }
 
+// Deals a list's matrices out to launches of at most `elements` parts of list elements and `most` matrices
+// together.  count(k): matrices of element k, of n.  take(part, k, b0, matrices, before): the part that holds
+// those of element k from b0 on, behind `before` others of the launch.  launch(parts, matrices): whether to go on.
+template <typename Count, typename Take, typename Launch>
+void deal(int n, int elements, int64_t most, Count count, Take take, Launch launch) {
+    int parts = 0;
+    int64_t used = 0;
+    for (int k = 0; k < n; ++k)
+        for (int64_t b = 0, all = count(k); b < all;) {
+            if (parts == elements || used == most) {
+                if (!launch(parts, used)) return;
+                parts = 0;
+                used = 0;
+            }
+            const int64_t here = std::min(all - b, most - used);
+            take(parts++, k, b, here, used);
+            used += here;
+            b += here;
+        }
+    if (parts > 0) launch(parts, used);
+}
+
 }  // namespace mk

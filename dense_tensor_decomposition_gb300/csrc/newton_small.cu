@@ -886,36 +886,37 @@ cudaError_t run_list(const NewtonArgs& a, int64_t matrices, int sms, cudaStream_
     p.status = a.status;
     for (int i = 0; i < 3 * a.steps; ++i) p.abc[i] = a.coefficients[i];
     cudaError_t e = cudaSuccess;
-    // a launch for every size of cluster and short side, of as many elements as a table holds
+    // a launch for every size of cluster and short side, of as many elements as a table holds and as many
+    // matrices as a grid
     for (int b = 1; b <= 2; ++b)
-        for (int c = 1; c <= 8; c *= 2) {
-            p.n = 0;
-            unsigned used = 0;
-            for (int k = 0; k <= a.n && e == cudaSuccess; ++k) {
-                if (p.n == kElements || (k == a.n && p.n > 0)) {
-                    e = b == 1 ? run<1>(c, used, s, p) : run<2>(c, used, s, p);
-                    p.n = 0;
-                    used = 0;
-                }
-                if (k == a.n) break;
-                const mttkrp_matrices& m = a.grad[k];
-                if (!newton_some(m) || !newton_is_small(m) || short_tiles(m) != b || cluster_of(m, matrices, sms) != c) continue;
-                p.shape[p.n] = Shape{0, (int)m.rows, (int)m.cols, (int)m.batch, {used, 0}};
-                Source& u = p.source[p.n];
-                u.g = store_of(m, 0);
-                u.m = u.out = Store{nullptr, 0, 0, 0, 0};
-                if (a.momentum != nullptr) {
-                    u.m = store_of(a.momentum[k], 0);
-                    u.out = store_of(a.momentum_out[k], 0);
-                }
-                Result& r = p.result[p.n];
-                r.out = store_of(a.out[k], 0);
-                r.w = a.weight != nullptr ? store_of(a.weight[k], 0) : Store{nullptr, 0, 0, 0, 0};
-                r.beta = a.beta[k];
-                used += (unsigned)m.batch;
-                ++p.n;
-            }
-        }
+        for (int c = 1; c <= 8; c *= 2)
+            deal(
+                a.n, kElements, INT32_MAX / c,
+                [&](int k) {
+                    const mttkrp_matrices& m = a.grad[k];
+                    const bool here = newton_some(m) && newton_is_small(m) && short_tiles(m) == b && cluster_of(m, matrices, sms) == c;
+                    return here ? m.batch : 0;
+                },
+                [&](int i, int k, int64_t b0, int64_t count, int64_t before) {
+                    const mttkrp_matrices& m = a.grad[k];
+                    p.shape[i] = Shape{0, (int)m.rows, (int)m.cols, (int)count, {(uint32_t)before, 0}};
+                    Source& u = p.source[i];
+                    u.g = store_of(m, b0);
+                    u.m = u.out = Store{nullptr, 0, 0, 0, 0};
+                    if (a.momentum != nullptr) {
+                        u.m = store_of(a.momentum[k], b0);
+                        u.out = store_of(a.momentum_out[k], b0);
+                    }
+                    Result& r = p.result[i];
+                    r.out = store_of(a.out[k], b0);
+                    r.w = a.weight != nullptr ? store_of(a.weight[k], b0) : Store{nullptr, 0, 0, 0, 0};
+                    r.beta = a.beta[k];
+                },
+                [&](int parts, int64_t used) {
+                    p.n = parts;
+                    if (e == cudaSuccess) e = b == 1 ? run<1>(c, (unsigned)used, s, p) : run<2>(c, (unsigned)used, s, p);
+                    return e == cudaSuccess;
+                });
     return e;
 }
 

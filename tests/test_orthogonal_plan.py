@@ -63,3 +63,51 @@ int main() {
 }
 """)
     assert out == ["0", "1"]
+
+
+def test_matrices_beyond_a_grid_go_in_several_launches(tmp_path):
+    """Every matrix of a list once, in the order of the list, in launches whose blocks, elements and counts of
+    matrices hold: elements of 2^31 - 1 matrices among them."""
+    out = run(tmp_path, r"""
+#include <cstdio>
+#include <vector>
+#include "newton_plan.h"
+int main() {
+    const int64_t full = INT32_MAX;
+    int wrong = 0, launches = 0;
+    for (int c : {1, 2, 4, 8})
+        for (const std::vector<int64_t>& counts : std::vector<std::vector<int64_t>>{
+                 {}, {0, 0}, {1}, {3, 0, 5}, std::vector<int64_t>(64, 2), std::vector<int64_t>(131, 1),
+                 {full, full, full}, {1, full, full, 7}, {full / 8, 1}, {full / 8 - 1, 2, 3}}) {
+            size_t at = 0;              // element and matrix that is next
+            int64_t b = 0, of_launch = 0;
+            int parts_of = 0;
+            mk::deal(
+                (int)counts.size(), 64, full / c, [&](int k) { return counts[k]; },
+                [&](int part, int k, int64_t b0, int64_t n, int64_t before) {
+                    while (at < counts.size() && b == counts[at]) ++at, b = 0;
+                    wrong += part != parts_of || (size_t)k != at || b0 != b || n < 1 || before != of_launch;
+                    b += n;
+                    of_launch += n;
+                    ++parts_of;
+                },
+                [&](int parts, int64_t n) {
+                    wrong += parts != parts_of || n != of_launch || n * c > full || parts > 64;
+                    of_launch = parts_of = 0;
+                    ++launches;
+                    return true;
+                });
+            while (at < counts.size() && b == counts[at]) ++at, b = 0;
+            wrong += at != counts.size() || parts_of != 0;
+        }
+    printf("%d %d", wrong, launches > 40);
+}
+""")
+    assert out == ["0", "1"]
+
+
+def test_the_small_matrices_are_dealt_out_so():
+    """The kernels for short sides take their lists by that rule."""
+    with open(f"{_build.CSRC}/newton_small.cu") as f:
+        text = f.read()
+    assert text.count("deal(") == 1 and "INT32_MAX / c" in text and "unsigned used" not in text
