@@ -14,6 +14,7 @@
 // turns back.  Its nearest quarter is taken off as an integer, so that what fp32 rounds is
 // at most an eighth of a turn (4.7e-8 radians).
 #include <algorithm>
+#include <atomic>
 
 #include "launch.cuh"
 #include "rotary.h"
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 // neighbours; 10 heads 78, 113 and 137 in rows of 83; one head 171, 286 and 209.)
 constexpr int kStageBytes = 24576;      // of rows, at most, but for one token that takes more
 constexpr int kMostStage = 98304;
+constexpr int kMostShared = kMostStage + 32;    // a piece of that at any offset, in whole vectors
 constexpr int kFewest = 608;            // CTAs before they take more than one token: four a multiprocessor
 
 struct Dense {
@@ -421,6 +423,19 @@ bool dense(const RotaryArgs& r, const mttkrp_rotary_tensor& t, Dense& d) {
     return true;
 }
 
+// Allows a form of the kernel what any call may take, once a device: the limit is the function's own, and
+// another thread's call may lie between the one here and the launch.
+template <typename T, bool kNeighbours, int kPairs>
+cudaError_t allow() {
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && allowed[dev])) return e;
+    e = cudaFuncSetAttribute(dense_kernel<T, kNeighbours, kPairs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    if (e == cudaSuccess && dev < 64) allowed[dev] = true;
+    return e;
+}
+
 template <typename T, int kPairs>
 cudaError_t run_dense(const RotaryArgs& r, cudaStream_t s, bool& taken) {
     DenseArgs<kPairs> a;
@@ -451,11 +466,9 @@ cudaError_t run_dense(const RotaryArgs& r, cudaStream_t s, bool& taken) {
     for (int i = 0; i < r.dims / 2; ++i) a.turns[i] = r.turns[i];
     taken = true;
     const size_t smem = (most + 15 + 16) / 16 * 16;     // and up to a vector before the first element
+    const cudaError_t e = r.interleaved ? allow<T, true, kPairs>() : allow<T, false, kPairs>();
+    if (e != cudaSuccess) return e;
     const auto kernel = r.interleaved ? dense_kernel<T, true, kPairs> : dense_kernel<T, false, kPairs>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     return launch_early(kernel, dim3((unsigned)blocks, (unsigned)r.n), kThreads, smem, s, a);
 }
 
