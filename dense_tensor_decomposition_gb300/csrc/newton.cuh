@@ -214,9 +214,12 @@ struct Raws {
     }
 };
 
-// factors whose product is 2^12 / (|U| + eps); two, as one may leave fp32's range
+// factors whose product is 2^12 / (|U| + eps); two, as one may leave fp32's range.  Zeros stay zeros, whatever
+// eps: 0 / 0 is taken as 0 (squares that leave fp32's range are in the sum's fp64 part, so that only a U of zeros
+// has the sum 0).
 __device__ __forceinline__ float2 factors(const Sum& total, double eps) {
     const float square = total.hi + total.lo;
+    if (square == 0.f && total.wide == 0.0) return make_float2(0.f, 0.f);
     if (total.wide == 0.0 && square >= 0x1p-100f && square <= 0x1p100f)
         return make_float2(1.f, kScale / (sqrtf(square) + (float)eps));
     const double f = (double)kScale / (sqrt((double)total.hi + (double)total.lo + total.wide) + eps);

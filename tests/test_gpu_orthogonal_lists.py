@@ -57,3 +57,22 @@ def test_steps_of_unlike_matrices(shapes):
     assert mk.device_status() == 0
     for g, w, m in zip(gs, ws, ms):
         assert torch.equal(w, cuda(-oo.orthogonalize(g, 1, (0.0, 1.0, 0.0), 0.0))) and torch.equal(m, cuda(g))
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-300, 1e-80, 1e-7])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_zeros_stay_zeros(dtype, eps):
+    """Whatever eps is, in both kinds of kernels and beside others; and the smallest number of each type is not zero."""
+    shapes = [(65, 30), (30, 700), (128, 128), (130, 129), (200, 300)]
+    gs = [torch.zeros(s, device="cuda", dtype=TYPES[dtype]) for s in shapes] + [cuda(signs(1, 140, 150, 3), TYPES[dtype])]
+    got = mk.orthogonalize(gs, eps=eps)
+    assert all(not x.any() for x in got[:-1]) and torch.isfinite(got[-1]).all() and got[-1].any()
+    ws = [torch.ones_like(g) for g in gs]
+    mk.orthogonal_step(ws, gs, [torch.zeros_like(g) for g in gs], 0.5, eps=eps)
+    assert all((w == 1).all() for w in ws[:-1]) and torch.isfinite(ws[-1]).all()
+    least = {"float32": 2.0 ** -149, "bfloat16": 2.0 ** -133, "float16": 2.0 ** -24}[dtype]
+    for shape in ((20, 33), (130, 150)):
+        g = torch.zeros(shape, device="cuda", dtype=TYPES[dtype])
+        g[3, 7] = least
+        x = mk.orthogonalize(g, 1, (1.0, 0.0, 0.0), eps=0.0)
+        assert x[3, 7] == 1 and x.sum() == 1
