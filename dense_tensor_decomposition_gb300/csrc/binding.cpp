@@ -484,8 +484,8 @@ mttkrp_matrices matrices_of(const at::Tensor& t, bool turn, const char* name, Py
     m.batch_stride = m.rows * m.row_stride;
     bool first = true;
     int64_t next = 0;           // stride that the dimension before has to have
-    for (int64_t i = d - 3; i >= 0; --i) {
-        m.batch *= t.size(i);
+    for (int64_t i = d - 3; i >= 0; --i) m.batch *= t.size(i);
+    for (int64_t i = d - 3; i >= 0 && t.numel() > 0; --i) {
         if (t.size(i) == 1) continue;
         if (first) m.batch_stride = t.stride(i);
         TORCH_CHECK_VALUE(first || t.stride(i) == next, name, "[", k, "]: matrices must lie at equal distances");

@@ -1,0 +1,110 @@
+"""The orthogonal maps' binding on a machine without a GPU: a preloaded library answers for the CUDA
+runtime and takes the place of the library's entry points, which note what they are given.  No GPU is used
+and no tensor's memory is touched."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+import dense_tensor_decomposition_gb300 as mk  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+pytestmark = pytest.mark.skipif(not hasattr(torch._C, "_construct_CUDA_Tensor_From_Storage_And_Metadata"),
+                                reason="this PyTorch makes no tensors of a given address")
+
+FAKE = r"""
+#include <cstddef>
+#include <cstdint>
+#include "mttkrp.h"
+static thread_local int current = 0;
+static mttkrp_matrices seen[8];
+static int64_t rows_seen[16];
+namespace c10::cuda {
+int MaybeSetDevice(int8_t d) { current = d; return 0; }
+}
+extern "C" {
+int cudaGetDeviceCount(int* n) { *n = 1; return 0; }
+int cudaGetDevice(int* d) { *d = current; return 0; }
+int cudaSetDevice(int d) { current = d; return 0; }
+int cudaDeviceGetStreamPriorityRange(int* least, int* greatest) { *least = 0; *greatest = -1; return 0; }
+void matrices_seen(int k, int64_t* at) {
+    const int64_t v[6] = {seen[k].batch, seen[k].rows, seen[k].cols, seen[k].batch_stride, seen[k].row_stride, seen[k].type};
+    for (int i = 0; i < 6; ++i) at[i] = v[i];
+}
+size_t mttkrp_orthogonalize_workspace_bytes(int, const mttkrp_matrices*) { return 0; }
+int mttkrp_orthogonalize(int n, const mttkrp_matrices* in, const mttkrp_matrices* out, int, const double*, double,
+                         const float*, void*, size_t, void*) {
+    for (int k = 0; k < n && k < 4; ++k) seen[k] = in[k], seen[4 + k] = out[k];
+    return 0;
+}
+}
+"""
+
+BEFORE = r"""
+import ctypes
+import torch
+import dense_tensor_decomposition_gb300 as mk
+
+AT, ROOM = 0x10000, 1 << 20             # a made-up address
+fake = ctypes.CDLL(None)
+CUDA = torch.device("cuda", 0)
+
+
+def strided(shape, strides, dtype=torch.float32, at=AT):
+    storage = torch._C._construct_storage_from_data_pointer(at, CUDA, ROOM)
+    meta = dict(size=tuple(shape), stride=tuple(strides), dtype=dtype, storage_offset=0, device=CUDA, nbytes=ROOM, data_ptr=at,
+                layout=torch.strided)
+    return torch._C._construct_CUDA_Tensor_From_Storage_And_Metadata(meta, storage)
+
+
+def tensor(*shape, **more):
+    strides = [1] * len(shape)
+    for k in range(len(shape) - 1, 0, -1):
+        strides[k - 1] = strides[k] * max(shape[k], 1)
+    return strided(shape, strides, **more)
+
+
+def matrices(k):
+    v = (ctypes.c_int64 * 6)()
+    fake.matrices_seen(k, v)
+    return list(v)
+
+
+def raises(kind, call):
+    try:
+        call()
+    except kind:
+        return True
+    return False
+
+"""
+
+
+def run(tmp_path, calls):
+    mk.build()
+    source, fake = tmp_path / "fake.cpp", tmp_path / "libfake.so"
+    source.write_text(FAKE)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", f"-I{os.path.join(ROOT, 'include')}", "-o", str(fake),
+                    str(source)], check=True)
+    res = subprocess.run([sys.executable, "-c", BEFORE + calls + "\nprint('done')\n"], cwd=ROOT,
+                         env={**os.environ, "LD_PRELOAD": str(fake)}, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and "done" in res.stdout, res.stderr[-2000:]
+
+
+def test_no_matrices_in_any_dimension(tmp_path):
+    """A dimension of size 0 anywhere in front leaves nothing to do, whatever the strides; others are as before."""
+    run(tmp_path, r"""
+for shape in ((0, 5, 5), (2, 0, 5, 5), (0, 2, 5, 5), (3, 0, 2, 5, 5), (2, 3, 0, 5), (2, 3, 5, 0)):
+    x, y = tensor(*shape), tensor(*shape, at=AT + ROOM)
+    assert mk.orthogonalize(x, outs=y) is y, shape
+    batch, rows, cols = matrices(0)[:3]
+    assert batch * rows * cols == 0 and (rows, cols) == shape[-2:]
+x, y = tensor(2, 3, 5, 4), tensor(2, 3, 5, 4, at=AT + ROOM)
+mk.orthogonalize(x, outs=y)
+assert matrices(0) == [6, 5, 4, 20, 4, 0] and matrices(4) == matrices(0)
+apart = strided((2, 3, 5, 4), (100, 20, 4, 1))
+assert raises(ValueError, lambda: mk.orthogonalize(apart, outs=y))
+""")
