@@ -99,7 +99,7 @@ def _torch_flags():
     flags = [f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", "-isystem", include, "-isystem",
              os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", os.path.join(cuda, "include"),
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    links = [f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10"]
+    links = [f"-L{os.path.join(home, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     return flags, links
 
 

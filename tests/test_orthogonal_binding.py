@@ -21,7 +21,6 @@ FAKE = r"""
 #include "mttkrp.h"
 static thread_local int current = 0;
 static mttkrp_matrices seen[8];
-static int64_t rows_seen[16];
 namespace c10::cuda {
 int MaybeSetDevice(int8_t d) { current = d; return 0; }
 }
@@ -40,6 +39,8 @@ int mttkrp_orthogonalize(int n, const mttkrp_matrices* in, const mttkrp_matrices
     for (int k = 0; k < n && k < 4; ++k) seen[k] = in[k], seen[4 + k] = out[k];
     return 0;
 }
+int mttkrp_rotary(int, const mttkrp_rotary_tensor*, int, int64_t, int64_t, int64_t, const void*, int, int64_t, int64_t,
+                  const double*, int, int, float, int, void*) { return 0; }
 }
 """
 
@@ -107,4 +108,33 @@ mk.orthogonalize(x, outs=y)
 assert matrices(0) == [6, 5, 4, 20, 4, 0] and matrices(4) == matrices(0)
 apart = strided((2, 3, 5, 4), (100, 20, 4, 1))
 assert raises(ValueError, lambda: mk.orthogonalize(apart, outs=y))
+""")
+
+
+def test_results_are_allocated_through_the_dispatcher(tmp_path):
+    """As every other operator's, so that a dispatch mode (and the filling of new memory in deterministic
+    mode) sees them: results of the tensors' layout, dense or not."""
+    run(tmp_path, r"""
+from torch.utils._python_dispatch import TorchDispatchMode
+
+
+class Allocations(TorchDispatchMode):
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        name = func._schema.name
+        if name in ("aten::empty", "aten::empty_strided"):
+            made.append(strided(args[0], args[1]) if name == "aten::empty_strided" else tensor(*args[0]))
+            return made[-1]
+        return func(*args, **(kwargs or {}))
+
+
+freqs, at = mk.rotary_frequencies(16), tensor(5, dtype=torch.int64)
+made = []
+for x in (tensor(5, 16), tensor(5, 3, 16), strided((5, 3, 16), (16, 80, 1)), strided((5, 3, 16), (60, 20, 1)),
+          strided((5, 3, 16), (48, 0, 1))):
+    made.clear()
+    with Allocations():
+        y = mk.rotary(x, at, freqs)
+    assert len(made) == 1 and y is made[0], x.stride()
+    dense = x.stride() not in ((60, 20, 1), (48, 0, 1))
+    assert y.stride() == (x.stride() if dense else (48, 16, 1))
 """)
