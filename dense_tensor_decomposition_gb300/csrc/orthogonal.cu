@@ -134,13 +134,13 @@ int check_list(const char* what, int n, const mttkrp_matrices* list, const mttkr
     return MTTKRP_OK;
 }
 
-// A list that is read, or written; where `place` (of the same length) is not NULL, an element
-// may be written in the place of that list's.
+// A list that is read, or written; an element of it may be written in the place of list number
+// `place`'s (-1: of none).  (Not known by its address: a caller may pass one array as several lists.)
 struct Listed {
     const char* what;
     const mttkrp_matrices* list;
     bool written;
-    const mttkrp_matrices* place;
+    int place;
 };
 
 // No result overlaps another result or a tensor, but for its own place.
@@ -173,7 +173,7 @@ int check_apart(int n, const Listed* lists, int count) {
             const Listed &lx = lists[x.list], &ly = lists[y.list];
             if (!lx.written && !ly.written) continue;
             const mttkrp_matrices &mx = lx.list[x.k], &my = ly.list[y.k];
-            if (x.k == y.k && (lx.place == ly.list || ly.place == lx.list) && same_place(mx, my)) continue;
+            if (x.k == y.k && (lx.place == y.list || ly.place == x.list) && same_place(mx, my)) continue;
             if (!disjoint(rows_of(mx), rows_of(my)))
                 return fail(MTTKRP_ERR_INVALID, "%s %d overlaps %s %d", lx.what, x.k, ly.what, y.k);
         }
@@ -341,7 +341,7 @@ int mttkrp_orthogonalize(int n, const mttkrp_matrices* in, const mttkrp_matrices
     if (int rc = check_list("matrix", n, in, in)) return rc;
     if (int rc = check_list("result", n, out, in)) return rc;
     if (int rc = check_steps(steps, coefficients, eps, abc)) return rc;
-    const Listed lists[2] = {{"matrix", in, false, nullptr}, {"result", out, true, in}};
+    const Listed lists[2] = {{"matrix", in, false, -1}, {"result", out, true, 0}};
     if (int rc = check_apart(n, lists, 2)) return rc;
     NewtonArgs a{};
     a.n = n;
@@ -372,9 +372,8 @@ int mttkrp_orthogonal_step(int n, const mttkrp_matrices* weights, const mttkrp_m
     if (!std::isfinite(lr) || !std::isfinite(momentum) || !std::isfinite(weight_decay))
         return fail(MTTKRP_ERR_INVALID, "lr, momentum and weight_decay must be finite");
     if (int rc = check_steps(steps, coefficients, eps, abc)) return rc;
-    const Listed lists[5] = {{"gradient", grads, false, nullptr}, {"weight", weights, false, nullptr},
-                             {"momentum", momenta, false, nullptr}, {"new weight", weights_out, true, weights},
-                             {"new momentum", momenta_out, true, momenta}};
+    const Listed lists[5] = {{"gradient", grads, false, -1}, {"weight", weights, false, -1}, {"momentum", momenta, false, -1},
+                             {"new weight", weights_out, true, 1}, {"new momentum", momenta_out, true, 2}};
     if (int rc = check_apart(n, lists, 5)) return rc;
     NewtonArgs a{};
     a.n = n;
