@@ -9,13 +9,13 @@
 #include "newton.h"
 #include "rotary.h"
 #include "tc.h"
+#include "turns.h"
 
 namespace mk {
 namespace {
 
 constexpr int64_t kMaxTokens = INT32_MAX;
 constexpr int64_t kMaxWidth = 65536;
-constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 // Rows of `width` consecutive elements at all combinations of three indices.
 struct Rows {
@@ -274,9 +274,9 @@ int mttkrp_rotary(int n, const mttkrp_rotary_tensor* tensors, int type, int64_t 
     uint64_t turns[MTTKRP_MAX_ROTARY_DIMS / 2];
     for (int i = 0; i < dims / 2; ++i) {
         if (!std::isfinite(frequencies[i])) return fail(MTTKRP_ERR_INVALID, "frequency %d is not finite", i);
-        double f = frequencies[i] / kTwoPi;
-        f -= std::floor(f);                             // in [0, 1]: a whole turn more changes nothing
-        turns[i] = f < 1.0 ? (uint64_t)std::ldexp(f, 64) : 0;
+        if (std::fabs(frequencies[i]) >= kMostRadians)
+            return fail(MTTKRP_ERR_INVALID, "frequency %d: 2^64 radians a position or more", i);
+        turns[i] = turns_of(frequencies[i]);
     }
     const int64_t e = (int64_t)type_bytes(type);
     mttkrp_rotary_tensor list[MTTKRP_MAX_ROTARY];

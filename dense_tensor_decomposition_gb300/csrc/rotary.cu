@@ -9,10 +9,10 @@
 // Heads are dealt out to as many threads as fill the GPU (few tokens: a head each).
 //
 // The angle.  p f_i in fp32 is off by p f_i 2^-24: 0.06 radians at a million.  Frequencies
-// come as turns a position in 64-bit fixed point instead; the product's low 64 bits are
-// the angle as a fraction of a turn, exact however far the position, and a negative one
-// turns back.  Its nearest quarter is taken off as an integer, so that what fp32 rounds is
-// at most an eighth of a turn (4.7e-8 radians).
+// come as turns a position in 64-bit fixed point instead, within half a unit (turns.h); the
+// product's low 64 bits are the angle as a fraction of a turn, within |p| 2^-65 of one (2e-7
+// radians at 2^40), and a negative position turns back.  Its nearest quarter is taken off as an
+// integer, so that what fp32 rounds, three times, is at most an eighth of a turn (1.2e-7 radians).
 #include <algorithm>
 #include <atomic>
 

@@ -484,8 +484,9 @@ typedef struct mttkrp_rotary_tensor {
  * positions   device, int32 or int64 (pos_bytes 4 or 8): of token (b, t) at element
  *             b * pos_batch_stride + t * pos_stride (strides of 0 share positions).  Any value
  *             is a position; negative ones turn back.
- * frequencies HOST, dims / 2 values in radians a position, finite.  The angle is taken modulo
- *             a whole turn in 64-bit fixed point, and so holds for positions of any size.
+ * frequencies HOST, dims / 2 values in radians a position, of a magnitude below 2^64.  The angle
+ *             is taken modulo a whole turn in 64-bit fixed point: what that leaves out is at most
+ *             |p| 2^-65 of a turn, 2e-7 radians at positions of 2^40 (and grows beyond).
  * Tokens and vectors of their rows: at most 2^31 - 1 tokens, and rows that the grid can hold.
  * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_CUDA.
  */

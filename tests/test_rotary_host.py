@@ -1,7 +1,10 @@
 """Host code of the rotation by position that no entry point shows by itself, in small programs that are
 compiled here and run on the CPU."""
+import ctypes
 import os
 import subprocess
+
+import pytest
 
 from dense_tensor_decomposition_gb300 import _build
 
@@ -48,3 +51,53 @@ int main() {
 }
 """)
     assert out == ["1"]
+
+
+def test_frequencies_become_turns_to_the_last_bit(tmp_path):
+    """Radians of every size and sign in units of 2^-64 turn, against whole numbers: pi to 1200 bits by Machin's
+    formula.  Half a unit off at most, so that positions of 2^40 turn by what the frequency says within 2^-25."""
+    def arctan_of_inverse(n, one):
+        term = total = one // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+
+    bits = 1200
+    one = 1 << bits
+    two_pi = 8 * (4 * arctan_of_inverse(5, one) - arctan_of_inverse(239, one))
+    values = [0.0, 1.0, -1.0, 0.5, -0.37, 1e-5, 2 * 3.141592653589793, 7.5, 1e-12, 1e-19, -1e-19, 3e-20, 1e-300, 5e-324, 1e10,
+              -1e10, 12345678.9, 2.0 ** 52 + 1, 1e18, -(2.0 ** 63), 1.8e19, 2.0 ** 64 * (1 - 2.0 ** -53)]
+    values += [10000.0 ** (-i / 64) for i in range(64)] + [-(500000.0 ** (-i / 64)) for i in range(64)]
+    code, program = tmp_path / "turns.cpp", tmp_path / "turns"
+    code.write_text(r"""
+#include <cinttypes>
+#include <cstdio>
+#include "turns.h"
+int main() {
+    const double all[] = {""" + ", ".join(v.hex() for v in values) + r"""};
+    for (double f : all) printf("%" PRIu64 " ", mk::turns_of(f));
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", f"-I{_build.CSRC}", "-o", str(program), str(code)], check=True)
+    got = [int(x) for x in subprocess.run([str(program)], check=True, capture_output=True, text=True).stdout.split()]
+    assert len(got) == len(values)
+    for f, turns in zip(values, got):
+        numerator, denominator = f.as_integer_ratio()
+        want = numerator * one * one * 2 ** 64 // (denominator * two_pi)        # turns 2^64, times `one`
+        off = (turns * one - want) % (one << 64)
+        off = min(off, (one << 64) - off)
+        assert off * 2 <= one + (one >> 30), (f, turns)
+
+
+def test_frequencies_out_of_range_are_refused():
+    """2^64 radians a position and more, which 53 bits say nothing about (nothing is dereferenced)."""
+    mk = pytest.importorskip("dense_tensor_decomposition_gb300")
+    mk.build()
+    lib = mk.load_library()
+    tensors = (ctypes.c_int64 * 9)()            # no heads: nothing to do once the frequencies are taken
+    for f, code in ((2.0 ** 64, 1), (-(2.0 ** 70), 1), (1e308, 1), (2.0 ** 64 * (1 - 2.0 ** -53), 0), (-1e19, 0)):
+        freqs = (ctypes.c_double * 1)(f)
+        assert lib.mttkrp_rotary(1, tensors, 0, 1, 1, 2, 0x1000, 8, 0, 0, freqs, 2, 0, 1.0, 0, None) == code, f
