@@ -76,3 +76,61 @@ def test_zeros_stay_zeros(dtype, eps):
         g[3, 7] = least
         x = mk.orthogonalize(g, 1, (1.0, 0.0, 0.0), eps=0.0)
         assert x[3, 7] == 1 and x.sum() == 1
+
+
+UNIT = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+# relative (Frobenius norm) errors of five quintic steps before the result's rounding, as include/mttkrp.h says:
+# products of 22 bits, and of 11 (but for X) where a result in bf16 has both sides above 128
+LONG, SHORT = 4e-6, 1.5e-3
+
+
+def gradient(gen, shape, dtype):
+    """A few strong directions over noise."""
+    r, c = shape
+    rank = max(1, min(r, c) // 16)
+    u = torch.randn(r, rank, generator=gen, device="cuda")
+    v = torch.randn(rank, c, generator=gen, device="cuda")
+    return (u @ v / rank ** 0.5 + 0.1 * torch.randn(r, c, generator=gen, device="cuda")).to(dtype)
+
+
+SIDES = [(90, 70), (33, 47), (257, 128), (70, 301), (256, 64), (129, 130), (201, 333), (501, 333), (512, 2000), (1100, 900),
+         (2048, 700)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", SIDES)
+def test_results_as_near_as_promised(shape, dtype):
+    """A rounding moves a value by half a step of its type at most, and so the whole by no more of its norm; fp16's
+    smallest numbers by 2^-25 each."""
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+    g = gradient(gen, shape, TYPES[dtype])
+    want = oo.orthogonalize(g.double().cpu(), 5, mk.QUINTIC)
+    size = np.linalg.norm(want)
+    short = dtype == "bfloat16" and min(shape) > 128
+    bound = (SHORT if short else LONG) + UNIT[TYPES[dtype]] + (2.0 ** -25 * want.size ** 0.5 / size if dtype == "float16" else 0)
+    x = mk.orthogonalize(g)
+    assert np.linalg.norm(x.double().cpu().numpy() - want) <= bound * size
+    # into fp32, whatever the input's type: nothing but the products
+    x = mk.orthogonalize(g, dtype=torch.float32)
+    assert np.linalg.norm(x.double().cpu().numpy() - want) <= (LONG + UNIT[torch.float32]) * size
+
+
+@pytest.mark.parametrize("weights", TYPES)
+@pytest.mark.parametrize("momenta", TYPES)
+@pytest.mark.parametrize("shape", SIDES)
+def test_updates_as_near_as_promised(shape, weights, momenta):
+    """What a step adds to weights of zeros: -lr scale O(U), U within two roundings of fp32 (4e-6 after five
+    steps: a direction a hundredth as strong as the whole is raised to 1 by up to 485, and its rounding with it)."""
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape) + 1)
+    g, m = gradient(gen, shape, torch.bfloat16), gradient(gen, shape, TYPES[momenta])
+    w = torch.zeros(shape, device="cuda", dtype=TYPES[weights])
+    before = m.double().cpu().numpy()
+    mk.orthogonal_step(w, g, m, 0.5, momentum=0.9, scale=2.0)
+    kept = 0.9 * before + g.double().cpu().numpy()
+    want = -oo.orthogonalize(g.double().cpu().numpy() + 0.9 * kept, 5, mk.QUINTIC)
+    size = np.linalg.norm(want)
+    short = weights == "bfloat16" and min(shape) > 128
+    bound = (SHORT if short else LONG) + 4e-6 + UNIT[w.dtype] + (2.0 ** -25 * want.size ** 0.5 / size if weights == "float16" else 0)
+    assert np.linalg.norm(w.double().cpu().numpy() - want) <= bound * size
+    assert np.all(np.abs(m.double().cpu().numpy() - kept) <= 2.0 ** -23 * (np.abs(before) + np.abs(kept)) * 2 +
+                  UNIT[m.dtype] * 1.01 * np.abs(kept) + (2.0 ** -25 if momenta == "float16" else 0))
