@@ -462,43 +462,44 @@ __device__ __forceinline__ void write_block(const ProductArgs& a, const Place& a
         }
     } else {
 #pragma unroll
-    for (int e = 0; e < 64; ++e) f[e] *= kUnscale;
-    if constexpr (kPhase == kSquare) {
-        if constexpr (kFull) {
-            polynomial_full(a, at, j, f);
-        } else {
-            polynomial_short(a, at, n, s, f, stage, lane);
-            if (n + 1 < blocks && j + 1 < at.mt) s.get(tile_of_s(a, at, n + 1), at, lane);
-        }
-    }
-    // 16 rows of a tile are 2 KB in one piece: hi and lo by way of shared memory (16-byte stores
-    // of every thread to its own row: 30 us of 138 in S of 2 x 4096 x 4096)
-    constexpr int kUnit = 2048;
-    constexpr bool kBoth = kStage >= 2 * kUnit;         // hi and lo at once
-    uint8_t* dst = a.tiles + (int64_t)(at.to + at.ti * at.mt + j) * kTileBytes + 128 * at.r0;
-#pragma unroll 1
-    for (int u = 0; u < (kBoth ? 2 : 4); ++u) {
-        const int half = kBoth ? u : u >> 1, low = kBoth ? 0 : u & 1;
-        if (lane == 0) bulk_wait_read();
-        __syncwarp();
-        if (lane >> 4 == half) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint4 hi, lo;
-                split8(f + 8 * q, hi, lo);
-                *reinterpret_cast<uint4*>(stage + piece(lane & 15, q)) = low ? lo : hi;
-                if (kBoth) *reinterpret_cast<uint4*>(stage + kUnit + piece(lane & 15, q)) = lo;
+        for (int e = 0; e < 64; ++e) f[e] *= kUnscale;
+        if constexpr (kPhase == kSquare) {
+            if constexpr (kFull) {
+                polynomial_full(a, at, j, f);
+            } else {
+                polynomial_short(a, at, n, s, f, stage, lane);
+                if (n + 1 < blocks && j + 1 < at.mt) s.get(tile_of_s(a, at, n + 1), at, lane);
             }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-            uint8_t* to = dst + half * kUnit;
-            const int64_t to_lo = (int64_t)at.lo * kTileBytes;
-            bulk_store(to + (low ? to_lo : 0), stage, kUnit);
-            if (kBoth) bulk_store(to + to_lo, stage + kUnit, kUnit);
+        // 16 rows of a tile are 2 KB in one piece: hi and lo by way of shared memory (16-byte stores
+        // of every thread to its own row: 30 us of 138 in S of 2 x 4096 x 4096)
+        constexpr int kUnit = 2048;
+        constexpr bool kBoth = kStage >= 2 * kUnit;         // hi and lo at once
+        uint8_t* dst = a.tiles + (int64_t)(at.to + at.ti * at.mt + j) * kTileBytes + 128 * at.r0;
+#pragma unroll 1
+        for (int u = 0; u < (kBoth ? 2 : 4); ++u) {
+            const int half = kBoth ? u : u >> 1, low = kBoth ? 0 : u & 1;
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+            if (lane >> 4 == half) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint4 hi, lo;
+                    split8(f + 8 * q, hi, lo);
+                    *reinterpret_cast<uint4*>(stage + piece(lane & 15, q)) = low ? lo : hi;
+                    if (kBoth) *reinterpret_cast<uint4*>(stage + kUnit + piece(lane & 15, q)) = lo;
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                uint8_t* to = dst + half * kUnit;
+                const int64_t to_lo = (int64_t)at.lo * kTileBytes;
+                bulk_store(to + (low ? to_lo : 0), stage, kUnit);
+                if (kBoth) bulk_store(to + to_lo, stage + kUnit, kUnit);
+            }
         }
-    }    }
+    }
 }
 
 // ---- shared memory: stages of A hi, B hi, then the low parts that are used

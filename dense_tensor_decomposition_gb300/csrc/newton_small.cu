@@ -214,13 +214,14 @@ __device__ __forceinline__ void load_slab(const A& a, const Shape& shape, const 
     __syncthreads();
 }
 
-// kC: CTAs a cluster; kB: tiles of 64 of the short side (2; narrow_kernel below is for 1)
-template <int kC, int kB>
+// The short side 65 to 128: kB tiles of 64.  kC: CTAs a cluster
+template <int kC>
 __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constant__ SmallArgs a) {
+    constexpr int kB = 2;
     constexpr int kM = 64 * kB;                 // rows of S
     constexpr int kCols = 16 * kB;              // of a thread, in S
     constexpr int kOwn = kM / kC;               // rows of S that a CTA adds up
-    constexpr int kGroup = 4 / kB;              // tiles of a wide slab (or, times 2 / kB, of a tall one) at once in P X
+    constexpr int kAtOnce = 2;                  // tiles of the long side at once in P X
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [2] of the accumulators' buffers
@@ -297,8 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     // a thread's columns of S from accumulators, added to v or put there
     auto drain = [&](uint32_t from, float* v, bool add) {
         uint32_t bits[kCols];
-        if constexpr (kB == 2) tmem_ld32(from, bits);
-        else tmem_ld16(from, bits);
+        tmem_ld32(from, bits);
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < kCols; ++e) v[e] = add ? v[e] + __uint_as_float(bits[e]) : __uint_as_float(bits[e]);
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
             const uint32_t at = xa + (uint32_t)t * t_step;
             Op o;
             if (wide) o = Op{sdesc128_lo(at), sdesc128_lo(at + x_lo), 2u};
-            else o = Op{mn_desc(at, kB > 1 ? s_step : kTileBytes), mn_desc(at + x_lo, kB > 1 ? s_step : kTileBytes), 128u};
+            else o = Op{mn_desc(at, s_step), mn_desc(at + x_lo, s_step), 128u};
             issue(tmem + (uint32_t)(t & 1) * kHalfTmem, o, o, slices_of(max(shape.rows, shape.cols), t0 + t), gram_desc, leader);
             commit<1>(&bars[t & 1], leader);
         };
@@ -338,14 +338,12 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         }
         if constexpr (kC > 1) {
             // to the CTA that adds up the row
-            if (r < kM) {
-                const uint32_t to = in_cta(smem_u32(exchange), (uint32_t)(r / kOwn)) +
-                                    (uint32_t)(((int)rank * kOwn + r % kOwn) * kM + col0) * 4u;
+            const uint32_t to = in_cta(smem_u32(exchange), (uint32_t)(r / kOwn)) +
+                                (uint32_t)(((int)rank * kOwn + r % kOwn) * kM + col0) * 4u;
 #pragma unroll
-                for (int c = 0; c < kCols; c += 4)
-                    put_in_cluster(to + 4u * c, make_uint4(__float_as_uint(part[c]), __float_as_uint(part[c + 1]),
-                                                           __float_as_uint(part[c + 2]), __float_as_uint(part[c + 3])));
-            }
+            for (int c = 0; c < kCols; c += 4)
+                put_in_cluster(to + 4u * c, make_uint4(__float_as_uint(part[c]), __float_as_uint(part[c + 1]),
+                                                       __float_as_uint(part[c + 2]), __float_as_uint(part[c + 3])));
             all_sync<kC>();
             for (int v = threadIdx.x; v < kOwn * kM / 8; v += kThreads) {
                 const int own = v / (kM / 8), col = v % (kM / 8) * 8, row = (int)rank * kOwn + own;
@@ -374,18 +372,16 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
             all_sync<kC>();
             fence_cluster();
         } else {
-            if (r < kM) {
 #pragma unroll
-                for (int c = 0; c < kCols; c += 8) {
-                    const int col = col0 + c;
+            for (int c = 0; c < kCols; c += 8) {
+                const int col = col0 + c;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) part[c + e] = uncut(part[c + e], n_short) * kUnscale;
-                    uint4 hi, lo;
-                    split8(part + c, hi, lo);
-                    uint8_t* at = s_hi + (col / 64 * kB + r / 64) * kTileBytes + piece(r & 63, (col & 63) >> 3);
-                    *reinterpret_cast<uint4*>(at) = hi;
-                    *reinterpret_cast<uint4*>(at + s_lo) = lo;
-                }
+                for (int e = 0; e < 8; ++e) part[c + e] = uncut(part[c + e], n_short) * kUnscale;
+                uint4 hi, lo;
+                split8(part + c, hi, lo);
+                uint8_t* at = s_hi + (col / 64 * kB + r / 64) * kTileBytes + piece(r & 63, (col & 63) >> 3);
+                *reinterpret_cast<uint4*>(at) = hi;
+                *reinterpret_cast<uint4*>(at + s_lo) = lo;
             }
             fence_shared();
             __syncthreads();
@@ -400,25 +396,23 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         }
         wait(0);
         drain(lanes + (uint32_t)col0, part, false);
-        if constexpr (kB == 2) drain(lanes + kHalfTmem + (uint32_t)col0, part, true);
+        drain(lanes + kHalfTmem + (uint32_t)col0, part, true);
         tc_fence_before();
-        if (r < kM) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 8) {
-                const int col = col0 + c;
-                uint8_t* at = s_hi + (col / 64 * kB + r / 64) * kTileBytes + piece(r & 63, (col & 63) >> 3);
-                float s[8];
-                join8(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + s_lo), s);
+        for (int c = 0; c < kCols; c += 8) {
+            const int col = col0 + c;
+            uint8_t* at = s_hi + (col / 64 * kB + r / 64) * kTileBytes + piece(r & 63, (col & 63) >> 3);
+            float s[8];
+            join8(*reinterpret_cast<const uint4*>(at), *reinterpret_cast<const uint4*>(at + s_lo), s);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    s[e] = fmaf(cc, uncut(part[c + e], m_short) * kUnscale, cb * s[e]);
-                    if (r == col + e && r < m) s[e] += ca * kScale;
-                }
-                uint4 hi, lo;
-                split8(s, hi, lo);
-                *reinterpret_cast<uint4*>(at) = hi;
-                *reinterpret_cast<uint4*>(at + s_lo) = lo;
+            for (int e = 0; e < 8; ++e) {
+                s[e] = fmaf(cc, uncut(part[c + e], m_short) * kUnscale, cb * s[e]);
+                if (r == col + e && r < m) s[e] += ca * kScale;
             }
+            uint4 hi, lo;
+            split8(s, hi, lo);
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + s_lo) = lo;
         }
         fence_shared();
         __syncthreads();
@@ -426,22 +420,19 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         // P X over X, some tiles of the long side at a time: 64 x 64 blocks of the result, each
         // from kB slices of 64 indices in accumulators of their own
         const bool last = step == a.steps - 1;
-        const int at_once = wide ? kGroup : 8 / (kB * kB);          // tiles of the long side
-        const int passes = (nt + at_once - 1) / at_once;
+        const int passes = (nt + kAtOnce - 1) / kAtOnce;
         auto update = [&](int n) {
             const uint32_t d = tmem + (uint32_t)(n & 1) * kHalfTmem;
-            const int first = n * at_once, count = min(at_once, nt - first);
+            const int first = n * kAtOnce, count = min(kAtOnce, nt - first);
             for (int s = 0; s < kB; ++s) {
                 if (wide) {
                     const uint32_t at = xa + tile_at(s, first);
                     const Op q{mn_desc(at, t_step), mn_desc(at + x_lo, t_step), 128u};
                     issue(d + (uint32_t)s * 128u, sym(s), q, slices_of(m, s), kF32 | kM128 | (1u << 16) | ((uint32_t)(8 * count) << 17), leader);
                 } else {
-                    for (int t = 0; t < count; t += 2) {
-                        const uint32_t at = xa + tile_at(s, first + t);
-                        const Op p{sdesc128_lo(at), sdesc128_lo(at + x_lo), 2u};
-                        issue(d + (uint32_t)s * 128u + (uint32_t)(t / 2 * kM), p, sym(s), slices_of(m, s), square_desc, leader);
-                    }
+                    const uint32_t at = xa + tile_at(s, first);
+                    const Op p{sdesc128_lo(at), sdesc128_lo(at + x_lo), 2u};
+                    issue(d + (uint32_t)s * 128u, p, sym(s), slices_of(m, s), square_desc, leader);
                 }
             }
             commit<1>(&bars[n & 1], leader);
@@ -452,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         }
         for (int n = 0; n < passes; ++n) {
             wait(n & 1);
-            const int first = n * at_once;
+            const int first = n * kAtOnce;
             // a thread's columns of its row: a quarter of the accumulators', in one tile
             constexpr int kWidth = 64 / kB;
             const int block = part_of / kB, c0 = part_of % kB * kWidth;     // of 64 columns; first one in it
@@ -461,35 +452,30 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
             {
                 uint32_t bits[64];
                 tmem_ld32(from, bits);
-                tmem_ld32(kB == 2 ? from + 128u : from + 32u, bits + 32);
+                tmem_ld32(from + 128u, bits + 32);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < kWidth; ++e)
-                    f[e] = uncut(kB == 2 ? __uint_as_float(bits[e]) + __uint_as_float(bits[32 + e % 32]) : __uint_as_float(bits[e]), m_short);
+                for (int e = 0; e < kWidth; ++e) f[e] = uncut(__uint_as_float(bits[e]) + __uint_as_float(bits[32 + e]), m_short);
             }
-            const int s = wide ? r / 64 : kB == 2 ? block : 0;
-            const int t = wide ? first + block : first + (kB == 2 ? 0 : 2 * block) + r / 64;
-            if (s < kB && t < nt) {                         // (the same for a warp)
+            const int s = wide ? r / 64 : block, t = first + (wide ? block : r / 64);
+            if (t < nt) {                                   // (the same for a warp)
                 uint8_t* const tile = x_hi + tile_at(s, t);
                 if (last) {
                     // by way of what these 32 rows of X were (hi or lo part, as two warps have a tile's
                     // rows): nobody reads them any more
                     const Result& o = a.result[k];
-                    uint8_t* const stage = tile + 4096 * (quad & 1) + (kB == 2 && c0 != 0 ? x_lo : 0u);
+                    uint8_t* const stage = tile + 4096 * (quad & 1) + (c0 != 0 ? x_lo : 0u);
                     const int row0 = (wide ? s : t0 + t) * 64 + 32 * (quad & 1), first_col = (wide ? t0 + t : s) * 64 + c0;
-#pragma unroll
-                    for (int c = 0; c < kWidth; c += 32) {
-                        if (first_col + c >= shape.cols) continue;
-                        __syncwarp();
+                    if (first_col < shape.cols) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const float* v = f + c + 4 * q;
+                            const float* v = f + 4 * q;
                             const float by = kUnscale * kUnscale;
                             *reinterpret_cast<float4*>(stage + staged<32>(lane, q)) =
                                 make_float4(o.beta * (v[0] * by), o.beta * (v[1] * by), o.beta * (v[2] * by), o.beta * (v[3] * by));
                         }
                         __syncwarp();
-                        write_rows<32, 1>(a.alpha, o, b, row0, first_col + c, shape.rows, shape.cols, stage, lane);
+                        write_rows<32, 1>(a.alpha, o, b, row0, first_col, shape.rows, shape.cols, stage, lane);
                     }
                 } else {
 #pragma unroll
@@ -839,7 +825,7 @@ template <int kC, int kB>
 cudaError_t run(unsigned matrices, cudaStream_t s, const SmallArgs& args) {
     void (*kernel)(SmallArgs) = nullptr;
     if constexpr (kB == 1) kernel = narrow_kernel<kC>;
-    else kernel = small_kernel<kC, kB>;
+    else kernel = small_kernel<kC>;
     static std::atomic<bool> allowed[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
