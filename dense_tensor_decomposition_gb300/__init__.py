@@ -804,9 +804,12 @@ def orthogonal_step(weights, grads, momenta, lr: float, momentum: float = 0.95, 
     (mttkrp_orthogonal_step):
         M' = momentum * M + G,  U = G + momentum * M' (nesterov) or M',
         W' = (1 - lr * weight_decay) * W - lr * scale * orthogonalize(U)
-    weights, grads, momenta: lists of CUDA tensors of the same shapes (or one tensor each), with
-    types and strides as `orthogonalize`'s.  W' and M' are written in place, or into `outs` and
-    `momenta_outs` (of their types and shapes).  scale: a number, one for every matrix, or None:
+    weights, grads, momenta: lists of CUDA tensors of the same shapes (or one tensor each), each of its
+    own type and row distance; all tensors of one matrix have consecutive rows, or all have consecutive columns
+    (a transposed view beside one that is not is refused).  W' and M' are written in place, or into `outs`
+    and `momenta_outs` (of their types and shapes).  The precision follows the weights' type, as
+    `orthogonalize`'s follows its results': for more on bfloat16 weights hold them in float32, or apply
+    orthogonalize(..., dtype=torch.float32) of your own momentum.  scale: a number, one for every matrix, or None:
     sqrt(max(1, rows / cols)), which makes updates of tall and wide matrices alike in size.
     Returns the list of new weights (the tensors that were written)."""
     if not isinstance(weights, (list, tuple)):

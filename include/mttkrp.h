@@ -525,16 +525,21 @@ typedef struct mttkrp_matrices {
  *              let a singular value grow beyond 3.9, or a + b s^2 + c s^4 beyond 15.9: the
  *              products run on fp16 images (twice 11 bits) with a fixed scale.
  * scales       one a list element, or NULL: 1.
- * Results in fp32 and fp16 are computed from products that are exact to about 2^-22 of their
- * terms; those in bf16 from products of the 11 leading bits but for X's: relative errors (in
- * the Frobenius norm) of about 2e-6 and 1.5e-3 at five steps of (3.4445, -4.775, 2.0315).
+ * Results in fp32 and fp16 are computed from products of 22 bits, no more than about twice as far off as fp32
+ * products; those in bf16 from products of the 11 leading bits but for X's: relative errors (in
+ * the Frobenius norm) of 1e-6 to 3e-6 and of about 1.5e-3 at five steps of (3.4445, -4.775, 2.0315), for a few
+ * strong directions over noise a tenth as large (fp32: 3e-5 over noise a thousandth as large, as fp32 products).
+ * Elements of X, S and a I + b S + c S^2 are held to 2^-22 of themselves or to 2^-37, whichever is more: rows
+ * far smaller than the rest keep fewer bits, and so does everything where a is 0 (one step of (0, 0, 1) on
+ * 2048 x 2048 normal numbers: 1.2e-4).
  * Matrices with a side of at most 128 whose other side is not too long for the shared memory
  * of eight SMs (5120 beside 64, 1536 beside 128) are done in one launch with the products of fp32
  * whatever the result's type.  Which form of the kernels runs follows the list, so that the last
  * bits of a result may depend on what else is in its call; a call repeats bit by bit.
  * A matrix with an infinite or NaN element becomes NaN; one of zeros stays zero.
- * workspace    device, 256-byte aligned, mttkrp_orthogonalize_workspace_bytes(n, in) bytes: 16
- *              to 32 bytes an element of up to 4 GB worth of matrices at a time.  0 for lists
+ * workspace    device, 256-byte aligned, mttkrp_orthogonalize_workspace_bytes(n, in) bytes: 8 (1 + short side /
+ *              long side) bytes an element, sides rounded up to 64, of up to 4 GB worth of matrices at a
+ *              time (or one matrix).  0 for lists
  *              of matrices that are done in one launch (above), without elements, or invalid.
  * Errors: MTTKRP_ERR_INVALID, MTTKRP_ERR_WORKSPACE, MTTKRP_ERR_HOST_ALLOC, MTTKRP_ERR_CUDA.
  */

@@ -134,3 +134,44 @@ def test_updates_as_near_as_promised(shape, weights, momenta):
     assert np.linalg.norm(w.double().cpu().numpy() - want) <= bound * size
     assert np.all(np.abs(m.double().cpu().numpy() - kept) <= 2.0 ** -23 * (np.abs(before) + np.abs(kept)) * 2 +
                   UNIT[m.dtype] * 1.01 * np.abs(kept) + (2.0 ** -25 if momenta == "float16" else 0))
+
+
+@pytest.mark.parametrize("shape", [(64, 64), (64, 6000), (128, 512), (129, 130), (512, 512), (2000, 512), (1024, 1100)])
+@pytest.mark.parametrize("abc", [mk.QUINTIC, (1.5, -0.5, 0.0), (15 / 8, -10 / 8, 3 / 8)])
+def test_sums_of_mixed_signs(shape, abc):
+    """One step of normal numbers, whose sums of P X have both signs and are led by the diagonal's term: the
+    parts of X and P are within 2^-23 of them; what is put back for additions that are cut off is 2.4e-7
+    (128 indices) at most, and never more off than that where they lose less; S and S S, of which P is a small
+    share beside a I, with the same errors: less than half as much again."""
+    gen = torch.Generator(device="cuda").manual_seed(shape[0])
+    g = torch.randn(shape, generator=gen, device="cuda")
+    want = oo.orthogonalize(g.double().cpu(), 1, abc, 0.0)
+    x = mk.orthogonalize(g, 1, abc, eps=0.0).double().cpu().numpy()
+    off = x - want
+    size = np.linalg.norm(want)
+    assert np.linalg.norm(off) <= 1.5 * (2 * 2.0 ** -23 + 2.4e-7) * size
+    assert abs((off * want).sum()) <= 2.4e-7 * size ** 2
+
+
+@pytest.mark.parametrize("noise", [1.0, 0.1, 1e-3])
+@pytest.mark.parametrize("shape", [(64, 300), (20, 128), (128, 1000), (128, 1833), (64, 6000), (70, 2900), (129, 130), (200, 200),
+                                   (333, 501), (1024, 256), (900, 1100)])
+def test_no_more_than_twice_as_far_as_fp32(shape, noise):
+    """Five steps, weak directions of several sizes: twice the error of fp32 products is what is documented."""
+    gen = torch.Generator(device="cuda").manual_seed(sum(shape))
+    r, c = shape
+    rank = max(1, min(r, c) // 16)
+    u = torch.randn(r, rank, generator=gen, device="cuda")
+    v = torch.randn(rank, c, generator=gen, device="cuda")
+    g = u @ v / rank ** 0.5 + noise * torch.randn(r, c, generator=gen, device="cuda")
+    want = oo.orthogonalize(g.double().cpu(), 5, mk.QUINTIC)
+    torch.backends.cuda.matmul.allow_tf32 = False
+    x = g / (g.norm() + 1e-7)
+    x = x.mT if r > c else x
+    for _ in range(5):
+        s = x @ x.mT
+        x = mk.QUINTIC[0] * x + (mk.QUINTIC[1] * s + mk.QUINTIC[2] * (s @ s)) @ x
+    x = x.mT if r > c else x
+    plain = np.linalg.norm(x.double().cpu().numpy() - want)
+    here = np.linalg.norm(mk.orthogonalize(g).double().cpu().numpy() - want)
+    assert here <= max(2 * plain, 1e-6 * np.linalg.norm(want))

@@ -138,3 +138,19 @@ for x in (tensor(5, 16), tensor(5, 3, 16), strided((5, 3, 16), (16, 80, 1)), str
     dense = x.stride() not in ((60, 20, 1), (48, 0, 1))
     assert y.stride() == (x.stride() if dense else (48, 16, 1))
 """)
+
+
+def test_all_tensors_of_a_matrix_lie_alike(tmp_path):
+    """Rows consecutive in all of them or columns in all of them; else the call is refused, before the library
+    is called."""
+    run(tmp_path, r"""
+rows = lambda k: strided((6, 4), (4, 1), at=AT + k * ROOM)
+columns = lambda k: strided((6, 4), (1, 6), at=AT + k * ROOM)
+for kinds in range(1, 15):
+    made = [columns(k) if kinds >> k & 1 else rows(k) for k in range(4)]
+    assert raises(ValueError, lambda: mk.orthogonal_step(made[0], made[1], made[2], 0.1, outs=made[3])), kinds
+    if kinds in (1, 2):
+        assert raises(ValueError, lambda: mk.orthogonalize(made[0], outs=made[1])), kinds
+x, y = columns(0), columns(1)
+assert mk.orthogonalize(x, outs=y) is y and matrices(0) == [1, 4, 6, 24, 6, 0]
+""")
