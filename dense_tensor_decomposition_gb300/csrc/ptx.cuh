@@ -1,5 +1,5 @@
-// PTX of the tensor-core kernels: mbarriers with bounded waits, fences, tensor memory, and
-// tcgen05.mma on fp16 operands in 128-byte swizzled shared memory.
+// PTX of the orthogonalisation's tensor-core kernels (tc.cu has its own): mbarriers with bounded
+// waits, fences, tensor memory, and tcgen05.mma on fp16 operands in 128-byte swizzled shared memory.
 //
 // Every wait is bounded: a kernel whose wait runs out sets a bit of the device's error word,
 // stops, waits (bounded) for what it has in flight and frees its tensor memory.
