@@ -112,6 +112,15 @@ __device__ __forceinline__ void issue(uint32_t d, const Op& p, const Op& q, int 
 // slices that indices [64 t, n) of a tile have
 __device__ __forceinline__ int slices_of(int n, int t) { return min(4, (n - 64 * t + 15) / 16); }
 
+// After a wait that ran out: the MMAs that are still in flight are waited for (bounded), so that none of them
+// writes tensor memory that another kernel has by then.  bars: the accumulators' two, and one for this.
+__device__ __forceinline__ void finish(uint64_t* bars, bool aborted, int warp, uint32_t leader, uint32_t* status) {
+    if (!aborted || warp != 0) return;
+    commit<1>(&bars[2], leader);
+    if (leader != 0u) wait_drain(&bars[2], 0, status);
+    __syncwarp();
+}
+
 // a warp's sum, in all its lanes
 __device__ __forceinline__ Sum warp_total(Sum s) {
 #pragma unroll
@@ -224,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     constexpr int kAtOnce = 2;                  // tiles of the long side at once in P X
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [2] of the accumulators' buffers
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 16);
-    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + 20);
-    float2* const found = reinterpret_cast<float2*>(smem + 24);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [3] of the accumulators' two buffers, and to drain
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 24);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + 28);
+    float2* const found = reinterpret_cast<float2*>(smem + 32);
     Partial* const sums = reinterpret_cast<Partial*>(smem + 64);                // [kC]
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = kC > 1 ? rank_in_cluster() : 0u;
@@ -235,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     if (threadIdx.x == 0) {
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
+        mbar_init(&bars[2], 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -500,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         }
     }
 
+    finish(bars, *abort_flag != 0, warp, leader, a.status);
     all_sync<kC>();
     if (warp == 0) {
         tc_fence_after();
@@ -520,10 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
     constexpr int kAtOnce = 2;                  // tiles of P X at once, in each of two buffers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [2] of the accumulators' buffers
-    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 16);
-    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + 20);
-    float2* const found = reinterpret_cast<float2*>(smem + 24);
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);                   // [3] of the accumulators' two buffers, and to drain
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + 24);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(smem + 28);
+    float2* const found = reinterpret_cast<float2*>(smem + 32);
     Partial* const sums = reinterpret_cast<Partial*>(smem + 64);                // [kC]
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = kC > 1 ? rank_in_cluster() : 0u;
@@ -531,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
     if (threadIdx.x == 0) {
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
+        mbar_init(&bars[2], 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -812,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1) narrow_kernel(const __grid_consta
         }
     }
 
+    finish(bars, *abort_flag != 0, warp, leader, a.status);
     all_sync<kC>();
     if (warp == 0) {
         tc_fence_after();

@@ -111,3 +111,15 @@ def test_the_small_matrices_are_dealt_out_so():
     with open(f"{_build.CSRC}/newton_small.cu") as f:
         text = f.read()
     assert text.count("deal(") == 1 and "INT32_MAX / c" in text and "unsigned used" not in text
+
+
+def test_kernels_wait_for_what_is_in_flight_before_they_free_tensor_memory():
+    """Read, not run: no wait of these kernels may run out on a GPU.  Each that frees tensor memory waits, with a
+    limit, for its MMAs first, also where it has given up."""
+    for name, waits in (("newton.cu", "wait_drain(done, 0"), ("newton_small.cu", "finish(bars, *abort_flag != 0")):
+        with open(f"{_build.CSRC}/{name}") as f:
+            kernels = f.read().split("__global__ void")[1:]
+        freeing = [k for k in kernels if "tcgen05.dealloc" in k]
+        assert len(freeing) == (1 if name == "newton.cu" else 2)
+        for k in freeing:
+            assert 0 <= k.find(waits) < k.find("tcgen05.dealloc"), name
