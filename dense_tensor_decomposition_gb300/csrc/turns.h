@@ -1,8 +1,8 @@
 // Radians as turns in 64-bit fixed point (host).
 #pragma once
 
-#include <cmath>
 #include <cstdint>
+#include <cstring>
 
 namespace mk {
 
@@ -14,9 +14,13 @@ constexpr double kMostRadians = 18446744073709551616.0;        // 2^64
 // it that lie behind the point.
 inline uint64_t turns_of(double radians) {
     constexpr uint64_t kInverse[3] = {0x36d8a5664f10e410u, 0x7f09d5f47d4d3770u, 0x28be60db9391054au};
-    int exponent = 0;
-    const uint64_t bits = (uint64_t)std::ldexp(std::frexp(std::fabs(radians), &exponent), 53);
-    const int shift = 128 - (exponent - 53);        // of the product, to units of 2^-64: 117 at least
+    // |radians| = bits 2^exponent (read from the number itself: a call makes up to 512 of these)
+    uint64_t number;
+    std::memcpy(&number, &radians, sizeof(number));
+    const int field = (int)(number >> 52) & 0x7FF;
+    const uint64_t bits = (number & 0xFFFFFFFFFFFFFu) | (field != 0 ? (uint64_t)1 << 52 : 0);
+    const int exponent = (field != 0 ? field : 1) - 1075;
+    const int shift = 128 - exponent;               // of the product, to units of 2^-64: 117 at least
     uint64_t product[4];
     unsigned __int128 carry = 0;
     for (int i = 0; i < 3; ++i) {
