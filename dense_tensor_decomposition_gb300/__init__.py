@@ -716,6 +716,9 @@ def rotary_frequencies(dims: int, base: float = 10000.0, scaling: str | None = N
     if scaling == "turns":
         kept = (f * (length / (2 * math.pi)) - low) / (high - low)
     else:
+        if not base > 1:            # the pairs' waves do not get longer: no pair has a place between two
+            raise ValueError("scaling \"parts\" needs base > 1")
+
         def pair(turns):            # where the waves turn that often in `length` positions
             return dims * math.log(length / (2 * math.pi * turns)) / (2 * math.log(base))
         first = max(math.floor(pair(high)), 0)

@@ -101,3 +101,12 @@ def test_frequencies_out_of_range_are_refused():
     for f, code in ((2.0 ** 64, 1), (-(2.0 ** 70), 1), (1e308, 1), (2.0 ** 64 * (1 - 2.0 ** -53), 0), (-1e19, 0)):
         freqs = (ctypes.c_double * 1)(f)
         assert lib.mttkrp_rotary(1, tensors, 0, 1, 1, 2, 0x1000, 8, 0, 0, freqs, 2, 0, 1.0, 0, None) == code, f
+
+
+@pytest.mark.parametrize("base", [1.0, 0.5])
+def test_frequencies_by_parts_need_waves_that_get_longer(base):
+    mk = pytest.importorskip("dense_tensor_decomposition_gb300")
+    pytest.importorskip("torch")
+    with pytest.raises(ValueError):
+        mk.rotary_frequencies(8, base, "parts", 4.0, 1000)
+    assert len(mk.rotary_frequencies(8, base, "turns", 4.0, 1000)) == len(mk.rotary_frequencies(8, base)) == 4
